@@ -24,6 +24,12 @@ from ._lib import (  # noqa: F401
     ple_gate_conv,
     ple_lookup_shard,
     ple_select_rows,
+    ple_kv_append,
+    ple_kv_attention,
+    ple_kv_attention_workspace,
+    ple_kv_block_bytes,
+    ple_kv_read,
+    ple_proj_w4,
     ple_version,
     PLE_DEVERR_BOUNDS,
     PLE_DEVERR_QSL,

@@ -87,6 +87,14 @@ SIGNATURES = {
     "ple_step_begin": [_P, _P, _P, _I32, _P, _P, _P],
     "ple_step_end": [_P, _P, _P, _I32, _P, _P],
     "ple_step": [_P, _P, _P, _P, _I32, _P, _P, _I32, _P, _P, _P],
+    "ple_kv_block_bytes": [_I32],
+    "ple_kv_append": [_P, _I64, _P, _I64, _P, _I64, _I64, _I32, _I32, _I32, _P, _I64, _I32, _I32,
+                      _P, _P, _I64, _I32, _P, _I32, _P, _I32, _P, _P, _I64, _P, _P],
+    "ple_kv_read": [_P, _I64, _I32, _P, _I32, _P, _I32, _P, _I64, _I32, _I32, _P, _P, _P, _P],
+    "ple_kv_attention_workspace": [_I32, _I32, _I32],
+    "ple_kv_attention": [_P, _I64, _I64, _I32, _I32, _I32, _P, _I64, _I32, _P, _I32, _P, _I32, _P,
+                         _I32, _F32, _I32, _I32, _P, _I64, _P, ctypes.c_size_t, _P, _P],
+    "ple_proj_w4": [_P, _I64, _I64, _I32, _I32, _P, _P, _P, _I32, _P, _P, _P],
     "ple_last_error": [],
     "ple_version": [],
 }
@@ -120,7 +128,7 @@ def lib():
             fn = getattr(handle, name)
             fn.argtypes = args
             fn.restype = (ctypes.c_char_p if name in ("ple_last_error", "ple_version") else
-                          ctypes.c_size_t if name.endswith("_workspace") else
+                          ctypes.c_size_t if name.endswith(("_workspace", "_bytes")) else
                           None if name in _VOID else ctypes.c_int)
         _lib = handle
     return _lib
@@ -361,6 +369,152 @@ def ple_gated_conv(kv, gate, query_start_loc, w, dilation, out, conv_state=None,
         _ptr(kv), _ptr(gate), _ptr(query_start_loc), query_start_loc.numel() - 1, T, C2 // 2,
         _ptr(w), w.shape[1], int(dilation), _ptr(conv_state), _ptr(conv_state_out), _ptr(out),
         _ptr(dev_err), _stream(stream)))
+
+
+# ---- the 4-bit step of the attention block: paged cache, attention, projection ----
+
+def _heads(name, t, head_dim=None):
+    """Row stride, heads and head dim of [T, heads, head_dim] bf16 rows: the
+    heads of a row lie together, the rows any distance apart."""
+    import torch
+    if t.dim() != 3 or t.dtype != torch.bfloat16 or not t.is_cuda:
+        raise ValueError(f"{name}: a CUDA bf16 tensor [T, heads, head_dim] is needed")
+    T, H, D = t.shape
+    stride, per_head, one = t.stride()
+    if (D > 1 and one != 1) or (H > 1 and per_head != D) or (head_dim is not None and D != head_dim):
+        raise ValueError(f"{name}: heads of {head_dim or D} elements must lie together in a row")
+    return (stride if T > 1 else H * D), H, D
+
+
+def _whole(name, t, dtype, dims):
+    if t.dtype != dtype or t.dim() != dims or not t.is_contiguous() or not t.is_cuda:
+        raise ValueError(f"{name}: a contiguous CUDA {dtype} tensor of {dims} dimensions is needed")
+
+
+def _cache_args(cache, block_table, query_start_loc, kv_lens, head_dim):
+    """(num_pages, page_size, kv heads) and the pointers shared by the cache's calls."""
+    import torch
+    _whole("cache", cache, torch.uint8, 4)
+    _whole("block_table", block_table, torch.int32, 2)
+    _whole("query_start_loc", query_start_loc, torch.int32, 1)
+    _whole("kv_lens", kv_lens, torch.int32, 1)
+    pages, hk, sub, nbytes = cache.shape
+    R = query_start_loc.numel() - 1
+    if nbytes != 16 * (head_dim + 8):
+        raise ValueError(f"cache: blocks of {nbytes} bytes, not {16 * (head_dim + 8)} (head_dim {head_dim})")
+    if kv_lens.numel() != R or block_table.shape[0] != R:
+        raise ValueError(f"block_table and kv_lens must have a row for each of the {R} requests")
+    return hk, (_ptr(cache), pages, sub * 16, _ptr(block_table), block_table.shape[1],
+                _ptr(query_start_loc), R, _ptr(kv_lens))
+
+
+def ple_kv_block_bytes(head_dim):
+    """Bytes of a cache block (16 tokens of one head); the cache is a uint8
+    tensor [num_pages, num_kv_heads, page_size / 16, block bytes]."""
+    return int(lib().ple_kv_block_bytes(int(head_dim)))
+
+
+def ple_kv_append(q, k, v, cos_sin, cache, block_table, query_start_loc, kv_lens, q_out,
+                  positions=None, interleaved=False, dev_err=None, stream=None):
+    """Rotate q and k and store k and v in the 4-bit cache. q [T, H, D] (or
+    None, with q_out None), k, v [T, Hk, D] bf16 (columns of one fused
+    projection will do); cos_sin float32 [num_positions, rotary_dim] or None;
+    cache uint8 [pages, Hk, page_size / 16, 16 * (D + 8)]; block_table int32
+    [R, max_pages], query_start_loc int32 [R + 1], kv_lens int32 [R] (these
+    tokens included); q_out like q, or q itself; positions int32 [T] or None."""
+    import torch
+    k_stride, Hk, D = _heads("k", k)
+    v_stride, Hv, _ = _heads("v", v, D)
+    hk, c = _cache_args(cache, block_table, query_start_loc, kv_lens, D)
+    T = k.shape[0]
+    H = q_stride = o_stride = 0
+    if q is not None:
+        q_stride, H, _ = _heads("q", q, D)
+        o_stride = _heads("q_out", q_out, D)[0]
+        if q_out.shape != q.shape:
+            raise ValueError("q_out must have q's shape")
+    if Hk != hk or Hv != hk or v.shape[0] != T or (q is not None and q.shape[0] != T):
+        raise ValueError("q, k, v and the cache differ in tokens or kv heads")
+    if cos_sin is not None:
+        _whole("cos_sin", cos_sin, torch.float32, 2)
+    if positions is not None:
+        _whole("positions", positions, torch.int32, 1)
+        if positions.numel() != T:
+            raise ValueError("positions must have one entry for each token")
+    return _check("ple_kv_append", lib().ple_kv_append(
+        _ptr(q), q_stride, _ptr(k), k_stride, _ptr(v), v_stride, T, H, hk, D, _ptr(cos_sin),
+        0 if cos_sin is None else cos_sin.shape[0], 0 if cos_sin is None else cos_sin.shape[1],
+        int(interleaved), _ptr(positions), *c, _ptr(q_out), o_stride, _ptr(dev_err),
+        _stream(stream)))
+
+
+def ple_kv_read(cache, block_table, query_start_loc, kv_lens, k_out, v_out, dev_err=None,
+                stream=None):
+    """Values of the tokens in query_start_loc's spans out of the 4-bit cache:
+    k_out, v_out bf16 [T, Hk, D], contiguous (either may be None)."""
+    import torch
+    some = k_out if k_out is not None else v_out
+    if some is None:
+        raise ValueError("k_out or v_out is needed")
+    for name, t in (("k_out", k_out), ("v_out", v_out)):
+        if t is not None:
+            _whole(name, t, torch.bfloat16, 3)
+            if t.shape != some.shape:
+                raise ValueError("k_out and v_out differ in shape")
+    T, Hk, D = some.shape
+    hk, c = _cache_args(cache, block_table, query_start_loc, kv_lens, D)
+    if Hk != hk:
+        raise ValueError(f"{Hk} kv heads, and {hk} in the cache")
+    return _check("ple_kv_read", lib().ple_kv_read(
+        *c, T, hk, D, _ptr(k_out), _ptr(v_out), _ptr(dev_err), _stream(stream)))
+
+
+def ple_kv_attention_workspace(num_heads, num_kv_heads, head_dim):
+    """Bytes of device workspace ple_kv_attention needs (0: heads it rejects)."""
+    return int(lib().ple_kv_attention_workspace(int(num_heads), int(num_kv_heads), int(head_dim)))
+
+
+def ple_kv_attention(q, cache, block_table, query_start_loc, kv_lens, out, workspace, scale=None,
+                     causal=True, window=0, max_query_len=0, dev_err=None, stream=None):
+    """Grouped-query attention of q [T, H, D] bf16 over the 4-bit cache into
+    out [T, H, D] bf16. workspace: a device uint8 tensor of at least
+    ple_kv_attention_workspace(H, Hk, D) bytes, zero-filled before its first
+    use. scale: 1 / sqrt(D) by default; max_query_len: the most query tokens
+    of a request, if known. Other arguments as in ple_kv_append."""
+    q_stride, H, D = _heads("q", q)
+    o_stride = _heads("out", out, D)[0]
+    if out.shape != q.shape:
+        raise ValueError("out must have q's shape")
+    hk, c = _cache_args(cache, block_table, query_start_loc, kv_lens, D)
+    return _check("ple_kv_attention", lib().ple_kv_attention(
+        _ptr(q), q_stride, q.shape[0], H, hk, D, *c, int(max_query_len),
+        float(scale) if scale is not None else D ** -0.5, int(causal), int(window), _ptr(out),
+        o_stride, _ptr(workspace), workspace.numel() * workspace.element_size(), _ptr(dev_err),
+        _stream(stream)))
+
+
+def ple_proj_w4(x, codes, scales, out, zeros=None, dev_err=None, stream=None):
+    """out [T, N] bf16 = x [T, E] bf16 times the transpose of a 4-bit weight:
+    codes uint8 [N, E / 2], scales bf16 [N, E / group], zeros uint8 like
+    scales, or None for 8 everywhere."""
+    import torch
+    _whole("codes", codes, torch.uint8, 2)
+    _whole("scales", scales, torch.bfloat16, 2)
+    _whole("out", out, torch.bfloat16, 2)
+    T, E = x.shape
+    N, groups = scales.shape
+    if x.dtype != torch.bfloat16 or not x.is_cuda or (E > 1 and x.stride(1) != 1):
+        raise ValueError("x: a CUDA bf16 tensor [T, E] with its columns together is needed")
+    if codes.shape != (N, E // 2) or out.shape != (T, N) or groups < 1 or E % groups != 0:
+        raise ValueError(f"x {tuple(x.shape)}, codes {tuple(codes.shape)}, scales "
+                         f"{tuple(scales.shape)} and out {tuple(out.shape)} do not fit")
+    if zeros is not None:
+        _whole("zeros", zeros, torch.uint8, 2)
+        if zeros.shape != scales.shape:
+            raise ValueError("zeros must have the shape of scales")
+    return _check("ple_proj_w4", lib().ple_proj_w4(
+        _ptr(x), x.stride(0) if T > 1 else E, T, E, N, _ptr(codes), _ptr(scales), _ptr(zeros),
+        E // groups, _ptr(out), _ptr(dev_err), _stream(stream)))
 
 
 def ple_version():

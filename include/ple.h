@@ -15,6 +15,9 @@
  * layer with the gate's reductions moved into the projection:
  *   ple_kv_proj_gate  projection + gate scalars -> v half of kv, g [T] f32
  *   ple_gated_conv    short conv of u = g * v   -> y   [T][C] bf16
+ * Beside the layer, the 4-bit step of its attention block (near the end of
+ * this file): ple_kv_append / ple_kv_read / ple_kv_attention over a paged
+ * key/value cache in 4 bits, and ple_proj_w4, a projection with 4-bit weights.
  *
  * Sources (page titles abbreviated):
  *   PR#54517 report "[Qwen3.8-Flash-Next] Fuse Qwen4Exp PLE kernels":
@@ -635,6 +638,149 @@ ple_status ple_step(cudaStream_t copy_in, cudaStream_t compute, cudaStream_t cop
                     const ple_copy* uploads, int32_t num_uploads, ple_graph graph,
                     const ple_copy* downloads, int32_t num_downloads, cudaEvent_t loaded,
                     cudaEvent_t computed, cudaEvent_t returned);
+
+/*
+ * The 4-bit step of the attention block beside the layer: a paged key/value
+ * cache held in 4 bits (ple_kv_append writes it, ple_kv_read returns its
+ * values, ple_kv_attention attends over it) and projections with 4-bit
+ * weights (ple_proj_w4).
+ *
+ * The cache. cache is [num_pages][num_kv_heads][page_size / 16] blocks of
+ * 16 * (head_dim + 8) bytes. A block holds 16 consecutive tokens of one page
+ * and head, everything a reader of them needs in one piece:
+ *   K codes [16][head_dim / 2] bytes     V codes [16][head_dim / 2] bytes
+ *   K (scale, offset) [16][2] bf16       V (scale, offset) [16][2] bf16
+ * Element d of a row is the low half (even d) or high half (odd d) of its
+ * byte d / 2 and stands for code * scale + offset. A row x is quantised with
+ *   offset = bf16(min x), scale = bf16((max x - min x) * (1 / 15)),
+ *   code = clamp(rint((x - offset) / scale), 0, 15)   (0 where scale is 0)
+ * in float32, 1 / 15 a float32 constant; a row with a NaN or an infinity in it reads back as NaN.
+ * Position p of request r is slot p % page_size of page
+ * block_table[r][p / page_size].
+ *
+ * Tokens. Request r's tokens [query_start_loc[r], query_start_loc[r + 1])
+ * are the last n_r of the kv_lens[r] positions its cache holds once they are
+ * in it: token i of the request is position kv_lens[r] - n_r + i. Tokens at
+ * or past query_start_loc[num_reqs] are padding: nothing is stored for them
+ * and their output rows are zeros.
+ *
+ * Common arguments:
+ *   cache         16-byte aligned device memory.
+ *   num_pages     pages in it; page_size a multiple of 16.
+ *   block_table   [num_reqs][max_pages] int32 device.
+ *   query_start_loc, kv_lens  [num_reqs + 1] and [num_reqs] int32 device.
+ *   head_dim      64, 128 or 256 (else PLE_ERR_UNSUPPORTED).
+ * A position that is negative, past max_pages * page_size, or in a page
+ * outside [0, num_pages) raises PLE_DEVERR_BOUNDS: it is not written, reads
+ * as zeros, and no query sees it.
+ */
+
+/* Bytes of a block of 16 tokens: 16 * (head_dim + 8); 0 for a head_dim that
+ * the cache does not have. */
+size_t ple_kv_block_bytes(int32_t head_dim);
+
+/*
+ * ple_kv_append -- rotate the queries and keys of a step's tokens by their
+ * positions and store the keys and values in the cache.
+ *   rotation (angles in float32 from the table; elements past rotary_dim
+ *   pass through): with a, b the two elements of a pair,
+ *     a' = a cos - b sin,   b' = b cos + a sin;
+ *   pair j is elements (j, j + rotary_dim / 2), or (2j, 2j + 1) interleaved.
+ *   q, k, v       bf16 rows of num_heads (k, v: num_kv_heads) heads of
+ *                 head_dim, rows q_stride (k_stride, v_stride) elements
+ *                 apart, so columns of one fused projection can be passed.
+ *                 16-byte aligned, strides multiples of 8. q may be NULL
+ *                 (with q_out NULL): keys and values alone.
+ *   cos_sin       [num_positions][rotary_dim] float32 device, 16-byte
+ *                 aligned: the cosines of the rotary_dim / 2 pairs, then the
+ *                 sines. NULL: no rotation.
+ *   rotary_dim    a multiple of 16, at most head_dim.
+ *   positions     [num_tokens] int32 device: the positions to rotate by, or
+ *                 NULL for the positions in the cache. One outside
+ *                 [0, num_positions) raises PLE_DEVERR_BOUNDS: the token is
+ *                 not stored and its row of q_out is zeros.
+ *   q_out         bf16 rows like q's, q_out_stride apart; may be q itself
+ *                 (same pointer and stride), rotated in place.
+ * Keys are quantised from the rotated float32 values. Two tokens of one call
+ * must not fall on the same slot.
+ */
+ple_status ple_kv_append(const ple_bf16_t* q, int64_t q_stride, const ple_bf16_t* k,
+                         int64_t k_stride, const ple_bf16_t* v, int64_t v_stride,
+                         int64_t num_tokens, int32_t num_heads, int32_t num_kv_heads,
+                         int32_t head_dim, const float* cos_sin, int64_t num_positions,
+                         int32_t rotary_dim, int32_t interleaved, const int32_t* positions,
+                         void* cache, int64_t num_pages, int32_t page_size,
+                         const int32_t* block_table, int32_t max_pages,
+                         const int32_t* query_start_loc, int32_t num_reqs,
+                         const int32_t* kv_lens, ple_bf16_t* q_out, int64_t q_out_stride,
+                         int32_t* dev_err, cudaStream_t stream);
+
+/*
+ * ple_kv_read -- the keys and values of the tokens in query_start_loc's
+ * spans, out of the cache: k_out, v_out [num_tokens][num_kv_heads][head_dim]
+ * bf16, 16-byte aligned (either may be NULL), each element
+ * bf16_rn(code * scale + offset). With n_r = kv_lens[r] a whole request.
+ */
+ple_status ple_kv_read(const void* cache, int64_t num_pages, int32_t page_size,
+                       const int32_t* block_table, int32_t max_pages,
+                       const int32_t* query_start_loc, int32_t num_reqs,
+                       const int32_t* kv_lens, int64_t num_tokens, int32_t num_kv_heads,
+                       int32_t head_dim, ple_bf16_t* k_out, ple_bf16_t* v_out,
+                       int32_t* dev_err, cudaStream_t stream);
+
+/*
+ * ple_kv_attention -- grouped-query attention of a step's tokens over the
+ * cache. Query head h reads kv head h / (num_heads / num_kv_heads). For
+ * token i of request r, with last = kv_lens[r] - n_r + i (causal; else
+ * last = kv_lens[r] - 1), over the positions p with
+ * max(0, last - window + 1) <= p <= last (window 0: from 0):
+ *   out[t][h] = sum_p softmax_p(scale * <q[t][h], K[p]>) V[p].
+ * A token that sees no position gets zeros. Whatever lies in the cache past
+ * what a token sees has no influence on it.
+ *   q             bf16 rows of num_heads heads, q_stride elements apart,
+ *                 16-byte aligned, stride a multiple of 8.
+ *   scale         finite, > 0 (usually 1 / sqrt(head_dim)).
+ *   window        >= 0; not 0 only with causal.
+ *   max_query_len the largest n_r, if the host knows it; 0 if not. It picks
+ *                 the kernel; results do not depend on it.
+ *   out           bf16 rows like q's, out_stride apart, 16-byte aligned.
+ *   workspace     device scratch of ple_kv_attention_workspace(...) bytes or
+ *                 more, 256-byte aligned, ZERO-FILLED before its first use;
+ *                 each completed call leaves its counters zero, so it is
+ *                 reused with no clearing, for any sizes it has room for.
+ *                 Calls in flight at once must not share one.
+ * num_heads must be a multiple of num_kv_heads.
+ */
+size_t ple_kv_attention_workspace(int32_t num_heads, int32_t num_kv_heads, int32_t head_dim);
+ple_status ple_kv_attention(const ple_bf16_t* q, int64_t q_stride, int64_t num_tokens,
+                            int32_t num_heads, int32_t num_kv_heads, int32_t head_dim,
+                            const void* cache, int64_t num_pages, int32_t page_size,
+                            const int32_t* block_table, int32_t max_pages,
+                            const int32_t* query_start_loc, int32_t num_reqs,
+                            const int32_t* kv_lens, int32_t max_query_len, float scale,
+                            int32_t causal, int32_t window, ple_bf16_t* out,
+                            int64_t out_stride, void* workspace, size_t workspace_bytes,
+                            int32_t* dev_err, cudaStream_t stream);
+
+/*
+ * ple_proj_w4 -- out = x W^T for a weight held in 4 bits, for steps of few
+ * tokens (the weight is read once for every 64 tokens).
+ *   W[n][e] = scales[n][e / group] * (code[n][e] - zeros[n][e / group]),
+ *   float32 accumulation, bf16 result.
+ *   x        bf16 rows of in_dim, x_stride elements apart, 16-byte aligned,
+ *            stride a multiple of 8.
+ *   codes    [out_dim][in_dim / 2] bytes, 16-byte aligned; column e is the
+ *            low (even e) or high (odd e) half of byte e / 2.
+ *   scales   [out_dim][in_dim / group] bf16.
+ *   zeros    [out_dim][in_dim / group] uint8, or NULL for 8 everywhere.
+ *   group    32, 64 or 128; in_dim a multiple of it (else
+ *            PLE_ERR_UNSUPPORTED).
+ *   out      [num_tokens][out_dim] bf16.
+ */
+ple_status ple_proj_w4(const ple_bf16_t* x, int64_t x_stride, int64_t num_tokens, int32_t in_dim,
+                       int32_t out_dim, const uint8_t* codes, const ple_bf16_t* scales,
+                       const uint8_t* zeros, int32_t group, ple_bf16_t* out, int32_t* dev_err,
+                       cudaStream_t stream);
 
 /* Text of the last non-OK status on this host thread ("" if none). */
 const char* ple_last_error(void);

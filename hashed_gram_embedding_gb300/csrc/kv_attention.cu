@@ -1,16 +1,11 @@
 // ple_kv_attention: grouped-query attention over the paged 4-bit cache.
-//
-// One warp per (token, query head). Scores are taken 32 positions at a time,
-// one position per lane; with a running maximum m and sum l the softmax
-// needs one pass: o and l are scaled by exp(m_old - m_new) when m grows.
 #include "kv_cache.cuh"
 
+#include <algorithm>
 #include <cmath>
 
 namespace ple {
 namespace {
-
-constexpr int kThreads = 128;
 
 struct AttentionArgs {
   const ple_bf16_t* q;
@@ -25,81 +20,690 @@ struct AttentionArgs {
   int32_t* dev_err;
 };
 
-template <int D>
-__global__ void __launch_bounds__(kThreads)
-attention_rows_kernel(const AttentionArgs a, const KvCache c) {
-  constexpr int kPer = D / 32;  // output elements of a lane
-  __shared__ float qs[kThreads / 32][D];
+// ---------------------------------------------------------------------------
+// Few query rows: the cache split over the card
+// ---------------------------------------------------------------------------
+// Work. An item is (request, tile of 8 NT query rows, kv head); its cost is
+// the number of 32-token steps of the cache it reads. The steps of all items
+// lie on one line, cut into equal pieces, one for each CTA, so a single long
+// request and hundreds of ragged ones load the card alike. An item that a cut
+// falls into leaves partial results (row maxima, sums, unnormalised outputs)
+// in the workspace, and the CTA that arrives last joins them in the order of
+// the pieces: results do not depend on timing. Every CTA finds its piece from
+// query_start_loc and kv_lens itself: one launch, no plan on the host.
+//
+// Streams. Each of a CTA's four warps has its own share of the piece's
+// steps and its own ring of stages in shared memory; a stage is two cache
+// blocks, each one bulk copy. No warp waits for another until the item ends,
+// and the next item's first copies fly while this one's results are joined.
+//
+// Products, on warp-wide matrix instructions (16 x 8 x 16, bf16 in, f32 out;
+// the reading of the cache, not their rate, is the bound):
+//   S^T = K Q^T     16 tokens x 8 query rows
+//   O^T = V^T P^T   16 elements x 8 query rows
+// so that a group of up to 8 query heads fills a tile, and the codes are the
+// A operand of both. A code c becomes bf16(128 + c) by OR-ing it into the
+// mantissa of 128 (exact); scale and offset meet the float32 sums instead of
+// the elements:
+//   <q, K_t> = s_t (S_t - 128 sum q) + m_t sum q
+//   sum_t p_t V_t = sum_t p'_t (128 + c_t) - 136 sum_t p'_t + sum_t p_t (m_t + 8 s_t)
+// with p' = bf16(p s): the only rounding to fewer bits, and it meets codes
+// centred on 8, so that an offset far from zero costs no precision.
+// The contraction index of a product may run in any order: a lane's 16 bytes
+// of a K row are 32 neighbouring elements, and the query's fragments follow
+// that order; two tokens' V bytes are interleaved with one permute a word.
+// Token rows are taken in the order t ^ (t >> 1 & 1), which lets the V loads
+// of neighbouring lanes fall on different banks.
+constexpr int kWarps = 4;
+constexpr int kStepTokens = 2 * kBlockTokens;
+
+// NT tiles of 8 query rows a warp; registers and shared memory set the CTAs an SM holds.
+template <int D, int NT>
+struct Split {
+  static constexpr int kRows = 8 * NT;
+  static constexpr int kStage = 2 * KvBlock<D>::kBytes;
+  static constexpr int kCtas = D == 256 || NT * D > 256 ? 2 : NT * D > 128 ? 3 : 4;  // per SM
+  static constexpr int kStages = D == 256 ? 2 : D == 64 || NT == 4 ? 4 : NT == 2 ? 3 : 2;
+  static constexpr bool kQRegs = NT * D <= 256;      // query fragments in registers
+  static constexpr int kPass = 8;                    // rows joined at a time
+  static constexpr int kGroup = D / 8 + 2;           // a lane group's elements, padded
+  static constexpr int kPitch = 8 * kGroup + 4;      // floats of a row in the joining buffer
+  static constexpr int kRing = kWarps * kStages * kStage;
+  static constexpr int kFrags = NT * (D / 16) * 32 * 8;  // bytes of query fragments
+  static constexpr int kJoin = kWarps * kPass * kPitch * 4;
+  static constexpr int kMl = kWarps * kRows * 8;
+  static constexpr int kSmem = kRing + kFrags + kJoin + kMl + kRows * 4 + kWarps * kStages * 8 + 16;
+};
+
+__device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                         uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Codes i and i + 4 of a word (i = 0..3) as bf16 pair (128 + c).
+__device__ __forceinline__ uint32_t code_pair(uint32_t word, int i) {
+  return ((word >> (4 * i)) & 0x000F000Fu) | 0x43004300u;
+}
+
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+  uint32_t y;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+
+// What a request asks of the kernel: steps [step0, step0 + steps) of the cache
+// for each of its tiles x kv heads.
+struct Span {
+  int64_t t0;      // first token
+  int n;           // tokens
+  int64_t len;     // cached positions
+  int step0, steps;
+  int tiles;
+  bool clipped;    // kv_lens past the block table
+};
+
+__device__ __forceinline__ Span span_of(const AttentionArgs& a, const KvCache& c, int r, int tile_rows) {
+  Span s;
+  int64_t end;
+  request_span(c.qsl, c.num_reqs + 1, a.T, r, &s.t0, &end);
+  s.n = static_cast<int>(end - s.t0);
+  s.len = __ldg(c.kv_lens + r);
+  const int64_t room = static_cast<int64_t>(c.max_pages) * c.page_size;
+  int64_t hi = s.len;
+  s.clipped = hi > room;
+  if (hi > room) hi = room;
+  int64_t lo = 0;
+  if (a.window > 0) lo = s.len - s.n - a.window + 1;
+  if (lo < 0) lo = 0;
+  s.step0 = static_cast<int>(lo / kStepTokens);
+  s.steps = hi > lo ? static_cast<int>((hi + kStepTokens - 1) / kStepTokens) - s.step0 : 0;
+  const int64_t rows = static_cast<int64_t>(s.n) * (a.num_heads / c.num_kv_heads);
+  s.tiles = static_cast<int>((rows + tile_rows - 1) / tile_rows);
+  return s;
+}
+
+__device__ __forceinline__ int64_t weight_of(const Span& s, int hk) {
+  return static_cast<int64_t>(s.tiles) * hk * (s.steps > 0 ? s.steps : 1);
+}
+
+template <int D, int NT>
+__global__ void __launch_bounds__(kWarps * 32, (Split<D, NT>::kCtas))
+attention_split_kernel(const AttentionArgs a, const KvCache c, unsigned* __restrict__ counters,
+                       float* __restrict__ partial) {
+  using L = Split<D, NT>;
+  using B = KvBlock<D>;
+  constexpr int kRows = L::kRows;
+  constexpr int kWords = D / 32;   // K words of a lane and token
+  constexpr int kVWords = D / 64;  // V words of a lane and token
+  extern __shared__ __align__(128) uint8_t smem[];
+  uint2* qf = reinterpret_cast<uint2*>(smem + L::kRing);
+  float* join = reinterpret_cast<float*>(smem + L::kRing + L::kFrags);
+  float2* ml = reinterpret_cast<float2*>(smem + L::kRing + L::kFrags + L::kJoin);
+  float* qsum = reinterpret_cast<float*>(smem + L::kRing + L::kFrags + L::kJoin + L::kMl);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
+  const int g = lane >> 2, j = lane & 3;
+  uint8_t* ring = smem + warp * L::kStages * L::kStage;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::kSmem - 16 - kWarps * L::kStages * 8);
+  const uint32_t bar0 = smem_u32(bars + warp * L::kStages);
+  int64_t* total = reinterpret_cast<int64_t*>(smem + L::kSmem - 16);
+  int* last_flag = reinterpret_cast<int*>(smem + L::kSmem - 8);
+
+  if (lane == 0) {
+    for (int s = 0; s < L::kStages; ++s) mbar_init(bar0 + 8 * s, 1);
+    mbar_fence_init();
+  }
+  if (threadIdx.x == 0) *total = 0;
+  __syncthreads();
   pdl_wait();
   pdl_trigger();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
-  const int64_t row = int64_t(blockIdx.x) * (kThreads / 32) + warp;
-  if (row >= a.T * a.num_heads) return;
-  const int64_t t = row / a.num_heads;
-  const int h = static_cast<int>(row % a.num_heads);
-  const int hk = h / (a.num_heads / c.num_kv_heads);
-  if (h == 0)
-    for (int64_t i = t * 32 + lane; i < c.num_reqs; i += a.T * 32) check_qsl(c.qsl, c.num_reqs, a.T, i, a.dev_err);
-  for (int i = lane; i < D; i += 32) qs[warp][i] = bf_lo(a.q[t * a.q_stride + int64_t(h) * D + i]);
-  __syncwarp();
-  float o[kPer] = {};
-  float m = -INFINITY, l = 0.0f;
-  const int r = request_of(c.qsl, c.num_reqs, t);
-  if (r >= 0) {
-    const int64_t len = __ldg(c.kv_lens + r);
-    const int64_t last = a.causal ? len - (__ldg(c.qsl + r + 1) - t) : len - 1;
-    const int64_t first = a.window > 0 && last - a.window + 1 > 0 ? last - a.window + 1 : 0;
-    for (int64_t p0 = first; p0 <= last; p0 += 32) {
-      const int64_t p = p0 + lane;
-      float s = -INFINITY;
-      const uint8_t* block = p <= last ? kv_block<D>(c, r, p, hk) : nullptr;
-      if (p <= last && block == nullptr) set_dev_err(a.dev_err, PLE_DEVERR_BOUNDS);
-      const int slot = static_cast<int>(p % kBlockTokens);
-      uint32_t vpair = 0;
-      if (block != nullptr) {
-        const uint32_t pair = *reinterpret_cast<const uint32_t*>(block + KvBlock<D>::kPairs + slot * 4);
-        vpair = *reinterpret_cast<const uint32_t*>(block + KvBlock<D>::kVPairs + slot * 4);
-        const uint32_t* k = reinterpret_cast<const uint32_t*>(block + slot * KvBlock<D>::kRow);
-        s = 0.0f;
-        for (int w = 0; w < D / 8; ++w) {
-          const uint32_t word = k[w];
+
+  const int G = a.num_heads / c.num_kv_heads;
+  const int hk = c.num_kv_heads;
+  // all items' steps
+  {
+    int64_t mine = 0;
+    for (int r = threadIdx.x; r < c.num_reqs; r += kWarps * 32) mine += weight_of(span_of(a, c, r, kRows), hk);
 #pragma unroll
-          for (int i = 0; i < 8; ++i)
-            s = fmaf(qs[warp][w * 8 + i], fmaf(static_cast<float>((word >> (4 * i)) & 15u), bf_lo(pair), bf_hi(pair)), s);
-        }
-        s *= a.scale_log2;
+    for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
+    if (lane == 0 && mine > 0) atomicAdd(reinterpret_cast<unsigned long long*>(total), static_cast<unsigned long long>(mine));
+    for (int64_t i = int64_t(blockIdx.x) * (kWarps * 32) + threadIdx.x; i < c.num_reqs; i += int64_t(gridDim.x) * (kWarps * 32))
+      check_qsl(c.qsl, c.num_reqs, a.T, i, a.dev_err);
+    // padding tokens' rows
+    int64_t pad = __ldg(c.qsl + c.num_reqs);
+    pad = pad < 0 ? 0 : pad;
+    const int64_t vecs = static_cast<int64_t>(a.num_heads) * (D / 8);
+    for (int64_t i = pad * vecs + int64_t(blockIdx.x) * (kWarps * 32) + threadIdx.x; i < a.T * vecs;
+         i += int64_t(gridDim.x) * (kWarps * 32))
+      *reinterpret_cast<uint4*>(a.out + i / vecs * a.out_stride + i % vecs * 8) = make_uint4(0, 0, 0, 0);
+  }
+  __syncthreads();
+  const int64_t W = *total;
+  // pieces of at least one step for each warp
+  const int64_t most = (W + kWarps - 1) / kWarps;
+  const int64_t S = most < gridDim.x ? most : gridDim.x;
+  if (blockIdx.x >= S) return;
+  int64_t x = blockIdx.x * W / S;
+  const int64_t x_end = (blockIdx.x + 1) * W / S;
+
+  // the request that x lies in; base: its first step on the line
+  int r = 0;
+  int64_t base = 0;
+  auto seek = [&]() {  // from request r at base on, the first request that ends past x
+    for (;;) {
+      int64_t w = r + lane < c.num_reqs ? weight_of(span_of(a, c, r + lane, kRows), hk) : 0;
+      int64_t sum = w;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t up = __shfl_up_sync(0xffffffffu, sum, o);
+        if (lane >= o) sum += up;
       }
-      float top = s;
+      const unsigned past = __ballot_sync(0xffffffffu, base + sum > x);
+      if (past != 0) {
+        const int at = __ffs(past) - 1;
+        base += __shfl_sync(0xffffffffu, sum - w, at);
+        r += at;
+        return;
+      }
+      base += __shfl_sync(0xffffffffu, sum, 31);
+      r += 32;
+      if (r >= c.num_reqs) return;  // not reached: x < W
+    }
+  };
+
+  // A CTA's share of one item.
+  struct Segment {
+    Span s;
+    int r, tile, h;
+    int from, to;       // steps of the item, relative to s.step0
+    int pieces, first;  // CTAs that share the item, the first of them
+    bool at_start;      // begins where this CTA's piece begins
+    bool item_at_start; // the item begins where the first CTA's piece begins
+  };
+  auto segment_at = [&]() {
+    Segment q;
+    q.s = span_of(a, c, r, kRows);
+    q.r = r;
+    const int per = q.s.steps > 0 ? q.s.steps : 1;
+    const int64_t item = (x - base) / per;
+    q.tile = static_cast<int>(item / hk);
+    q.h = static_cast<int>(item % hk);
+    const int64_t i0 = base + item * per, i1 = i0 + per;
+    q.from = static_cast<int>(x - i0);
+    q.to = static_cast<int>((x_end < i1 ? x_end : i1) - i0);
+    q.at_start = x == blockIdx.x * W / S;
+    q.first = static_cast<int>(((i0 + 1) * S - 1) / W);
+    q.item_at_start = i0 == q.first * W / S;
+    q.pieces = static_cast<int>((i1 * S - 1) / W) - q.first + 1;
+    if (q.s.steps == 0) q.to = q.from;  // nothing to read
+    return q;
+  };
+
+  // this warp's copies
+  const int per_page = c.page_size / kBlockTokens;
+  uint32_t phases = 0, armed = 0, present = 0;  // by stage: parity, a copy issued, blocks present (2 bits)
+  bool dead = false;                            // a wait gave up: no more copies
+  int issue_step = 0, issue_end = 0;            // absolute steps
+  int pages_at = 0;                             // first block of `pages`
+  int pages = -1, pages_next = -1;              // lane's page of blocks pages_at + lane and + 32
+  const int32_t* table = c.block_table;
+  int block_end = 0;                            // blocks that hold positions
+  int issue_h = 0;
+  int stage_in = 0, stage_out = 0;
+  auto page_at = [&](int block) { return block < block_end ? __ldg(table + block / per_page) : -1; };
+  auto issue = [&]() {
+    if (issue_step >= issue_end || dead) return;
+    const int b = 2 * issue_step;
+    if (b - pages_at >= 32) {
+      pages_at += 32;
+      pages = pages_next;
+      pages_next = page_at(pages_at + 32 + lane);
+    }
+    const int mine = b + (lane & 1);
+    const int64_t page = __shfl_sync(0xffffffffu, pages, mine - pages_at);
+    const bool wanted = lane < 2 && mine < block_end;
+    const bool ok = wanted && page >= 0 && page < c.num_pages;
+    if (wanted && !ok) set_dev_err(a.dev_err, PLE_DEVERR_BOUNDS);
+    const unsigned mask = __ballot_sync(0xffffffffu, ok);
+    const uint32_t bar = bar0 + 8 * stage_in;
+    if (lane == 0) mbar_arrive_expect_tx(bar, __popc(mask) * B::kBytes);
+    __syncwarp();
+    if (ok) {
+      const int64_t block = (page * hk + issue_h) * per_page + mine % per_page;
+      bulk_copy_g2s(smem_u32(ring + stage_in * L::kStage + lane * B::kBytes), c.base + block * B::kBytes,
+                    B::kBytes, bar);
+    }
+    present = (present & ~(3u << (2 * stage_in))) | (mask << (2 * stage_in));
+    armed |= 1u << stage_in;
+    ++issue_step;
+    if (++stage_in == L::kStages) stage_in = 0;
+  };
+  auto share = [&](const Segment& q, int& from, int& to) {  // of this warp
+    const int per = (q.to - q.from + kWarps - 1) / kWarps;
+    from = min(q.from + warp * per, q.to);
+    to = min(from + per, q.to);
+  };
+  auto start = [&](const Segment& q) {
+    int from, to;
+    share(q, from, to);
+    issue_step = q.s.step0 + from;
+    issue_end = q.s.step0 + to;
+    issue_h = q.h;
+    table = c.block_table + static_cast<int64_t>(q.r) * c.max_pages;
+    const int64_t room = static_cast<int64_t>(c.max_pages) * per_page;
+    const int64_t blocks = (q.s.len + kBlockTokens - 1) / kBlockTokens;
+    block_end = static_cast<int>(blocks < room ? blocks : room);
+    if (q.s.clipped && lane == 0) set_dev_err(a.dev_err, PLE_DEVERR_BOUNDS);
+    pages_at = 2 * issue_step;
+    if (issue_step < issue_end) {
+      pages = page_at(pages_at + lane);
+      pages_next = page_at(pages_at + 32 + lane);
+    }
+#pragma unroll 1
+    for (int s = 0; s < L::kStages; ++s) issue();
+  };
+
+  seek();
+  Segment q = segment_at();
+  start(q);
+  for (;;) {
+    // the tile's query rows as B fragments, and their sums
+    const int rows = min(kRows, static_cast<int>(static_cast<int64_t>(q.s.n) * G - static_cast<int64_t>(q.tile) * kRows));
+    for (int nt = warp; nt < NT; nt += kWarps) {
+      const int rr = nt * 8 + g;
+      const int64_t flat = static_cast<int64_t>(q.tile) * kRows + rr;
+      const ple_bf16_t* src = a.q + (q.s.t0 + flat / G) * a.q_stride + (static_cast<int64_t>(q.h) * G + flat % G) * D + j * (D / 4);
+      float sum = 0.0f;
 #pragma unroll
-      for (int x = 16; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
-      const float next = fmaxf(m, top);
-      const float base = next == -INFINITY ? 0.0f : next;
-      const float keep = exp2f(m - base);
-      const float w = block != nullptr ? exp2f(s - base) : 0.0f;
-      l = l * keep + warp_sum(w);
-      m = next;
+      for (int w = 0; w < kWords; ++w) {
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if (rr < rows) v = *reinterpret_cast<const uint4*>(src + 8 * w);
+        float f[8];
+        unpack8(v, f);
 #pragma unroll
-      for (int i = 0; i < kPer; ++i) o[i] *= keep;
-      for (int i = 0; i < 32; ++i) {
-        const uint64_t at = __shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(block), i);
-        if (at == 0) continue;
-        const float wi = __shfl_sync(0xffffffffu, w, i);
-        const uint32_t pair = __shfl_sync(0xffffffffu, vpair, i);
-        const uint8_t* v = reinterpret_cast<const uint8_t*>(at) + KvBlock<D>::kV +
-                           static_cast<int>((p0 + i) % kBlockTokens) * KvBlock<D>::kRow;
+        for (int i = 0; i < 8; ++i) sum += f[i];
+        qf[((2 * w) * NT + nt) * 32 + lane] = make_uint2(__byte_perm(v.x, v.z, 0x5410), __byte_perm(v.x, v.z, 0x7632));
+        qf[((2 * w + 1) * NT + nt) * 32 + lane] = make_uint2(__byte_perm(v.y, v.w, 0x5410), __byte_perm(v.y, v.w, 0x7632));
+      }
+      sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+      sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+      if (j == 0) qsum[rr] = sum;
+    }
+    __syncthreads();
+    uint2 qr[L::kQRegs ? NT * (D / 16) : 1];
+    if constexpr (L::kQRegs) {
 #pragma unroll
-        for (int n = 0; n < kPer; n += 2) {
-          const uint32_t b = v[lane * (kPer / 2) + n / 2];
-          o[n] = fmaf(wi, fmaf(static_cast<float>(b & 15u), bf_lo(pair), bf_hi(pair)), o[n]);
-          o[n + 1] = fmaf(wi, fmaf(static_cast<float>(b >> 4), bf_lo(pair), bf_hi(pair)), o[n + 1]);
+      for (int i = 0; i < NT * (D / 16); ++i) qr[i] = qf[i * 32 + lane];
+    }
+    float sq[2 * NT];
+    int last[2 * NT];  // the last position of each of this lane's rows
+#pragma unroll
+    for (int i = 0; i < 2 * NT; ++i) {
+      const int rr = (i / 2) * 8 + 2 * j + (i & 1);
+      sq[i] = qsum[rr];
+      const int64_t tok = (static_cast<int64_t>(q.tile) * kRows + rr) / G;
+      const int64_t p = a.causal ? q.s.len - q.s.n + tok : q.s.len - 1;
+      last[i] = rr < rows ? static_cast<int>(p) : -1;
+    }
+    // positions that every row of the tile sees: [all_from, all_to]
+    const int64_t tok0 = static_cast<int64_t>(q.tile) * kRows / G;
+    const int64_t tok1 = (static_cast<int64_t>(q.tile) * kRows + rows - 1) / G;
+    const int64_t all_to = a.causal ? q.s.len - q.s.n + tok0 : q.s.len - 1;
+    const int64_t all_from = a.window > 0 ? q.s.len - q.s.n + tok1 - a.window + 1 : 0;
+
+    float o[NT][D / 16][4];
+    float ones[NT][4];  // column sums of the rounded weights
+    float m[2 * NT], l[2 * NT], off[2 * NT];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+#pragma unroll
+      for (int u = 0; u < D / 16; ++u)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[n][u][i] = 0.0f;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) ones[n][i] = 0.0f;
+    }
+#pragma unroll
+    for (int i = 0; i < 2 * NT; ++i) { m[i] = -INFINITY; l[i] = 0.0f; off[i] = 0.0f; }
+
+    int from, to;
+    share(q, from, to);
+#pragma unroll 1
+    for (int step = from; step < to; ++step) {
+      const int64_t p0 = static_cast<int64_t>(q.s.step0 + step) * kStepTokens;
+      uint32_t here = 0;
+      if (!dead) {
+        const bool ok = mbar_try_wait(bar0 + 8 * stage_out, (phases >> stage_out) & 1u) ||
+                        mbar_wait(bar0 + 8 * stage_out, (phases >> stage_out) & 1u, nullptr);
+        if (__all_sync(0xffffffffu, ok)) {
+          here = (present >> (2 * stage_out)) & 3u;
+          phases ^= 1u << stage_out;
+          armed &= ~(1u << stage_out);
+        } else {
+          dead = true;
+          if (lane == 0) set_dev_err(a.dev_err, PLE_DEVERR_TIMEOUT);
+        }
+      }
+      const uint8_t* st = ring + stage_out * L::kStage;
+      const bool masked = here != 3u || p0 < all_from || p0 + kStepTokens - 1 > all_to;
+      if (here != 0) {
+        const int r0 = g ^ ((g >> 1) & 1);  // token of row g
+        float s[NT][2][4];                  // [query tile][block][(token r0, r0 + 8) x (row 2j, 2j + 1)]
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) s[n][b][i] = 0.0f;
+          const uint8_t* kb = st + b * B::kBytes;
+          uint32_t lo[kWords], hi[kWords];
+          {
+            const uint8_t* p = kb + r0 * B::kRow + j * (D / 8);
+            const uint8_t* p8 = p + 8 * B::kRow;
+            if constexpr (kWords >= 4) {
+#pragma unroll
+              for (int w = 0; w < kWords; w += 4) {
+                *reinterpret_cast<uint4*>(lo + w) = *reinterpret_cast<const uint4*>(p + 4 * w);
+                *reinterpret_cast<uint4*>(hi + w) = *reinterpret_cast<const uint4*>(p8 + 4 * w);
+              }
+            } else {
+              *reinterpret_cast<uint2*>(lo) = *reinterpret_cast<const uint2*>(p);
+              *reinterpret_cast<uint2*>(hi) = *reinterpret_cast<const uint2*>(p8);
+            }
+          }
+#pragma unroll
+          for (int w = 0; w < kWords; ++w)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const uint32_t a0 = code_pair(lo[w], 2 * h), a1 = code_pair(hi[w], 2 * h);
+              const uint32_t a2 = code_pair(lo[w], 2 * h + 1), a3 = code_pair(hi[w], 2 * h + 1);
+#pragma unroll
+              for (int n = 0; n < NT; ++n) {
+                uint2 f;
+                if constexpr (L::kQRegs) f = qr[(2 * w + h) * NT + n];
+                else f = qf[((2 * w + h) * NT + n) * 32 + lane];
+                mma16816(s[n][b], a0, a1, a2, a3, f.x, f.y);
+              }
+            }
+        }
+        // scores in units of log2: scale and offset, then the mask
+        float vs[2][2], vm[2][2];  // the values' scale, and offset + 8 scales
+        uint32_t unseen = 0;       // bit (query tile, block, token, row)
+#pragma unroll
+        for (int b = 0; b < 2; ++b)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int tok = r0 + 8 * e;
+            const uint32_t kp = *reinterpret_cast<const uint32_t*>(st + b * B::kBytes + B::kPairs + tok * 4);
+            const uint32_t vp = *reinterpret_cast<const uint32_t*>(st + b * B::kBytes + B::kVPairs + tok * 4);
+            const float ks = bf_lo(kp) * a.scale_log2;
+            const float km = fmaf(-128.0f, ks, bf_hi(kp) * a.scale_log2);
+            vs[b][e] = bf_lo(vp);
+            vm[b][e] = fmaf(8.0f, bf_lo(vp), bf_hi(vp));
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                float& v = s[n][b][2 * e + i];
+                v = fmaf(ks, v, km * sq[2 * n + i]);
+              }
+            if (masked) {
+              const int64_t p = p0 + b * kBlockTokens + tok;
+              const bool there = (here >> b) & 1u;
+#pragma unroll
+              for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                  const int64_t q_last = last[2 * n + i];
+                  if (!there || p > q_last || (a.window > 0 && p <= q_last - a.window)) {
+                    s[n][b][2 * e + i] = -INFINITY;
+                    unseen |= 1u << (n * 8 + b * 4 + e * 2 + i);
+                  }
+                }
+            }
+          }
+        // The running maximum is raised only when a score passes it by 2^8:
+        // weights of up to 256 cost no precision in float32 or bf16, and a
+        // step without a raise needs no exchange between lanes.
+        bool raise = false;
+        float top[2 * NT];
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const float t = fmaxf(fmaxf(s[n][0][i], s[n][0][2 + i]), fmaxf(s[n][1][i], s[n][1][2 + i]));
+            top[2 * n + i] = t;
+            raise |= t > m[2 * n + i] + 8.0f;
+          }
+        if (__any_sync(0xffffffffu, raise)) {
+#pragma unroll
+          for (int i = 0; i < 2 * NT; ++i) {
+            float t = top[i];
+#pragma unroll
+            for (int x = 4; x < 32; x <<= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, x));
+            const float next = fmaxf(m[i], t);
+            const float keep = next == -INFINITY ? 1.0f : ex2(m[i] - next);
+            m[i] = next;
+            l[i] *= keep;
+            off[i] *= keep;
+            const int n = i / 2, e = i & 1;
+            ones[n][e] *= keep;
+            ones[n][2 + e] *= keep;
+#pragma unroll
+            for (int u = 0; u < D / 16; ++u) { o[n][u][e] *= keep; o[n][u][2 + e] *= keep; }
+          }
+        }
+        uint32_t pt[NT][2][2];  // weights times the values' scale, bf16, as B fragments
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int b = 0; b < 2; ++b) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              float w[2];
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                const float mi = m[2 * n + i] == -INFINITY ? 0.0f : m[2 * n + i];
+                const float p = ex2(s[n][b][2 * e + i] - mi);
+                // a value that is not seen meets no weight, not even zero: it may be NaN
+                const bool skip = masked && ((unseen >> (n * 8 + b * 4 + e * 2 + i)) & 1u);
+                l[2 * n + i] += p;
+                off[2 * n + i] = skip ? off[2 * n + i] : fmaf(p, vm[b][e], off[2 * n + i]);
+                w[i] = skip ? 0.0f : p * vs[b][e];
+              }
+              pt[n][b][e] = transpose8x8(pack2(w[0], w[1]));
+            }
+          }
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+          const uint8_t* vb = st + b * B::kBytes + B::kV + g * (D / 16);
+          uint32_t v[4][kVWords];  // tokens 2j, 2j + 1, 2j + 8, 2j + 9 in the rows' order
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int row = 2 * j + (i & 1);
+            const uint8_t* p = vb + ((row ^ ((row >> 1) & 1)) + 8 * (i >> 1)) * B::kRow;
+            if constexpr (kVWords == 4) *reinterpret_cast<uint4*>(v[i]) = *reinterpret_cast<const uint4*>(p);
+            else if constexpr (kVWords == 2) *reinterpret_cast<uint2*>(v[i]) = *reinterpret_cast<const uint2*>(p);
+            else v[i][0] = *reinterpret_cast<const uint32_t*>(p);
+          }
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+            mma16816(ones[n], 0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u, pt[n][b][0], pt[n][b][1]);
+#pragma unroll
+          for (int w = 0; w < kVWords; ++w)
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+              const unsigned sel = half == 0 ? 0x5410u : 0x7632u;
+              const uint32_t x0 = __byte_perm(v[0][w], v[1][w], sel), x1 = __byte_perm(v[2][w], v[3][w], sel);
+#pragma unroll
+              for (int k = 0; k < 2; ++k) {
+                const uint32_t a0 = code_pair(x0, 2 * k), a1 = code_pair(x0, 2 * k + 1);
+                const uint32_t a2 = code_pair(x1, 2 * k), a3 = code_pair(x1, 2 * k + 1);
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+                  mma16816(o[n][w * 4 + half * 2 + k], a0, a1, a2, a3, pt[n][b][0], pt[n][b][1]);
+              }
+            }
+        }
+      }
+      __syncwarp();  // every lane has read the stage
+      if (++stage_out == L::kStages) stage_out = 0;
+      issue();
+    }
+
+    // the next item's copies fly while this one's results are joined
+    const Segment cur = q;
+    const int cur_rows = rows;
+    x += cur.to > cur.from ? cur.to - cur.from : 1;
+    const bool more = x < x_end;
+    if (more) {
+      const int per = cur.s.steps > 0 ? cur.s.steps : 1;
+      const int64_t end = base + static_cast<int64_t>(cur.s.tiles) * hk * per;
+      if (x >= end) {
+        base = end;
+        ++r;
+        seek();
+      }
+      q = segment_at();
+      start(q);
+    }
+
+    // join the warps
+#pragma unroll
+    for (int i = 0; i < 2 * NT; ++i) {
+#pragma unroll
+      for (int sh = 4; sh < 32; sh <<= 1) {
+        l[i] += __shfl_xor_sync(0xffffffffu, l[i], sh);
+        off[i] += __shfl_xor_sync(0xffffffffu, off[i], sh);
+      }
+      off[i] = fmaf(-136.0f, ones[i / 2][i & 1], off[i]);
+      if (g == 0) ml[warp * kRows + (i / 2) * 8 + 2 * j + (i & 1)] = make_float2(m[i], l[i]);
+    }
+    const int slot = 2 * blockIdx.x + (cur.at_start ? 0 : 1);
+    float* part = partial + static_cast<int64_t>(slot) * kRows * (D + 2);
+#pragma unroll
+    for (int pass = 0; pass < kRows / L::kPass; ++pass) {
+      __syncthreads();  // ml is written; the last pass's readers are done
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        if (n * 8 / L::kPass != pass) continue;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float* dst = join + (warp * L::kPass + n * 8 % L::kPass + 2 * j + e) * L::kPitch + g * L::kGroup;
+#pragma unroll
+          for (int u = 0; u < D / 16; ++u)
+            *reinterpret_cast<float2*>(dst + 2 * u) = make_float2(o[n][u][e] + off[2 * n + e], o[n][u][2 + e] + off[2 * n + e]);
+        }
+      }
+      __syncthreads();
+      // four elements a thread
+      for (int i = threadIdx.x; i < L::kPass * (D / 4); i += kWarps * 32) {
+        const int pr = i / (D / 4), d = i % (D / 4) * 4;
+        const int rr = pass * L::kPass + pr;
+        if (rr >= cur_rows) break;
+        float top = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) top = fmaxf(top, ml[w * kRows + rr].x);
+        const float safe = top == -INFINITY ? 0.0f : top;
+        float sum = 0.0f;
+        float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+          const float2 t = ml[w * kRows + rr];
+          const float k = ex2(t.x - safe);
+          sum = fmaf(k, t.y, sum);
+          const float* src = join + (w * L::kPass + pr) * L::kPitch + d + 2 * (d / (D / 8));
+          const float2 u0 = *reinterpret_cast<const float2*>(src), u1 = *reinterpret_cast<const float2*>(src + 2);
+          v.x = fmaf(k, u0.x, v.x); v.y = fmaf(k, u0.y, v.y); v.z = fmaf(k, u1.x, v.z); v.w = fmaf(k, u1.y, v.w);
+        }
+        if (cur.pieces == 1) {
+          const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+          const int64_t flat = static_cast<int64_t>(cur.tile) * kRows + rr;
+          ple_bf16_t* dst = a.out + (cur.s.t0 + flat / G) * a.out_stride + (static_cast<int64_t>(cur.h) * G + flat % G) * D + d;
+          *reinterpret_cast<uint2*>(dst) = make_uint2(pack2(v.x * inv, v.y * inv), pack2(v.z * inv, v.w * inv));
+        } else {
+          *reinterpret_cast<float4*>(part + rr * D + d) = v;
+          if (d == 0) *reinterpret_cast<float2*>(part + kRows * D + 2 * rr) = make_float2(top, sum);
         }
       }
     }
+    if (cur.pieces > 1) {
+      __threadfence();
+      __syncthreads();
+      if (threadIdx.x == 0) *last_flag = atomicAdd(counters + cur.first, 1u) == static_cast<unsigned>(cur.pieces - 1);
+      __syncthreads();
+      if (*last_flag) {
+        __threadfence();
+        if (threadIdx.x == 0) counters[cur.first] = 0;
+        for (int i = threadIdx.x; i < cur_rows * (D / 4); i += kWarps * 32) {
+          const int rr = i / (D / 4), d = i % (D / 4) * 4;
+          float top = -INFINITY, sum = 0.0f;
+          float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+          for (int k = 0; k < cur.pieces; ++k) {
+            const int sl = 2 * (cur.first + k) + (k == 0 && !cur.item_at_start ? 1 : 0);
+            const float* src = partial + static_cast<int64_t>(sl) * kRows * (D + 2);
+            const float2 t = __ldcg(reinterpret_cast<const float2*>(src + kRows * D + 2 * rr));
+            const float4 u = __ldcg(reinterpret_cast<const float4*>(src + rr * D + d));
+            const float next = fmaxf(top, t.x);
+            const float safe = next == -INFINITY ? 0.0f : next;
+            const float ka = ex2(top - safe), kb = ex2(t.x - safe);
+            sum = fmaf(kb, t.y, sum * ka);
+            v.x = fmaf(kb, u.x, v.x * ka); v.y = fmaf(kb, u.y, v.y * ka);
+            v.z = fmaf(kb, u.z, v.z * ka); v.w = fmaf(kb, u.w, v.w * ka);
+            top = next;
+          }
+          const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+          const int64_t flat = static_cast<int64_t>(cur.tile) * kRows + rr;
+          ple_bf16_t* dst = a.out + (cur.s.t0 + flat / G) * a.out_stride + (static_cast<int64_t>(cur.h) * G + flat % G) * D + d;
+          *reinterpret_cast<uint2*>(dst) = make_uint2(pack2(v.x * inv, v.y * inv), pack2(v.z * inv, v.w * inv));
+        }
+      }
+    }
+    __syncthreads();  // the buffers are free for the next item
+    if (!more) break;
   }
-  const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-  ple_bf16_t* dst = a.out + t * a.out_stride + int64_t(h) * D + lane * kPer;
-#pragma unroll
-  for (int i = 0; i < kPer; i += 2) *reinterpret_cast<uint32_t*>(dst + i) = pack2(o[i] * inv, o[i + 1] * inv);
+  // never leave with a copy in flight
+  for (int s = 0; s < L::kStages; ++s)
+    if ((armed >> s) & 1u) mbar_wait(bar0 + 8 * s, (phases >> s) & 1u, nullptr);
+}
+
+constexpr int kMaxCtas = 4;  // per SM, of any variant
+
+size_t counter_bytes() { return (size_t(num_sms()) * kMaxCtas * 4 + 255) / 256 * 256; }
+
+template <int D, int NT>
+size_t partial_bytes() {
+  return size_t(num_sms()) * Split<D, NT>::kCtas * 2 * Split<D, NT>::kRows * (D + 2) * 4;
+}
+
+// Counters, then two partial results a CTA of the variant that needs most.
+size_t workspace_bytes_of(int head_dim) {
+  size_t n = 0;
+  if (head_dim == 64) n = std::max(partial_bytes<64, 1>(), std::max(partial_bytes<64, 2>(), partial_bytes<64, 4>()));
+  if (head_dim == 128) n = std::max(partial_bytes<128, 1>(), std::max(partial_bytes<128, 2>(), partial_bytes<128, 4>()));
+  if (head_dim == 256) n = std::max(partial_bytes<256, 1>(), partial_bytes<256, 2>());
+  return counter_bytes() + (n + 255) / 256 * 256;
+}
+
+template <int D, int NT>
+cudaError_t launch_split(const AttentionArgs& a, const KvCache& c, unsigned* counters, float* partial,
+                         cudaStream_t stream) {
+  using L = Split<D, NT>;
+  const auto kernel = attention_split_kernel<D, NT>;
+  const cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kSmem);
+  if (err != cudaSuccess) return err;
+  return launch_kernel(kernel, dim3(num_sms() * L::kCtas), dim3(kWarps * 32), L::kSmem, stream, 1, a, c,
+                       counters, partial);
 }
 
 }  // namespace
@@ -110,7 +714,7 @@ using namespace ple;
 PLE_EXPORT size_t ple_kv_attention_workspace(int32_t num_heads, int32_t num_kv_heads, int32_t head_dim) {
   if (num_heads < 1 || num_kv_heads < 1 || num_heads % num_kv_heads != 0 || ple_kv_block_bytes(head_dim) == 0)
     return 0;
-  return 256;
+  return workspace_bytes_of(head_dim);
 }
 
 PLE_EXPORT ple_status ple_kv_attention(const ple_bf16_t* q, int64_t q_stride, int64_t num_tokens,
@@ -145,9 +749,22 @@ PLE_EXPORT ple_status ple_kv_attention(const ple_bf16_t* q, int64_t q_stride, in
                         window, out, out_stride, dev_err};
   const KvCache c{const_cast<uint8_t*>(static_cast<const uint8_t*>(cache)), num_pages, page_size,
                   num_kv_heads, block_table, max_pages, query_start_loc, num_reqs, kv_lens};
-  const int64_t rows = num_tokens * num_heads;
-  const dim3 grid(static_cast<unsigned>((rows + 3) / 4));
-  const auto kernel = head_dim == 64 ? attention_rows_kernel<64> : head_dim == 128 ? attention_rows_kernel<128>
-                                                                                  : attention_rows_kernel<256>;
-  return check_cuda(launch_kernel(kernel, grid, dim3(kThreads), 0, stream, 1, a, c), name);
+  // the rows of a request and kv head, at most
+  const int64_t tokens = max_query_len > 0 && max_query_len < num_tokens ? max_query_len : num_tokens;
+  const int64_t rows = tokens * (num_heads / num_kv_heads);
+  unsigned* counters = static_cast<unsigned*>(workspace);
+  float* partial = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + counter_bytes());
+  cudaError_t err;
+  if (head_dim == 64)
+    err = rows <= 8 ? launch_split<64, 1>(a, c, counters, partial, stream)
+        : rows <= 16 ? launch_split<64, 2>(a, c, counters, partial, stream)
+                     : launch_split<64, 4>(a, c, counters, partial, stream);
+  else if (head_dim == 128)
+    err = rows <= 8 ? launch_split<128, 1>(a, c, counters, partial, stream)
+        : rows <= 16 ? launch_split<128, 2>(a, c, counters, partial, stream)
+                     : launch_split<128, 4>(a, c, counters, partial, stream);
+  else
+    err = rows <= 8 ? launch_split<256, 1>(a, c, counters, partial, stream)
+                    : launch_split<256, 2>(a, c, counters, partial, stream);
+  return check_cuda(err, name);
 }

@@ -1,8 +1,12 @@
 // ple_kv_attention: grouped-query attention over the paged 4-bit cache.
 #include "kv_cache.cuh"
 
+#include <cuda_fp16.h>
+
 #include <algorithm>
+#include <cfloat>
 #include <cmath>
+#include <type_traits>
 
 namespace ple {
 namespace {
@@ -37,18 +41,26 @@ struct AttentionArgs {
 // blocks, each one bulk copy. No warp waits for another until the item ends,
 // and the next item's first copies fly while this one's results are joined.
 //
-// Products, on warp-wide matrix instructions (16 x 8 x 16, bf16 in, f32 out;
-// the reading of the cache, not their rate, is the bound):
-//   S^T = K Q^T     16 tokens x 8 query rows
-//   O^T = V^T P^T   16 elements x 8 query rows
+// Products, on warp-wide matrix instructions (16 x 8 x 16, f32 sums; reading
+// the cache and unpacking it, not their rate, is the bound):
+//   S^T = K Q^T     16 tokens x 8 query rows, f16
+//   O^T = V^T P^T   16 elements x 8 query rows, bf16
 // so that a group of up to 8 query heads fills a tile, and the codes are the
-// A operand of both. A code c becomes bf16(128 + c) by OR-ing it into the
-// mantissa of 128 (exact); scale and offset meet the float32 sums instead of
-// the elements:
-//   <q, K_t> = s_t (S_t - 128 sum q) + m_t sum q
-//   sum_t p_t V_t = sum_t p'_t (128 + c_t) - 136 sum_t p'_t + sum_t p_t (m_t + 8 s_t)
-// with p' = bf16(p s): the only rounding to fewer bits, and it meets codes
-// centred on 8, so that an offset far from zero costs no precision.
+// A operand of both. Unpacking a word of 8 codes:
+//   K: two neighbouring codes of a byte are OR-ed into the mantissa of f16
+//     1024 as they stand, giving 1024 + c and 1024 + 16 c; the query elements
+//     that meet the second kind are divided by 16, and the sum starts at
+//     -1024 times the query's sum: one shift and four logic operations.
+//   V: codes are OR-ed into the mantissa of bf16 128 and one fused operation
+//     takes 136 off again, so that sums over long caches hold c - 8 itself.
+// Query rows are scaled to [1, 2) by a power of two each, which keeps f16
+// exact for bf16 queries (elements below 2^-14 of the row's largest round at
+// 2^-24 of it). Scale and offset of a token meet the float32 sums instead of
+// its elements:
+//   <q, K_t> = s_t sum_d q_d c_td + m_t sum_d q_d
+//   sum_t p_t V_t = sum_t p'_t (c_t - 8) + sum_t p_t (m_t + 8 s_t),  p' = bf16(p s)
+// p' is the only rounding to fewer bits, and it meets codes centred on 8, so
+// that an offset far from zero costs no precision.
 // The contraction index of a product may run in any order: a lane's 16 bytes
 // of a K row are 32 neighbouring elements, and the query's fragments follow
 // that order; two tokens' V bytes are interleaved with one permute a word.
@@ -62,7 +74,7 @@ template <int D, int NT>
 struct Split {
   static constexpr int kRows = 8 * NT;
   static constexpr int kStage = 2 * KvBlock<D>::kBytes;
-  static constexpr int kCtas = D == 256 || NT * D > 256 ? 2 : NT * D > 128 ? 3 : 4;  // per SM
+  static constexpr int kCtas = D == 256 || NT == 4 ? 2 : NT == 2 ? 3 : 4;  // per SM
   static constexpr int kStages = D == 256 ? 2 : D == 64 || NT == 4 ? 4 : NT == 2 ? 3 : 2;
   static constexpr bool kQRegs = NT * D <= 256;      // query fragments in registers
   static constexpr int kPass = 8;                    // rows joined at a time
@@ -72,10 +84,21 @@ struct Split {
   static constexpr int kFrags = NT * (D / 16) * 32 * 8;  // bytes of query fragments
   static constexpr int kJoin = kWarps * kPass * kPitch * 4;
   static constexpr int kMl = kWarps * kRows * 8;
-  static constexpr int kSmem = kRing + kFrags + kJoin + kMl + kRows * 4 + kWarps * kStages * 8 + 16;
+  static constexpr int kRowInfo = kRows * 16;        // a query row's factor, sum, first value and last position
+  static constexpr int kSegments = 2 * 128;  // the present and the next segment
+  static constexpr int kSmem = kRing + kFrags + kJoin + kMl + kRowInfo + kSegments + kWarps * kStages * 8 + 16;
 };
 
-__device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+__device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                        uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                          uint32_t b0, uint32_t b1) {
   asm volatile(
       "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
@@ -90,9 +113,23 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
-// Codes i and i + 4 of a word (i = 0..3) as bf16 pair (128 + c).
-__device__ __forceinline__ uint32_t code_pair(uint32_t word, int i) {
-  return ((word >> (4 * i)) & 0x000F000Fu) | 0x43004300u;
+// Codes i and i + 4 of a word (i = 0..3) as f16 pair: 1024 + c for even i,
+// 1024 + 16 c for odd i.
+__device__ __forceinline__ uint32_t k_pair(uint32_t word, int i) {
+  return ((i < 2 ? word : word >> 8) & (i % 2 == 0 ? 0x000F000Fu : 0x00F000F0u)) | 0x64006400u;
+}
+
+// Codes i of the two halves of a word (i = 0..3) as bf16 pair c - 8.
+__device__ __forceinline__ uint32_t v_pair(uint32_t word, int i) {
+  const uint32_t x = ((word >> (4 * i)) & 0x000F000Fu) | 0x43004300u;  // 128 + c
+  uint32_t y;
+  asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(y) : "r"(x), "r"(0x3F803F80u), "r"(0xC308C308u));  // - 136
+  return y;
+}
+
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
 }
 
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
@@ -108,6 +145,7 @@ struct Span {
   int n;           // tokens
   int64_t len;     // cached positions
   int step0, steps;
+  int block0;      // first block that any token sees
   int tiles;
   bool clipped;    // kv_lens past the block table
 };
@@ -125,16 +163,31 @@ __device__ __forceinline__ Span span_of(const AttentionArgs& a, const KvCache& c
   int64_t lo = 0;
   if (a.window > 0) lo = s.len - s.n - a.window + 1;
   if (lo < 0) lo = 0;
-  s.step0 = static_cast<int>(lo / kStepTokens);
+  s.block0 = static_cast<int>(lo / kBlockTokens);
+  s.step0 = s.block0 / 2;
   s.steps = hi > lo ? static_cast<int>((hi + kStepTokens - 1) / kStepTokens) - s.step0 : 0;
   const int64_t rows = static_cast<int64_t>(s.n) * (a.num_heads / c.num_kv_heads);
   s.tiles = static_cast<int>((rows + tile_rows - 1) / tile_rows);
   return s;
 }
 
+// An item's length on the line: what starting and joining it costs, in steps,
+// then its steps; 1 for an item that only writes zeros.
+constexpr int kItemCost = 4;
+__device__ __forceinline__ int units_of(const Span& s) { return s.steps > 0 ? kItemCost + s.steps : 1; }
+
 __device__ __forceinline__ int64_t weight_of(const Span& s, int hk) {
-  return static_cast<int64_t>(s.tiles) * hk * (s.steps > 0 ? s.steps : 1);
+  return static_cast<int64_t>(s.tiles) * hk * units_of(s);
 }
+
+// A CTA's share of one item.
+struct Segment {
+  Span s;
+  int64_t end;        // where the request's items end on the line
+  int r, tile, h, rows;
+  int from, to;       // steps, relative to s.step0
+  int pieces, first;  // CTAs that share the item's steps, the first of them
+};
 
 template <int D, int NT>
 __global__ void __launch_bounds__(kWarps * 32, (Split<D, NT>::kCtas))
@@ -149,7 +202,10 @@ attention_split_kernel(const AttentionArgs a, const KvCache c, unsigned* __restr
   uint2* qf = reinterpret_cast<uint2*>(smem + L::kRing);
   float* join = reinterpret_cast<float*>(smem + L::kRing + L::kFrags);
   float2* ml = reinterpret_cast<float2*>(smem + L::kRing + L::kFrags + L::kJoin);
-  float* qsum = reinterpret_cast<float*>(smem + L::kRing + L::kFrags + L::kJoin + L::kMl);
+  // float2 (pairs of rows): factor to log2 units, sum, first value of S; then last positions
+  float* row_info = reinterpret_cast<float*>(smem + L::kRing + L::kFrags + L::kJoin + L::kMl);
+  Segment* segments = reinterpret_cast<Segment*>(smem + L::kRing + L::kFrags + L::kJoin + L::kMl + L::kRowInfo);
+  static_assert(sizeof(Segment) <= 128, "two segments a warp");
   const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
   const int g = lane >> 2, j = lane & 3;
   uint8_t* ring = smem + warp * L::kStages * L::kStage;
@@ -189,7 +245,7 @@ attention_split_kernel(const AttentionArgs a, const KvCache c, unsigned* __restr
   __syncthreads();
   const int64_t W = *total;
   // pieces of at least one step for each warp
-  const int64_t most = (W + kWarps - 1) / kWarps;
+  const int64_t most = (W + kWarps + kItemCost - 1) / (kWarps + kItemCost);
   const int64_t S = most < gridDim.x ? most : gridDim.x;
   if (blockIdx.x >= S) return;
   int64_t x = blockIdx.x * W / S;
@@ -220,32 +276,46 @@ attention_split_kernel(const AttentionArgs a, const KvCache c, unsigned* __restr
     }
   };
 
-  // A CTA's share of one item.
-  struct Segment {
-    Span s;
-    int r, tile, h;
-    int from, to;       // steps of the item, relative to s.step0
-    int pieces, first;  // CTAs that share the item, the first of them
-    bool at_start;      // begins where this CTA's piece begins
-    bool item_at_start; // the item begins where the first CTA's piece begins
-  };
-  auto segment_at = [&]() {
-    Segment q;
-    q.s = span_of(a, c, r, kRows);
-    q.r = r;
-    const int per = q.s.steps > 0 ? q.s.steps : 1;
-    const int64_t item = (x - base) / per;
-    q.tile = static_cast<int>(item / hk);
-    q.h = static_cast<int>(item % hk);
-    const int64_t i0 = base + item * per, i1 = i0 + per;
-    q.from = static_cast<int>(x - i0);
-    q.to = static_cast<int>((x_end < i1 ? x_end : i1) - i0);
-    q.at_start = x == blockIdx.x * W / S;
-    q.first = static_cast<int>(((i0 + 1) * S - 1) / W);
-    q.item_at_start = i0 == q.first * W / S;
-    q.pieces = static_cast<int>((i1 * S - 1) / W) - q.first + 1;
-    if (q.s.steps == 0) q.to = q.from;  // nothing to read
-    return q;
+  // The next segment with something to do, from x on; false if there is none.
+  // Every warp finds it for itself and writes the same values down.
+  auto next_segment = [&](Segment* out) {
+    while (x < x_end) {
+      const Span sp = span_of(a, c, r, kRows);
+      const int units = units_of(sp);
+      const int64_t end = base + static_cast<int64_t>(sp.tiles) * hk * units;
+      if (x >= end) {
+        base = end;
+        ++r;
+        seek();
+        continue;
+      }
+      const int64_t item = (x - base) / units;
+      const int64_t i0 = base + item * units, i1 = i0 + units;
+      const int64_t to = x_end < i1 ? x_end : i1;
+      const int cost = units - sp.steps;
+      const int from = x - i0 > cost ? static_cast<int>(x - i0) - cost : 0;
+      const int upto = static_cast<int>(to - i0) - cost;
+      x = to;
+      if (sp.steps > 0 && upto <= from) continue;  // the item's steps are all another CTA's
+      if (lane == 0) {
+        Segment q;
+        q.s = sp;
+        q.end = end;
+        q.r = r;
+        q.tile = static_cast<int>(item / hk);
+        q.h = static_cast<int>(item % hk);
+        q.rows = static_cast<int>(min(static_cast<int64_t>(kRows), static_cast<int64_t>(sp.n) * G - static_cast<int64_t>(q.tile) * kRows));
+        q.from = from;
+        q.to = sp.steps > 0 ? upto : from;
+        const int64_t j0 = sp.steps > 0 ? i0 + cost : i0;
+        q.first = static_cast<int>(((j0 + 1) * S - 1) / W);
+        q.pieces = static_cast<int>((i1 * S - 1) / W) - q.first + 1;
+        *out = q;
+      }
+      __syncwarp();
+      return true;
+    }
+    return false;
   };
 
   // this warp's copies
@@ -253,34 +323,37 @@ attention_split_kernel(const AttentionArgs a, const KvCache c, unsigned* __restr
   uint32_t phases = 0, armed = 0, present = 0;  // by stage: parity, a copy issued, blocks present (2 bits)
   bool dead = false;                            // a wait gave up: no more copies
   int issue_step = 0, issue_end = 0;            // absolute steps
-  int pages_at = 0;                             // first block of `pages`
-  int pages = -1, pages_next = -1;              // lane's page of blocks pages_at + lane and + 32
+  int pages_at = 0;                             // first block of `blocks`
+  int blocks = -1, blocks_next = -1;            // where request blocks pages_at + lane and + 32 lie; -1: nowhere
   const int32_t* table = c.block_table;
-  int block_end = 0;                            // blocks that hold positions
+  int block_begin = 0, block_end = 0;           // blocks that this warp's rows may see
   int issue_h = 0;
   int stage_in = 0, stage_out = 0;
-  auto page_at = [&](int block) { return block < block_end ? __ldg(table + block / per_page) : -1; };
+  auto block_at = [&](int block) {
+    if (block < block_begin || block >= block_end) return -1;
+    const int col = block / per_page;
+    const int64_t page = __ldg(table + col);
+    if (page < 0 || page >= c.num_pages) {
+      set_dev_err(a.dev_err, PLE_DEVERR_BOUNDS);
+      return -1;
+    }
+    return static_cast<int>((page * hk + issue_h) * per_page + (block - col * per_page));
+  };
   auto issue = [&]() {
     if (issue_step >= issue_end || dead) return;
-    const int b = 2 * issue_step;
-    if (b - pages_at >= 32) {
-      pages_at += 32;
-      pages = pages_next;
-      pages_next = page_at(pages_at + 32 + lane);
-    }
-    const int mine = b + (lane & 1);
-    const int64_t page = __shfl_sync(0xffffffffu, pages, mine - pages_at);
-    const bool wanted = lane < 2 && mine < block_end;
-    const bool ok = wanted && page >= 0 && page < c.num_pages;
-    if (wanted && !ok) set_dev_err(a.dev_err, PLE_DEVERR_BOUNDS);
-    const unsigned mask = __ballot_sync(0xffffffffu, ok);
+    const int b = 2 * issue_step - pages_at;
+    const int at = __shfl_sync(0xffffffffu, blocks, b + (lane & 1));
+    const unsigned mask = __ballot_sync(0xffffffffu, at >= 0) & 3u;
     const uint32_t bar = bar0 + 8 * stage_in;
     if (lane == 0) mbar_arrive_expect_tx(bar, __popc(mask) * B::kBytes);
     __syncwarp();
-    if (ok) {
-      const int64_t block = (page * hk + issue_h) * per_page + mine % per_page;
-      bulk_copy_g2s(smem_u32(ring + stage_in * L::kStage + lane * B::kBytes), c.base + block * B::kBytes,
-                    B::kBytes, bar);
+    if (lane < 2 && at >= 0)
+      bulk_copy_g2s(smem_u32(ring + stage_in * L::kStage + lane * B::kBytes),
+                    c.base + static_cast<int64_t>(at) * B::kBytes, B::kBytes, bar);
+    if (b == 30) {
+      pages_at += 32;
+      blocks = blocks_next;
+      blocks_next = block_at(pages_at + 32 + lane);
     }
     present = (present & ~(3u << (2 * stage_in))) | (mask << (2 * stage_in));
     armed |= 1u << stage_in;
@@ -300,43 +373,76 @@ attention_split_kernel(const AttentionArgs a, const KvCache c, unsigned* __restr
     issue_h = q.h;
     table = c.block_table + static_cast<int64_t>(q.r) * c.max_pages;
     const int64_t room = static_cast<int64_t>(c.max_pages) * per_page;
-    const int64_t blocks = (q.s.len + kBlockTokens - 1) / kBlockTokens;
-    block_end = static_cast<int>(blocks < room ? blocks : room);
+    const int64_t held = (q.s.len + kBlockTokens - 1) / kBlockTokens;
+    block_end = static_cast<int>(held < room ? held : room);
+    block_begin = q.s.block0;
+    // not past this warp's own steps: what it never reads raises no flag
+    block_end = min(block_end, 2 * issue_end);
     if (q.s.clipped && lane == 0) set_dev_err(a.dev_err, PLE_DEVERR_BOUNDS);
     pages_at = 2 * issue_step;
-    if (issue_step < issue_end) {
-      pages = page_at(pages_at + lane);
-      pages_next = page_at(pages_at + 32 + lane);
-    }
+    blocks = block_at(pages_at + lane);
+    blocks_next = block_at(pages_at + 32 + lane);
 #pragma unroll 1
     for (int s = 0; s < L::kStages; ++s) issue();
   };
 
   seek();
-  Segment q = segment_at();
-  start(q);
-  for (;;) {
-    // the tile's query rows as B fragments, and their sums
-    const int rows = min(kRows, static_cast<int>(static_cast<int64_t>(q.s.n) * G - static_cast<int64_t>(q.tile) * kRows));
+  if (!next_segment(segments)) return;
+  start(segments[0]);
+  for (int which = 0;; which ^= 1) {
+    const Segment& q = segments[which];
+    // the tile's query rows as B fragments, and what a score needs of them
+    const int rows = q.rows;
     for (int nt = warp; nt < NT; nt += kWarps) {
       const int rr = nt * 8 + g;
       const int64_t flat = static_cast<int64_t>(q.tile) * kRows + rr;
-      const ple_bf16_t* src = a.q + (q.s.t0 + flat / G) * a.q_stride + (static_cast<int64_t>(q.h) * G + flat % G) * D + j * (D / 4);
-      float sum = 0.0f;
+      const int64_t token = flat / G;
+      const ple_bf16_t* src = a.q + (q.s.t0 + token) * a.q_stride + (static_cast<int64_t>(q.h) * G + (flat - token * G)) * D + j * (D / 4);
+      uint4 v[kWords];
+      float top = 0.0f;
 #pragma unroll
       for (int w = 0; w < kWords; ++w) {
-        uint4 v = make_uint4(0, 0, 0, 0);
-        if (rr < rows) v = *reinterpret_cast<const uint4*>(src + 8 * w);
+        v[w] = make_uint4(0, 0, 0, 0);
+        if (rr < rows) v[w] = *reinterpret_cast<const uint4*>(src + 8 * w);
         float f[8];
-        unpack8(v, f);
+        unpack8(v[w], f);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) sum += f[i];
-        qf[((2 * w) * NT + nt) * 32 + lane] = make_uint2(__byte_perm(v.x, v.z, 0x5410), __byte_perm(v.x, v.z, 0x7632));
-        qf[((2 * w + 1) * NT + nt) * 32 + lane] = make_uint2(__byte_perm(v.y, v.w, 0x5410), __byte_perm(v.y, v.w, 0x7632));
+        for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(f[i]));
       }
-      sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-      sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-      if (j == 0) qsum[rr] = sum;
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      // 2^k <= top < 2^(k + 1)
+      const int k = top > 0.0f && top < INFINITY ? max(ilogbf(top), -126) : 0;
+      const float down = ldexpf(1.0f, -k);
+      float even = 0.0f, odd = 0.0f;  // sums of the elements; the odd ones' are of sixteenths
+#pragma unroll
+      for (int w = 0; w < kWords; ++w) {
+        float f[8];
+        unpack8(v[w], f);
+        uint32_t p[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float by = i % 2 == 0 ? down : down * 0.0625f;
+          p[i] = pack_f16(f[i] * by, f[i + 4] * by);
+          const float2 r2 = __half22float2(*reinterpret_cast<const __half2*>(&p[i]));
+          if (i % 2 == 0) even += r2.x + r2.y;
+          else odd += r2.x + r2.y;
+        }
+        qf[((2 * w) * NT + nt) * 32 + lane] = make_uint2(p[0], p[1]);
+        qf[((2 * w + 1) * NT + nt) * 32 + lane] = make_uint2(p[2], p[3]);
+      }
+#pragma unroll
+      for (int x2 = 1; x2 < 4; x2 <<= 1) {
+        even += __shfl_xor_sync(0xffffffffu, even, x2);
+        odd += __shfl_xor_sync(0xffffffffu, odd, x2);
+      }
+      if (j == 0) {
+        const int64_t p = a.causal ? q.s.len - q.s.n + token : q.s.len - 1;
+        row_info[rr] = ldexpf(a.scale_log2, k);
+        row_info[kRows + rr] = fmaf(16.0f, odd, even);
+        row_info[2 * kRows + rr] = -1024.0f * (even + odd);
+        reinterpret_cast<int*>(row_info)[3 * kRows + rr] = rr < rows ? static_cast<int>(p) : -1;
+      }
     }
     __syncthreads();
     uint2 qr[L::kQRegs ? NT * (D / 16) : 1];
@@ -344,42 +450,32 @@ attention_split_kernel(const AttentionArgs a, const KvCache c, unsigned* __restr
 #pragma unroll
       for (int i = 0; i < NT * (D / 16); ++i) qr[i] = qf[i * 32 + lane];
     }
-    float sq[2 * NT];
-    int last[2 * NT];  // the last position of each of this lane's rows
-#pragma unroll
-    for (int i = 0; i < 2 * NT; ++i) {
-      const int rr = (i / 2) * 8 + 2 * j + (i & 1);
-      sq[i] = qsum[rr];
-      const int64_t tok = (static_cast<int64_t>(q.tile) * kRows + rr) / G;
-      const int64_t p = a.causal ? q.s.len - q.s.n + tok : q.s.len - 1;
-      last[i] = rr < rows ? static_cast<int>(p) : -1;
-    }
     // positions that every row of the tile sees: [all_from, all_to]
-    const int64_t tok0 = static_cast<int64_t>(q.tile) * kRows / G;
-    const int64_t tok1 = (static_cast<int64_t>(q.tile) * kRows + rows - 1) / G;
-    const int64_t all_to = a.causal ? q.s.len - q.s.n + tok0 : q.s.len - 1;
-    const int64_t all_from = a.window > 0 ? q.s.len - q.s.n + tok1 - a.window + 1 : 0;
+    int all_from = 0, all_to;
+    {
+      const int64_t tok0 = static_cast<int64_t>(q.tile) * kRows / G;
+      const int64_t tok1 = (static_cast<int64_t>(q.tile) * kRows + rows - 1) / G;
+      all_to = static_cast<int>(a.causal ? q.s.len - q.s.n + tok0 : q.s.len - 1);
+      if (a.window > 0) all_from = static_cast<int>(max(q.s.len - q.s.n + tok1 - a.window + 1, int64_t(0)));
+    }
 
     float o[NT][D / 16][4];
-    float ones[NT][4];  // column sums of the rounded weights
     float m[2 * NT], l[2 * NT], off[2 * NT];
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
+    for (int n = 0; n < NT; ++n)
 #pragma unroll
       for (int u = 0; u < D / 16; ++u)
 #pragma unroll
         for (int i = 0; i < 4; ++i) o[n][u][i] = 0.0f;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) ones[n][i] = 0.0f;
-    }
-#pragma unroll
-    for (int i = 0; i < 2 * NT; ++i) { m[i] = -INFINITY; l[i] = 0.0f; off[i] = 0.0f; }
+    for (int i = 0; i < 2 * NT; ++i) { m[i] = -FLT_MAX; l[i] = 0.0f; off[i] = 0.0f; }
+    const int step0 = q.s.step0;
 
     int from, to;
     share(q, from, to);
 #pragma unroll 1
     for (int step = from; step < to; ++step) {
-      const int64_t p0 = static_cast<int64_t>(q.s.step0 + step) * kStepTokens;
+      const int p0 = (step0 + step) * kStepTokens;
       uint32_t here = 0;
       if (!dead) {
         const bool ok = mbar_try_wait(bar0 + 8 * stage_out, (phases >> stage_out) & 1u) ||
@@ -401,9 +497,11 @@ attention_split_kernel(const AttentionArgs a, const KvCache c, unsigned* __restr
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
 #pragma unroll
-          for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) s[n][b][i] = 0.0f;
+          for (int n = 0; n < NT; ++n) {
+            const float2 s0 = *reinterpret_cast<const float2*>(row_info + 2 * kRows + n * 8 + 2 * j);
+            s[n][b][0] = s[n][b][2] = s0.x;
+            s[n][b][1] = s[n][b][3] = s0.y;
+          }
           const uint8_t* kb = st + b * B::kBytes;
           uint32_t lo[kWords], hi[kWords];
           {
@@ -424,14 +522,14 @@ attention_split_kernel(const AttentionArgs a, const KvCache c, unsigned* __restr
           for (int w = 0; w < kWords; ++w)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-              const uint32_t a0 = code_pair(lo[w], 2 * h), a1 = code_pair(hi[w], 2 * h);
-              const uint32_t a2 = code_pair(lo[w], 2 * h + 1), a3 = code_pair(hi[w], 2 * h + 1);
+              const uint32_t a0 = k_pair(lo[w], 2 * h), a1 = k_pair(hi[w], 2 * h);
+              const uint32_t a2 = k_pair(lo[w], 2 * h + 1), a3 = k_pair(hi[w], 2 * h + 1);
 #pragma unroll
               for (int n = 0; n < NT; ++n) {
                 uint2 f;
                 if constexpr (L::kQRegs) f = qr[(2 * w + h) * NT + n];
                 else f = qf[((2 * w + h) * NT + n) * 32 + lane];
-                mma16816(s[n][b], a0, a1, a2, a3, f.x, f.y);
+                mma_f16(s[n][b], a0, a1, a2, a3, f.x, f.y);
               }
             }
         }
@@ -445,30 +543,31 @@ attention_split_kernel(const AttentionArgs a, const KvCache c, unsigned* __restr
             const int tok = r0 + 8 * e;
             const uint32_t kp = *reinterpret_cast<const uint32_t*>(st + b * B::kBytes + B::kPairs + tok * 4);
             const uint32_t vp = *reinterpret_cast<const uint32_t*>(st + b * B::kBytes + B::kVPairs + tok * 4);
-            const float ks = bf_lo(kp) * a.scale_log2;
-            const float km = fmaf(-128.0f, ks, bf_hi(kp) * a.scale_log2);
+            const float ks = bf_lo(kp), km = bf_hi(kp);
             vs[b][e] = bf_lo(vp);
             vm[b][e] = fmaf(8.0f, bf_lo(vp), bf_hi(vp));
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-              for (int i = 0; i < 2; ++i) {
-                float& v = s[n][b][2 * e + i];
-                v = fmaf(ks, v, km * sq[2 * n + i]);
-              }
+            for (int n = 0; n < NT; ++n) {
+              const float2 f = *reinterpret_cast<const float2*>(row_info + n * 8 + 2 * j);
+              const float2 sq = *reinterpret_cast<const float2*>(row_info + kRows + n * 8 + 2 * j);
+              s[n][b][2 * e] = f.x * fmaf(ks, s[n][b][2 * e], km * sq.x);
+              s[n][b][2 * e + 1] = f.y * fmaf(ks, s[n][b][2 * e + 1], km * sq.y);
+            }
             if (masked) {
-              const int64_t p = p0 + b * kBlockTokens + tok;
+              const int p = p0 + b * kBlockTokens + tok;
               const bool there = (here >> b) & 1u;
 #pragma unroll
-              for (int n = 0; n < NT; ++n)
+              for (int n = 0; n < NT; ++n) {
+                const int2 lasts = *reinterpret_cast<const int2*>(row_info + 3 * kRows + n * 8 + 2 * j);
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                  const int64_t q_last = last[2 * n + i];
-                  if (!there || p > q_last || (a.window > 0 && p <= q_last - a.window)) {
+                  const int last = i == 0 ? lasts.x : lasts.y;
+                  if (!there || p > last || (a.window > 0 && p <= last - a.window)) {
                     s[n][b][2 * e + i] = -INFINITY;
                     unseen |= 1u << (n * 8 + b * 4 + e * 2 + i);
                   }
                 }
+              }
             }
           }
         // The running maximum is raised only when a score passes it by 2^8:
@@ -489,40 +588,42 @@ attention_split_kernel(const AttentionArgs a, const KvCache c, unsigned* __restr
           for (int i = 0; i < 2 * NT; ++i) {
             float t = top[i];
 #pragma unroll
-            for (int x = 4; x < 32; x <<= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, x));
+            for (int x2 = 4; x2 < 32; x2 <<= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, x2));
             const float next = fmaxf(m[i], t);
-            const float keep = next == -INFINITY ? 1.0f : ex2(m[i] - next);
+            const float keep = ex2(m[i] - next);
             m[i] = next;
             l[i] *= keep;
             off[i] *= keep;
             const int n = i / 2, e = i & 1;
-            ones[n][e] *= keep;
-            ones[n][2 + e] *= keep;
 #pragma unroll
             for (int u = 0; u < D / 16; ++u) { o[n][u][e] *= keep; o[n][u][2 + e] *= keep; }
           }
         }
         uint32_t pt[NT][2][2];  // weights times the values' scale, bf16, as B fragments
+        auto weights = [&](auto with_mask) {
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
+          for (int n = 0; n < NT; ++n)
 #pragma unroll
-          for (int b = 0; b < 2; ++b) {
+            for (int b = 0; b < 2; ++b)
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              float w[2];
+              for (int e = 0; e < 2; ++e) {
+                float w[2];
 #pragma unroll
-              for (int i = 0; i < 2; ++i) {
-                const float mi = m[2 * n + i] == -INFINITY ? 0.0f : m[2 * n + i];
-                const float p = ex2(s[n][b][2 * e + i] - mi);
-                // a value that is not seen meets no weight, not even zero: it may be NaN
-                const bool skip = masked && ((unseen >> (n * 8 + b * 4 + e * 2 + i)) & 1u);
-                l[2 * n + i] += p;
-                off[2 * n + i] = skip ? off[2 * n + i] : fmaf(p, vm[b][e], off[2 * n + i]);
-                w[i] = skip ? 0.0f : p * vs[b][e];
+                for (int i = 0; i < 2; ++i) {
+                  const float p = ex2(s[n][b][2 * e + i] - m[2 * n + i]);
+                  l[2 * n + i] += p;
+                  w[i] = p * vs[b][e];
+                  const float next = fmaf(p, vm[b][e], off[2 * n + i]);
+                  // a value that is not seen meets no weight, not even zero: it may be NaN
+                  const bool skip = decltype(with_mask)::value && ((unseen >> (n * 8 + b * 4 + e * 2 + i)) & 1u);
+                  off[2 * n + i] = skip ? off[2 * n + i] : next;
+                  w[i] = skip ? 0.0f : w[i];
+                }
+                pt[n][b][e] = transpose8x8(pack2(w[0], w[1]));
               }
-              pt[n][b][e] = transpose8x8(pack2(w[0], w[1]));
-            }
-          }
+        };
+        if (masked) weights(std::true_type{});
+        else weights(std::false_type{});
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
           const uint8_t* vb = st + b * B::kBytes + B::kV + g * (D / 16);
@@ -536,9 +637,6 @@ attention_split_kernel(const AttentionArgs a, const KvCache c, unsigned* __restr
             else v[i][0] = *reinterpret_cast<const uint32_t*>(p);
           }
 #pragma unroll
-          for (int n = 0; n < NT; ++n)
-            mma16816(ones[n], 0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u, pt[n][b][0], pt[n][b][1]);
-#pragma unroll
           for (int w = 0; w < kVWords; ++w)
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
@@ -546,11 +644,11 @@ attention_split_kernel(const AttentionArgs a, const KvCache c, unsigned* __restr
               const uint32_t x0 = __byte_perm(v[0][w], v[1][w], sel), x1 = __byte_perm(v[2][w], v[3][w], sel);
 #pragma unroll
               for (int k = 0; k < 2; ++k) {
-                const uint32_t a0 = code_pair(x0, 2 * k), a1 = code_pair(x0, 2 * k + 1);
-                const uint32_t a2 = code_pair(x1, 2 * k), a3 = code_pair(x1, 2 * k + 1);
+                const uint32_t a0 = v_pair(x0, 2 * k), a1 = v_pair(x0, 2 * k + 1);
+                const uint32_t a2 = v_pair(x1, 2 * k), a3 = v_pair(x1, 2 * k + 1);
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
-                  mma16816(o[n][w * 4 + half * 2 + k], a0, a1, a2, a3, pt[n][b][0], pt[n][b][1]);
+                  mma_bf16(o[n][w * 4 + half * 2 + k], a0, a1, a2, a3, pt[n][b][0], pt[n][b][1]);
               }
             }
         }
@@ -561,21 +659,8 @@ attention_split_kernel(const AttentionArgs a, const KvCache c, unsigned* __restr
     }
 
     // the next item's copies fly while this one's results are joined
-    const Segment cur = q;
-    const int cur_rows = rows;
-    x += cur.to > cur.from ? cur.to - cur.from : 1;
-    const bool more = x < x_end;
-    if (more) {
-      const int per = cur.s.steps > 0 ? cur.s.steps : 1;
-      const int64_t end = base + static_cast<int64_t>(cur.s.tiles) * hk * per;
-      if (x >= end) {
-        base = end;
-        ++r;
-        seek();
-      }
-      q = segment_at();
-      start(q);
-    }
+    const bool more = next_segment(segments + (which ^ 1));
+    if (more) start(segments[which ^ 1]);
 
     // join the warps
 #pragma unroll
@@ -585,10 +670,10 @@ attention_split_kernel(const AttentionArgs a, const KvCache c, unsigned* __restr
         l[i] += __shfl_xor_sync(0xffffffffu, l[i], sh);
         off[i] += __shfl_xor_sync(0xffffffffu, off[i], sh);
       }
-      off[i] = fmaf(-136.0f, ones[i / 2][i & 1], off[i]);
       if (g == 0) ml[warp * kRows + (i / 2) * 8 + 2 * j + (i & 1)] = make_float2(m[i], l[i]);
     }
-    const int slot = 2 * blockIdx.x + (cur.at_start ? 0 : 1);
+    // a CTA is the first piece of one item that goes on, and a later piece of one, at most
+    const int slot = 2 * blockIdx.x + (static_cast<int>(blockIdx.x) == q.first ? 1 : 0);
     float* part = partial + static_cast<int64_t>(slot) * kRows * (D + 2);
 #pragma unroll
     for (int pass = 0; pass < kRows / L::kPass; ++pass) {
@@ -609,26 +694,25 @@ attention_split_kernel(const AttentionArgs a, const KvCache c, unsigned* __restr
       for (int i = threadIdx.x; i < L::kPass * (D / 4); i += kWarps * 32) {
         const int pr = i / (D / 4), d = i % (D / 4) * 4;
         const int rr = pass * L::kPass + pr;
-        if (rr >= cur_rows) break;
-        float top = -INFINITY;
+        if (rr >= rows) break;
+        float top = -FLT_MAX;
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) top = fmaxf(top, ml[w * kRows + rr].x);
-        const float safe = top == -INFINITY ? 0.0f : top;
         float sum = 0.0f;
         float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) {
           const float2 t = ml[w * kRows + rr];
-          const float k = ex2(t.x - safe);
+          const float k = ex2(t.x - top);
           sum = fmaf(k, t.y, sum);
           const float* src = join + (w * L::kPass + pr) * L::kPitch + d + 2 * (d / (D / 8));
           const float2 u0 = *reinterpret_cast<const float2*>(src), u1 = *reinterpret_cast<const float2*>(src + 2);
           v.x = fmaf(k, u0.x, v.x); v.y = fmaf(k, u0.y, v.y); v.z = fmaf(k, u1.x, v.z); v.w = fmaf(k, u1.y, v.w);
         }
-        if (cur.pieces == 1) {
+        if (q.pieces == 1) {
           const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-          const int64_t flat = static_cast<int64_t>(cur.tile) * kRows + rr;
-          ple_bf16_t* dst = a.out + (cur.s.t0 + flat / G) * a.out_stride + (static_cast<int64_t>(cur.h) * G + flat % G) * D + d;
+          const int64_t flat = static_cast<int64_t>(q.tile) * kRows + rr;
+          ple_bf16_t* dst = a.out + (q.s.t0 + flat / G) * a.out_stride + (static_cast<int64_t>(q.h) * G + flat % G) * D + d;
           *reinterpret_cast<uint2*>(dst) = make_uint2(pack2(v.x * inv, v.y * inv), pack2(v.z * inv, v.w * inv));
         } else {
           *reinterpret_cast<float4*>(part + rr * D + d) = v;
@@ -636,35 +720,34 @@ attention_split_kernel(const AttentionArgs a, const KvCache c, unsigned* __restr
         }
       }
     }
-    if (cur.pieces > 1) {
+    if (q.pieces > 1) {
       __threadfence();
       __syncthreads();
-      if (threadIdx.x == 0) *last_flag = atomicAdd(counters + cur.first, 1u) == static_cast<unsigned>(cur.pieces - 1);
+      if (threadIdx.x == 0) *last_flag = atomicAdd(counters + q.first, 1u) == static_cast<unsigned>(q.pieces - 1);
       __syncthreads();
       if (*last_flag) {
         __threadfence();
-        if (threadIdx.x == 0) counters[cur.first] = 0;
-        for (int i = threadIdx.x; i < cur_rows * (D / 4); i += kWarps * 32) {
+        if (threadIdx.x == 0) counters[q.first] = 0;
+        for (int i = threadIdx.x; i < rows * (D / 4); i += kWarps * 32) {
           const int rr = i / (D / 4), d = i % (D / 4) * 4;
-          float top = -INFINITY, sum = 0.0f;
+          float top = -FLT_MAX, sum = 0.0f;
           float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll 4
-          for (int k = 0; k < cur.pieces; ++k) {
-            const int sl = 2 * (cur.first + k) + (k == 0 && !cur.item_at_start ? 1 : 0);
+          for (int k = 0; k < q.pieces; ++k) {
+            const int sl = 2 * (q.first + k) + (k == 0 ? 1 : 0);
             const float* src = partial + static_cast<int64_t>(sl) * kRows * (D + 2);
             const float2 t = __ldcg(reinterpret_cast<const float2*>(src + kRows * D + 2 * rr));
             const float4 u = __ldcg(reinterpret_cast<const float4*>(src + rr * D + d));
             const float next = fmaxf(top, t.x);
-            const float safe = next == -INFINITY ? 0.0f : next;
-            const float ka = ex2(top - safe), kb = ex2(t.x - safe);
+            const float ka = ex2(top - next), kb = ex2(t.x - next);
             sum = fmaf(kb, t.y, sum * ka);
             v.x = fmaf(kb, u.x, v.x * ka); v.y = fmaf(kb, u.y, v.y * ka);
             v.z = fmaf(kb, u.z, v.z * ka); v.w = fmaf(kb, u.w, v.w * ka);
             top = next;
           }
           const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-          const int64_t flat = static_cast<int64_t>(cur.tile) * kRows + rr;
-          ple_bf16_t* dst = a.out + (cur.s.t0 + flat / G) * a.out_stride + (static_cast<int64_t>(cur.h) * G + flat % G) * D + d;
+          const int64_t flat = static_cast<int64_t>(q.tile) * kRows + rr;
+          ple_bf16_t* dst = a.out + (q.s.t0 + flat / G) * a.out_stride + (static_cast<int64_t>(q.h) * G + flat % G) * D + d;
           *reinterpret_cast<uint2*>(dst) = make_uint2(pack2(v.x * inv, v.y * inv), pack2(v.z * inv, v.w * inv));
         }
       }
@@ -733,6 +816,9 @@ PLE_EXPORT ple_status ple_kv_attention(const ple_bf16_t* q, int64_t q_stride, in
   if (ple_status s = check_cache(name, cache, num_pages, page_size, block_table, max_pages,
                                  query_start_loc, num_reqs, kv_lens, num_kv_heads, head_dim))
     return s;
+  // block numbers are 32-bit in the kernel (2^31 blocks would be a cache of terabytes)
+  if (num_pages > 0 && num_pages > (int64_t(1) << 31) / num_kv_heads / (page_size / kBlockTokens))
+    return fail(PLE_ERR_UNSUPPORTED, "%s: %lld pages", name, static_cast<long long>(num_pages));
   if (num_heads < 1 || num_heads % num_kv_heads != 0)
     return fail(PLE_ERR_INVALID_ARG, "%s: %d heads over %d kv heads", name, num_heads, num_kv_heads);
   if (q == nullptr || out == nullptr || !aligned16(q) || !aligned16(out) || q_stride % 8 != 0 || out_stride % 8 != 0)

@@ -132,6 +132,14 @@ def test_pages_outside_the_cache_are_not_seen():
         check(out, *oracle.attention(bits(q), b.cache, b.table, b.qsl, b.lens, 128 ** -0.5))
 
 
+@pytest.mark.parametrize("tokens", [1, 3, 100])
+def test_pages_behind_the_window_may_be_gone(tokens):
+    """What lies wholly behind every token's window is not looked up."""
+    b = Batch([tokens], [300], 8, 2, 128, 16, seed=27)
+    b.table[0, :(300 - tokens - 20 + 1) // 16] = -1
+    run(b, window=20)
+
+
 def test_lengths_past_the_block_table_are_flagged():
     b = Batch([1], [40], 4, 2, 128, 16, seed=29)
     b.lens[0] = 16 * b.table.shape[1] + 500

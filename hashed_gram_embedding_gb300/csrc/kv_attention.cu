@@ -47,12 +47,14 @@ struct AttentionArgs {
 //   O^T = V^T P^T   16 elements x 8 query rows, bf16
 // so that a group of up to 8 query heads fills a tile, and the codes are the
 // A operand of both. Unpacking a word of 8 codes:
-//   K: two neighbouring codes of a byte are OR-ed into the mantissa of f16
-//     1024 as they stand, giving 1024 + c and 1024 + 16 c; the query elements
-//     that meet the second kind are divided by 16, and the sum starts at
-//     -1024 times the query's sum: one shift and four logic operations.
-//   V: codes are OR-ed into the mantissa of bf16 128 and one fused operation
-//     takes 136 off again, so that sums over long caches hold c - 8 itself.
+//   Masked out where they stand, a byte's codes are subnormal numbers that no
+//   bit has to be added to: bits 0-3 of a half are c 2^-24 as f16 (c 2^-133
+//   as bf16), bits 4-7 sixteen times that. So a word of eight codes takes
+//   four masks and one shift by a byte.
+//   K: f16 subnormals multiply as they are; the query elements that meet the
+//     second kind are divided by 16, and 2^24 goes into the rows' factors.
+//   V: one fused multiply-add makes bf16 (c - 8) / 64 or (c - 8) / 4, so that
+//     sums over long caches hold no offset; 64 and 4 are taken out at the end.
 // Query rows are scaled to [1, 2) by a power of two each, which keeps f16
 // exact for bf16 queries (elements below 2^-14 of the row's largest round at
 // 2^-24 of it). Scale and offset of a token meet the float32 sums instead of
@@ -84,7 +86,7 @@ struct Split {
   static constexpr int kFrags = NT * (D / 16) * 32 * 8;  // bytes of query fragments
   static constexpr int kJoin = kWarps * kPass * kPitch * 4;
   static constexpr int kMl = kWarps * kRows * 8;
-  static constexpr int kRowInfo = kRows * 16;        // a query row's factor, sum, first value and last position
+  static constexpr int kRowInfo = kRows * 24;        // a query row's factor, sum, last position, place in the output
   static constexpr int kSegments = 2 * 128;  // the present and the next segment
   static constexpr int kSmem = kRing + kFrags + kJoin + kMl + kRowInfo + kSegments + kWarps * kStages * 8 + 16;
 };
@@ -113,17 +115,18 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
-// Codes i and i + 4 of a word (i = 0..3) as f16 pair: 1024 + c for even i,
-// 1024 + 16 c for odd i.
+// Codes i and i + 4 of a word (i = 0..3) as f16 pair: c 2^-24 for even i,
+// c 2^-20 for odd i.
 __device__ __forceinline__ uint32_t k_pair(uint32_t word, int i) {
-  return ((i < 2 ? word : word >> 8) & (i % 2 == 0 ? 0x000F000Fu : 0x00F000F0u)) | 0x64006400u;
+  return (i < 2 ? word : word >> 8) & (i % 2 == 0 ? 0x000F000Fu : 0x00F000F0u);
 }
 
-// Codes i of the two halves of a word (i = 0..3) as bf16 pair c - 8.
+// Codes i of the two halves of a word (i = 0..3) as bf16 pair: (c - 8) / 64
+// for even i, (c - 8) / 4 for odd i.
 __device__ __forceinline__ uint32_t v_pair(uint32_t word, int i) {
-  const uint32_t x = ((word >> (4 * i)) & 0x000F000Fu) | 0x43004300u;  // 128 + c
   uint32_t y;
-  asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(y) : "r"(x), "r"(0x3F803F80u), "r"(0xC308C308u));  // - 136
+  asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(y) : "r"(k_pair(word, i)), "r"(0x7F007F00u) /* 2^127 */,
+      "r"(i % 2 == 0 ? 0xBE00BE00u /* -1/8 */ : 0xC000C000u /* -2 */));
   return y;
 }
 
@@ -141,9 +144,9 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
 // What a request asks of the kernel: steps [step0, step0 + steps) of the cache
 // for each of its tiles x kv heads.
 struct Span {
-  int64_t t0;      // first token
+  int t0;          // first token
   int n;           // tokens
-  int64_t len;     // cached positions
+  int len;         // cached positions
   int step0, steps;
   int block0;      // first block that any token sees
   int tiles;
@@ -152,22 +155,23 @@ struct Span {
 
 __device__ __forceinline__ Span span_of(const AttentionArgs& a, const KvCache& c, int r, int tile_rows) {
   Span s;
-  int64_t end;
-  request_span(c.qsl, c.num_reqs + 1, a.T, r, &s.t0, &end);
-  s.n = static_cast<int>(end - s.t0);
-  s.len = __ldg(c.kv_lens + r);
+  int64_t t0, end;
+  request_span(c.qsl, c.num_reqs + 1, a.T, r, &t0, &end);
+  s.t0 = static_cast<int>(t0);
+  s.n = static_cast<int>(end - t0);
+  s.len = max(__ldg(c.kv_lens + r), 0);
   const int64_t room = static_cast<int64_t>(c.max_pages) * c.page_size;
-  int64_t hi = s.len;
-  s.clipped = hi > room;
-  if (hi > room) hi = room;
-  int64_t lo = 0;
-  if (a.window > 0) lo = s.len - s.n - a.window + 1;
-  if (lo < 0) lo = 0;
-  s.block0 = static_cast<int>(lo / kBlockTokens);
+  s.clipped = s.len > room;
+  const int hi = s.clipped ? static_cast<int>(room) : s.len;
+  int lo = 0;
+  if (a.window > 0) {
+    const int64_t first = static_cast<int64_t>(s.len) - s.n - a.window + 1;
+    if (first > 0) lo = static_cast<int>(first);
+  }
+  s.block0 = lo / kBlockTokens;
   s.step0 = s.block0 / 2;
-  s.steps = hi > lo ? static_cast<int>((hi + kStepTokens - 1) / kStepTokens) - s.step0 : 0;
-  const int64_t rows = static_cast<int64_t>(s.n) * (a.num_heads / c.num_kv_heads);
-  s.tiles = static_cast<int>((rows + tile_rows - 1) / tile_rows);
+  s.steps = hi > lo ? (hi - 1) / kStepTokens + 1 - s.step0 : 0;
+  s.tiles = (s.n * (a.num_heads / c.num_kv_heads) + tile_rows - 1) / tile_rows;
   return s;
 }
 
@@ -202,9 +206,11 @@ attention_split_kernel(const AttentionArgs a, const KvCache c, unsigned* __restr
   uint2* qf = reinterpret_cast<uint2*>(smem + L::kRing);
   float* join = reinterpret_cast<float*>(smem + L::kRing + L::kFrags);
   float2* ml = reinterpret_cast<float2*>(smem + L::kRing + L::kFrags + L::kJoin);
-  // float2 (pairs of rows): factor to log2 units, sum, first value of S; then last positions
+  // for each query row: factor to log2 units, sum, last position, place in the output
   float* row_info = reinterpret_cast<float*>(smem + L::kRing + L::kFrags + L::kJoin + L::kMl);
   Segment* segments = reinterpret_cast<Segment*>(smem + L::kRing + L::kFrags + L::kJoin + L::kMl + L::kRowInfo);
+  const int* row_last = reinterpret_cast<const int*>(row_info + 2 * kRows);
+  int64_t* row_out = reinterpret_cast<int64_t*>(row_info + 4 * kRows);
   static_assert(sizeof(Segment) <= 128, "two segments a warp");
   const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
   const int g = lane >> 2, j = lane & 3;
@@ -289,8 +295,8 @@ attention_split_kernel(const AttentionArgs a, const KvCache c, unsigned* __restr
         seek();
         continue;
       }
-      const int64_t item = (x - base) / units;
-      const int64_t i0 = base + item * units, i1 = i0 + units;
+      const int item = static_cast<int>((x - base) / units);
+      const int64_t i0 = base + static_cast<int64_t>(item) * units, i1 = i0 + units;
       const int64_t to = x_end < i1 ? x_end : i1;
       const int cost = units - sp.steps;
       const int from = x - i0 > cost ? static_cast<int>(x - i0) - cost : 0;
@@ -302,9 +308,9 @@ attention_split_kernel(const AttentionArgs a, const KvCache c, unsigned* __restr
         q.s = sp;
         q.end = end;
         q.r = r;
-        q.tile = static_cast<int>(item / hk);
-        q.h = static_cast<int>(item % hk);
-        q.rows = static_cast<int>(min(static_cast<int64_t>(kRows), static_cast<int64_t>(sp.n) * G - static_cast<int64_t>(q.tile) * kRows));
+        q.tile = item / hk;
+        q.h = item - q.tile * hk;
+        q.rows = min(kRows, sp.n * G - q.tile * kRows);
         q.from = from;
         q.to = sp.steps > 0 ? upto : from;
         const int64_t j0 = sp.steps > 0 ? i0 + cost : i0;
@@ -395,9 +401,10 @@ attention_split_kernel(const AttentionArgs a, const KvCache c, unsigned* __restr
     const int rows = q.rows;
     for (int nt = warp; nt < NT; nt += kWarps) {
       const int rr = nt * 8 + g;
-      const int64_t flat = static_cast<int64_t>(q.tile) * kRows + rr;
-      const int64_t token = flat / G;
-      const ple_bf16_t* src = a.q + (q.s.t0 + token) * a.q_stride + (static_cast<int64_t>(q.h) * G + (flat - token * G)) * D + j * (D / 4);
+      const int flat = q.tile * kRows + rr;
+      const int token = flat / G;
+      const int64_t head = static_cast<int64_t>(q.h * G + (flat - token * G)) * D;
+      const ple_bf16_t* src = a.q + static_cast<int64_t>(q.s.t0 + token) * a.q_stride + head + j * (D / 4);
       uint4 v[kWords];
       float top = 0.0f;
 #pragma unroll
@@ -437,11 +444,11 @@ attention_split_kernel(const AttentionArgs a, const KvCache c, unsigned* __restr
         odd += __shfl_xor_sync(0xffffffffu, odd, x2);
       }
       if (j == 0) {
-        const int64_t p = a.causal ? q.s.len - q.s.n + token : q.s.len - 1;
-        row_info[rr] = ldexpf(a.scale_log2, k);
-        row_info[kRows + rr] = fmaf(16.0f, odd, even);
-        row_info[2 * kRows + rr] = -1024.0f * (even + odd);
-        reinterpret_cast<int*>(row_info)[3 * kRows + rr] = rr < rows ? static_cast<int>(p) : -1;
+        row_info[rr] = ldexpf(a.scale_log2, k + 24);
+        row_info[kRows + rr] = ldexpf(fmaf(16.0f, odd, even), -24);
+        const int last = a.causal ? q.s.len - q.s.n + token : q.s.len - 1;
+        reinterpret_cast<int*>(row_info)[2 * kRows + rr] = rr < rows ? last : -1;
+        row_out[rr] = static_cast<int64_t>(q.s.t0 + token) * a.out_stride + head;
       }
     }
     __syncthreads();
@@ -453,10 +460,9 @@ attention_split_kernel(const AttentionArgs a, const KvCache c, unsigned* __restr
     // positions that every row of the tile sees: [all_from, all_to]
     int all_from = 0, all_to;
     {
-      const int64_t tok0 = static_cast<int64_t>(q.tile) * kRows / G;
-      const int64_t tok1 = (static_cast<int64_t>(q.tile) * kRows + rows - 1) / G;
-      all_to = static_cast<int>(a.causal ? q.s.len - q.s.n + tok0 : q.s.len - 1);
-      if (a.window > 0) all_from = static_cast<int>(max(q.s.len - q.s.n + tok1 - a.window + 1, int64_t(0)));
+      const int last0 = row_last[0], last1 = row_last[rows - 1];
+      all_to = last0;
+      if (a.window > 0) all_from = max(last1 - a.window + 1, 0);
     }
 
     float o[NT][D / 16][4];
@@ -497,11 +503,9 @@ attention_split_kernel(const AttentionArgs a, const KvCache c, unsigned* __restr
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
 #pragma unroll
-          for (int n = 0; n < NT; ++n) {
-            const float2 s0 = *reinterpret_cast<const float2*>(row_info + 2 * kRows + n * 8 + 2 * j);
-            s[n][b][0] = s[n][b][2] = s0.x;
-            s[n][b][1] = s[n][b][3] = s0.y;
-          }
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) s[n][b][i] = 0.0f;
           const uint8_t* kb = st + b * B::kBytes;
           uint32_t lo[kWords], hi[kWords];
           {
@@ -558,7 +562,7 @@ attention_split_kernel(const AttentionArgs a, const KvCache c, unsigned* __restr
               const bool there = (here >> b) & 1u;
 #pragma unroll
               for (int n = 0; n < NT; ++n) {
-                const int2 lasts = *reinterpret_cast<const int2*>(row_info + 3 * kRows + n * 8 + 2 * j);
+                const int2 lasts = *reinterpret_cast<const int2*>(row_last + n * 8 + 2 * j);
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
                   const int last = i == 0 ? lasts.x : lasts.y;
@@ -686,7 +690,8 @@ attention_split_kernel(const AttentionArgs a, const KvCache c, unsigned* __restr
           float* dst = join + (warp * L::kPass + n * 8 % L::kPass + 2 * j + e) * L::kPitch + g * L::kGroup;
 #pragma unroll
           for (int u = 0; u < D / 16; ++u)
-            *reinterpret_cast<float2*>(dst + 2 * u) = make_float2(o[n][u][e] + off[2 * n + e], o[n][u][2 + e] + off[2 * n + e]);
+            *reinterpret_cast<float2*>(dst + 2 * u) =
+                make_float2(fmaf(64.0f, o[n][u][e], off[2 * n + e]), fmaf(4.0f, o[n][u][2 + e], off[2 * n + e]));
         }
       }
       __syncthreads();
@@ -711,9 +716,7 @@ attention_split_kernel(const AttentionArgs a, const KvCache c, unsigned* __restr
         }
         if (q.pieces == 1) {
           const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-          const int64_t flat = static_cast<int64_t>(q.tile) * kRows + rr;
-          ple_bf16_t* dst = a.out + (q.s.t0 + flat / G) * a.out_stride + (static_cast<int64_t>(q.h) * G + flat % G) * D + d;
-          *reinterpret_cast<uint2*>(dst) = make_uint2(pack2(v.x * inv, v.y * inv), pack2(v.z * inv, v.w * inv));
+          *reinterpret_cast<uint2*>(a.out + row_out[rr] + d) = make_uint2(pack2(v.x * inv, v.y * inv), pack2(v.z * inv, v.w * inv));
         } else {
           *reinterpret_cast<float4*>(part + rr * D + d) = v;
           if (d == 0) *reinterpret_cast<float2*>(part + kRows * D + 2 * rr) = make_float2(top, sum);
@@ -728,27 +731,47 @@ attention_split_kernel(const AttentionArgs a, const KvCache c, unsigned* __restr
       if (*last_flag) {
         __threadfence();
         if (threadIdx.x == 0) counters[q.first] = 0;
-        for (int i = threadIdx.x; i < rows * (D / 4); i += kWarps * 32) {
-          const int rr = i / (D / 4), d = i % (D / 4) * 4;
-          float top = -FLT_MAX, sum = 0.0f;
-          float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 4
-          for (int k = 0; k < q.pieces; ++k) {
-            const int sl = 2 * (q.first + k) + (k == 0 ? 1 : 0);
-            const float* src = partial + static_cast<int64_t>(sl) * kRows * (D + 2);
-            const float2 t = __ldcg(reinterpret_cast<const float2*>(src + kRows * D + 2 * rr));
-            const float4 u = __ldcg(reinterpret_cast<const float4*>(src + rr * D + d));
-            const float next = fmaxf(top, t.x);
-            const float ka = ex2(top - next), kb = ex2(t.x - next);
-            sum = fmaf(kb, t.y, sum * ka);
-            v.x = fmaf(kb, u.x, v.x * ka); v.y = fmaf(kb, u.y, v.y * ka);
-            v.z = fmaf(kb, u.z, v.z * ka); v.w = fmaf(kb, u.w, v.w * ka);
-            top = next;
+        // a thread's elements lie in one row: its maximum first, then the sums
+        constexpr int kLanes = kWarps * 32 / kRows;  // threads of a row
+        const int rr = threadIdx.x / kLanes, lane_in_row = threadIdx.x % kLanes;
+        constexpr int64_t kSlot = kRows * (D + 2);
+        // piece 0 in slot 1 of its CTA, the others in slot 0 of theirs
+        auto piece = [&](int k) { return partial + (2 * static_cast<int64_t>(q.first + k) + (k == 0 ? 1 : 0)) * kSlot; };
+        if (rr < rows) {
+          float top = -FLT_MAX;
+          for (int k = lane_in_row; k < q.pieces; k += kLanes)
+            top = fmaxf(top, __ldcg(piece(k) + kRows * D + 2 * rr));
+          if constexpr (kLanes > 1) {
+            const unsigned peers = (kLanes < 32 ? (1u << (kLanes & 31)) - 1u : 0xffffffffu) << (lane / kLanes * kLanes);
+#pragma unroll
+            for (int x2 = kLanes / 2; x2 > 0; x2 >>= 1) top = fmaxf(top, __shfl_xor_sync(peers, top, x2));
           }
-          const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-          const int64_t flat = static_cast<int64_t>(q.tile) * kRows + rr;
-          ple_bf16_t* dst = a.out + (q.s.t0 + flat / G) * a.out_stride + (static_cast<int64_t>(q.h) * G + flat % G) * D + d;
-          *reinterpret_cast<uint2*>(dst) = make_uint2(pack2(v.x * inv, v.y * inv), pack2(v.z * inv, v.w * inv));
+          constexpr int kVecs = D / 4 / kLanes;  // float4 of a thread
+          constexpr int kAtOnce = kVecs < 4 ? kVecs : 4;
+          for (int v0 = 0; v0 < kVecs; v0 += kAtOnce) {
+            float4 v[kAtOnce];
+            float sum = 0.0f;
+#pragma unroll
+            for (int i = 0; i < kAtOnce; ++i) v[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll(16 / kAtOnce)
+            for (int k = 0; k < q.pieces; ++k) {
+              const float* src = piece(k);
+              const float2 t = __ldcg(reinterpret_cast<const float2*>(src + kRows * D + 2 * rr));
+              const float w = ex2(t.x - top);
+              sum = fmaf(w, t.y, sum);
+#pragma unroll
+              for (int i = 0; i < kAtOnce; ++i) {
+                const float4 u = __ldcg(reinterpret_cast<const float4*>(src + rr * D) + (v0 + i) * kLanes + lane_in_row);
+                v[i].x = fmaf(w, u.x, v[i].x); v[i].y = fmaf(w, u.y, v[i].y);
+                v[i].z = fmaf(w, u.z, v[i].z); v[i].w = fmaf(w, u.w, v[i].w);
+              }
+            }
+            const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+#pragma unroll
+            for (int i = 0; i < kAtOnce; ++i)
+              *reinterpret_cast<uint2*>(a.out + row_out[rr] + ((v0 + i) * kLanes + lane_in_row) * 4) =
+                  make_uint2(pack2(v[i].x * inv, v[i].y * inv), pack2(v[i].z * inv, v[i].w * inv));
+          }
         }
       }
     }
@@ -816,9 +839,11 @@ PLE_EXPORT ple_status ple_kv_attention(const ple_bf16_t* q, int64_t q_stride, in
   if (ple_status s = check_cache(name, cache, num_pages, page_size, block_table, max_pages,
                                  query_start_loc, num_reqs, kv_lens, num_kv_heads, head_dim))
     return s;
-  // block numbers are 32-bit in the kernel (2^31 blocks would be a cache of terabytes)
+  // query rows are 32-bit in the kernel, and so are block numbers in the kernel (2^31 blocks would be a cache of terabytes)
   if (num_pages > 0 && num_pages > (int64_t(1) << 31) / num_kv_heads / (page_size / kBlockTokens))
     return fail(PLE_ERR_UNSUPPORTED, "%s: %lld pages", name, static_cast<long long>(num_pages));
+  if (num_heads > 0 && num_tokens > INT32_MAX / 2 / num_heads)
+    return fail(PLE_ERR_UNSUPPORTED, "%s: %lld tokens of %d heads", name, static_cast<long long>(num_tokens), num_heads);
   if (num_heads < 1 || num_heads % num_kv_heads != 0)
     return fail(PLE_ERR_INVALID_ARG, "%s: %d heads over %d kv heads", name, num_heads, num_kv_heads);
   if (q == nullptr || out == nullptr || !aligned16(q) || !aligned16(out) || q_stride % 8 != 0 || out_stride % 8 != 0)

@@ -29,17 +29,21 @@ struct AttentionArgs {
 // ---------------------------------------------------------------------------
 // Work. An item is (request, tile of 8 NT query rows, kv head); its cost is
 // the number of 32-token steps of the cache it reads. The steps of all items
-// lie on one line, cut into equal pieces, one for each CTA, so a single long
-// request and hundreds of ragged ones load the card alike. An item that a cut
-// falls into leaves partial results (row maxima, sums, unnormalised outputs)
-// in the workspace, and the CTA that arrives last joins them in the order of
-// the pieces: results do not depend on timing. Every CTA finds its piece from
-// query_start_loc and kv_lens itself: one launch, no plan on the host.
+// lie on one line, cut into equal pieces, one a warp, so a single long request
+// and hundreds of ragged ones load the card alike; every warp finds its piece
+// from query_start_loc and kv_lens itself (one launch, no plan on the host).
+// An item that a cut falls into leaves partial results (row maxima, sums,
+// unnormalised outputs, as they lie in a warp's registers) in the workspace;
+// the piece that arrives last in its group of eight joins the group, the group
+// that arrives last joins the groups, and so on, each in the order of the
+// pieces: results do not depend on timing.
 //
-// Streams. Each of a CTA's four warps has its own share of the piece's
-// steps and its own ring of stages in shared memory; a stage is two cache
-// blocks, each one bulk copy. No warp waits for another until the item ends,
-// and the next item's first copies fly while this one's results are joined.
+// Warps share nothing. Each has a ring of stages in shared memory (a stage is
+// a step: two cache blocks, each one bulk copy) and fills it itself; no warp
+// ever waits for another, and a warp's next item is looked up and its first
+// copies fly before the last one's results are written. (A producer warp for
+// seven others, which meet where an item ends, took 355 us where this takes
+// the time stated below: steps handed out in turn are held up by the slowest.)
 //
 // Products, on warp-wide matrix instructions (16 x 8 x 16, f32 sums; reading
 // the cache and unpacking it, not their rate, is the bound):
@@ -68,27 +72,28 @@ struct AttentionArgs {
 // that order; two tokens' V bytes are interleaved with one permute a word.
 // Token rows are taken in the order t ^ (t >> 1 & 1), which lets the V loads
 // of neighbouring lanes fall on different banks.
-constexpr int kWarps = 4;
 constexpr int kStepTokens = 2 * kBlockTokens;
 
-// NT tiles of 8 query rows a warp; registers and shared memory set the CTAs an SM holds.
+// NT tiles of 8 query rows. What an SM holds follows from the registers of a
+// warp's outputs, D NT / 4 a thread: 16 warps of 128 registers, 12 of 168, or
+// 8; the ring takes the shared memory that is left.
+constexpr int kWarps = 4;  // of a CTA
+
 template <int D, int NT>
 struct Split {
   static constexpr int kRows = 8 * NT;
   static constexpr int kStage = 2 * KvBlock<D>::kBytes;
-  static constexpr int kCtas = D == 256 || NT == 4 ? 2 : NT == 2 ? 3 : 4;  // per SM
-  static constexpr int kStages = D == 256 ? 2 : D == 64 || NT == 4 ? 4 : NT == 2 ? 3 : 2;
-  static constexpr bool kQRegs = NT * D <= 256;      // query fragments in registers
-  static constexpr int kPass = 8;                    // rows joined at a time
-  static constexpr int kGroup = D / 8 + 2;           // a lane group's elements, padded
-  static constexpr int kPitch = 8 * kGroup + 4;      // floats of a row in the joining buffer
-  static constexpr int kRing = kWarps * kStages * kStage;
-  static constexpr int kFrags = NT * (D / 16) * 32 * 8;  // bytes of query fragments
-  static constexpr int kJoin = kWarps * kPass * kPitch * 4;
-  static constexpr int kMl = kWarps * kRows * 8;
+  static constexpr int kCtas = D == 256 || NT == 4 ? 2 : NT == 2 ? 3 : 4;  // an SM holds
+  static constexpr int kStages = D == 256 ? (NT == 1 ? 3 : 2) : D == 64 ? 5 : 3 + NT / 4;
+  static constexpr bool kQRegs = NT == 1;            // query fragments in registers
+  static constexpr int kFrags = kQRegs ? 0 : NT * (D / 16) * 32 * 8;
   static constexpr int kRowInfo = kRows * 24;        // a query row's factor, sum, last position, place in the output
-  static constexpr int kSegments = 2 * 128;  // the present and the next segment
-  static constexpr int kSmem = kRing + kFrags + kJoin + kMl + kRowInfo + kSegments + kWarps * kStages * 8 + 16;
+  static constexpr int kAtRows = kStages * kStage + kFrags;
+  static constexpr int kAtItems = kAtRows + kRowInfo;
+  static constexpr int kAtBars = kAtItems + 3 * 64;
+  static constexpr int kWarpBytes = (kAtBars + kStages * 8 + 127) / 128 * 128;
+  static constexpr int kSmem = kWarps * kWarpBytes + 16;
+  static constexpr int kSlot = kRows * (D + 2);      // floats of a partial result
 };
 
 __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
@@ -177,21 +182,145 @@ __device__ __forceinline__ Span span_of(const AttentionArgs& a, const KvCache& c
 
 // An item's length on the line: what starting and joining it costs, in steps,
 // then its steps; 1 for an item that only writes zeros.
-constexpr int kItemCost = 4;
+constexpr int kItemCost = 6;
 __device__ __forceinline__ int units_of(const Span& s) { return s.steps > 0 ? kItemCost + s.steps : 1; }
 
 __device__ __forceinline__ int64_t weight_of(const Span& s, int hk) {
   return static_cast<int64_t>(s.tiles) * hk * units_of(s);
 }
 
-// A CTA's share of one item.
-struct Segment {
-  Span s;
-  int64_t end;        // where the request's items end on the line
+// Pieces of the line, one a warp; none so short that starting it is most of it.
+constexpr int kMinPiece = 8;
+__device__ __forceinline__ int pieces_of(int64_t W, int warps) {
+  const int64_t p = (W + kMinPiece - 1) / kMinPiece;
+  return p < warps ? static_cast<int>(p) : warps;
+}
+
+// A piece's share of one item.
+struct Item {
   int r, tile, h, rows;
-  int from, to;       // steps, relative to s.step0
-  int pieces, first;  // CTAs that share the item's steps, the first of them
+  int t0, n, len;         // of the request
+  int block0, block_end;  // blocks that rows may see, up to this share's end
+  int step, steps;        // first step, and how many
+  int pieces, first;      // that share the item's steps, the first of them
+  bool clipped;
 };
+
+// Where a warp stands on the line (in shared memory: the steps need none of it).
+struct Cursor {
+  int64_t W;         // the line's length
+  int64_t x, x_end;  // what is left of the piece
+  int64_t base;      // where request r begins
+  int r;
+};
+
+constexpr int kFan = 8;  // pieces joined at a time
+
+// Slot of an item's piece k. A piece is the first of one item that goes on,
+// and a later one of one item, at most.
+__device__ __forceinline__ int slot_of(int first, int k) { return 2 * (first + k) + (k == 0 ? 1 : 0); }
+
+// An item's results in a warp's registers. Lane (g, j) holds elements
+// g D / 8 + 2 u and + 1 (u < D / 16) of rows 8 n + 2 j and + 1.
+template <int D, int NT>
+struct Results {
+  float o[NT][D / 16][4];  // (row, element): (0, 0), (1, 0), (0, 1), (1, 1)
+  float m[2 * NT], l[2 * NT];
+};
+
+template <int D, int NT>
+__device__ __forceinline__ void store_partial(const Results<D, NT>& x, float* slot) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+#pragma unroll
+    for (int u = 0; u < D / 16; ++u)
+      reinterpret_cast<float4*>(slot)[(n * (D / 16) + u) * 32 + lane] =
+          make_float4(x.o[n][u][0], x.o[n][u][1], x.o[n][u][2], x.o[n][u][3]);
+  if (lane < 4) {
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+      reinterpret_cast<float4*>(slot + 8 * NT * D)[n * 4 + lane] =
+          make_float4(x.m[2 * n], x.l[2 * n], x.m[2 * n + 1], x.l[2 * n + 1]);
+  }
+}
+
+// Join the partial results of pieces k0, k0 + stride, ... (count of them).
+template <int D, int NT>
+__device__ __forceinline__ void load_joined(Results<D, NT>& x, const float* partial, int first, int k0, int stride, int count) {
+  constexpr int kSlot = Split<D, NT>::kSlot;
+  constexpr int kAtOnce = D / 16 < 4 ? D / 16 : 4;
+  const int lane = threadIdx.x & 31, j = lane & 3;
+  auto slot = [&](int k) { return partial + static_cast<int64_t>(slot_of(first, k0 + k * stride)) * kSlot; };
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+    float4 ml[kFan];
+#pragma unroll
+    for (int k = 0; k < kFan; ++k)  // past the last: it again, with no weight
+      ml[k] = __ldcg(reinterpret_cast<const float4*>(slot(min(k, count - 1)) + 8 * NT * D) + n * 4 + j);
+    float m0 = ml[0].x, m1 = ml[0].z;
+#pragma unroll
+    for (int k = 1; k < kFan; ++k) { m0 = fmaxf(m0, ml[k].x); m1 = fmaxf(m1, ml[k].z); }
+    float w0[kFan], w1[kFan], l0 = 0.0f, l1 = 0.0f;
+#pragma unroll
+    for (int k = 0; k < kFan; ++k) {
+      w0[k] = k < count ? ex2(ml[k].x - m0) : 0.0f;
+      w1[k] = k < count ? ex2(ml[k].z - m1) : 0.0f;
+      if (k < count) { l0 = fmaf(w0[k], ml[k].y, l0); l1 = fmaf(w1[k], ml[k].w, l1); }
+    }
+    x.m[2 * n] = m0; x.m[2 * n + 1] = m1;
+    x.l[2 * n] = l0; x.l[2 * n + 1] = l1;
+#pragma unroll
+    for (int u0 = 0; u0 < D / 16; u0 += kAtOnce) {
+      float4 acc[kAtOnce];
+#pragma unroll
+      for (int u = 0; u < kAtOnce; ++u) acc[u] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+      for (int k = 0; k < kFan; k += 4) {
+        if (k < count) {
+          float4 v[4][kAtOnce];
+#pragma unroll
+          for (int f = 0; f < 4; ++f)
+#pragma unroll
+            for (int u = 0; u < kAtOnce; ++u)
+              v[f][u] = __ldcg(reinterpret_cast<const float4*>(slot(min(k + f, count - 1))) + (n * (D / 16) + u0 + u) * 32 + lane);
+#pragma unroll
+          for (int f = 0; f < 4; ++f)
+            if (k + f < count)
+#pragma unroll
+              for (int u = 0; u < kAtOnce; ++u) {
+                acc[u].x = fmaf(w0[k + f], v[f][u].x, acc[u].x); acc[u].y = fmaf(w1[k + f], v[f][u].y, acc[u].y);
+                acc[u].z = fmaf(w0[k + f], v[f][u].z, acc[u].z); acc[u].w = fmaf(w1[k + f], v[f][u].w, acc[u].w);
+              }
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < kAtOnce; ++u) {
+        x.o[n][u0 + u][0] = acc[u].x; x.o[n][u0 + u][1] = acc[u].y;
+        x.o[n][u0 + u][2] = acc[u].z; x.o[n][u0 + u][3] = acc[u].w;
+      }
+    }
+  }
+}
+
+template <int D, int NT>
+__device__ __forceinline__ void store_out(const Results<D, NT>& x, ple_bf16_t* out, const int64_t* row_out, int rows) {
+  const int lane = threadIdx.x & 31, g = lane >> 2, j = lane & 3;
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int rr = n * 8 + 2 * j + e;
+      const float l = x.l[2 * n + e], inv = l == 0.0f ? 0.0f : 1.0f / l;
+      if (rr < rows) {
+        uint2* dst = reinterpret_cast<uint2*>(out + row_out[rr] + g * (D / 8));
+#pragma unroll
+        for (int u = 0; u < D / 16; u += 2)
+          dst[u / 2] = make_uint2(pack2(x.o[n][u][e] * inv, x.o[n][u][2 + e] * inv),
+                                  pack2(x.o[n][u + 1][e] * inv, x.o[n][u + 1][2 + e] * inv));
+      }
+    }
+}
 
 template <int D, int NT>
 __global__ void __launch_bounds__(kWarps * 32, (Split<D, NT>::kCtas))
@@ -203,22 +332,18 @@ attention_split_kernel(const AttentionArgs a, const KvCache c, unsigned* __restr
   constexpr int kWords = D / 32;   // K words of a lane and token
   constexpr int kVWords = D / 64;  // V words of a lane and token
   extern __shared__ __align__(128) uint8_t smem[];
-  uint2* qf = reinterpret_cast<uint2*>(smem + L::kRing);
-  float* join = reinterpret_cast<float*>(smem + L::kRing + L::kFrags);
-  float2* ml = reinterpret_cast<float2*>(smem + L::kRing + L::kFrags + L::kJoin);
-  // for each query row: factor to log2 units, sum, last position, place in the output
-  float* row_info = reinterpret_cast<float*>(smem + L::kRing + L::kFrags + L::kJoin + L::kMl);
-  Segment* segments = reinterpret_cast<Segment*>(smem + L::kRing + L::kFrags + L::kJoin + L::kMl + L::kRowInfo);
-  const int* row_last = reinterpret_cast<const int*>(row_info + 2 * kRows);
-  int64_t* row_out = reinterpret_cast<int64_t*>(row_info + 4 * kRows);
-  static_assert(sizeof(Segment) <= 128, "two segments a warp");
   const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
   const int g = lane >> 2, j = lane & 3;
-  uint8_t* ring = smem + warp * L::kStages * L::kStage;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::kSmem - 16 - kWarps * L::kStages * 8);
-  const uint32_t bar0 = smem_u32(bars + warp * L::kStages);
-  int64_t* total = reinterpret_cast<int64_t*>(smem + L::kSmem - 16);
-  int* last_flag = reinterpret_cast<int*>(smem + L::kSmem - 8);
+  uint8_t* const ring = smem + warp * L::kWarpBytes;
+  uint2* const qf = reinterpret_cast<uint2*>(ring + L::kStages * L::kStage);
+  float* const row_info = reinterpret_cast<float*>(ring + L::kAtRows);  // factors to log2 units, sums, ...
+  int* const row_last = reinterpret_cast<int*>(row_info + 2 * kRows);
+  int64_t* const row_out = reinterpret_cast<int64_t*>(row_info + 4 * kRows);
+  Item* const items = reinterpret_cast<Item*>(ring + L::kAtItems);  // the present and the next
+  Cursor* const cursor = reinterpret_cast<Cursor*>(items + 2);
+  static_assert(sizeof(Item) <= 64 && sizeof(Item) % 8 == 0 && sizeof(Cursor) <= 64 && L::kStages <= 8, "room in shared memory and in the stages' bits");
+  const uint32_t bar0 = smem_u32(ring + L::kAtBars);
+  unsigned long long* const total = reinterpret_cast<unsigned long long*>(smem + kWarps * L::kWarpBytes);
 
   if (lane == 0) {
     for (int s = 0; s < L::kStages; ++s) mbar_init(bar0 + 8 * s, 1);
@@ -229,98 +354,118 @@ attention_split_kernel(const AttentionArgs a, const KvCache c, unsigned* __restr
   pdl_wait();
   pdl_trigger();
 
-  const int G = a.num_heads / c.num_kv_heads;
-  const int hk = c.num_kv_heads;
-  // all items' steps
-  {
-    int64_t mine = 0;
-    for (int r = threadIdx.x; r < c.num_reqs; r += kWarps * 32) mine += weight_of(span_of(a, c, r, kRows), hk);
+  const int G = a.num_heads / c.num_kv_heads, hk = c.num_kv_heads;
+  // the line's length
+  int64_t W = 0;
+  if (c.num_reqs <= 32) {
+    if (lane < c.num_reqs) W = weight_of(span_of(a, c, lane, kRows), hk);
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
-    if (lane == 0 && mine > 0) atomicAdd(reinterpret_cast<unsigned long long*>(total), static_cast<unsigned long long>(mine));
-    for (int64_t i = int64_t(blockIdx.x) * (kWarps * 32) + threadIdx.x; i < c.num_reqs; i += int64_t(gridDim.x) * (kWarps * 32))
-      check_qsl(c.qsl, c.num_reqs, a.T, i, a.dev_err);
-    // padding tokens' rows
-    int64_t pad = __ldg(c.qsl + c.num_reqs);
-    pad = pad < 0 ? 0 : pad;
-    const int64_t vecs = static_cast<int64_t>(a.num_heads) * (D / 8);
-    for (int64_t i = pad * vecs + int64_t(blockIdx.x) * (kWarps * 32) + threadIdx.x; i < a.T * vecs;
-         i += int64_t(gridDim.x) * (kWarps * 32))
-      *reinterpret_cast<uint4*>(a.out + i / vecs * a.out_stride + i % vecs * 8) = make_uint4(0, 0, 0, 0);
+    for (int o = 16; o > 0; o >>= 1) W += __shfl_xor_sync(0xffffffffu, W, o);
+  } else {
+    for (int r = threadIdx.x; r < c.num_reqs; r += kWarps * 32) W += weight_of(span_of(a, c, r, kRows), hk);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) W += __shfl_xor_sync(0xffffffffu, W, o);
+    if (lane == 0 && W > 0) atomicAdd(total, static_cast<unsigned long long>(W));
+    __syncthreads();
+    W = static_cast<int64_t>(*total);
   }
-  __syncthreads();
-  const int64_t W = *total;
-  // pieces of at least one step for each warp
-  const int64_t most = (W + kWarps + kItemCost - 1) / (kWarps + kItemCost);
-  const int64_t S = most < gridDim.x ? most : gridDim.x;
-  if (blockIdx.x >= S) return;
-  int64_t x = blockIdx.x * W / S;
-  const int64_t x_end = (blockIdx.x + 1) * W / S;
-
-  // the request that x lies in; base: its first step on the line
-  int r = 0;
-  int64_t base = 0;
-  auto seek = [&]() {  // from request r at base on, the first request that ends past x
-    for (;;) {
-      int64_t w = r + lane < c.num_reqs ? weight_of(span_of(a, c, r + lane, kRows), hk) : 0;
-      int64_t sum = w;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int64_t up = __shfl_up_sync(0xffffffffu, sum, o);
-        if (lane >= o) sum += up;
-      }
-      const unsigned past = __ballot_sync(0xffffffffu, base + sum > x);
-      if (past != 0) {
-        const int at = __ffs(past) - 1;
-        base += __shfl_sync(0xffffffffu, sum - w, at);
-        r += at;
-        return;
-      }
-      base += __shfl_sync(0xffffffffu, sum, 31);
-      r += 32;
-      if (r >= c.num_reqs) return;  // not reached: x < W
-    }
+  const int warps = gridDim.x * kWarps;
+  const int P = pieces_of(W, warps);
+  const int piece = warp * gridDim.x + blockIdx.x;  // few pieces: on as many SMs
+  // what is done beside the items: checks, and padding tokens' rows
+  auto rest = [&]() {
+    const int64_t at = int64_t(blockIdx.x) * (kWarps * 32) + threadIdx.x, all = int64_t(gridDim.x) * (kWarps * 32);
+    for (int64_t i = at; i < c.num_reqs; i += all) check_qsl(c.qsl, c.num_reqs, a.T, i, a.dev_err);
+    const int64_t pad = max(__ldg(c.qsl + c.num_reqs), 0);
+    const int64_t vecs = static_cast<int64_t>(a.num_heads) * (D / 8);
+    for (int64_t i = pad * vecs + at; i < a.T * vecs; i += all)
+      *reinterpret_cast<uint4*>(a.out + i / vecs * a.out_stride + i % vecs * 8) = make_uint4(0, 0, 0, 0);
   };
+  if (piece >= P) {
+    rest();
+    return;
+  }
 
-  // The next segment with something to do, from x on; false if there is none.
-  // Every warp finds it for itself and writes the same values down.
-  auto next_segment = [&](Segment* out) {
+  // quotients of products up to W * P, in 32 bits where they fit
+  auto div = [](int64_t n, int64_t d, int64_t most) {
+    return most < (int64_t(1) << 31) ? static_cast<int64_t>(static_cast<uint32_t>(n) / static_cast<uint32_t>(d)) : n / d;
+  };
+  if (lane == 0) {
+    Cursor at;
+    at.W = W;
+    at.x = div(piece * W, P, W * P);
+    at.x_end = div((piece + 1) * W, P, W * P);
+    at.base = 0;
+    at.r = 0;
+    *cursor = at;
+  }
+  __syncwarp();
+  // The next item with steps of this piece; false if there is none.
+  auto next_item = [&](Item* out) {
+    const int64_t W = cursor->W, x_end = cursor->x_end;
+    const int P = pieces_of(W, gridDim.x * kWarps);
+    int64_t x = cursor->x, base = cursor->base;
+    int r = cursor->r;
+    __syncwarp();
     while (x < x_end) {
+      while (r < c.num_reqs) {  // the request that x lies in
+        const int64_t w = r + lane < c.num_reqs ? weight_of(span_of(a, c, r + lane, kRows), hk) : 0;
+        int64_t sum = w;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int64_t up = __shfl_up_sync(0xffffffffu, sum, o);
+          if (lane >= o) sum += up;
+        }
+        const unsigned past = __ballot_sync(0xffffffffu, base + sum > x);
+        if (past != 0) {
+          const int at = __ffs(past) - 1;
+          base += __shfl_sync(0xffffffffu, sum - w, at);
+          r += at;
+          break;
+        }
+        base += __shfl_sync(0xffffffffu, sum, 31);
+        r += 32;
+      }
+      if (r >= c.num_reqs) return false;  // kv_lens changed under way
       const Span sp = span_of(a, c, r, kRows);
       const int units = units_of(sp);
-      const int64_t end = base + static_cast<int64_t>(sp.tiles) * hk * units;
-      if (x >= end) {
-        base = end;
-        ++r;
-        seek();
-        continue;
-      }
-      const int item = static_cast<int>((x - base) / units);
+      const int item = static_cast<int>(div(x - base, units, W * P));
       const int64_t i0 = base + static_cast<int64_t>(item) * units, i1 = i0 + units;
-      const int64_t to = x_end < i1 ? x_end : i1;
+      const int64_t end = x_end < i1 ? x_end : i1;
       const int cost = units - sp.steps;
       const int from = x - i0 > cost ? static_cast<int>(x - i0) - cost : 0;
-      const int upto = static_cast<int>(to - i0) - cost;
-      x = to;
-      if (sp.steps > 0 && upto <= from) continue;  // the item's steps are all another CTA's
+      const int to = sp.steps > 0 ? static_cast<int>(end - i0) - cost : 0;
+      x = end;
+      if (sp.steps > 0 && to <= from) continue;  // its steps all lie in another piece
       if (lane == 0) {
-        Segment q;
-        q.s = sp;
-        q.end = end;
-        q.r = r;
-        q.tile = item / hk;
-        q.h = item - q.tile * hk;
-        q.rows = min(kRows, sp.n * G - q.tile * kRows);
-        q.from = from;
-        q.to = sp.steps > 0 ? upto : from;
+        Item it;
+        it.r = r;
+        it.tile = item / hk;
+        it.h = item - it.tile * hk;
+        it.rows = min(kRows, sp.n * G - it.tile * kRows);
+        it.t0 = sp.t0;
+        it.n = sp.n;
+        it.len = sp.len;
+        it.clipped = sp.clipped;
+        it.step = sp.step0 + from;
+        it.steps = to - from;
+        it.block0 = sp.block0;
+        const int64_t room = static_cast<int64_t>(c.max_pages) * (c.page_size / kBlockTokens);
+        const int held = (sp.len + kBlockTokens - 1) / kBlockTokens;
+        it.block_end = min(static_cast<int>(held < room ? held : room), 2 * (it.step + it.steps));
         const int64_t j0 = sp.steps > 0 ? i0 + cost : i0;
-        q.first = static_cast<int>(((j0 + 1) * S - 1) / W);
-        q.pieces = static_cast<int>((i1 * S - 1) / W) - q.first + 1;
-        *out = q;
+        it.first = static_cast<int>(div((j0 + 1) * P - 1, W, W * P));
+        it.pieces = static_cast<int>(div(i1 * P - 1, W, W * P)) - it.first + 1;
+        *out = it;
+        cursor->x = x;
+        cursor->base = base;
+        cursor->r = r;
       }
       __syncwarp();
       return true;
     }
+    if (lane == 0) cursor->x = x;
+    __syncwarp();
     return false;
   };
 
@@ -328,27 +473,32 @@ attention_split_kernel(const AttentionArgs a, const KvCache c, unsigned* __restr
   const int per_page = c.page_size / kBlockTokens;
   uint32_t phases = 0, armed = 0, present = 0;  // by stage: parity, a copy issued, blocks present (2 bits)
   bool dead = false;                            // a wait gave up: no more copies
-  int issue_step = 0, issue_end = 0;            // absolute steps
-  int pages_at = 0;                             // first block of `blocks`
-  int blocks = -1, blocks_next = -1;            // where request blocks pages_at + lane and + 32 lie; -1: nowhere
-  const int32_t* table = c.block_table;
-  int block_begin = 0, block_end = 0;           // blocks that this warp's rows may see
-  int issue_h = 0;
+  int ahead = 0;                                // steps still to issue
+  int blocks_left = 0;                          // of `blocks`, not yet used
+  int block = 0;                                // behind blocks_next
+  int blocks = -1, blocks_next = -1;            // where the next 32 blocks lie, and the 32 behind them; -1: nowhere
   int stage_in = 0, stage_out = 0;
-  auto block_at = [&](int block) {
-    if (block < block_begin || block >= block_end) return -1;
-    const int col = block / per_page;
-    const int64_t page = __ldg(table + col);
+  const Item* source = items;                   // the item being copied
+  auto block_at = [&](int b) {
+    if (b < source->block0 || b >= source->block_end) return -1;
+    const int col = b / per_page;
+    const int64_t page = __ldg(c.block_table + static_cast<int64_t>(source->r) * c.max_pages + col);
     if (page < 0 || page >= c.num_pages) {
       set_dev_err(a.dev_err, PLE_DEVERR_BOUNDS);
       return -1;
     }
-    return static_cast<int>((page * hk + issue_h) * per_page + (block - col * per_page));
+    return static_cast<int>((page * hk + source->h) * per_page + (b - col * per_page));
   };
   auto issue = [&]() {
-    if (issue_step >= issue_end || dead) return;
-    const int b = 2 * issue_step - pages_at;
-    const int at = __shfl_sync(0xffffffffu, blocks, b + (lane & 1));
+    if (ahead == 0 || dead) return;
+    if (blocks_left == 0) {
+      blocks = blocks_next;
+      blocks_next = block_at(block + lane);
+      block += 32;
+      blocks_left = 32;
+    }
+    const int at = __shfl_sync(0xffffffffu, blocks, 32 - blocks_left + (lane & 1));
+    blocks_left -= 2;
     const unsigned mask = __ballot_sync(0xffffffffu, at >= 0) & 3u;
     const uint32_t bar = bar0 + 8 * stage_in;
     if (lane == 0) mbar_arrive_expect_tx(bar, __popc(mask) * B::kBytes);
@@ -356,61 +506,51 @@ attention_split_kernel(const AttentionArgs a, const KvCache c, unsigned* __restr
     if (lane < 2 && at >= 0)
       bulk_copy_g2s(smem_u32(ring + stage_in * L::kStage + lane * B::kBytes),
                     c.base + static_cast<int64_t>(at) * B::kBytes, B::kBytes, bar);
-    if (b == 30) {
-      pages_at += 32;
-      blocks = blocks_next;
-      blocks_next = block_at(pages_at + 32 + lane);
-    }
     present = (present & ~(3u << (2 * stage_in))) | (mask << (2 * stage_in));
     armed |= 1u << stage_in;
-    ++issue_step;
+    --ahead;
     if (++stage_in == L::kStages) stage_in = 0;
   };
-  auto share = [&](const Segment& q, int& from, int& to) {  // of this warp
-    const int per = (q.to - q.from + kWarps - 1) / kWarps;
-    from = min(q.from + warp * per, q.to);
-    to = min(from + per, q.to);
-  };
-  auto start = [&](const Segment& q) {
-    int from, to;
-    share(q, from, to);
-    issue_step = q.s.step0 + from;
-    issue_end = q.s.step0 + to;
-    issue_h = q.h;
-    table = c.block_table + static_cast<int64_t>(q.r) * c.max_pages;
-    const int64_t room = static_cast<int64_t>(c.max_pages) * per_page;
-    const int64_t held = (q.s.len + kBlockTokens - 1) / kBlockTokens;
-    block_end = static_cast<int>(held < room ? held : room);
-    block_begin = q.s.block0;
-    // not past this warp's own steps: what it never reads raises no flag
-    block_end = min(block_end, 2 * issue_end);
-    if (q.s.clipped && lane == 0) set_dev_err(a.dev_err, PLE_DEVERR_BOUNDS);
-    pages_at = 2 * issue_step;
-    blocks = block_at(pages_at + lane);
-    blocks_next = block_at(pages_at + 32 + lane);
+  auto start = [&](const Item* it) {
+    source = it;
+    ahead = it->steps;
+    if (it->clipped && lane == 0) set_dev_err(a.dev_err, PLE_DEVERR_BOUNDS);
+    block = 2 * it->step;
+    blocks = block_at(block + lane);
+    blocks_next = block_at(block + 32 + lane);
+    block += 64;
+    blocks_left = 32;
 #pragma unroll 1
     for (int s = 0; s < L::kStages; ++s) issue();
   };
 
-  seek();
-  if (!next_segment(segments)) return;
-  start(segments[0]);
-  for (int which = 0;; which ^= 1) {
-    const Segment& q = segments[which];
-    // the tile's query rows as B fragments, and what a score needs of them
-    const int rows = q.rows;
-    for (int nt = warp; nt < NT; nt += kWarps) {
+  bool more = next_item(items);
+  if (more) start(items);
+  rest();
+#pragma unroll 1
+  for (int which = 0; more; which ^= 1) {
+    const Item* const it = items + which;
+    const int rows = it->rows;
+    // The query rows as B fragments, and what a score needs of each row: the
+    // factor that takes it to log2 units, the sum of its elements, its last
+    // position, its place in the output.
+    uint2 qr[L::kQRegs ? D / 16 : 1];
+#pragma unroll 1
+    for (int nt = 0; nt < NT; ++nt) {
       const int rr = nt * 8 + g;
-      const int flat = q.tile * kRows + rr;
+      const int flat = it->tile * kRows + rr;
       const int token = flat / G;
-      const int64_t head = static_cast<int64_t>(q.h * G + (flat - token * G)) * D;
-      const ple_bf16_t* src = a.q + static_cast<int64_t>(q.s.t0 + token) * a.q_stride + head + j * (D / 4);
+      const int64_t head = static_cast<int64_t>(it->h * G + (flat - token * G)) * D;
+      const ple_bf16_t* src = a.q + static_cast<int64_t>(it->t0 + token) * a.q_stride + head + j * (D / 4);
       uint4 v[kWords];
       float top = 0.0f;
 #pragma unroll
       for (int w = 0; w < kWords; ++w) {
         v[w] = make_uint4(0, 0, 0, 0);
         if (rr < rows) v[w] = *reinterpret_cast<const uint4*>(src + 8 * w);
+      }
+#pragma unroll
+      for (int w = 0; w < kWords; ++w) {
         float f[8];
         unpack8(v[w], f);
 #pragma unroll
@@ -435,8 +575,13 @@ attention_split_kernel(const AttentionArgs a, const KvCache c, unsigned* __restr
           if (i % 2 == 0) even += r2.x + r2.y;
           else odd += r2.x + r2.y;
         }
-        qf[((2 * w) * NT + nt) * 32 + lane] = make_uint2(p[0], p[1]);
-        qf[((2 * w + 1) * NT + nt) * 32 + lane] = make_uint2(p[2], p[3]);
+        if constexpr (L::kQRegs) {
+          qr[2 * w] = make_uint2(p[0], p[1]);
+          qr[2 * w + 1] = make_uint2(p[2], p[3]);
+        } else {
+          qf[((2 * w) * NT + nt) * 32 + lane] = make_uint2(p[0], p[1]);
+          qf[((2 * w + 1) * NT + nt) * 32 + lane] = make_uint2(p[2], p[3]);
+        }
       }
 #pragma unroll
       for (int x2 = 1; x2 < 4; x2 <<= 1) {
@@ -446,27 +591,21 @@ attention_split_kernel(const AttentionArgs a, const KvCache c, unsigned* __restr
       if (j == 0) {
         row_info[rr] = ldexpf(a.scale_log2, k + 24);
         row_info[kRows + rr] = ldexpf(fmaf(16.0f, odd, even), -24);
-        const int last = a.causal ? q.s.len - q.s.n + token : q.s.len - 1;
-        reinterpret_cast<int*>(row_info)[2 * kRows + rr] = rr < rows ? last : -1;
-        row_out[rr] = static_cast<int64_t>(q.s.t0 + token) * a.out_stride + head;
+        const int last = a.causal ? it->len - it->n + token : it->len - 1;
+        row_last[rr] = rr < rows ? last : -1;
+        row_out[rr] = static_cast<int64_t>(it->t0 + token) * a.out_stride + head;
       }
     }
-    __syncthreads();
-    uint2 qr[L::kQRegs ? NT * (D / 16) : 1];
-    if constexpr (L::kQRegs) {
-#pragma unroll
-      for (int i = 0; i < NT * (D / 16); ++i) qr[i] = qf[i * 32 + lane];
-    }
-    // positions that every row of the tile sees: [all_from, all_to]
-    int all_from = 0, all_to;
-    {
-      const int last0 = row_last[0], last1 = row_last[rows - 1];
-      all_to = last0;
-      if (a.window > 0) all_from = max(last1 - a.window + 1, 0);
-    }
+    __syncwarp();
+    // positions that every row sees: [all_from, all_to]
+    const int all_to = row_last[0];
+    const int all_from = a.window > 0 ? max(row_last[rows - 1] - a.window + 1, 0) : 0;
 
-    float o[NT][D / 16][4];
-    float m[2 * NT], l[2 * NT], off[2 * NT];
+    Results<D, NT> res;
+    auto& o = res.o;
+    auto& m = res.m;
+    auto& l = res.l;
+    float off[2 * NT];  // sums of p (m + 8 s)
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -475,13 +614,10 @@ attention_split_kernel(const AttentionArgs a, const KvCache c, unsigned* __restr
         for (int i = 0; i < 4; ++i) o[n][u][i] = 0.0f;
 #pragma unroll
     for (int i = 0; i < 2 * NT; ++i) { m[i] = -FLT_MAX; l[i] = 0.0f; off[i] = 0.0f; }
-    const int step0 = q.s.step0;
 
-    int from, to;
-    share(q, from, to);
+    const int p_end = (it->step + it->steps) * kStepTokens;
 #pragma unroll 1
-    for (int step = from; step < to; ++step) {
-      const int p0 = (step0 + step) * kStepTokens;
+    for (int p0 = it->step * kStepTokens; p0 < p_end; p0 += kStepTokens) {
       uint32_t here = 0;
       if (!dead) {
         const bool ok = mbar_try_wait(bar0 + 8 * stage_out, (phases >> stage_out) & 1u) ||
@@ -662,11 +798,10 @@ attention_split_kernel(const AttentionArgs a, const KvCache c, unsigned* __restr
       issue();
     }
 
-    // the next item's copies fly while this one's results are joined
-    const bool more = next_segment(segments + (which ^ 1));
-    if (more) start(segments[which ^ 1]);
+    // the next item's copies fly while this one's results are written
+    more = next_item(items + (which ^ 1));
+    if (more) start(items + (which ^ 1));
 
-    // join the warps
 #pragma unroll
     for (int i = 0; i < 2 * NT; ++i) {
 #pragma unroll
@@ -674,125 +809,66 @@ attention_split_kernel(const AttentionArgs a, const KvCache c, unsigned* __restr
         l[i] += __shfl_xor_sync(0xffffffffu, l[i], sh);
         off[i] += __shfl_xor_sync(0xffffffffu, off[i], sh);
       }
-      if (g == 0) ml[warp * kRows + (i / 2) * 8 + 2 * j + (i & 1)] = make_float2(m[i], l[i]);
-    }
-    // a CTA is the first piece of one item that goes on, and a later piece of one, at most
-    const int slot = 2 * blockIdx.x + (static_cast<int>(blockIdx.x) == q.first ? 1 : 0);
-    float* part = partial + static_cast<int64_t>(slot) * kRows * (D + 2);
 #pragma unroll
-    for (int pass = 0; pass < kRows / L::kPass; ++pass) {
-      __syncthreads();  // ml is written; the last pass's readers are done
-#pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        if (n * 8 / L::kPass != pass) continue;
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          float* dst = join + (warp * L::kPass + n * 8 % L::kPass + 2 * j + e) * L::kPitch + g * L::kGroup;
-#pragma unroll
-          for (int u = 0; u < D / 16; ++u)
-            *reinterpret_cast<float2*>(dst + 2 * u) =
-                make_float2(fmaf(64.0f, o[n][u][e], off[2 * n + e]), fmaf(4.0f, o[n][u][2 + e], off[2 * n + e]));
-        }
-      }
-      __syncthreads();
-      // four elements a thread
-      for (int i = threadIdx.x; i < L::kPass * (D / 4); i += kWarps * 32) {
-        const int pr = i / (D / 4), d = i % (D / 4) * 4;
-        const int rr = pass * L::kPass + pr;
-        if (rr >= rows) break;
-        float top = -FLT_MAX;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) top = fmaxf(top, ml[w * kRows + rr].x);
-        float sum = 0.0f;
-        float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-          const float2 t = ml[w * kRows + rr];
-          const float k = ex2(t.x - top);
-          sum = fmaf(k, t.y, sum);
-          const float* src = join + (w * L::kPass + pr) * L::kPitch + d + 2 * (d / (D / 8));
-          const float2 u0 = *reinterpret_cast<const float2*>(src), u1 = *reinterpret_cast<const float2*>(src + 2);
-          v.x = fmaf(k, u0.x, v.x); v.y = fmaf(k, u0.y, v.y); v.z = fmaf(k, u1.x, v.z); v.w = fmaf(k, u1.y, v.w);
-        }
-        if (q.pieces == 1) {
-          const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-          *reinterpret_cast<uint2*>(a.out + row_out[rr] + d) = make_uint2(pack2(v.x * inv, v.y * inv), pack2(v.z * inv, v.w * inv));
-        } else {
-          *reinterpret_cast<float4*>(part + rr * D + d) = v;
-          if (d == 0) *reinterpret_cast<float2*>(part + kRows * D + 2 * rr) = make_float2(top, sum);
-        }
+      for (int u = 0; u < D / 16; ++u) {
+        o[i / 2][u][i & 1] = fmaf(64.0f, o[i / 2][u][i & 1], off[i]);
+        o[i / 2][u][2 + (i & 1)] = fmaf(4.0f, o[i / 2][u][2 + (i & 1)], off[i]);
       }
     }
-    if (q.pieces > 1) {
-      __threadfence();
-      __syncthreads();
-      if (threadIdx.x == 0) *last_flag = atomicAdd(counters + q.first, 1u) == static_cast<unsigned>(q.pieces - 1);
-      __syncthreads();
-      if (*last_flag) {
+    const int first = it->first;
+    int count = it->pieces;  // of this level
+    if (count > 1) {
+      store_partial<D, NT>(res, partial + static_cast<int64_t>(slot_of(first, piece - first)) * L::kSlot);
+      // level by level: the last to arrive in a group of kFan goes on for it
+      unsigned* counter = counters;
+      int k = piece - first, stride = 1;
+      for (;;) {
+        const int lead = k / kFan * kFan;  // of the group, in units of stride
+        const int members = min(kFan, count - lead);
         __threadfence();
-        if (threadIdx.x == 0) counters[q.first] = 0;
-        // a thread's elements lie in one row: its maximum first, then the sums
-        constexpr int kLanes = kWarps * 32 / kRows;  // threads of a row
-        const int rr = threadIdx.x / kLanes, lane_in_row = threadIdx.x % kLanes;
-        constexpr int64_t kSlot = kRows * (D + 2);
-        // piece 0 in slot 1 of its CTA, the others in slot 0 of theirs
-        auto piece = [&](int k) { return partial + (2 * static_cast<int64_t>(q.first + k) + (k == 0 ? 1 : 0)) * kSlot; };
-        if (rr < rows) {
-          float top = -FLT_MAX;
-          for (int k = lane_in_row; k < q.pieces; k += kLanes)
-            top = fmaxf(top, __ldcg(piece(k) + kRows * D + 2 * rr));
-          if constexpr (kLanes > 1) {
-            const unsigned peers = (kLanes < 32 ? (1u << (kLanes & 31)) - 1u : 0xffffffffu) << (lane / kLanes * kLanes);
-#pragma unroll
-            for (int x2 = kLanes / 2; x2 > 0; x2 >>= 1) top = fmaxf(top, __shfl_xor_sync(peers, top, x2));
-          }
-          constexpr int kVecs = D / 4 / kLanes;  // float4 of a thread
-          constexpr int kAtOnce = kVecs < 4 ? kVecs : 4;
-          for (int v0 = 0; v0 < kVecs; v0 += kAtOnce) {
-            float4 v[kAtOnce];
-            float sum = 0.0f;
-#pragma unroll
-            for (int i = 0; i < kAtOnce; ++i) v[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll(16 / kAtOnce)
-            for (int k = 0; k < q.pieces; ++k) {
-              const float* src = piece(k);
-              const float2 t = __ldcg(reinterpret_cast<const float2*>(src + kRows * D + 2 * rr));
-              const float w = ex2(t.x - top);
-              sum = fmaf(w, t.y, sum);
-#pragma unroll
-              for (int i = 0; i < kAtOnce; ++i) {
-                const float4 u = __ldcg(reinterpret_cast<const float4*>(src + rr * D) + (v0 + i) * kLanes + lane_in_row);
-                v[i].x = fmaf(w, u.x, v[i].x); v[i].y = fmaf(w, u.y, v[i].y);
-                v[i].z = fmaf(w, u.z, v[i].z); v[i].w = fmaf(w, u.w, v[i].w);
-              }
-            }
-            const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-#pragma unroll
-            for (int i = 0; i < kAtOnce; ++i)
-              *reinterpret_cast<uint2*>(a.out + row_out[rr] + ((v0 + i) * kLanes + lane_in_row) * 4) =
-                  make_uint2(pack2(v[i].x * inv, v[i].y * inv), pack2(v[i].z * inv, v[i].w * inv));
-          }
+        __syncwarp();
+        unsigned before = 0;
+        if (lane == 0) {
+          unsigned* at = counter + slot_of(first, lead * stride);
+          before = atomicAdd(at, 1u);
+          if (before == static_cast<unsigned>(members - 1)) *at = 0;
         }
+        before = __shfl_sync(0xffffffffu, before, 0);
+        if (before != static_cast<unsigned>(members - 1)) break;
+        __threadfence();
+        load_joined<D, NT>(res, partial, first, lead * stride, stride, members);
+        if (count <= kFan) {
+          count = 1;
+          break;
+        }
+        __syncwarp();  // every lane has read what is written over
+        store_partial<D, NT>(res, partial + static_cast<int64_t>(slot_of(first, lead * stride)) * L::kSlot);
+        k /= kFan;
+        count = (count + kFan - 1) / kFan;
+        stride *= kFan;
+        counter += 2 * gridDim.x * kWarps;
       }
     }
-    __syncthreads();  // the buffers are free for the next item
-    if (!more) break;
+    if (count == 1) store_out<D, NT>(res, a.out, row_out, rows);
+    __syncwarp();  // row_info and the item are free
   }
   // never leave with a copy in flight
   for (int s = 0; s < L::kStages; ++s)
     if ((armed >> s) & 1u) mbar_wait(bar0 + 8 * s, (phases >> s) & 1u, nullptr);
 }
 
-constexpr int kMaxCtas = 4;  // per SM, of any variant
+constexpr int kMaxCtas = 4;  // an SM holds, of any variant
+constexpr int kLevels = 4;   // of joining: more than 8^4 warps there are not
 
-size_t counter_bytes() { return (size_t(num_sms()) * kMaxCtas * 4 + 255) / 256 * 256; }
+// Arrivals, by level and slot.
+size_t counter_bytes() { return size_t(kLevels) * 2 * num_sms() * kMaxCtas * kWarps * 4 / 256 * 256 + 256; }
 
 template <int D, int NT>
 size_t partial_bytes() {
-  return size_t(num_sms()) * Split<D, NT>::kCtas * 2 * Split<D, NT>::kRows * (D + 2) * 4;
+  return size_t(2) * num_sms() * Split<D, NT>::kCtas * kWarps * Split<D, NT>::kSlot * 4;
 }
 
-// Counters, then two partial results a CTA of the variant that needs most.
+// Counters, then two partial results a piece of the variant that needs most.
 size_t workspace_bytes_of(int head_dim) {
   size_t n = 0;
   if (head_dim == 64) n = std::max(partial_bytes<64, 1>(), std::max(partial_bytes<64, 2>(), partial_bytes<64, 4>()));

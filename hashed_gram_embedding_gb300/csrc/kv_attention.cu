@@ -57,16 +57,20 @@ struct AttentionArgs {
 //   four masks and one shift by a byte.
 //   K: f16 subnormals multiply as they are; the query elements that meet the
 //     second kind are divided by 16, and 2^24 goes into the rows' factors.
-//   V: one fused multiply-add makes bf16 (c - 8) / 64 or (c - 8) / 4, so that
-//     sums over long caches hold no offset; 64 and 4 are taken out at the end.
+//   V: bf16 subnormals as they are, too: the weights carry a factor of 2^100
+//     that brings the products back among the normal numbers (2^-33 of the
+//     result, 2^-29 for the second kind). Weights that 2^100 might carry out
+//     of range - a value's scale above 2^18 - meet codes multiplied by 2^100
+//     instead, on a path of their own.
 // Query rows are scaled to [1, 2) by a power of two each, which keeps f16
 // exact for bf16 queries (elements below 2^-14 of the row's largest round at
 // 2^-24 of it). Scale and offset of a token meet the float32 sums instead of
 // its elements:
 //   <q, K_t> = s_t sum_d q_d c_td + m_t sum_d q_d
-//   sum_t p_t V_t = sum_t p'_t (c_t - 8) + sum_t p_t (m_t + 8 s_t),  p' = bf16(p s)
+//   sum_t p_t V_t = sum_t p'_t c_t - 8 sum_t p'_t + sum_t p_t (m_t + 8 s_t),  p' = bf16(p s)
 // p' is the only rounding to fewer bits, and it meets codes centred on 8, so
-// that an offset far from zero costs no precision.
+// that an offset far from zero costs no precision; sum p' is one more row of
+// the product, by constants.
 // The contraction index of a product may run in any order: a lane's 16 bytes
 // of a K row are 32 neighbouring elements, and the query's fragments follow
 // that order; two tokens' V bytes are interleaved with one permute a word.
@@ -74,16 +78,15 @@ struct AttentionArgs {
 // of neighbouring lanes fall on different banks.
 constexpr int kStepTokens = 2 * kBlockTokens;
 
-// NT tiles of 8 query rows. What an SM holds follows from the registers of a
-// warp's outputs, D NT / 4 a thread: 16 warps of 128 registers, 12 of 168, or
-// 8; the ring takes the shared memory that is left.
-constexpr int kWarps = 4;  // of a CTA
+// NT tiles of 8 query rows. One CTA an SM; its warps follow from the registers
+// of a warp's outputs, D NT / 4 a thread: 16 of 128 registers, 12 of 168, or 8;
+// the rings take the shared memory that is left.
 
 template <int D, int NT>
 struct Split {
   static constexpr int kRows = 8 * NT;
   static constexpr int kStage = 2 * KvBlock<D>::kBytes;
-  static constexpr int kCtas = D == 256 || NT == 4 ? 2 : NT == 2 ? 3 : 4;  // an SM holds
+  static constexpr int kWarps = D == 256 || NT == 4 ? 8 : NT == 2 ? 12 : 16;
   static constexpr int kStages = D == 256 ? (NT == 1 ? 3 : 2) : D == 64 ? 5 : 3 + NT / 4;
   static constexpr bool kQRegs = NT == 1;            // query fragments in registers
   static constexpr int kFrags = kQRegs ? 0 : NT * (D / 16) * 32 * 8;
@@ -126,13 +129,17 @@ __device__ __forceinline__ uint32_t k_pair(uint32_t word, int i) {
   return (i < 2 ? word : word >> 8) & (i % 2 == 0 ? 0x000F000Fu : 0x00F000F0u);
 }
 
-// Codes i of the two halves of a word (i = 0..3) as bf16 pair: (c - 8) / 64
-// for even i, (c - 8) / 4 for odd i.
-__device__ __forceinline__ uint32_t v_pair(uint32_t word, int i) {
+// A pair of bf16 subnormals times 2^100.
+__device__ __forceinline__ uint32_t times_2_100(uint32_t x) {
   uint32_t y;
-  asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(y) : "r"(k_pair(word, i)), "r"(0x7F007F00u) /* 2^127 */,
-      "r"(i % 2 == 0 ? 0xBE00BE00u /* -1/8 */ : 0xC000C000u /* -2 */));
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(y) : "r"(x), "r"(0x71807180u));
   return y;
+}
+
+__device__ __forceinline__ uint64_t f2_add(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
 }
 
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
@@ -323,12 +330,12 @@ __device__ __forceinline__ void store_out(const Results<D, NT>& x, ple_bf16_t* o
 }
 
 template <int D, int NT>
-__global__ void __launch_bounds__(kWarps * 32, (Split<D, NT>::kCtas))
+__global__ void __launch_bounds__(Split<D, NT>::kWarps * 32, 1)
 attention_split_kernel(const AttentionArgs a, const KvCache c, unsigned* __restrict__ counters,
                        float* __restrict__ partial) {
   using L = Split<D, NT>;
   using B = KvBlock<D>;
-  constexpr int kRows = L::kRows;
+  constexpr int kRows = L::kRows, kWarps = L::kWarps;
   constexpr int kWords = D / 32;   // K words of a lane and token
   constexpr int kVWords = D / 64;  // V words of a lane and token
   extern __shared__ __align__(128) uint8_t smem[];
@@ -604,8 +611,9 @@ attention_split_kernel(const AttentionArgs a, const KvCache c, unsigned* __restr
     Results<D, NT> res;
     auto& o = res.o;
     auto& m = res.m;
-    auto& l = res.l;
-    float off[2 * NT];  // sums of p (m + 8 s)
+    auto& l = res.l;  // once the steps are done
+    uint64_t l2[NT], off2[NT];  // for two rows: sums of p, and of p (m + 8 s)
+    float sum[NT][4];           // of p' (rows 0 and 1 twice)
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -613,7 +621,13 @@ attention_split_kernel(const AttentionArgs a, const KvCache c, unsigned* __restr
 #pragma unroll
         for (int i = 0; i < 4; ++i) o[n][u][i] = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 2 * NT; ++i) { m[i] = -FLT_MAX; l[i] = 0.0f; off[i] = 0.0f; }
+    for (int i = 0; i < 2 * NT; ++i) m[i] = -FLT_MAX;
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      l2[n] = off2[n] = f2(0.0f, 0.0f);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) sum[n][i] = 0.0f;
+    }
 
     const int p_end = (it->step + it->steps) * kStepTokens;
 #pragma unroll 1
@@ -673,9 +687,10 @@ attention_split_kernel(const AttentionArgs a, const KvCache c, unsigned* __restr
               }
             }
         }
-        // scores in units of log2: scale and offset, then the mask
+        // scores in units of log2: scale and offset, then the mask; two rows at a time
         float vs[2][2], vm[2][2];  // the values' scale, and offset + 8 scales
         uint32_t unseen = 0;       // bit (query tile, block, token, row)
+        bool large = false;        // a scale that 2^100 would carry out of range
 #pragma unroll
         for (int b = 0; b < 2; ++b)
 #pragma unroll
@@ -683,15 +698,16 @@ attention_split_kernel(const AttentionArgs a, const KvCache c, unsigned* __restr
             const int tok = r0 + 8 * e;
             const uint32_t kp = *reinterpret_cast<const uint32_t*>(st + b * B::kBytes + B::kPairs + tok * 4);
             const uint32_t vp = *reinterpret_cast<const uint32_t*>(st + b * B::kBytes + B::kVPairs + tok * 4);
-            const float ks = bf_lo(kp), km = bf_hi(kp);
+            const uint64_t ks = f2(bf_lo(kp), bf_lo(kp)), km = f2(bf_hi(kp), bf_hi(kp));
             vs[b][e] = bf_lo(vp);
             vm[b][e] = fmaf(8.0f, bf_lo(vp), bf_hi(vp));
+            large |= !(vs[b][e] <= 262144.0f);
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
-              const float2 f = *reinterpret_cast<const float2*>(row_info + n * 8 + 2 * j);
-              const float2 sq = *reinterpret_cast<const float2*>(row_info + kRows + n * 8 + 2 * j);
-              s[n][b][2 * e] = f.x * fmaf(ks, s[n][b][2 * e], km * sq.x);
-              s[n][b][2 * e + 1] = f.y * fmaf(ks, s[n][b][2 * e + 1], km * sq.y);
+              const uint64_t f = *reinterpret_cast<const uint64_t*>(row_info + n * 8 + 2 * j);
+              const uint64_t sq = *reinterpret_cast<const uint64_t*>(row_info + kRows + n * 8 + 2 * j);
+              const uint64_t z = f2_mul(f, f2_fma(ks, f2(s[n][b][2 * e], s[n][b][2 * e + 1]), f2_mul(km, sq)));
+              f2_split(z, s[n][b][2 * e], s[n][b][2 * e + 1]);
             }
             if (masked) {
               const int p = p0 + b * kBlockTokens + tok;
@@ -732,38 +748,54 @@ attention_split_kernel(const AttentionArgs a, const KvCache c, unsigned* __restr
             const float next = fmaxf(m[i], t);
             const float keep = ex2(m[i] - next);
             m[i] = next;
-            l[i] *= keep;
-            off[i] *= keep;
             const int n = i / 2, e = i & 1;
+            float la, lb;
+            f2_split(l2[n], la, lb);
+            l2[n] = e == 0 ? f2(la * keep, lb) : f2(la, lb * keep);
+            f2_split(off2[n], la, lb);
+            off2[n] = e == 0 ? f2(la * keep, lb) : f2(la, lb * keep);
+            sum[n][e] *= keep;
 #pragma unroll
             for (int u = 0; u < D / 16; ++u) { o[n][u][e] *= keep; o[n][u][2 + e] *= keep; }
           }
         }
-        uint32_t pt[NT][2][2];  // weights times the values' scale, bf16, as B fragments
+        large = __any_sync(0xffffffffu, large);
+        uint32_t pt[NT][2][2];  // weights times the values' scale (times 2^100), bf16, as B fragments
         auto weights = [&](auto with_mask) {
 #pragma unroll
-          for (int n = 0; n < NT; ++n)
+          for (int b = 0; b < 2; ++b)
 #pragma unroll
-            for (int b = 0; b < 2; ++b)
+            for (int e = 0; e < 2; ++e) {
+              const float by = large ? vs[b][e] : vs[b][e] * 0x1p100f;
+              const uint64_t by2 = f2(by, by), vm2 = f2(vm[b][e], vm[b][e]);
 #pragma unroll
-              for (int e = 0; e < 2; ++e) {
-                float w[2];
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                  const float p = ex2(s[n][b][2 * e + i] - m[2 * n + i]);
-                  l[2 * n + i] += p;
-                  w[i] = p * vs[b][e];
-                  const float next = fmaf(p, vm[b][e], off[2 * n + i]);
+              for (int n = 0; n < NT; ++n) {
+                float p[2], w[2];
+                f2_split(f2_add(f2(s[n][b][2 * e], s[n][b][2 * e + 1]), f2(-m[2 * n], -m[2 * n + 1])), p[0], p[1]);
+                p[0] = ex2(p[0]);
+                p[1] = ex2(p[1]);
+                const uint64_t p2 = f2(p[0], p[1]);
+                l2[n] = f2_add(l2[n], p2);
+                f2_split(f2_mul(p2, by2), w[0], w[1]);
+                uint64_t next = f2_fma(p2, vm2, off2[n]);
+                if constexpr (decltype(with_mask)::value) {
                   // a value that is not seen meets no weight, not even zero: it may be NaN
-                  const bool skip = decltype(with_mask)::value && ((unseen >> (n * 8 + b * 4 + e * 2 + i)) & 1u);
-                  off[2 * n + i] = skip ? off[2 * n + i] : next;
-                  w[i] = skip ? 0.0f : w[i];
+                  float was[2], now[2];
+                  f2_split(off2[n], was[0], was[1]);
+                  f2_split(next, now[0], now[1]);
+#pragma unroll
+                  for (int i = 0; i < 2; ++i)
+                    if ((unseen >> (n * 8 + b * 4 + e * 2 + i)) & 1u) { now[i] = was[i]; w[i] = 0.0f; }
+                  next = f2(now[0], now[1]);
                 }
+                off2[n] = next;
                 pt[n][b][e] = transpose8x8(pack2(w[0], w[1]));
               }
+            }
         };
         if (masked) weights(std::true_type{});
         else weights(std::false_type{});
+        auto values = [&](auto scaled) {  // scaled: 2^100 is in the codes, not in the weights
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
           const uint8_t* vb = st + b * B::kBytes + B::kV + g * (D / 16);
@@ -776,6 +808,10 @@ attention_split_kernel(const AttentionArgs a, const KvCache c, unsigned* __restr
             else if constexpr (kVWords == 2) *reinterpret_cast<uint2*>(v[i]) = *reinterpret_cast<const uint2*>(p);
             else v[i][0] = *reinterpret_cast<const uint32_t*>(p);
           }
+          constexpr uint32_t kOne = decltype(scaled)::value ? 0x3F803F80u : 0x0D800D80u;  // 1, or 2^-100
+#pragma unroll
+          for (int n = 0; n < NT; ++n) mma_bf16(sum[n], kOne, kOne, kOne, kOne, pt[n][b][0], pt[n][b][1]);
+          auto code = [](uint32_t x, int i) { return decltype(scaled)::value ? times_2_100(k_pair(x, i)) : k_pair(x, i); };
 #pragma unroll
           for (int w = 0; w < kVWords; ++w)
 #pragma unroll
@@ -784,14 +820,17 @@ attention_split_kernel(const AttentionArgs a, const KvCache c, unsigned* __restr
               const uint32_t x0 = __byte_perm(v[0][w], v[1][w], sel), x1 = __byte_perm(v[2][w], v[3][w], sel);
 #pragma unroll
               for (int k = 0; k < 2; ++k) {
-                const uint32_t a0 = v_pair(x0, 2 * k), a1 = v_pair(x0, 2 * k + 1);
-                const uint32_t a2 = v_pair(x1, 2 * k), a3 = v_pair(x1, 2 * k + 1);
+                const uint32_t a0 = code(x0, 2 * k), a1 = code(x0, 2 * k + 1);
+                const uint32_t a2 = code(x1, 2 * k), a3 = code(x1, 2 * k + 1);
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
                   mma_bf16(o[n][w * 4 + half * 2 + k], a0, a1, a2, a3, pt[n][b][0], pt[n][b][1]);
               }
             }
         }
+        };
+        if (large) values(std::true_type{});
+        else values(std::false_type{});
       }
       __syncwarp();  // every lane has read the stage
       if (++stage_out == L::kStages) stage_out = 0;
@@ -803,16 +842,23 @@ attention_split_kernel(const AttentionArgs a, const KvCache c, unsigned* __restr
     if (more) start(items + (which ^ 1));
 
 #pragma unroll
-    for (int i = 0; i < 2 * NT; ++i) {
+    for (int n = 0; n < NT; ++n) {
+      float off[2];
+      f2_split(l2[n], l[2 * n], l[2 * n + 1]);
+      f2_split(off2[n], off[0], off[1]);
 #pragma unroll
-      for (int sh = 4; sh < 32; sh <<= 1) {
-        l[i] += __shfl_xor_sync(0xffffffffu, l[i], sh);
-        off[i] += __shfl_xor_sync(0xffffffffu, off[i], sh);
-      }
+      for (int e = 0; e < 2; ++e) {
 #pragma unroll
-      for (int u = 0; u < D / 16; ++u) {
-        o[i / 2][u][i & 1] = fmaf(64.0f, o[i / 2][u][i & 1], off[i]);
-        o[i / 2][u][2 + (i & 1)] = fmaf(4.0f, o[i / 2][u][2 + (i & 1)], off[i]);
+        for (int sh = 4; sh < 32; sh <<= 1) {
+          l[2 * n + e] += __shfl_xor_sync(0xffffffffu, l[2 * n + e], sh);
+          off[e] += __shfl_xor_sync(0xffffffffu, off[e], sh);
+        }
+        off[e] = fmaf(-8.0f, sum[n][e], off[e]);
+#pragma unroll
+        for (int u = 0; u < D / 16; ++u) {
+          o[n][u][e] = fmaf(0x1p33f, o[n][u][e], off[e]);
+          o[n][u][2 + e] = fmaf(0x1p29f, o[n][u][2 + e], off[e]);
+        }
       }
     }
     const int first = it->first;
@@ -857,15 +903,15 @@ attention_split_kernel(const AttentionArgs a, const KvCache c, unsigned* __restr
     if ((armed >> s) & 1u) mbar_wait(bar0 + 8 * s, (phases >> s) & 1u, nullptr);
 }
 
-constexpr int kMaxCtas = 4;  // an SM holds, of any variant
+constexpr int kMaxWarps = 16;  // of an SM, of any variant
 constexpr int kLevels = 4;   // of joining: more than 8^4 warps there are not
 
 // Arrivals, by level and slot.
-size_t counter_bytes() { return size_t(kLevels) * 2 * num_sms() * kMaxCtas * kWarps * 4 / 256 * 256 + 256; }
+size_t counter_bytes() { return size_t(kLevels) * 2 * num_sms() * kMaxWarps * 4 / 256 * 256 + 256; }
 
 template <int D, int NT>
 size_t partial_bytes() {
-  return size_t(2) * num_sms() * Split<D, NT>::kCtas * kWarps * Split<D, NT>::kSlot * 4;
+  return size_t(2) * num_sms() * Split<D, NT>::kWarps * Split<D, NT>::kSlot * 4;
 }
 
 // Counters, then two partial results a piece of the variant that needs most.
@@ -884,7 +930,7 @@ cudaError_t launch_split(const AttentionArgs& a, const KvCache& c, unsigned* cou
   const auto kernel = attention_split_kernel<D, NT>;
   const cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kSmem);
   if (err != cudaSuccess) return err;
-  return launch_kernel(kernel, dim3(num_sms() * L::kCtas), dim3(kWarps * 32), L::kSmem, stream, 1, a, c,
+  return launch_kernel(kernel, dim3(num_sms()), dim3(L::kWarps * 32), L::kSmem, stream, 1, a, c,
                        counters, partial);
 }
 

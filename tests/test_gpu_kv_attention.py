@@ -231,3 +231,14 @@ def test_cache_past_32_bit_offsets(tokens):
                           out, ws)
     check(out, *oracle.attention(bits(q), small.cache, small.table, small.qsl, small.lens, 128 ** -0.5))
     assert math.isclose(where[-1], big - 1)
+
+
+@pytest.mark.parametrize("factor", [1e-20, 1e4, 3e6, 1e12])
+def test_values_of_any_size(factor):
+    """Values far below and above one; a scale above 2^18 takes a path of its own."""
+    for queries, lens in (([1, 3], [150, 40]), ([100], [150])):
+        b = Batch(queries, lens, 8, 2, 128, 16, seed=61)
+        for r, n in enumerate(lens):
+            for p in range(0, n, 2):  # every other position, so that both kinds meet in a step
+                b.put(r, p, b.rng.normal(0, 1, (2, 128)), b.rng.normal(0, factor, (2, 128)))
+        run(b)

@@ -10,6 +10,7 @@ import ctypes
 import os
 
 import numpy as np
+import torch
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libple.so")
 
@@ -372,40 +373,50 @@ def ple_gated_conv(kv, gate, query_start_loc, w, dilation, out, conv_state=None,
 
 
 # ---- the 4-bit step of the attention block: paged cache, attention, projection ----
+#
+# These calls are made several times a layer for steps of a few microseconds,
+# so their checks read each attribute once and pointers go to ctypes as plain
+# integers.
+
+def _raw_stream(stream, t):
+    if stream is not None:
+        return stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(t.device.index)
+
 
 def _heads(name, t, head_dim=None):
-    """Row stride, heads and head dim of [T, heads, head_dim] bf16 rows: the
-    heads of a row lie together, the rows any distance apart."""
-    import torch
-    if t.dim() != 3 or t.dtype != torch.bfloat16 or not t.is_cuda:
+    """Row stride and shape of [T, heads, head_dim] bf16 rows: the heads of a
+    row lie together, the rows any distance apart."""
+    if t.dtype is not torch.bfloat16 or not t.is_cuda or t.dim() != 3:
         raise ValueError(f"{name}: a CUDA bf16 tensor [T, heads, head_dim] is needed")
     T, H, D = t.shape
     stride, per_head, one = t.stride()
-    if (D > 1 and one != 1) or (H > 1 and per_head != D) or (head_dim is not None and D != head_dim):
+    if (one != 1 and D > 1) or (per_head != D and H > 1) or (head_dim is not None and D != head_dim):
         raise ValueError(f"{name}: heads of {head_dim or D} elements must lie together in a row")
-    return (stride if T > 1 else H * D), H, D
+    return (stride if T > 1 else H * D), T, H, D
 
 
 def _whole(name, t, dtype, dims):
-    if t.dtype != dtype or t.dim() != dims or not t.is_contiguous() or not t.is_cuda:
+    if t.dtype is not dtype or not t.is_contiguous() or not t.is_cuda or t.dim() != dims:
         raise ValueError(f"{name}: a contiguous CUDA {dtype} tensor of {dims} dimensions is needed")
+    return t.data_ptr()
 
 
 def _cache_args(cache, block_table, query_start_loc, kv_lens, head_dim):
-    """(num_pages, page_size, kv heads) and the pointers shared by the cache's calls."""
-    import torch
-    _whole("cache", cache, torch.uint8, 4)
-    _whole("block_table", block_table, torch.int32, 2)
-    _whole("query_start_loc", query_start_loc, torch.int32, 1)
-    _whole("kv_lens", kv_lens, torch.int32, 1)
+    """Kv heads, and the arguments shared by the cache's calls."""
+    at = _whole("cache", cache, torch.uint8, 4)
+    table = _whole("block_table", block_table, torch.int32, 2)
+    qsl = _whole("query_start_loc", query_start_loc, torch.int32, 1)
+    lens = _whole("kv_lens", kv_lens, torch.int32, 1)
     pages, hk, sub, nbytes = cache.shape
-    R = query_start_loc.numel() - 1
+    R = kv_lens.shape[0]
+    rows, max_pages = block_table.shape
     if nbytes != 16 * (head_dim + 8):
         raise ValueError(f"cache: blocks of {nbytes} bytes, not {16 * (head_dim + 8)} (head_dim {head_dim})")
-    if kv_lens.numel() != R or block_table.shape[0] != R:
-        raise ValueError(f"block_table and kv_lens must have a row for each of the {R} requests")
-    return hk, (_ptr(cache), pages, sub * 16, _ptr(block_table), block_table.shape[1],
-                _ptr(query_start_loc), R, _ptr(kv_lens))
+    if rows != R or query_start_loc.shape[0] != R + 1:
+        raise ValueError(f"block_table must have a row, and query_start_loc an entry and one more, for "
+                         f"each of the {R} requests of kv_lens")
+    return hk, (at, pages, sub * 16, table, max_pages, qsl, R, lens)
 
 
 def ple_kv_block_bytes(head_dim):
@@ -422,51 +433,52 @@ def ple_kv_append(q, k, v, cos_sin, cache, block_table, query_start_loc, kv_lens
     cache uint8 [pages, Hk, page_size / 16, 16 * (D + 8)]; block_table int32
     [R, max_pages], query_start_loc int32 [R + 1], kv_lens int32 [R] (these
     tokens included); q_out like q, or q itself; positions int32 [T] or None."""
-    import torch
-    k_stride, Hk, D = _heads("k", k)
-    v_stride, Hv, _ = _heads("v", v, D)
+    k_stride, T, Hk, D = _heads("k", k)
+    v_stride, Tv, Hv, _ = _heads("v", v, D)
     hk, c = _cache_args(cache, block_table, query_start_loc, kv_lens, D)
-    T = k.shape[0]
-    H = q_stride = o_stride = 0
+    H, q_at, q_stride, o_at, o_stride, Tq = 0, None, 0, None, 0, T
     if q is not None:
-        q_stride, H, _ = _heads("q", q, D)
-        o_stride = _heads("q_out", q_out, D)[0]
-        if q_out.shape != q.shape:
+        q_stride, Tq, H, _ = _heads("q", q, D)
+        o_stride, To, Ho, _ = _heads("q_out", q_out, D)
+        if To != Tq or Ho != H:
             raise ValueError("q_out must have q's shape")
-    if Hk != hk or Hv != hk or v.shape[0] != T or (q is not None and q.shape[0] != T):
+        q_at, o_at = q.data_ptr(), q_out.data_ptr()
+    if Hk != hk or Hv != hk or Tv != T or Tq != T:
         raise ValueError("q, k, v and the cache differ in tokens or kv heads")
+    cs, entries, rot = None, 0, 0
     if cos_sin is not None:
-        _whole("cos_sin", cos_sin, torch.float32, 2)
+        cs = _whole("cos_sin", cos_sin, torch.float32, 2)
+        entries, rot = cos_sin.shape
+    at = None
     if positions is not None:
-        _whole("positions", positions, torch.int32, 1)
-        if positions.numel() != T:
+        at = _whole("positions", positions, torch.int32, 1)
+        if positions.shape[0] != T:
             raise ValueError("positions must have one entry for each token")
-    return _check("ple_kv_append", lib().ple_kv_append(
-        _ptr(q), q_stride, _ptr(k), k_stride, _ptr(v), v_stride, T, H, hk, D, _ptr(cos_sin),
-        0 if cos_sin is None else cos_sin.shape[0], 0 if cos_sin is None else cos_sin.shape[1],
-        int(interleaved), _ptr(positions), *c, _ptr(q_out), o_stride, _ptr(dev_err),
-        _stream(stream)))
+    status = lib().ple_kv_append(
+        q_at, q_stride, k.data_ptr(), k_stride, v.data_ptr(), v_stride, T, H, hk, D, cs, entries, rot,
+        1 if interleaved else 0, at, *c, o_at, o_stride, None if dev_err is None else dev_err.data_ptr(),
+        _raw_stream(stream, k))
+    return status if status == PLE_OK else _check("ple_kv_append", status)
 
 
 def ple_kv_read(cache, block_table, query_start_loc, kv_lens, k_out, v_out, dev_err=None,
                 stream=None):
     """Values of the tokens in query_start_loc's spans out of the 4-bit cache:
     k_out, v_out bf16 [T, Hk, D], contiguous (either may be None)."""
-    import torch
     some = k_out if k_out is not None else v_out
     if some is None:
         raise ValueError("k_out or v_out is needed")
-    for name, t in (("k_out", k_out), ("v_out", v_out)):
-        if t is not None:
-            _whole(name, t, torch.bfloat16, 3)
-            if t.shape != some.shape:
-                raise ValueError("k_out and v_out differ in shape")
+    k_at = None if k_out is None else _whole("k_out", k_out, torch.bfloat16, 3)
+    v_at = None if v_out is None else _whole("v_out", v_out, torch.bfloat16, 3)
+    if k_at is not None and v_at is not None and k_out.shape != v_out.shape:
+        raise ValueError("k_out and v_out differ in shape")
     T, Hk, D = some.shape
     hk, c = _cache_args(cache, block_table, query_start_loc, kv_lens, D)
     if Hk != hk:
         raise ValueError(f"{Hk} kv heads, and {hk} in the cache")
-    return _check("ple_kv_read", lib().ple_kv_read(
-        *c, T, hk, D, _ptr(k_out), _ptr(v_out), _ptr(dev_err), _stream(stream)))
+    status = lib().ple_kv_read(*c, T, hk, D, k_at, v_at, None if dev_err is None else dev_err.data_ptr(),
+                               _raw_stream(stream, some))
+    return status if status == PLE_OK else _check("ple_kv_read", status)
 
 
 def ple_kv_attention_workspace(num_heads, num_kv_heads, head_dim):
@@ -481,40 +493,47 @@ def ple_kv_attention(q, cache, block_table, query_start_loc, kv_lens, out, works
     ple_kv_attention_workspace(H, Hk, D) bytes, zero-filled before its first
     use. scale: 1 / sqrt(D) by default; max_query_len: the most query tokens
     of a request, if known. Other arguments as in ple_kv_append."""
-    q_stride, H, D = _heads("q", q)
-    o_stride = _heads("out", out, D)[0]
-    if out.shape != q.shape:
+    q_stride, T, H, D = _heads("q", q)
+    o_stride, To, Ho, _ = _heads("out", out, D)
+    if To != T or Ho != H:
         raise ValueError("out must have q's shape")
     hk, c = _cache_args(cache, block_table, query_start_loc, kv_lens, D)
-    return _check("ple_kv_attention", lib().ple_kv_attention(
-        _ptr(q), q_stride, q.shape[0], H, hk, D, *c, int(max_query_len),
-        float(scale) if scale is not None else D ** -0.5, int(causal), int(window), _ptr(out),
-        o_stride, _ptr(workspace), workspace.numel() * workspace.element_size(), _ptr(dev_err),
-        _stream(stream)))
+    room = _whole("workspace", workspace, torch.uint8, 1)
+    status = lib().ple_kv_attention(
+        q.data_ptr(), q_stride, T, H, hk, D, *c, max_query_len, D ** -0.5 if scale is None else scale,
+        1 if causal else 0, window, out.data_ptr(), o_stride, room, workspace.shape[0],
+        None if dev_err is None else dev_err.data_ptr(), _raw_stream(stream, q))
+    return status if status == PLE_OK else _check("ple_kv_attention", status)
 
 
 def ple_proj_w4(x, codes, scales, out, zeros=None, dev_err=None, stream=None):
     """out [T, N] bf16 = x [T, E] bf16 times the transpose of a 4-bit weight:
     codes uint8 [N, E / 2], scales bf16 [N, E / group], zeros uint8 like
     scales, or None for 8 everywhere."""
-    import torch
-    _whole("codes", codes, torch.uint8, 2)
-    _whole("scales", scales, torch.bfloat16, 2)
-    _whole("out", out, torch.bfloat16, 2)
+    code_at = _whole("codes", codes, torch.uint8, 2)
+    scale_at = _whole("scales", scales, torch.bfloat16, 2)
+    out_at = _whole("out", out, torch.bfloat16, 2)
+    if x.dtype is not torch.bfloat16 or not x.is_cuda or x.dim() != 2:
+        raise ValueError("x: a CUDA bf16 tensor [T, E] is needed")
     T, E = x.shape
     N, groups = scales.shape
-    if x.dtype != torch.bfloat16 or not x.is_cuda or (E > 1 and x.stride(1) != 1):
-        raise ValueError("x: a CUDA bf16 tensor [T, E] with its columns together is needed")
-    if codes.shape != (N, E // 2) or out.shape != (T, N) or groups < 1 or E % groups != 0:
+    stride, one = x.stride()
+    if one != 1 and E > 1:
+        raise ValueError("x: the columns of a row must lie together")
+    Nc, half = codes.shape
+    To, No = out.shape
+    if Nc != N or half * 2 != E or To != T or No != N or groups < 1 or E % groups != 0:
         raise ValueError(f"x {tuple(x.shape)}, codes {tuple(codes.shape)}, scales "
                          f"{tuple(scales.shape)} and out {tuple(out.shape)} do not fit")
+    zero_at = None
     if zeros is not None:
-        _whole("zeros", zeros, torch.uint8, 2)
+        zero_at = _whole("zeros", zeros, torch.uint8, 2)
         if zeros.shape != scales.shape:
             raise ValueError("zeros must have the shape of scales")
-    return _check("ple_proj_w4", lib().ple_proj_w4(
-        _ptr(x), x.stride(0) if T > 1 else E, T, E, N, _ptr(codes), _ptr(scales), _ptr(zeros),
-        E // groups, _ptr(out), _ptr(dev_err), _stream(stream)))
+    status = lib().ple_proj_w4(
+        x.data_ptr(), stride if T > 1 else E, T, E, N, code_at, scale_at, zero_at, E // groups, out_at,
+        None if dev_err is None else dev_err.data_ptr(), _raw_stream(stream, x))
+    return status if status == PLE_OK else _check("ple_proj_w4", status)
 
 
 def ple_version():

@@ -1,5 +1,5 @@
 // ple_kv_attention: grouped-query attention over the paged 4-bit cache.
-#include "kv_cache.cuh"
+#include "kv_attention.cuh"
 
 #include <cuda_fp16.h>
 
@@ -10,19 +10,6 @@
 
 namespace ple {
 namespace {
-
-struct AttentionArgs {
-  const ple_bf16_t* q;
-  int64_t q_stride;
-  int64_t T;
-  int num_heads;
-  float scale_log2;  // scale * log2(e)
-  bool causal;
-  int window;
-  ple_bf16_t* out;
-  int64_t out_stride;
-  int32_t* dev_err;
-};
 
 // ---------------------------------------------------------------------------
 // Few query rows: the cache split over the card
@@ -117,18 +104,6 @@ __device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
-// Codes i and i + 4 of a word (i = 0..3) as f16 pair: c 2^-24 for even i,
-// c 2^-20 for odd i.
-__device__ __forceinline__ uint32_t k_pair(uint32_t word, int i) {
-  return (i < 2 ? word : word >> 8) & (i % 2 == 0 ? 0x000F000Fu : 0x00F000F0u);
-}
-
 // A pair of bf16 subnormals times 2^100.
 __device__ __forceinline__ uint32_t times_2_100(uint32_t x) {
   uint32_t y;
@@ -183,7 +158,8 @@ __device__ __forceinline__ Span span_of(const AttentionArgs& a, const KvCache& c
   s.block0 = lo / kBlockTokens;
   s.step0 = s.block0 / 2;
   s.steps = hi > lo ? (hi - 1) / kStepTokens + 1 - s.step0 : 0;
-  s.tiles = (s.n * (a.num_heads / c.num_kv_heads) + tile_rows - 1) / tile_rows;
+  const int rows = s.n * (a.num_heads / c.num_kv_heads);
+  s.tiles = rows < a.many_rows ? (rows + tile_rows - 1) / tile_rows : 0;
   return s;
 }
 
@@ -676,8 +652,8 @@ attention_split_kernel(const AttentionArgs a, const KvCache c, unsigned* __restr
           for (int w = 0; w < kWords; ++w)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-              const uint32_t a0 = k_pair(lo[w], 2 * h), a1 = k_pair(hi[w], 2 * h);
-              const uint32_t a2 = k_pair(lo[w], 2 * h + 1), a3 = k_pair(hi[w], 2 * h + 1);
+              const uint32_t a0 = code_bits(lo[w], 2 * h), a1 = code_bits(hi[w], 2 * h);
+              const uint32_t a2 = code_bits(lo[w], 2 * h + 1), a3 = code_bits(hi[w], 2 * h + 1);
 #pragma unroll
               for (int n = 0; n < NT; ++n) {
                 uint2 f;
@@ -811,7 +787,7 @@ attention_split_kernel(const AttentionArgs a, const KvCache c, unsigned* __restr
           constexpr uint32_t kOne = decltype(scaled)::value ? 0x3F803F80u : 0x0D800D80u;  // 1, or 2^-100
 #pragma unroll
           for (int n = 0; n < NT; ++n) mma_bf16(sum[n], kOne, kOne, kOne, kOne, pt[n][b][0], pt[n][b][1]);
-          auto code = [](uint32_t x, int i) { return decltype(scaled)::value ? times_2_100(k_pair(x, i)) : k_pair(x, i); };
+          auto code = [](uint32_t x, int i) { return decltype(scaled)::value ? times_2_100(code_bits(x, i)) : code_bits(x, i); };
 #pragma unroll
           for (int w = 0; w < kVWords; ++w)
 #pragma unroll
@@ -903,6 +879,10 @@ attention_split_kernel(const AttentionArgs a, const KvCache c, unsigned* __restr
     if ((armed >> s) & 1u) mbar_wait(bar0 + 8 * s, (phases >> s) & 1u, nullptr);
 }
 
+// From this many rows on a request's cache is read for 256 rows at a time, by
+// the 5th-generation tensor cores.
+constexpr int kManyRows = 96;
+
 constexpr int kMaxWarps = 16;  // of an SM, of any variant
 constexpr int kLevels = 4;   // of joining: more than 8^4 warps there are not
 
@@ -978,16 +958,19 @@ PLE_EXPORT ple_status ple_kv_attention(const ple_bf16_t* q, int64_t q_stride, in
   const size_t need = ple_kv_attention_workspace(num_heads, num_kv_heads, head_dim);
   if (workspace == nullptr || workspace_bytes < need || (reinterpret_cast<uintptr_t>(workspace) & 255) != 0)
     return fail(PLE_ERR_INVALID_ARG, "%s: workspace of %zu bytes, 256-byte aligned, needed", name, need);
-  const AttentionArgs a{q, q_stride, num_tokens, num_heads, scale * 1.4426950408889634f, causal != 0,
-                        window, out, out_stride, dev_err};
-  const KvCache c{const_cast<uint8_t*>(static_cast<const uint8_t*>(cache)), num_pages, page_size,
-                  num_kv_heads, block_table, max_pages, query_start_loc, num_reqs, kv_lens};
   // the rows of a request and kv head, at most
   const int64_t tokens = max_query_len > 0 && max_query_len < num_tokens ? max_query_len : num_tokens;
   const int64_t rows = tokens * (num_heads / num_kv_heads);
+  const int many = head_dim <= 128 ? kManyRows : INT32_MAX;
+  const AttentionArgs a{q, q_stride, num_tokens, num_heads, scale * 1.4426950408889634f, causal != 0,
+                        window, out, out_stride, dev_err, many};
+  const KvCache c{const_cast<uint8_t*>(static_cast<const uint8_t*>(cache)), num_pages, page_size,
+                  num_kv_heads, block_table, max_pages, query_start_loc, num_reqs, kv_lens};
   unsigned* counters = static_cast<unsigned*>(workspace);
   float* partial = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + counter_bytes());
-  cudaError_t err;
+  cudaError_t err = cudaSuccess;
+  if (rows >= many) err = launch_prefill(a, c, head_dim, stream);
+  if (err != cudaSuccess) return check_cuda(err, name);
   if (head_dim == 64)
     err = rows <= 8 ? launch_split<64, 1>(a, c, counters, partial, stream)
         : rows <= 16 ? launch_split<64, 2>(a, c, counters, partial, stream)

@@ -1,0 +1,38 @@
+// What the two kernels of ple_kv_attention share: one for requests of few
+// query rows (kv_attention.cu), one for requests of many (kv_prefill.cu).
+#pragma once
+
+#include "kv_cache.cuh"
+
+namespace ple {
+
+struct AttentionArgs {
+  const ple_bf16_t* q;
+  int64_t q_stride;
+  int64_t T;
+  int num_heads;
+  float scale_log2;  // scale * log2(e)
+  bool causal;
+  int window;
+  ple_bf16_t* out;
+  int64_t out_stride;
+  int32_t* dev_err;
+  int many_rows;     // requests with this many query rows a kv head or more go to the second kernel
+};
+
+// Attention of the requests with many rows, for head_dim 64 and 128.
+cudaError_t launch_prefill(const AttentionArgs& a, const KvCache& c, int head_dim, cudaStream_t stream);
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Codes i and i + 4 of a word (i = 0..3) where they stand: read as f16 pair,
+// c 2^-24 for even i and c 2^-20 for odd i; read as bf16, c 2^-133 and c 2^-129.
+__device__ __forceinline__ uint32_t code_bits(uint32_t word, int i) {
+  return (i < 2 ? word : word >> 8) & (i % 2 == 0 ? 0x000F000Fu : 0x00F000F0u);
+}
+
+}  // namespace ple

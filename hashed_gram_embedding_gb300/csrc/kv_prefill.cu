@@ -1,0 +1,710 @@
+// ple_kv_attention for requests of many query rows (prefill chunks): 256 rows
+// against 128 positions at a time on the 5th-generation tensor cores.
+//
+// Work. A CTA takes 256 query rows of one request and kv head (rows are
+// (token, head of the group), so a group's heads share every key) as two
+// tiles of 128, and walks the positions they see in tiles of 128. Rows of
+// long requests come first, so that the last CTAs are short ones.
+//
+// Mathematics. For each tile of positions, S = Q K^T (f16 operands, f32 in
+// tensor memory), P = exp2(f S - m) rounded to bf16 over S in tensor memory,
+// O += P V (bf16 operands, f32 in tensor memory). The running maximum m of a
+// row is raised only when a score passes it by 2^8, and only then is O scaled:
+// weights of up to 256 cost no precision.
+// Roundings: a key enters as f16(code * scale + offset), because a score of
+// hundreds must not move by a bf16's 2^-8 of it; rows of Q are scaled to
+// [1, 2) by a power of two (in the row's f), and a key row outside
+// [2^-6, 512) by one of its own, which is multiplied back on a path of its
+// own. Values and weights enter as bf16, and their errors only ever average.
+//
+// Roles (13 warps): warps 0-3 and 4-7 each own a tile of rows, a row a
+// thread: they read S, write P, scale O and write the result. Warps 8-11 turn
+// the cache's codes into operand tiles (K: positions x D; V transposed:
+// D x positions, both K-major with 128-byte swizzle), two buffers each, the
+// next tile's codes held in registers meanwhile. One thread of warp 12 issues
+// the products: while one tile of rows is exponentiated the other's are
+// multiplied. The order of a group of 8 elements in Q and K is (0, 4, 1, 5, 2,
+// 6, 3, 7), as two masks of a word of codes give them.
+//
+// A code masked out where it stands is a subnormal number: one product makes
+// c / 512 (f16) or c / 64 (bf16) of it, one multiply-add code * scale + offset.
+//
+// What is masked never meets what it must not: a position outside the cache
+// enters as zeros, and a value that is not finite is left out of V and makes
+// NaN of the rows that see it, instead of all rows of its tile.
+#include "kv_attention.cuh"
+
+#include <cuda_fp16.h>
+
+#include <cfloat>
+#include <cmath>
+
+namespace ple {
+namespace {
+
+constexpr int kTile = 128;        // rows of a tile, and positions
+constexpr int kGroupThreads = 128;
+constexpr int kThreads = 13 * 32;
+constexpr int kMaskRing = 4;      // tiles whose masks are kept
+
+template <int D>
+struct Prefill {
+  static constexpr int kQ = kTile * D * 2;       // bytes of an operand tile
+  static constexpr int kAtK = 2 * kQ;
+  static constexpr int kAtV = kAtK + 2 * kQ;
+  static constexpr int kAtPairs = kAtV + 2 * kQ;             // [2][128] (scale, offset) of V
+  static constexpr int kAtMasks = kAtPairs + 2 * kTile * 4;  // [ring][3][4] present; V not finite; K has a factor
+  static constexpr int kAtFactors = kAtMasks + kMaskRing * 12 * 4;  // [ring][128] of K rows
+  static constexpr int kAtBars = kAtFactors + kMaskRing * kTile * 4;
+  static constexpr int kAtWords = kAtBars + 16 * 8;
+  static constexpr int kSmem = kAtWords + 64 + 1024;         // and alignment
+};
+
+// Instruction descriptor, kind::f16: f32 sums, f16 (0) or bf16 (1) operands,
+// both K-major, M = 128.
+constexpr uint32_t idesc(int n, uint32_t type) {
+  return (1u << 4) | (type << 7) | (type << 10) | (uint32_t(n >> 3) << 17) | (uint32_t(kTile >> 4) << 24);
+}
+
+// Descriptor of a K-major operand with 128-byte swizzle: rows of 128 bytes,
+// groups of 8 rows 1024 bytes apart.
+__device__ __forceinline__ uint64_t operand(uint32_t saddr) {
+  return static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4) | (uint64_t(1) << 16) | (uint64_t(1024 >> 4) << 32) |
+         (uint64_t(1) << 46) | (uint64_t(2) << 61);
+}
+
+__device__ __forceinline__ void mma_smem(uint32_t d, uint64_t a, uint64_t b, uint32_t desc, bool add) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(desc),
+      "r"(static_cast<uint32_t>(add))
+      : "memory");
+}
+
+// The A operand in tensor memory: two elements a column.
+__device__ __forceinline__ void mma_tmem(uint32_t d, uint32_t a, uint64_t b, uint32_t desc, bool add) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d), "r"(a), "l"(b), "r"(desc),
+      "r"(static_cast<uint32_t>(add))
+      : "memory");
+}
+
+__device__ __forceinline__ void mma_commit(uint32_t bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+
+__device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void fence_operands() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+// 32 columns of this thread's row.
+__device__ __forceinline__ void tmem_load(uint32_t at, float (&r)[32]) {
+  uint32_t* u = reinterpret_cast<uint32_t*>(r);
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]), "=r"(u[7]),
+        "=r"(u[8]), "=r"(u[9]), "=r"(u[10]), "=r"(u[11]), "=r"(u[12]), "=r"(u[13]), "=r"(u[14]), "=r"(u[15]),
+        "=r"(u[16]), "=r"(u[17]), "=r"(u[18]), "=r"(u[19]), "=r"(u[20]), "=r"(u[21]), "=r"(u[22]), "=r"(u[23]),
+        "=r"(u[24]), "=r"(u[25]), "=r"(u[26]), "=r"(u[27]), "=r"(u[28]), "=r"(u[29]), "=r"(u[30]), "=r"(u[31])
+      : "r"(at)
+      : "memory");
+}
+
+__device__ __forceinline__ void tmem_store32(uint32_t at, const float (&r)[32]) {
+  const uint32_t* u = reinterpret_cast<const uint32_t*>(r);
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31};" ::"r"(u[0]), "r"(u[1]),
+      "r"(u[2]), "r"(u[3]), "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7]), "r"(u[8]), "r"(u[9]), "r"(u[10]), "r"(u[11]),
+      "r"(u[12]), "r"(u[13]), "r"(u[14]), "r"(u[15]), "r"(u[16]), "r"(u[17]), "r"(u[18]), "r"(u[19]), "r"(u[20]),
+      "r"(u[21]), "r"(u[22]), "r"(u[23]), "r"(u[24]), "r"(u[25]), "r"(u[26]), "r"(u[27]), "r"(u[28]), "r"(u[29]),
+      "r"(u[30]), "r"(u[31]), "r"(at)
+      : "memory");
+}
+
+__device__ __forceinline__ void tmem_store16(uint32_t at, const uint32_t (&u)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15};" ::"r"(u[0]), "r"(u[1]), "r"(u[2]),
+      "r"(u[3]), "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7]), "r"(u[8]), "r"(u[9]), "r"(u[10]), "r"(u[11]), "r"(u[12]),
+      "r"(u[13]), "r"(u[14]), "r"(u[15]), "r"(at)
+      : "memory");
+}
+
+__device__ __forceinline__ void tmem_stored() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// Byte of 16-byte chunk `chunk` of row `row` in an operand tile of `rows` rows.
+__device__ __forceinline__ uint32_t chunk_at(int rows, int row, int chunk) {
+  return static_cast<uint32_t>((chunk >> 3) * rows * 128 + row * 128 + (((chunk & 7) ^ (row & 7)) << 4));
+}
+
+__device__ __forceinline__ uint32_t bf2_mul(uint32_t a, uint32_t b) {
+  uint32_t y;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(y) : "r"(a), "r"(b));
+  return y;
+}
+__device__ __forceinline__ uint32_t bf2_mad(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t y;
+  asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(y) : "r"(a), "r"(b), "r"(c));
+  return y;
+}
+
+__device__ __forceinline__ uint32_t f16_mul(uint32_t a, uint32_t b) {
+  uint32_t y;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(y) : "r"(a), "r"(b));
+  return y;
+}
+__device__ __forceinline__ uint32_t f16_mad(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t y;
+  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(y) : "r"(a), "r"(b), "r"(c));
+  return y;
+}
+__device__ __forceinline__ uint32_t f16_pair(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// Codes i and i + 4 of a word as f16 pair c / 512.
+__device__ __forceinline__ uint32_t code_512ths(uint32_t word, int i) {
+  return f16_mul(code_bits(word, i), i % 2 == 0 ? 0x78007800u /* 2^15 */ : 0x68006800u /* 2^11 */);
+}
+
+// Codes i and i + 4 of a word as bf16 pair c / 64.
+__device__ __forceinline__ uint32_t code_64ths(uint32_t word, int i) {
+  return bf2_mul(code_bits(word, i), i % 2 == 0 ? 0x7F007F00u : 0x7D007D00u);
+}
+
+// A CTA's share of the work.
+struct Job {
+  int r, tile, h;     // request, 256-row tile, kv head
+  int t0, n, len;     // of the request
+  int rows;           // in the tile
+  int first, tiles;   // first position tile, and how many
+  int block0, block_end;
+  bool clipped;
+};
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+attention_prefill_kernel(const AttentionArgs a, const KvCache c) {
+  using L = Prefill<D>;
+  using B = KvBlock<D>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* const smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t base = smem_u32(smem);
+  const uint32_t bar0 = base + L::kAtBars;
+  const uint32_t q_full = bar0, o_full = bar0 + 8;
+  auto k_full = [&](int b) { return bar0 + 16 + 8u * b; };
+  auto k_free = [&](int b) { return bar0 + 32 + 8u * b; };
+  auto v_full = [&](int b) { return bar0 + 48 + 8u * b; };
+  auto v_free = [&](int b) { return bar0 + 64 + 8u * b; };
+  auto s_full = [&](int t) { return bar0 + 80 + 8u * t; };
+  auto p_full = [&](int t) { return bar0 + 96 + 8u * t; };
+  const uint32_t pairs_full = bar0 + 112;
+  uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kAtWords);
+  volatile int* const abort_flag = reinterpret_cast<volatile int*>(smem + L::kAtWords + 4);
+  Job* const job = reinterpret_cast<Job*>(smem + L::kAtWords + 8);
+  static_assert(sizeof(Job) <= 56, "room in shared memory");
+  const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
+  const int G = a.num_heads / c.num_kv_heads, hk = c.num_kv_heads;
+
+  if (threadIdx.x == 0) {
+    mbar_init(q_full, 2 * kGroupThreads);
+    mbar_init(o_full, 1);
+    mbar_init(pairs_full, kGroupThreads);
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(k_full(b), kGroupThreads);
+      mbar_init(k_free(b), 1);
+      mbar_init(v_full(b), kGroupThreads);
+      mbar_init(v_free(b), 1);
+      mbar_init(s_full(b), 1);
+      mbar_init(p_full(b), kGroupThreads);
+    }
+    mbar_fence_init();
+    *abort_flag = 0;
+  }
+  pdl_wait();
+  pdl_trigger();
+  if (warp == 0) {  // this CTA's share: tiles of a request from the last one on, its heads side by side
+    int left = blockIdx.x, r0 = 0;
+    Job x;
+    x.r = -1;
+    while (r0 < c.num_reqs) {
+      const int r = r0 + lane;
+      int64_t t0 = 0, end = 0;
+      if (r < c.num_reqs) request_span(c.qsl, c.num_reqs + 1, a.T, r, &t0, &end);
+      const int rows = static_cast<int>(end - t0) * G;
+      const int tiles = rows >= a.many_rows ? (rows + 2 * kTile - 1) / (2 * kTile) : 0;
+      int sum = tiles * hk;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int up = __shfl_up_sync(0xffffffffu, sum, o);
+        if (lane >= o) sum += up;
+      }
+      const unsigned past = __ballot_sync(0xffffffffu, sum > left);
+      if (past != 0) {
+        if (lane == __ffs(past) - 1) {
+          const int at = left - (sum - tiles * hk);
+          x.r = r;
+          x.tile = tiles - 1 - at / hk;
+          x.h = at % hk;
+          x.t0 = static_cast<int>(t0);
+          x.n = static_cast<int>(end - t0);
+          x.len = max(__ldg(c.kv_lens + r), 0);
+          x.rows = min(2 * kTile, rows - x.tile * 2 * kTile);
+          // the positions that its rows see
+          const int tok0 = x.tile * 2 * kTile / G, tok1 = (x.tile * 2 * kTile + x.rows - 1) / G;
+          const int64_t room = static_cast<int64_t>(c.max_pages) * c.page_size;
+          int64_t hi = a.causal ? int64_t(x.len) - x.n + tok1 + 1 : x.len;
+          x.clipped = hi > room;
+          hi = min(hi, room);
+          int64_t lo = a.window > 0 ? int64_t(x.len) - x.n + tok0 - a.window + 1 : 0;
+          lo = max(lo, int64_t(0));
+          x.first = static_cast<int>(lo / kTile);
+          x.tiles = hi > lo ? static_cast<int>((hi + kTile - 1) / kTile) - x.first : 0;
+          x.block0 = static_cast<int>(lo / kBlockTokens);
+          x.block_end = hi > 0 ? static_cast<int>((hi + kBlockTokens - 1) / kBlockTokens) : 0;
+          *job = x;
+        }
+        break;
+      }
+      left -= __shfl_sync(0xffffffffu, sum, 31);
+      r0 += 32;
+    }
+    if (r0 >= c.num_reqs && lane == 0) job->r = -1;
+    __syncwarp();
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(tmem_slot)) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  fence_before();
+  __syncthreads();
+  fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const Job x = *job;
+  const bool two = x.rows > kTile;  // both tiles have rows
+  const int n = x.r >= 0 ? x.tiles : 0;
+  auto gave_up = [&](bool ok) {
+    if (!ok) {
+      *abort_flag = 1;
+      set_dev_err(a.dev_err, PLE_DEVERR_TIMEOUT);
+    }
+    return !ok;
+  };
+  uint32_t* const masks = reinterpret_cast<uint32_t*>(smem + L::kAtMasks);
+
+  if (x.r >= 0 && warp < 8) {
+    // ---------------- a row a thread ----------------
+    const int t = warp / 4;                       // tile of rows
+    const int row = threadIdx.x % kGroupThreads;
+    const int in_tile = t * kTile + row;
+    const int flat = x.tile * 2 * kTile + in_tile;
+    const bool live = in_tile < x.rows;
+    const int token = flat / G;
+    const int64_t head = static_cast<int64_t>(x.h * G + (flat - token * G)) * D;
+    float factor = a.scale_log2;                  // takes a row's scores to log2 units
+    if (t == 0 || two) {
+      const ple_bf16_t* src = a.q + static_cast<int64_t>(x.t0 + token) * a.q_stride + head;
+      uint8_t* dst = smem + t * L::kQ;
+      float top = 0.0f;
+#pragma unroll 4
+      for (int i = 0; i < D / 8; ++i) {
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if (live) v = *reinterpret_cast<const uint4*>(src + 8 * i);
+        float e[8];
+        unpack8(v, e);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) top = fmaxf(top, fabsf(e[k]));
+      }
+      // 2^k <= top < 2^(k + 1)
+      const int k = top > 0.0f && top < INFINITY ? max(ilogbf(top), -126) : 0;
+      const float down = ldexpf(1.0f, -k);
+      factor = ldexpf(a.scale_log2, k);
+#pragma unroll 4
+      for (int i = 0; i < D / 8; ++i) {
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if (live) v = *reinterpret_cast<const uint4*>(src + 8 * i);
+        float e[8];
+        unpack8(v, e);
+#pragma unroll
+        for (int h = 0; h < 8; ++h) e[h] *= down;
+        *reinterpret_cast<uint4*>(dst + chunk_at(kTile, row, i)) =
+            make_uint4(f16_pair(e[0], e[4]), f16_pair(e[1], e[5]), f16_pair(e[2], e[6]), f16_pair(e[3], e[7]));
+      }
+    }
+    fence_operands();
+    mbar_arrive(q_full);
+    const int last = !live ? -1 : a.causal ? x.len - x.n + token : x.len - 1;
+    const int from = a.window > 0 && last - a.window + 1 > 0 ? last - a.window + 1 : 0;
+    // what every live row of the warp sees
+    const int all_to = __reduce_min_sync(0xffffffffu, live ? last : INT32_MAX);
+    const int all_from = __reduce_max_sync(0xffffffffu, live ? from : 0);
+    const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t s_at = tmem + lanes + t * kTile;
+    const uint32_t o_at = tmem + lanes + 2 * kTile + t * D;
+    float m = -FLT_MAX, l = 0.0f;
+    bool ok = true;
+    if (t == 0 || two) {
+#pragma unroll 1
+      for (int j = 0; j < n; ++j) {
+        ok = mbar_wait(s_full(t), j & 1, abort_flag);
+        if (gave_up(__all_sync(0xffffffffu, ok))) { ok = false; break; }
+        fence_after();
+        const int p0 = (x.first + j) * kTile;
+        const uint32_t* mask = masks + (j % kMaskRing) * 12;
+        const float* factors = reinterpret_cast<const float*>(smem + L::kAtFactors) + (j % kMaskRing) * kTile;
+        // bits of the columns that the row may see
+        const uint4 present = *reinterpret_cast<const uint4*>(mask);
+        const uint4 broken = *reinterpret_cast<const uint4*>(mask + 4);
+        const uint4 scaled4 = *reinterpret_cast<const uint4*>(mask + 8);
+        const bool scaled = (scaled4.x | scaled4.y | scaled4.z | scaled4.w) != 0;
+        const bool masked = p0 < all_from || p0 + kTile - 1 > all_to ||
+                            (present.x & present.y & present.z & present.w) != 0xffffffffu ||
+                            (broken.x | broken.y | broken.z | broken.w) != 0;
+        uint32_t see[4] = {present.x, present.y, present.z, present.w};
+        if (masked) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const int hi = last - p0 - 32 * q, lo = from - p0 - 32 * q;  // bits lo..hi
+            uint32_t bits = hi < 0 ? 0u : hi >= 31 ? 0xffffffffu : (2u << hi) - 1u;
+            if (lo > 0) bits &= lo >= 32 ? 0u : 0xffffffffu << lo;
+            see[q] &= bits;
+          }
+          const uint32_t bad = (see[0] & broken.x) | (see[1] & broken.y) | (see[2] & broken.z) | (see[3] & broken.w);
+          if (bad != 0) l = NAN;
+        }
+        float s[32];
+        float top = -FLT_MAX;
+#pragma unroll 1
+        for (int q = 0; q < 4; ++q) {
+          tmem_load(s_at + 32 * q, s);
+          if (scaled) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) s[i] *= factors[32 * q + i];
+          }
+          if (masked) {
+            const uint32_t bits = q == 0 ? see[0] : q == 1 ? see[1] : q == 2 ? see[2] : see[3];
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (!((bits >> i) & 1u)) s[i] = -INFINITY;
+          }
+          float tops[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+          for (int i = 4; i < 32; ++i) tops[i & 3] = fmaxf(tops[i & 3], s[i]);
+          top = fmaxf(top, fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])));
+        }
+        top *= factor;
+        if (__any_sync(0xffffffffu, top > m + 8.0f)) {
+          const float next = fmaxf(m, top);
+          const float keep = ex2(m - next);
+          m = next;
+          l *= keep;
+          if (j > 0) {
+            // S(j) done means that the products of tile j - 1, issued before it, are done
+#pragma unroll 1
+            for (int q = 0; q < D / 32; ++q) {
+              tmem_load(o_at + 32 * q, s);
+#pragma unroll
+              for (int i = 0; i < 32; ++i) s[i] *= keep;
+              tmem_store32(o_at + 32 * q, s);
+            }
+          }
+        }
+        float sums[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 1
+        for (int q = 0; q < 4; ++q) {
+          tmem_load(s_at + 32 * q, s);
+          if (scaled) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) s[i] *= factors[32 * q + i];
+          }
+          if (masked) {
+            const uint32_t bits = q == 0 ? see[0] : q == 1 ? see[1] : q == 2 ? see[2] : see[3];
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (!((bits >> i) & 1u)) s[i] = -INFINITY;
+          }
+          uint32_t p[16];
+#pragma unroll
+          for (int i = 0; i < 32; i += 2) {
+            const float p0v = ex2(fmaf(s[i], factor, -m)), p1v = ex2(fmaf(s[i + 1], factor, -m));
+            sums[(i >> 1) & 3] += p0v + p1v;
+            p[i >> 1] = pack2(p0v, p1v);
+          }
+          tmem_store16(s_at + 16 * q, p);  // over columns already read
+        }
+        l += (sums[0] + sums[1]) + (sums[2] + sums[3]);
+        tmem_stored();
+        fence_before();
+        mbar_arrive(p_full(t));
+      }
+      if (n > 0 && ok) {
+        ok = mbar_wait(o_full, 0, abort_flag);
+        ok = !gave_up(__all_sync(0xffffffffu, ok));
+        fence_after();
+      }
+      const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+      ple_bf16_t* dst = a.out + static_cast<int64_t>(x.t0 + token) * a.out_stride + head;
+#pragma unroll 1
+      for (int q = 0; q < D / 32; ++q) {
+        float o[32];
+        if (n > 0 && ok) tmem_load(o_at + 32 * q, o);
+        else {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) o[i] = 0.0f;
+        }
+        if (live) {
+#pragma unroll
+          for (int i = 0; i < 32; i += 8)
+            *reinterpret_cast<uint4*>(dst + 32 * q + i) =
+                make_uint4(pack2(o[i] * inv, o[i + 1] * inv), pack2(o[i + 2] * inv, o[i + 3] * inv),
+                           pack2(o[i + 4] * inv, o[i + 5] * inv), pack2(o[i + 6] * inv, o[i + 7] * inv));
+        }
+      }
+    }
+  } else if (x.r >= 0 && warp < 12) {
+    // ---------------- codes to operands ----------------
+    const int id = threadIdx.x - 8 * 32;  // a position of the tile, for K
+    const int dw = warp - 8;
+    constexpr int kWords = D / 8;         // words of a row
+    constexpr int kUnits = D / 64;        // (8 positions, word) pieces of V a thread takes
+    const int word = (lane >> 3) + 4 * (dw % (kWords / 4));
+    const int eights0 = (lane & 7) + 8 * (dw / (kWords / 4));  // of its first piece
+    const int per_page = c.page_size / kBlockTokens;
+    const int32_t* table = c.block_table + static_cast<int64_t>(x.r) * c.max_pages;
+    if (x.clipped && id == 0) set_dev_err(a.dev_err, PLE_DEVERR_BOUNDS);
+    auto block_at = [&](int b) {
+      if (b < x.block0 || b >= x.block_end) return -1;
+      const int col = b / per_page;
+      const int64_t page = __ldg(table + col);
+      if (page < 0 || page >= c.num_pages) {
+        set_dev_err(a.dev_err, PLE_DEVERR_BOUNDS);
+        return -1;
+      }
+      return static_cast<int>((page * hk + x.h) * per_page + (b - col * per_page));
+    };
+    // the next tile: blocks, then codes
+    int kb, vb[kUnits];
+    bool here;  // the fetched tile's position is in the cache
+    uint4 kw[kWords / 4];
+    uint32_t kp, vp, vw[kUnits][8];
+    auto find = [&](int j) {
+      const int b = (x.first + j) * (kTile / kBlockTokens);
+      kb = j < n ? block_at(b + id / kBlockTokens) : -1;
+#pragma unroll
+      for (int u = 0; u < kUnits; ++u) vb[u] = j < n ? block_at(b + (eights0 + 8 * u) / 2) : -1;
+    };
+    auto fetch = [&](int j) {
+      kp = vp = 0;
+#pragma unroll
+      for (int i = 0; i < kWords / 4; ++i) kw[i] = make_uint4(0, 0, 0, 0);
+      here = kb >= 0 && (x.first + j) * kTile + id < x.len;
+      if (here) {
+        const uint8_t* p = c.base + static_cast<int64_t>(kb) * B::kBytes;
+        const int slot = id % kBlockTokens;
+#pragma unroll
+        for (int i = 0; i < kWords / 4; ++i) kw[i] = __ldg(reinterpret_cast<const uint4*>(p + slot * B::kRow) + i);
+        kp = __ldg(reinterpret_cast<const uint32_t*>(p + B::kPairs + slot * 4));
+        vp = __ldg(reinterpret_cast<const uint32_t*>(p + B::kVPairs + slot * 4));
+      }
+#pragma unroll
+      for (int u = 0; u < kUnits; ++u) {
+        const uint8_t* p = c.base + static_cast<int64_t>(vb[u]) * B::kBytes + B::kV +
+                           ((eights0 + 8 * u) & 1) * 8 * B::kRow + word * 4;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) vw[u][i] = vb[u] >= 0 ? __ldg(reinterpret_cast<const uint32_t*>(p + i * B::kRow)) : 0u;
+      }
+    };
+    uint32_t* const pairs = reinterpret_cast<uint32_t*>(smem + L::kAtPairs);
+    if (n > 0) {
+      find(0);
+      fetch(0);
+      find(1);
+    }
+    bool ok = true;
+#pragma unroll 1
+    for (int j = 0; j < n; ++j) {
+      const int b = j & 1;
+      const uint32_t parity = ((j >> 1) & 1) ^ 1u;
+      ok = mbar_wait(k_free(b), parity, abort_flag);
+      if (gave_up(__all_sync(0xffffffffu, ok))) break;
+      // K, and the masks and value pairs of the tile
+      const bool finite = (vp & 0x7F80u) != 0x7F80u && (vp & 0x7F800000u) != 0x7F800000u;
+      const uint32_t present = __ballot_sync(0xffffffffu, here);
+      const uint32_t broken = __ballot_sync(0xffffffffu, !finite);
+      // the key row's largest magnitude decides whether it needs a factor
+      float ks = bf_lo(kp), km = bf_hi(kp);
+      const float most = fmaxf(fabsf(km), fabsf(fmaf(15.0f, ks, km)));
+      const bool odd = most > 0.0f && most < INFINITY && !(most >= 0.015625f && most < 512.0f);
+      const uint32_t scaled = __ballot_sync(0xffffffffu, odd);
+      if (scaled != 0) {
+        const int k = odd ? max(ilogbf(most), -126) : 0;
+        reinterpret_cast<float*>(smem + L::kAtFactors)[(j % kMaskRing) * kTile + id] = ldexpf(1.0f, k);
+        ks *= ldexpf(1.0f, -k);
+        km *= ldexpf(1.0f, -k);
+      } else {
+        reinterpret_cast<float*>(smem + L::kAtFactors)[(j % kMaskRing) * kTile + id] = 1.0f;
+      }
+      if (lane == 0) {
+        uint32_t* mask = masks + (j % kMaskRing) * 12 + dw;
+        mask[0] = present;
+        mask[4] = broken;
+        mask[8] = scaled;
+      }
+      pairs[b * kTile + id] = finite ? vp : 0u;
+      {
+        const uint32_t s512 = f16_pair(512.0f * ks, 512.0f * ks), off = f16_pair(km, km);
+        uint8_t* dst = smem + L::kAtK + b * L::kQ;
+#pragma unroll
+        for (int i = 0; i < kWords / 4; ++i) {
+          const uint32_t w[4] = {kw[i].x, kw[i].y, kw[i].z, kw[i].w};
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            uint4 v;
+            v.x = f16_mad(code_512ths(w[k], 0), s512, off);
+            v.y = f16_mad(code_512ths(w[k], 1), s512, off);
+            v.z = f16_mad(code_512ths(w[k], 2), s512, off);
+            v.w = f16_mad(code_512ths(w[k], 3), s512, off);
+            *reinterpret_cast<uint4*>(dst + chunk_at(kTile, id, 4 * i + k)) = v;
+          }
+        }
+      }
+      fence_operands();
+      mbar_arrive(k_full(b));
+      mbar_arrive(pairs_full);  // all four warps' value pairs
+      ok = mbar_wait(pairs_full, j & 1, abort_flag) && mbar_wait(v_free(b), parity, abort_flag);
+      if (gave_up(__all_sync(0xffffffffu, ok))) break;
+      {
+        uint8_t* dst = smem + L::kAtV + b * L::kQ;
+#pragma unroll
+        for (int u = 0; u < kUnits; ++u) {
+          const int eights = eights0 + 8 * u;
+          const uint4 p0 = *reinterpret_cast<const uint4*>(pairs + b * kTile + eights * 8);
+          const uint4 p1 = *reinterpret_cast<const uint4*>(pairs + b * kTile + eights * 8 + 4);
+          const uint32_t sm[8] = {p0.x, p0.y, p0.z, p0.w, p1.x, p1.y, p1.z, p1.w};
+          uint32_t s64[4], off[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            s64[i] = bf2_mul(__byte_perm(sm[2 * i], sm[2 * i + 1], 0x5410), 0x42804280u);
+            off[i] = __byte_perm(sm[2 * i], sm[2 * i + 1], 0x7632);
+          }
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            uint32_t y[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) y[i] = __byte_perm(vw[u][2 * i], vw[u][2 * i + 1], half == 0 ? 0x5410 : 0x7632);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              uint4 v;
+              v.x = bf2_mad(code_64ths(y[0], k), s64[0], off[0]);
+              v.y = bf2_mad(code_64ths(y[1], k), s64[1], off[1]);
+              v.z = bf2_mad(code_64ths(y[2], k), s64[2], off[2]);
+              v.w = bf2_mad(code_64ths(y[3], k), s64[3], off[3]);
+              *reinterpret_cast<uint4*>(dst + chunk_at(D, word * 8 + half * 4 + k, eights)) = v;
+            }
+          }
+        }
+      }
+      fence_operands();
+      mbar_arrive(v_full(b));
+      // the next tile's codes fly while this one is multiplied
+      fetch(j + 1);
+      find(j + 2);
+    }
+  } else if (warp == 12 && lane == 0 && n > 0) {
+    // ---------------- products ----------------
+    auto scores = [&](int t, int b) {  // S = Q K^T of one tile of rows
+#pragma unroll
+      for (int k = 0; k < D / 16; ++k) {
+        const uint32_t at = (k / 4) * kTile * 128 + (k % 4) * 32;
+        mma_smem(tmem + t * kTile, operand(base + t * L::kQ + at), operand(base + L::kAtK + b * L::kQ + at), idesc(kTile, 0), k > 0);
+      }
+    };
+    auto outputs = [&](int t, int b, bool add) {  // O += P V
+#pragma unroll
+      for (int k = 0; k < kTile / 16; ++k) {
+        const uint32_t at = (k / 4) * D * 128 + (k % 4) * 32;
+        mma_tmem(tmem + 2 * kTile + t * D, tmem + t * kTile + 8 * k, operand(base + L::kAtV + b * L::kQ + at), idesc(D, 1), add || k > 0);
+      }
+    };
+    bool ok = mbar_wait(q_full, 0, abort_flag) && mbar_wait(k_full(0), 0, abort_flag);
+    if (ok) {
+      fence_after();
+      scores(0, 0);
+      mma_commit(s_full(0));
+      if (two) {
+        scores(1, 0);
+        mma_commit(s_full(1));
+      }
+      mma_commit(k_free(0));
+    }
+#pragma unroll 1
+    for (int j = 0; ok && j < n; ++j) {
+      const int b = j & 1, nb = b ^ 1;
+      ok = mbar_wait(v_full(b), (j >> 1) & 1, abort_flag) && mbar_wait(p_full(0), j & 1, abort_flag);
+      if (!ok) break;
+      fence_after();
+      outputs(0, b, j > 0);
+      const bool more = j + 1 < n;
+      if (more) {
+        ok = mbar_wait(k_full(nb), ((j + 1) >> 1) & 1, abort_flag);
+        if (!ok) break;
+        fence_after();
+        scores(0, nb);
+        mma_commit(s_full(0));
+      }
+      if (two) {
+        ok = mbar_wait(p_full(1), j & 1, abort_flag);
+        if (!ok) break;
+        fence_after();
+        outputs(1, b, j > 0);
+      }
+      mma_commit(v_free(b));
+      if (more) {
+        if (two) {
+          scores(1, nb);
+          mma_commit(s_full(1));
+        }
+        mma_commit(k_free(nb));
+      }
+    }
+    gave_up(ok);
+    // every product issued has completed once this flips
+    mma_commit(o_full);
+    mbar_wait(o_full, 0, nullptr);
+  }
+  __syncwarp();
+  fence_before();
+  __syncthreads();
+  if (warp == 0) {
+    fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+  }
+}
+
+template <int D>
+cudaError_t launch(const AttentionArgs& a, const KvCache& c, cudaStream_t stream) {
+  const auto kernel = attention_prefill_kernel<D>;
+  const cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Prefill<D>::kSmem);
+  if (err != cudaSuccess) return err;
+  // no more tiles than this: every request's last one may be short
+  const int64_t rows = a.T * (a.num_heads / c.num_kv_heads);
+  const int64_t requests = rows / a.many_rows < c.num_reqs ? rows / a.many_rows : c.num_reqs;
+  const int64_t tiles = rows / (2 * kTile) + requests;
+  return launch_kernel(kernel, dim3(static_cast<unsigned>(tiles * c.num_kv_heads)), dim3(kThreads), Prefill<D>::kSmem,
+                       stream, 1, a, c);
+}
+
+}  // namespace
+
+cudaError_t launch_prefill(const AttentionArgs& a, const KvCache& c, int head_dim, cudaStream_t stream) {
+  return head_dim == 64 ? launch<64>(a, c, stream) : launch<128>(a, c, stream);
+}
+
+}  // namespace ple

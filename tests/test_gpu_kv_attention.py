@@ -242,3 +242,17 @@ def test_values_of_any_size(factor):
             for p in range(0, n, 2):  # every other position, so that both kinds meet in a step
                 b.put(r, p, b.rng.normal(0, 1, (2, 128)), b.rng.normal(0, factor, (2, 128)))
         run(b)
+
+
+@pytest.mark.parametrize("factor,q_scale", [(1e-4, 1e3), (1e3, 1e-2), (1e12, 1e-12), (1e-20, 1e18)])
+def test_keys_of_any_size(factor, q_scale):
+    """Keys far below and above one, among ordinary ones, and queries to match."""
+    for queries, lens in (([1, 3], [150, 40]), ([100], [150])):
+        b = Batch(queries, lens, 8, 2, 128, 16, seed=67, k_mean=0.0)
+        for r, n in enumerate(lens):
+            for p in range(n):
+                if p % 2 == 0 or q_scale < 1:  # ordinary keys meet small queries as nothing, large ones not at all
+                    b.put(r, p, b.rng.normal(0, factor, (2, 128)), b.rng.normal(0, 1, (2, 128)))
+                else:
+                    b.put(r, p, np.zeros((2, 128)), b.rng.normal(0, 1, (2, 128)))
+        run(b, q_scale=q_scale)

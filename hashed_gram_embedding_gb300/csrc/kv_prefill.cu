@@ -17,12 +17,12 @@
 // [2^-6, 512) by one of its own, which is multiplied back on a path of its
 // own. Values and weights enter as bf16, and their errors only ever average.
 //
-// Roles (13 warps): warps 0-3 and 4-7 each own a tile of rows, a row a
+// Roles (20 warps): warps 0-3 and 4-7 each own a tile of rows, a row a
 // thread: they read S, write P, scale O and write the result. Warps 8-11 turn
-// the cache's codes into operand tiles (K: positions x D; V transposed:
-// D x positions, both K-major with 128-byte swizzle), two buffers each, the
-// next tile's codes held in registers meanwhile. One thread of warp 12 issues
-// the products: while one tile of rows is exponentiated the other's are
+// the cache's codes into K operands (positions x D), warps 12-15 into V
+// operands (transposed: D x positions), both K-major with 128-byte swizzle,
+// two buffers each, the next tile's codes on their way meanwhile. Warp 16
+// issues the products: while one tile of rows is exponentiated the other's are
 // multiplied. The order of a group of 8 elements in Q and K is (0, 4, 1, 5, 2,
 // 6, 3, 7), as two masks of a word of codes give them.
 //
@@ -44,7 +44,10 @@ namespace {
 
 constexpr int kTile = 128;        // rows of a tile, and positions
 constexpr int kGroupThreads = 128;
-constexpr int kThreads = 13 * 32;
+constexpr int kThreads = 20 * 32;
+// Registers a thread is launched with, and each role's share of the CTA's.
+constexpr int kRegisters = 96, kRowRegisters = 152, kCodeRegisters = 72, kProductRegisters = 32;
+static_assert(2 * kRowRegisters + 2 * kCodeRegisters + kProductRegisters <= 5 * kRegisters, "more would never be had");
 constexpr int kMaskRing = 4;      // tiles whose masks are kept
 
 template <int D>
@@ -52,8 +55,7 @@ struct Prefill {
   static constexpr int kQ = kTile * D * 2;       // bytes of an operand tile
   static constexpr int kAtK = 2 * kQ;
   static constexpr int kAtV = kAtK + 2 * kQ;
-  static constexpr int kAtPairs = kAtV + 2 * kQ;             // [2][128] (scale, offset) of V
-  static constexpr int kAtMasks = kAtPairs + 2 * kTile * 4;  // [ring][3][4] present; V not finite; K has a factor
+  static constexpr int kAtMasks = kAtV + 2 * kQ;             // [ring][3][4] present; V not finite; K has a factor
   static constexpr int kAtFactors = kAtMasks + kMaskRing * 12 * 4;  // [ring][128] of K rows
   static constexpr int kAtBars = kAtFactors + kMaskRing * kTile * 4;
   static constexpr int kAtWords = kAtBars + 16 * 8;
@@ -67,29 +69,44 @@ constexpr uint32_t idesc(int n, uint32_t type) {
 }
 
 // Descriptor of a K-major operand with 128-byte swizzle: rows of 128 bytes,
-// groups of 8 rows 1024 bytes apart.
-__device__ __forceinline__ uint64_t operand(uint32_t saddr) {
-  return static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4) | (uint64_t(1) << 16) | (uint64_t(1024 >> 4) << 32) |
-         (uint64_t(1) << 46) | (uint64_t(2) << 61);
-}
+// groups of 8 rows 1024 bytes apart. The low word holds the address and is
+// all that changes.
+constexpr uint32_t kOperandHigh = (1024u >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t operand(uint32_t saddr) { return ((saddr & 0x3FFFFu) >> 4) | (1u << 16); }
 
-__device__ __forceinline__ void mma_smem(uint32_t d, uint64_t a, uint64_t b, uint32_t desc, bool add) {
+template <bool kAdd>
+__device__ __forceinline__ void mma_smem(uint32_t d, uint32_t a, uint32_t b, uint32_t desc) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
+      "{\n\t.reg .pred p;\n\t.reg .b64 x, y;\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(desc),
-      "r"(static_cast<uint32_t>(add))
+      "mov.b64 x, {%1, %5};\n\t"
+      "mov.b64 y, {%2, %5};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n\t}" ::"r"(d), "r"(a), "r"(b), "r"(desc),
+      "n"(kAdd ? 1 : 0), "n"(kOperandHigh)
       : "memory");
 }
 
 // The A operand in tensor memory: two elements a column.
-__device__ __forceinline__ void mma_tmem(uint32_t d, uint32_t a, uint64_t b, uint32_t desc, bool add) {
+__device__ __forceinline__ void mma_tmem(uint32_t d, uint32_t a, uint32_t b, uint32_t desc, bool add) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 y;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "mov.b64 y, {%2, %5};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %3, p;\n\t}" ::"r"(d), "r"(a), "r"(b), "r"(desc),
+      "r"(static_cast<uint32_t>(add)), "n"(kOperandHigh)
+      : "memory");
+}
+
+// One lane of a converged warp: the products are issued by it, in code that
+// the whole warp runs (their operands are uniform registers).
+__device__ __forceinline__ bool elected() {
+  uint32_t r;
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d), "r"(a), "l"(b), "r"(desc),
-      "r"(static_cast<uint32_t>(add))
-      : "memory");
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r));
+  return r != 0;
 }
 
 __device__ __forceinline__ void mma_commit(uint32_t bar) {
@@ -116,29 +133,43 @@ __device__ __forceinline__ void tmem_load(uint32_t at, float (&r)[32]) {
       : "memory");
 }
 
-__device__ __forceinline__ void tmem_store32(uint32_t at, const float (&r)[32]) {
-  const uint32_t* u = reinterpret_cast<const uint32_t*>(r);
+// 64 columns of it.
+__device__ __forceinline__ void tmem_load64(uint32_t at, float (&r)[64]) {
+  uint32_t* u = reinterpret_cast<uint32_t*>(r);
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], "
-      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31};" ::"r"(u[0]), "r"(u[1]),
-      "r"(u[2]), "r"(u[3]), "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7]), "r"(u[8]), "r"(u[9]), "r"(u[10]), "r"(u[11]),
-      "r"(u[12]), "r"(u[13]), "r"(u[14]), "r"(u[15]), "r"(u[16]), "r"(u[17]), "r"(u[18]), "r"(u[19]), "r"(u[20]),
-      "r"(u[21]), "r"(u[22]), "r"(u[23]), "r"(u[24]), "r"(u[25]), "r"(u[26]), "r"(u[27]), "r"(u[28]), "r"(u[29]),
-      "r"(u[30]), "r"(u[31]), "r"(at)
+      "tcgen05.ld.sync.aligned.32x32b.x64.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32, %33, %34, %35, %36, %37, %38, %39, %40, %41, %42, %43, %44, %45, %46, %47, %48, %49, %50, %51, %52, %53, %54, %55, %56, %57, %58, %59, %60, %61, %62, %63}, [%64];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]), "=r"(u[7]),
+        "=r"(u[8]), "=r"(u[9]), "=r"(u[10]), "=r"(u[11]), "=r"(u[12]), "=r"(u[13]), "=r"(u[14]), "=r"(u[15]),
+        "=r"(u[16]), "=r"(u[17]), "=r"(u[18]), "=r"(u[19]), "=r"(u[20]), "=r"(u[21]), "=r"(u[22]), "=r"(u[23]),
+        "=r"(u[24]), "=r"(u[25]), "=r"(u[26]), "=r"(u[27]), "=r"(u[28]), "=r"(u[29]), "=r"(u[30]), "=r"(u[31]),
+        "=r"(u[32]), "=r"(u[33]), "=r"(u[34]), "=r"(u[35]), "=r"(u[36]), "=r"(u[37]), "=r"(u[38]), "=r"(u[39]),
+        "=r"(u[40]), "=r"(u[41]), "=r"(u[42]), "=r"(u[43]), "=r"(u[44]), "=r"(u[45]), "=r"(u[46]), "=r"(u[47]),
+        "=r"(u[48]), "=r"(u[49]), "=r"(u[50]), "=r"(u[51]), "=r"(u[52]), "=r"(u[53]), "=r"(u[54]), "=r"(u[55]),
+        "=r"(u[56]), "=r"(u[57]), "=r"(u[58]), "=r"(u[59]), "=r"(u[60]), "=r"(u[61]), "=r"(u[62]), "=r"(u[63])
+      : "r"(at)
       : "memory");
 }
 
-__device__ __forceinline__ void tmem_store16(uint32_t at, const uint32_t (&u)[16]) {
+__device__ __forceinline__ void tmem_store32(uint32_t at, const uint32_t (&u)[32]) {
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], "
-      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15};" ::"r"(u[0]), "r"(u[1]), "r"(u[2]),
-      "r"(u[3]), "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7]), "r"(u[8]), "r"(u[9]), "r"(u[10]), "r"(u[11]), "r"(u[12]),
-      "r"(u[13]), "r"(u[14]), "r"(u[15]), "r"(at)
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31};" ::"r"(u[0]), "r"(u[1]), "r"(u[2]), "r"(u[3]), "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7]), "r"(u[8]), "r"(u[9]), "r"(u[10]), "r"(u[11]), "r"(u[12]), "r"(u[13]), "r"(u[14]), "r"(u[15]), "r"(u[16]), "r"(u[17]), "r"(u[18]), "r"(u[19]), "r"(u[20]), "r"(u[21]), "r"(u[22]), "r"(u[23]), "r"(u[24]), "r"(u[25]), "r"(u[26]), "r"(u[27]), "r"(u[28]), "r"(u[29]), "r"(u[30]), "r"(u[31]), "r"(at)
       : "memory");
 }
 
 __device__ __forceinline__ void tmem_stored() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// mbar_wait, in line: the roles' register shares leave no room for calls.
+__device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity, const volatile int* abort_flag) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = global_ns();
+  for (;;) {
+#pragma unroll 1
+    for (int i = 0; i < 32; ++i)
+      if (mbar_try_wait(bar, parity)) return true;
+    if ((abort_flag != nullptr && *abort_flag) || global_ns() - t0 > kWaitLimitNs) return false;
+  }
+}
 
 // Byte of 16-byte chunk `chunk` of row `row` in an operand tile of `rows` rows.
 __device__ __forceinline__ uint32_t chunk_at(int rows, int row, int chunk) {
@@ -181,6 +212,37 @@ __device__ __forceinline__ uint32_t code_64ths(uint32_t word, int i) {
   return bf2_mul(code_bits(word, i), i % 2 == 0 ? 0x7F007F00u : 0x7D007D00u);
 }
 
+__device__ __forceinline__ uint64_t f2_add(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+
+// A row's outputs, and the weights of the tile's first half, times `keep`
+// (a power of two). Rare.
+template <int D>
+__device__ __forceinline__ void rescale(uint32_t o_at, uint32_t p_at, float keep, bool outputs, bool weights) {
+  float o[32];
+  uint32_t u[32];
+  if (weights) {
+    tmem_stored();
+    const uint32_t keep2 = pack2(keep, keep);
+    tmem_load(p_at, o);
+#pragma unroll
+    for (int i = 0; i < 32; ++i) u[i] = bf2_mul(__float_as_uint(o[i]), keep2);
+    tmem_store32(p_at, u);
+  }
+  if (outputs) {
+#pragma unroll 1
+    for (int q = 0; q < D / 32; ++q) {
+      tmem_load(o_at + 32 * q, o);
+#pragma unroll
+      for (int i = 0; i < 32; ++i) u[i] = __float_as_uint(o[i] * keep);
+      tmem_store32(o_at + 32 * q, u);
+    }
+  }
+}
+
 // A CTA's share of the work.
 struct Job {
   int r, tile, h;     // request, 256-row tile, kv head
@@ -207,7 +269,6 @@ attention_prefill_kernel(const AttentionArgs a, const KvCache c) {
   auto v_free = [&](int b) { return bar0 + 64 + 8u * b; };
   auto s_full = [&](int t) { return bar0 + 80 + 8u * t; };
   auto p_full = [&](int t) { return bar0 + 96 + 8u * t; };
-  const uint32_t pairs_full = bar0 + 112;
   uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kAtWords);
   volatile int* const abort_flag = reinterpret_cast<volatile int*>(smem + L::kAtWords + 4);
   Job* const job = reinterpret_cast<Job*>(smem + L::kAtWords + 8);
@@ -218,7 +279,6 @@ attention_prefill_kernel(const AttentionArgs a, const KvCache c) {
   if (threadIdx.x == 0) {
     mbar_init(q_full, 2 * kGroupThreads);
     mbar_init(o_full, 1);
-    mbar_init(pairs_full, kGroupThreads);
     for (int b = 0; b < 2; ++b) {
       mbar_init(k_full(b), kGroupThreads);
       mbar_init(k_free(b), 1);
@@ -301,6 +361,7 @@ attention_prefill_kernel(const AttentionArgs a, const KvCache c) {
 
   if (x.r >= 0 && warp < 8) {
     // ---------------- a row a thread ----------------
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRowRegisters));
     const int t = warp / 4;                       // tile of rows
     const int row = threadIdx.x % kGroupThreads;
     const int in_tile = t * kTile + row;
@@ -353,7 +414,7 @@ attention_prefill_kernel(const AttentionArgs a, const KvCache c) {
     if (t == 0 || two) {
 #pragma unroll 1
       for (int j = 0; j < n; ++j) {
-        ok = mbar_wait(s_full(t), j & 1, abort_flag);
+        ok = wait_for(s_full(t), j & 1, abort_flag);
         if (gave_up(__all_sync(0xffffffffu, ok))) { ok = false; break; }
         fence_after();
         const int p0 = (x.first + j) * kTile;
@@ -379,73 +440,58 @@ attention_prefill_kernel(const AttentionArgs a, const KvCache c) {
           const uint32_t bad = (see[0] & broken.x) | (see[1] & broken.y) | (see[2] & broken.z) | (see[3] & broken.w);
           if (bad != 0) l = NAN;
         }
-        float s[32];
-        float top = -FLT_MAX;
-#pragma unroll 1
-        for (int q = 0; q < 4; ++q) {
-          tmem_load(s_at + 32 * q, s);
+        // half a row at a time, each read once
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          float s[64];
+          tmem_load64(s_at + 64 * h, s);
           if (scaled) {
 #pragma unroll
-            for (int i = 0; i < 32; ++i) s[i] *= factors[32 * q + i];
+            for (int i = 0; i < 64; ++i) s[i] *= factors[64 * h + i];
           }
           if (masked) {
-            const uint32_t bits = q == 0 ? see[0] : q == 1 ? see[1] : q == 2 ? see[2] : see[3];
 #pragma unroll
-            for (int i = 0; i < 32; ++i)
-              if (!((bits >> i) & 1u)) s[i] = -INFINITY;
+            for (int i = 0; i < 64; ++i)
+              if (!((see[2 * h + i / 32] >> (i & 31)) & 1u)) s[i] = -INFINITY;
           }
           float tops[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
-          for (int i = 4; i < 32; ++i) tops[i & 3] = fmaxf(tops[i & 3], s[i]);
-          top = fmaxf(top, fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])));
-        }
-        top *= factor;
-        if (__any_sync(0xffffffffu, top > m + 8.0f)) {
-          const float next = fmaxf(m, top);
-          const float keep = ex2(m - next);
-          m = next;
-          l *= keep;
-          if (j > 0) {
+          for (int i = 4; i < 64; i += 4)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) tops[k] = fmaxf(tops[k], s[i + k]);
+          const float top = factor * fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
+          if (__any_sync(0xffffffffu, top > m + 8.0f)) {
+            // by a whole number, so that what is scaled is scaled exactly
+            const float next = top > m ? (m == -FLT_MAX ? ceilf(top) : m + ceilf(top - m)) : m;
+            const float keep = ex2(m - next);
+            m = next;
+            l *= keep;
             // S(j) done means that the products of tile j - 1, issued before it, are done
-#pragma unroll 1
-            for (int q = 0; q < D / 32; ++q) {
-              tmem_load(o_at + 32 * q, s);
-#pragma unroll
-              for (int i = 0; i < 32; ++i) s[i] *= keep;
-              tmem_store32(o_at + 32 * q, s);
-            }
+            rescale<D>(o_at, s_at, keep, j > 0, h > 0);
           }
+          const uint64_t f2v = f2(factor, factor), m2 = f2(-m, -m);
+          uint64_t sums[2] = {f2(0.0f, 0.0f), f2(0.0f, 0.0f)};
+          uint32_t p[32];
+#pragma unroll
+          for (int i = 0; i < 64; i += 2) {
+            float e0, e1;
+            f2_split(f2_fma(f2(s[i], s[i + 1]), f2v, m2), e0, e1);
+            e0 = ex2(e0);
+            e1 = ex2(e1);
+            sums[(i >> 1) & 1] = f2_add(sums[(i >> 1) & 1], f2(e0, e1));
+            p[i >> 1] = pack2(e0, e1);
+          }
+          tmem_store32(s_at + 32 * h, p);  // over columns already read
+          float l0, l1;
+          f2_split(f2_add(sums[0], sums[1]), l0, l1);
+          l += l0 + l1;
         }
-        float sums[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll 1
-        for (int q = 0; q < 4; ++q) {
-          tmem_load(s_at + 32 * q, s);
-          if (scaled) {
-#pragma unroll
-            for (int i = 0; i < 32; ++i) s[i] *= factors[32 * q + i];
-          }
-          if (masked) {
-            const uint32_t bits = q == 0 ? see[0] : q == 1 ? see[1] : q == 2 ? see[2] : see[3];
-#pragma unroll
-            for (int i = 0; i < 32; ++i)
-              if (!((bits >> i) & 1u)) s[i] = -INFINITY;
-          }
-          uint32_t p[16];
-#pragma unroll
-          for (int i = 0; i < 32; i += 2) {
-            const float p0v = ex2(fmaf(s[i], factor, -m)), p1v = ex2(fmaf(s[i + 1], factor, -m));
-            sums[(i >> 1) & 3] += p0v + p1v;
-            p[i >> 1] = pack2(p0v, p1v);
-          }
-          tmem_store16(s_at + 16 * q, p);  // over columns already read
-        }
-        l += (sums[0] + sums[1]) + (sums[2] + sums[3]);
         tmem_stored();
         fence_before();
         mbar_arrive(p_full(t));
       }
       if (n > 0 && ok) {
-        ok = mbar_wait(o_full, 0, abort_flag);
+        ok = wait_for(o_full, 0, abort_flag);
         ok = !gave_up(__all_sync(0xffffffffu, ok));
         fence_after();
       }
@@ -468,17 +514,13 @@ attention_prefill_kernel(const AttentionArgs a, const KvCache c) {
         }
       }
     }
-  } else if (x.r >= 0 && warp < 12) {
+  } else if (x.r >= 0 && warp < 16) {
     // ---------------- codes to operands ----------------
-    const int id = threadIdx.x - 8 * 32;  // a position of the tile, for K
-    const int dw = warp - 8;
-    constexpr int kWords = D / 8;         // words of a row
-    constexpr int kUnits = D / 64;        // (8 positions, word) pieces of V a thread takes
-    const int word = (lane >> 3) + 4 * (dw % (kWords / 4));
-    const int eights0 = (lane & 7) + 8 * (dw / (kWords / 4));  // of its first piece
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kCodeRegisters));
+    const int id = threadIdx.x % kGroupThreads, dw = warp & 3;
     const int per_page = c.page_size / kBlockTokens;
     const int32_t* table = c.block_table + static_cast<int64_t>(x.r) * c.max_pages;
-    if (x.clipped && id == 0) set_dev_err(a.dev_err, PLE_DEVERR_BOUNDS);
+    const uint8_t* const cache = c.base;
     auto block_at = [&](int b) {
       if (b < x.block0 || b >= x.block_end) return -1;
       const int col = b / per_page;
@@ -489,81 +531,73 @@ attention_prefill_kernel(const AttentionArgs a, const KvCache c) {
       }
       return static_cast<int>((page * hk + x.h) * per_page + (b - col * per_page));
     };
-    // the next tile: blocks, then codes
-    int kb, vb[kUnits];
-    bool here;  // the fetched tile's position is in the cache
-    uint4 kw[kWords / 4];
-    uint32_t kp, vp, vw[kUnits][8];
-    auto find = [&](int j) {
-      const int b = (x.first + j) * (kTile / kBlockTokens);
-      kb = j < n ? block_at(b + id / kBlockTokens) : -1;
+    constexpr int kWords = D / 8;  // words of a row
+    bool ok = true;
+    if (warp < 12) {
+      // K: a position a thread
+      if (x.clipped && id == 0) set_dev_err(a.dev_err, PLE_DEVERR_BOUNDS);
+      const int slot = id % kBlockTokens;
+      int block;                    // of the tile to fetch
+      uint4 next[kWords / 4];
+      uint32_t next_kp, next_vp;
+      bool next_here;
+      auto find = [&](int j) { block = j < n ? block_at((x.first + j) * (kTile / kBlockTokens) + id / kBlockTokens) : -1; };
+      auto fetch = [&](int j) {
+        next_kp = next_vp = 0;
+        next_here = block >= 0 && (x.first + j) * kTile + id < x.len;
+        if (next_here) {
+          const uint8_t* p = cache + static_cast<int64_t>(block) * B::kBytes;
 #pragma unroll
-      for (int u = 0; u < kUnits; ++u) vb[u] = j < n ? block_at(b + (eights0 + 8 * u) / 2) : -1;
-    };
-    auto fetch = [&](int j) {
-      kp = vp = 0;
+          for (int i = 0; i < kWords / 4; ++i) next[i] = __ldg(reinterpret_cast<const uint4*>(p + slot * B::kRow) + i);
+          next_kp = __ldg(reinterpret_cast<const uint32_t*>(p + B::kPairs + slot * 4));
+          next_vp = __ldg(reinterpret_cast<const uint32_t*>(p + B::kVPairs + slot * 4));
+        }
+      };
 #pragma unroll
-      for (int i = 0; i < kWords / 4; ++i) kw[i] = make_uint4(0, 0, 0, 0);
-      here = kb >= 0 && (x.first + j) * kTile + id < x.len;
-      if (here) {
-        const uint8_t* p = c.base + static_cast<int64_t>(kb) * B::kBytes;
-        const int slot = id % kBlockTokens;
-#pragma unroll
-        for (int i = 0; i < kWords / 4; ++i) kw[i] = __ldg(reinterpret_cast<const uint4*>(p + slot * B::kRow) + i);
-        kp = __ldg(reinterpret_cast<const uint32_t*>(p + B::kPairs + slot * 4));
-        vp = __ldg(reinterpret_cast<const uint32_t*>(p + B::kVPairs + slot * 4));
-      }
-#pragma unroll
-      for (int u = 0; u < kUnits; ++u) {
-        const uint8_t* p = c.base + static_cast<int64_t>(vb[u]) * B::kBytes + B::kV +
-                           ((eights0 + 8 * u) & 1) * 8 * B::kRow + word * 4;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) vw[u][i] = vb[u] >= 0 ? __ldg(reinterpret_cast<const uint32_t*>(p + i * B::kRow)) : 0u;
-      }
-    };
-    uint32_t* const pairs = reinterpret_cast<uint32_t*>(smem + L::kAtPairs);
-    if (n > 0) {
+      for (int i = 0; i < kWords / 4; ++i) next[i] = make_uint4(0, 0, 0, 0);
       find(0);
       fetch(0);
       find(1);
-    }
-    bool ok = true;
 #pragma unroll 1
-    for (int j = 0; j < n; ++j) {
-      const int b = j & 1;
-      const uint32_t parity = ((j >> 1) & 1) ^ 1u;
-      ok = mbar_wait(k_free(b), parity, abort_flag);
-      if (gave_up(__all_sync(0xffffffffu, ok))) break;
-      // K, and the masks and value pairs of the tile
-      const bool finite = (vp & 0x7F80u) != 0x7F80u && (vp & 0x7F800000u) != 0x7F800000u;
-      const uint32_t present = __ballot_sync(0xffffffffu, here);
-      const uint32_t broken = __ballot_sync(0xffffffffu, !finite);
-      // the key row's largest magnitude decides whether it needs a factor
-      float ks = bf_lo(kp), km = bf_hi(kp);
-      const float most = fmaxf(fabsf(km), fabsf(fmaf(15.0f, ks, km)));
-      const bool odd = most > 0.0f && most < INFINITY && !(most >= 0.015625f && most < 512.0f);
-      const uint32_t scaled = __ballot_sync(0xffffffffu, odd);
-      if (scaled != 0) {
-        const int k = odd ? max(ilogbf(most), -126) : 0;
-        reinterpret_cast<float*>(smem + L::kAtFactors)[(j % kMaskRing) * kTile + id] = ldexpf(1.0f, k);
-        ks *= ldexpf(1.0f, -k);
-        km *= ldexpf(1.0f, -k);
-      } else {
-        reinterpret_cast<float*>(smem + L::kAtFactors)[(j % kMaskRing) * kTile + id] = 1.0f;
-      }
-      if (lane == 0) {
-        uint32_t* mask = masks + (j % kMaskRing) * 12 + dw;
-        mask[0] = present;
-        mask[4] = broken;
-        mask[8] = scaled;
-      }
-      pairs[b * kTile + id] = finite ? vp : 0u;
-      {
+      for (int j = 0; j < n; ++j) {
+        const int b = j & 1;
+        uint4 codes[kWords / 4];
+#pragma unroll
+        for (int i = 0; i < kWords / 4; ++i) codes[i] = next[i];
+        const uint32_t kp = next_kp, vp = next_vp;
+        const bool here = next_here;
+        fetch(j + 1);  // on its way while this tile is laid out
+        find(j + 2);
+        // the key row's largest magnitude decides whether it needs a factor
+        float ks = bf_lo(kp), km = bf_hi(kp);
+        const float most = fmaxf(fabsf(km), fabsf(fmaf(15.0f, ks, km)));
+        const bool odd = most > 0.0f && most < INFINITY && !(most >= 0.015625f && most < 512.0f);
+        const bool finite = (vp & 0x7F80u) != 0x7F80u && (vp & 0x7F800000u) != 0x7F800000u;
+        const uint32_t present = __ballot_sync(0xffffffffu, here);
+        const uint32_t broken = __ballot_sync(0xffffffffu, !finite);
+        const uint32_t scaled = __ballot_sync(0xffffffffu, odd);
+        ok = wait_for(k_free(b), ((j >> 1) & 1) ^ 1u, abort_flag);
+        if (gave_up(__all_sync(0xffffffffu, ok))) break;
+        float* factors = reinterpret_cast<float*>(smem + L::kAtFactors) + (j % kMaskRing) * kTile;
+        if (scaled != 0) {
+          const int k = odd ? max(ilogbf(most), -126) : 0;
+          factors[id] = ldexpf(1.0f, k);
+          ks *= ldexpf(1.0f, -k);
+          km *= ldexpf(1.0f, -k);
+        } else {
+          factors[id] = 1.0f;
+        }
+        if (lane == 0) {
+          uint32_t* mask = masks + (j % kMaskRing) * 12 + dw;
+          mask[0] = present;
+          mask[4] = broken;
+          mask[8] = scaled;
+        }
         const uint32_t s512 = f16_pair(512.0f * ks, 512.0f * ks), off = f16_pair(km, km);
         uint8_t* dst = smem + L::kAtK + b * L::kQ;
 #pragma unroll
         for (int i = 0; i < kWords / 4; ++i) {
-          const uint32_t w[4] = {kw[i].x, kw[i].y, kw[i].z, kw[i].w};
+          const uint32_t w[4] = {codes[i].x, codes[i].y, codes[i].z, codes[i].w};
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             uint4 v;
@@ -574,110 +608,175 @@ attention_prefill_kernel(const AttentionArgs a, const KvCache c) {
             *reinterpret_cast<uint4*>(dst + chunk_at(kTile, id, 4 * i + k)) = v;
           }
         }
+        fence_operands();
+        mbar_arrive(k_full(b));
       }
-      fence_operands();
-      mbar_arrive(k_full(b));
-      mbar_arrive(pairs_full);  // all four warps' value pairs
-      ok = mbar_wait(pairs_full, j & 1, abort_flag) && mbar_wait(v_free(b), parity, abort_flag);
-      if (gave_up(__all_sync(0xffffffffu, ok))) break;
-      {
-        uint8_t* dst = smem + L::kAtV + b * L::kQ;
+    } else {
+      // V: eight positions and D / 64 words of them a thread; neighbouring
+      // lanes hold neighbouring eights, whose chunks share a row
+      constexpr int kPer = D / 64;
+      const int eights = (lane & 7) + 8 * (dw >> 1);
+      const int word = ((lane >> 3) + 4 * (dw & 1)) * kPer;
+      int block;
+      uint32_t next[8][kPer];
+      uint4 next_pairs[2];
+      auto find = [&](int j) { block = j < n ? block_at((x.first + j) * (kTile / kBlockTokens) + eights / 2) : -1; };
+      auto fetch = [&](int j) {
+        next_pairs[0] = next_pairs[1] = make_uint4(0, 0, 0, 0);
+        const int left = x.len - ((x.first + j) * kTile + eights * 8);  // positions of these in the cache
+        if (block >= 0 && left > 0) {
+          const uint8_t* p = cache + static_cast<int64_t>(block) * B::kBytes;
+          const int slot = (eights & 1) * 8;
+          next_pairs[0] = __ldg(reinterpret_cast<const uint4*>(p + B::kVPairs + slot * 4));
+          next_pairs[1] = __ldg(reinterpret_cast<const uint4*>(p + B::kVPairs + slot * 4) + 1);
+          p += B::kV + slot * B::kRow + word * 4;
 #pragma unroll
-        for (int u = 0; u < kUnits; ++u) {
-          const int eights = eights0 + 8 * u;
-          const uint4 p0 = *reinterpret_cast<const uint4*>(pairs + b * kTile + eights * 8);
-          const uint4 p1 = *reinterpret_cast<const uint4*>(pairs + b * kTile + eights * 8 + 4);
-          const uint32_t sm[8] = {p0.x, p0.y, p0.z, p0.w, p1.x, p1.y, p1.z, p1.w};
-          uint32_t s64[4], off[4];
+          for (int i = 0; i < 8; ++i) {
+            if constexpr (kPer == 2) {
+              const uint2 v = __ldg(reinterpret_cast<const uint2*>(p + i * B::kRow));
+              next[i][0] = v.x;
+              next[i][1] = v.y;
+            } else {
+              next[i][0] = __ldg(reinterpret_cast<const uint32_t*>(p + i * B::kRow));
+            }
+          }
+          if (left < 8) {  // what lies behind the last position enters as zeros
+            uint32_t* pair = reinterpret_cast<uint32_t*>(next_pairs);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              if (i >= left) pair[i] = 0;
+          }
+        }
+      };
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+#pragma unroll
+        for (int k = 0; k < kPer; ++k) next[i][k] = 0;
+      find(0);
+      fetch(0);
+      find(1);
+#pragma unroll 1
+      for (int j = 0; j < n; ++j) {
+        const int b = j & 1;
+        uint32_t codes[8][kPer];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+#pragma unroll
+          for (int k = 0; k < kPer; ++k) codes[i][k] = next[i][k];
+        uint32_t s64[4], off[4];
+        {
+          uint32_t pair[8] = {next_pairs[0].x, next_pairs[0].y, next_pairs[0].z, next_pairs[0].w,
+                              next_pairs[1].x, next_pairs[1].y, next_pairs[1].z, next_pairs[1].w};
+#pragma unroll
+          for (int i = 0; i < 8; ++i)  // not finite: the rows that see it become NaN by the mask
+            if ((pair[i] & 0x7F80u) == 0x7F80u || (pair[i] & 0x7F800000u) == 0x7F800000u) pair[i] = 0;
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            s64[i] = bf2_mul(__byte_perm(sm[2 * i], sm[2 * i + 1], 0x5410), 0x42804280u);
-            off[i] = __byte_perm(sm[2 * i], sm[2 * i + 1], 0x7632);
+            s64[i] = bf2_mul(__byte_perm(pair[2 * i], pair[2 * i + 1], 0x5410), 0x42804280u);
+            off[i] = __byte_perm(pair[2 * i], pair[2 * i + 1], 0x7632);
           }
+        }
+        fetch(j + 1);
+        find(j + 2);
+        ok = wait_for(v_free(b), ((j >> 1) & 1) ^ 1u, abort_flag);
+        if (gave_up(__all_sync(0xffffffffu, ok))) break;
+        uint8_t* dst = smem + L::kAtV + b * L::kQ;
+#pragma unroll
+        for (int k = 0; k < kPer; ++k)
 #pragma unroll
           for (int half = 0; half < 2; ++half) {
             uint32_t y[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) y[i] = __byte_perm(vw[u][2 * i], vw[u][2 * i + 1], half == 0 ? 0x5410 : 0x7632);
+            for (int i = 0; i < 4; ++i) y[i] = __byte_perm(codes[2 * i][k], codes[2 * i + 1][k], half == 0 ? 0x5410 : 0x7632);
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
+            for (int q = 0; q < 4; ++q) {
               uint4 v;
-              v.x = bf2_mad(code_64ths(y[0], k), s64[0], off[0]);
-              v.y = bf2_mad(code_64ths(y[1], k), s64[1], off[1]);
-              v.z = bf2_mad(code_64ths(y[2], k), s64[2], off[2]);
-              v.w = bf2_mad(code_64ths(y[3], k), s64[3], off[3]);
-              *reinterpret_cast<uint4*>(dst + chunk_at(D, word * 8 + half * 4 + k, eights)) = v;
+              v.x = bf2_mad(code_64ths(y[0], q), s64[0], off[0]);
+              v.y = bf2_mad(code_64ths(y[1], q), s64[1], off[1]);
+              v.z = bf2_mad(code_64ths(y[2], q), s64[2], off[2]);
+              v.w = bf2_mad(code_64ths(y[3], q), s64[3], off[3]);
+              *reinterpret_cast<uint4*>(dst + chunk_at(D, (word + k) * 8 + half * 4 + q, eights)) = v;
             }
           }
-        }
+        fence_operands();
+        mbar_arrive(v_full(b));
       }
-      fence_operands();
-      mbar_arrive(v_full(b));
-      // the next tile's codes fly while this one is multiplied
-      fetch(j + 1);
-      find(j + 2);
     }
-  } else if (warp == 12 && lane == 0 && n > 0) {
+  } else if (x.r >= 0) {
     // ---------------- products ----------------
-    auto scores = [&](int t, int b) {  // S = Q K^T of one tile of rows
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kProductRegisters));
+    if (warp == 16 && n > 0) {
+      const uint32_t acc = __shfl_sync(0xffffffffu, tmem, 0);
+      const uint32_t q_op = operand(base), k_op = operand(base + L::kAtK), v_op = operand(base + L::kAtV);
+      constexpr uint32_t kTileOp = L::kQ >> 4;
+      auto scores = [&](int t, int b) {  // S = Q K^T of one tile of rows
+        if (elected()) {
+          const uint32_t d = acc + t * kTile, q = q_op + t * kTileOp, k = k_op + b * kTileOp;
+          mma_smem<false>(d, q, k, idesc(kTile, 0));
 #pragma unroll
-      for (int k = 0; k < D / 16; ++k) {
-        const uint32_t at = (k / 4) * kTile * 128 + (k % 4) * 32;
-        mma_smem(tmem + t * kTile, operand(base + t * L::kQ + at), operand(base + L::kAtK + b * L::kQ + at), idesc(kTile, 0), k > 0);
-      }
-    };
-    auto outputs = [&](int t, int b, bool add) {  // O += P V
-#pragma unroll
-      for (int k = 0; k < kTile / 16; ++k) {
-        const uint32_t at = (k / 4) * D * 128 + (k % 4) * 32;
-        mma_tmem(tmem + 2 * kTile + t * D, tmem + t * kTile + 8 * k, operand(base + L::kAtV + b * L::kQ + at), idesc(D, 1), add || k > 0);
-      }
-    };
-    bool ok = mbar_wait(q_full, 0, abort_flag) && mbar_wait(k_full(0), 0, abort_flag);
-    if (ok) {
-      fence_after();
-      scores(0, 0);
-      mma_commit(s_full(0));
-      if (two) {
-        scores(1, 0);
-        mma_commit(s_full(1));
-      }
-      mma_commit(k_free(0));
-    }
-#pragma unroll 1
-    for (int j = 0; ok && j < n; ++j) {
-      const int b = j & 1, nb = b ^ 1;
-      ok = mbar_wait(v_full(b), (j >> 1) & 1, abort_flag) && mbar_wait(p_full(0), j & 1, abort_flag);
-      if (!ok) break;
-      fence_after();
-      outputs(0, b, j > 0);
-      const bool more = j + 1 < n;
-      if (more) {
-        ok = mbar_wait(k_full(nb), ((j + 1) >> 1) & 1, abort_flag);
-        if (!ok) break;
-        fence_after();
-        scores(0, nb);
-        mma_commit(s_full(0));
-      }
-      if (two) {
-        ok = mbar_wait(p_full(1), j & 1, abort_flag);
-        if (!ok) break;
-        fence_after();
-        outputs(1, b, j > 0);
-      }
-      mma_commit(v_free(b));
-      if (more) {
-        if (two) {
-          scores(1, nb);
-          mma_commit(s_full(1));
+          for (int i = 1; i < D / 16; ++i) {
+            const uint32_t at = ((i / 4) * kTile * 128 + (i % 4) * 32) >> 4;
+            mma_smem<true>(d, q + at, k + at, idesc(kTile, 0));
+          }
+          mma_commit(s_full(t));
         }
-        mma_commit(k_free(nb));
+        __syncwarp();
+      };
+      auto outputs = [&](int t, int b, bool add) {  // O += P V
+        if (elected()) {
+          const uint32_t d = acc + 2 * kTile + t * D, p = acc + t * kTile, v = v_op + b * kTileOp;
+#pragma unroll
+          for (int i = 0; i < kTile / 16; ++i)
+            mma_tmem(d, p + 8 * i, v + (((i / 4) * D * 128 + (i % 4) * 32) >> 4), idesc(D, 1), i > 0 || add);
+        }
+        __syncwarp();
+      };
+      auto commit = [&](uint32_t bar) {
+        if (elected()) mma_commit(bar);
+        __syncwarp();
+      };
+      auto wait_all = [&](uint32_t bar, uint32_t parity) {
+        const bool ok = wait_for(bar, parity, abort_flag);
+        return __all_sync(0xffffffffu, ok) != 0;
+      };
+      bool ok = wait_all(q_full, 0) && wait_all(k_full(0), 0);
+      if (ok) {
+        fence_after();
+        scores(0, 0);
+        if (two) scores(1, 0);
+        commit(k_free(0));
       }
+#pragma unroll 1
+      for (int j = 0; ok && j < n; ++j) {
+        const int b = j & 1, nb = b ^ 1;
+        const bool more = j + 1 < n;
+        ok = wait_all(v_full(b), (j >> 1) & 1) && wait_all(p_full(0), j & 1);
+        if (!ok) break;
+        fence_after();
+        outputs(0, b, j > 0);
+        if (more) {
+          ok = wait_all(k_full(nb), ((j + 1) >> 1) & 1);
+          if (!ok) break;
+          fence_after();
+          scores(0, nb);
+        }
+        if (two) {
+          ok = wait_all(p_full(1), j & 1);
+          if (!ok) break;
+          fence_after();
+          outputs(1, b, j > 0);
+        }
+        commit(v_free(b));
+        if (more) {
+          if (two) scores(1, nb);
+          commit(k_free(nb));
+        }
+      }
+      gave_up(ok);
+      // every product issued has completed once this flips
+      commit(o_full);
+      wait_for(o_full, 0, nullptr);
     }
-    gave_up(ok);
-    // every product issued has completed once this flips
-    mma_commit(o_full);
-    mbar_wait(o_full, 0, nullptr);
   }
   __syncwarp();
   fence_before();

@@ -8,9 +8,11 @@
 //
 // Mathematics. For each tile of positions, S = Q K^T (f16 operands, f32 in
 // tensor memory), P = exp2(f S - m) rounded to bf16 over S in tensor memory,
-// O += P V (bf16 operands, f32 in tensor memory). The running maximum m of a
-// row is raised only when a score passes it by 2^8, and only then is O scaled:
-// weights of up to 256 cost no precision.
+// O += P V (bf16 operands, f32 in tensor memory). m need not be the largest
+// score for that, only near it: weights and sums are floating point. So a
+// tile's weights are taken with the m there is while its maximum is being
+// found, and m is raised (and O scaled) between tiles, when a score passed it
+// by 2^8. Only a score 2^64 above m - a row's first, mostly - raises it at once.
 // Roundings: a key enters as f16(code * scale + offset), because a score of
 // hundreds must not move by a bf16's 2^-8 of it; rows of Q are scaled to
 // [1, 2) by a power of two (in the row's f), and a key row outside
@@ -55,8 +57,8 @@ struct Prefill {
   static constexpr int kQ = kTile * D * 2;       // bytes of an operand tile
   static constexpr int kAtK = 2 * kQ;
   static constexpr int kAtV = kAtK + 2 * kQ;
-  static constexpr int kAtMasks = kAtV + 2 * kQ;             // [ring][3][4] present; V not finite; K has a factor
-  static constexpr int kAtFactors = kAtMasks + kMaskRing * 12 * 4;  // [ring][128] of K rows
+  static constexpr int kAtMasks = kAtV + 2 * kQ;             // [ring][4][4] present; V not finite; K has a factor; any such
+  static constexpr int kAtFactors = kAtMasks + kMaskRing * 16 * 4;  // [ring][128] of K rows
   static constexpr int kAtBars = kAtFactors + kMaskRing * kTile * 4;
   static constexpr int kAtWords = kAtBars + 16 * 8;
   static constexpr int kSmem = kAtWords + 64 + 1024;         // and alignment
@@ -133,21 +135,9 @@ __device__ __forceinline__ void tmem_load(uint32_t at, float (&r)[32]) {
       : "memory");
 }
 
-// 64 columns of it.
-__device__ __forceinline__ void tmem_load64(uint32_t at, float (&r)[64]) {
-  uint32_t* u = reinterpret_cast<uint32_t*>(r);
+__device__ __forceinline__ void tmem_store16(uint32_t at, const uint32_t (&u)[16]) {
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x64.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32, %33, %34, %35, %36, %37, %38, %39, %40, %41, %42, %43, %44, %45, %46, %47, %48, %49, %50, %51, %52, %53, %54, %55, %56, %57, %58, %59, %60, %61, %62, %63}, [%64];\n\t"
-      "tcgen05.wait::ld.sync.aligned;"
-      : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]), "=r"(u[7]),
-        "=r"(u[8]), "=r"(u[9]), "=r"(u[10]), "=r"(u[11]), "=r"(u[12]), "=r"(u[13]), "=r"(u[14]), "=r"(u[15]),
-        "=r"(u[16]), "=r"(u[17]), "=r"(u[18]), "=r"(u[19]), "=r"(u[20]), "=r"(u[21]), "=r"(u[22]), "=r"(u[23]),
-        "=r"(u[24]), "=r"(u[25]), "=r"(u[26]), "=r"(u[27]), "=r"(u[28]), "=r"(u[29]), "=r"(u[30]), "=r"(u[31]),
-        "=r"(u[32]), "=r"(u[33]), "=r"(u[34]), "=r"(u[35]), "=r"(u[36]), "=r"(u[37]), "=r"(u[38]), "=r"(u[39]),
-        "=r"(u[40]), "=r"(u[41]), "=r"(u[42]), "=r"(u[43]), "=r"(u[44]), "=r"(u[45]), "=r"(u[46]), "=r"(u[47]),
-        "=r"(u[48]), "=r"(u[49]), "=r"(u[50]), "=r"(u[51]), "=r"(u[52]), "=r"(u[53]), "=r"(u[54]), "=r"(u[55]),
-        "=r"(u[56]), "=r"(u[57]), "=r"(u[58]), "=r"(u[59]), "=r"(u[60]), "=r"(u[61]), "=r"(u[62]), "=r"(u[63])
-      : "r"(at)
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15};" ::"r"(u[0]), "r"(u[1]), "r"(u[2]), "r"(u[3]), "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7]), "r"(u[8]), "r"(u[9]), "r"(u[10]), "r"(u[11]), "r"(u[12]), "r"(u[13]), "r"(u[14]), "r"(u[15]), "r"(at)
       : "memory");
 }
 
@@ -218,29 +208,29 @@ __device__ __forceinline__ uint64_t f2_add(uint64_t a, uint64_t b) {
   return d;
 }
 
-// A row's outputs, and the weights of the tile's first half, times `keep`
-// (a power of two). Rare.
+// A row's outputs times `keep`. Rare.
 template <int D>
-__device__ __forceinline__ void rescale(uint32_t o_at, uint32_t p_at, float keep, bool outputs, bool weights) {
-  float o[32];
-  uint32_t u[32];
-  if (weights) {
-    tmem_stored();
-    const uint32_t keep2 = pack2(keep, keep);
-    tmem_load(p_at, o);
-#pragma unroll
-    for (int i = 0; i < 32; ++i) u[i] = bf2_mul(__float_as_uint(o[i]), keep2);
-    tmem_store32(p_at, u);
-  }
-  if (outputs) {
+__device__ __forceinline__ void rescale_outputs(uint32_t at, float keep) {
 #pragma unroll 1
-    for (int q = 0; q < D / 32; ++q) {
-      tmem_load(o_at + 32 * q, o);
+  for (int q = 0; q < D / 32; ++q) {
+    float o[32];
+    uint32_t u[32];
+    tmem_load(at + 32 * q, o);
 #pragma unroll
-      for (int i = 0; i < 32; ++i) u[i] = __float_as_uint(o[i] * keep);
-      tmem_store32(o_at + 32 * q, u);
-    }
+    for (int i = 0; i < 32; ++i) u[i] = __float_as_uint(o[i] * keep);
+    tmem_store32(at + 32 * q, u);
   }
+}
+
+// 32 weights of a row, already in tensor memory, times `keep` (a power of two). Rare.
+__device__ __forceinline__ void rescale_weights(uint32_t at, float keep) {
+  float w[32];
+  uint32_t u[16];
+  const uint32_t keep2 = pack2(keep, keep);
+  tmem_load(at, w);
+#pragma unroll
+  for (int i = 0; i < 16; ++i) u[i] = bf2_mul(__float_as_uint(w[i]), keep2);
+  tmem_store16(at, u);
 }
 
 // A CTA's share of the work.
@@ -409,7 +399,7 @@ attention_prefill_kernel(const AttentionArgs a, const KvCache c) {
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t s_at = tmem + lanes + t * kTile;
     const uint32_t o_at = tmem + lanes + 2 * kTile + t * D;
-    float m = -FLT_MAX, l = 0.0f;
+    float m = -FLT_MAX, l = 0.0f, top = -FLT_MAX;
     bool ok = true;
     if (t == 0 || two) {
 #pragma unroll 1
@@ -418,72 +408,71 @@ attention_prefill_kernel(const AttentionArgs a, const KvCache c) {
         if (gave_up(__all_sync(0xffffffffu, ok))) { ok = false; break; }
         fence_after();
         const int p0 = (x.first + j) * kTile;
-        const uint32_t* mask = masks + (j % kMaskRing) * 12;
-        const float* factors = reinterpret_cast<const float*>(smem + L::kAtFactors) + (j % kMaskRing) * kTile;
-        // bits of the columns that the row may see
-        const uint4 present = *reinterpret_cast<const uint4*>(mask);
-        const uint4 broken = *reinterpret_cast<const uint4*>(mask + 4);
-        const uint4 scaled4 = *reinterpret_cast<const uint4*>(mask + 8);
-        const bool scaled = (scaled4.x | scaled4.y | scaled4.z | scaled4.w) != 0;
-        const bool masked = p0 < all_from || p0 + kTile - 1 > all_to ||
-                            (present.x & present.y & present.z & present.w) != 0xffffffffu ||
-                            (broken.x | broken.y | broken.z | broken.w) != 0;
-        uint32_t see[4] = {present.x, present.y, present.z, present.w};
-        if (masked) {
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const int hi = last - p0 - 32 * q, lo = from - p0 - 32 * q;  // bits lo..hi
-            uint32_t bits = hi < 0 ? 0u : hi >= 31 ? 0xffffffffu : (2u << hi) - 1u;
-            if (lo > 0) bits &= lo >= 32 ? 0u : 0xffffffffu << lo;
-            see[q] &= bits;
-          }
-          const uint32_t bad = (see[0] & broken.x) | (see[1] & broken.y) | (see[2] & broken.z) | (see[3] & broken.w);
-          if (bad != 0) l = NAN;
+        const uint32_t* mask = masks + (j % kMaskRing) * 16;
+        const uint4 any = *reinterpret_cast<const uint4*>(mask + 12);
+        const bool special = p0 < all_from || p0 + kTile - 1 > all_to || (any.x | any.y | any.z | any.w) != 0;
+        if (__any_sync(0xffffffffu, top > m + 8.0f)) {
+          const float next = fmaxf(m, top);
+          const float keep = ex2(m - next);
+          m = next;
+          l *= keep;
+          // S(j) done means that the products of tile j - 1, issued before it, are done
+          if (j > 0) rescale_outputs<D>(o_at, keep);
         }
-        // half a row at a time, each read once
+        // a quarter of the row at a time, in a loop: what the roles run side
+        // by side has to fit the instruction caches
+#pragma unroll 1
+        for (int q = 0; q < 4; ++q) {
+          float v[32];
+          tmem_load(s_at + 32 * q, v);
+          if (special) {
+            const float* factors = reinterpret_cast<const float*>(smem + L::kAtFactors) + (j % kMaskRing) * kTile + 32 * q;
+            // bits of the columns that the row may see
+            const int hi = last - p0 - 32 * q, lo = from - p0 - 32 * q;  // lo..hi
+            uint32_t see = hi < 0 ? 0u : hi >= 31 ? 0xffffffffu : (2u << hi) - 1u;
+            if (lo > 0) see &= lo >= 32 ? 0u : 0xffffffffu << lo;
+            see &= mask[q];
+            if ((see & mask[4 + q]) != 0) l = NAN;
+            if (mask[8 + q] != 0) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          float s[64];
-          tmem_load64(s_at + 64 * h, s);
-          if (scaled) {
+              for (int i = 0; i < 32; ++i) v[i] *= factors[i];
+            }
 #pragma unroll
-            for (int i = 0; i < 64; ++i) s[i] *= factors[64 * h + i];
+            for (int i = 0; i < 32; ++i)
+              if (!((see >> i) & 1u)) v[i] = -INFINITY;
           }
-          if (masked) {
+          float tops[2] = {v[0], v[1]};
 #pragma unroll
-            for (int i = 0; i < 64; ++i)
-              if (!((see[2 * h + i / 32] >> (i & 31)) & 1u)) s[i] = -INFINITY;
+          for (int i = 2; i < 32; i += 2) {
+            tops[0] = fmaxf(tops[0], v[i]);
+            tops[1] = fmaxf(tops[1], v[i + 1]);
           }
-          float tops[4] = {s[0], s[1], s[2], s[3]};
-#pragma unroll
-          for (int i = 4; i < 64; i += 4)
-#pragma unroll
-            for (int k = 0; k < 4; ++k) tops[k] = fmaxf(tops[k], s[i + k]);
-          const float top = factor * fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
-          if (__any_sync(0xffffffffu, top > m + 8.0f)) {
-            // by a whole number, so that what is scaled is scaled exactly
+          top = fmaxf(top, factor * fmaxf(tops[0], tops[1]));
+          if (__any_sync(0xffffffffu, top > m + 64.0f)) {  // at once, by a power of two: what is scaled is scaled exactly
             const float next = top > m ? (m == -FLT_MAX ? ceilf(top) : m + ceilf(top - m)) : m;
             const float keep = ex2(m - next);
             m = next;
             l *= keep;
-            // S(j) done means that the products of tile j - 1, issued before it, are done
-            rescale<D>(o_at, s_at, keep, j > 0, h > 0);
+            tmem_stored();
+#pragma unroll 1
+            for (int k = 0; k < q; ++k) rescale_weights(s_at + 16 * k, keep);
+            if (j > 0) rescale_outputs<D>(o_at, keep);
           }
           const uint64_t f2v = f2(factor, factor), m2 = f2(-m, -m);
-          uint64_t sums[2] = {f2(0.0f, 0.0f), f2(0.0f, 0.0f)};
-          uint32_t p[32];
+          uint64_t sum = f2(0.0f, 0.0f);
+          uint32_t p[16];
 #pragma unroll
-          for (int i = 0; i < 64; i += 2) {
+          for (int i = 0; i < 32; i += 2) {
             float e0, e1;
-            f2_split(f2_fma(f2(s[i], s[i + 1]), f2v, m2), e0, e1);
+            f2_split(f2_fma(f2(v[i], v[i + 1]), f2v, m2), e0, e1);
             e0 = ex2(e0);
             e1 = ex2(e1);
-            sums[(i >> 1) & 1] = f2_add(sums[(i >> 1) & 1], f2(e0, e1));
+            sum = f2_add(sum, f2(e0, e1));
             p[i >> 1] = pack2(e0, e1);
           }
-          tmem_store32(s_at + 32 * h, p);  // over columns already read
+          tmem_store16(s_at + 16 * q, p);  // over columns already read
           float l0, l1;
-          f2_split(f2_add(sums[0], sums[1]), l0, l1);
+          f2_split(sum, l0, l1);
           l += l0 + l1;
         }
         tmem_stored();
@@ -588,10 +577,11 @@ attention_prefill_kernel(const AttentionArgs a, const KvCache c) {
           factors[id] = 1.0f;
         }
         if (lane == 0) {
-          uint32_t* mask = masks + (j % kMaskRing) * 12 + dw;
+          uint32_t* mask = masks + (j % kMaskRing) * 16 + dw;
           mask[0] = present;
           mask[4] = broken;
           mask[8] = scaled;
+          mask[12] = ~present | broken | scaled;
         }
         const uint32_t s512 = f16_pair(512.0f * ks, 512.0f * ks), off = f16_pair(km, km);
         uint8_t* dst = smem + L::kAtK + b * L::kQ;

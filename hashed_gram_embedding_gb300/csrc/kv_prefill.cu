@@ -48,7 +48,9 @@ constexpr int kTile = 128;        // rows of a tile, and positions
 constexpr int kGroupThreads = 128;
 constexpr int kThreads = 20 * 32;
 // Registers a thread is launched with, and each role's share of the CTA's.
-constexpr int kRegisters = 96, kRowRegisters = 152, kCodeRegisters = 72, kProductRegisters = 32;
+constexpr int kRegisters = 96, kRowRegisters = 120, kCodeRegisters = 88, kProductRegisters = 64;
+static_assert(kRowRegisters >= kRegisters && kCodeRegisters <= kRegisters && kProductRegisters <= kRegisters,
+              "rows ask for more than they start with, the others give back");
 static_assert(2 * kRowRegisters + 2 * kCodeRegisters + kProductRegisters <= 5 * kRegisters, "more would never be had");
 constexpr int kMaskRing = 4;      // tiles whose masks are kept
 
@@ -60,7 +62,7 @@ struct Prefill {
   static constexpr int kAtMasks = kAtV + 2 * kQ;             // [ring][4][4] present; V not finite; K has a factor; any such
   static constexpr int kAtFactors = kAtMasks + kMaskRing * 16 * 4;  // [ring][128] of K rows
   static constexpr int kAtBars = kAtFactors + kMaskRing * kTile * 4;
-  static constexpr int kAtWords = kAtBars + 16 * 8;
+  static constexpr int kAtWords = kAtBars + 20 * 8;
   static constexpr int kSmem = kAtWords + 64 + 1024;         // and alignment
 };
 
@@ -258,7 +260,8 @@ attention_prefill_kernel(const AttentionArgs a, const KvCache c) {
   auto v_full = [&](int b) { return bar0 + 48 + 8u * b; };
   auto v_free = [&](int b) { return bar0 + 64 + 8u * b; };
   auto s_full = [&](int t) { return bar0 + 80 + 8u * t; };
-  auto p_full = [&](int t) { return bar0 + 96 + 8u * t; };
+  auto p_full = [&](int t, int half) { return bar0 + 96 + 16u * half + 8u * t; };
+  auto half_done = [&](int t) { return bar0 + 128 + 8u * t; };
   uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kAtWords);
   volatile int* const abort_flag = reinterpret_cast<volatile int*>(smem + L::kAtWords + 4);
   Job* const job = reinterpret_cast<Job*>(smem + L::kAtWords + 8);
@@ -275,7 +278,9 @@ attention_prefill_kernel(const AttentionArgs a, const KvCache c) {
       mbar_init(v_full(b), kGroupThreads);
       mbar_init(v_free(b), 1);
       mbar_init(s_full(b), 1);
-      mbar_init(p_full(b), kGroupThreads);
+      mbar_init(p_full(b, 0), kGroupThreads);
+      mbar_init(p_full(b, 1), kGroupThreads);
+      mbar_init(half_done(b), 1);
     }
     mbar_fence_init();
     *abort_flag = 0;
@@ -405,7 +410,8 @@ attention_prefill_kernel(const AttentionArgs a, const KvCache c) {
 #pragma unroll 1
       for (int j = 0; j < n; ++j) {
         ok = wait_for(s_full(t), j & 1, abort_flag);
-        if (gave_up(__all_sync(0xffffffffu, ok))) { ok = false; break; }
+        ok = !gave_up(__all_sync(0xffffffffu, ok));
+        if (!ok) break;
         fence_after();
         const int p0 = (x.first + j) * kTile;
         const uint32_t* mask = masks + (j % kMaskRing) * 16;
@@ -454,9 +460,12 @@ attention_prefill_kernel(const AttentionArgs a, const KvCache c) {
             m = next;
             l *= keep;
             tmem_stored();
+            // the first half's weights may be in the products already: then they are in O
+            if (q >= 2) ok = wait_for(half_done(t), j & 1, abort_flag);
+            fence_after();
 #pragma unroll 1
-            for (int k = 0; k < q; ++k) rescale_weights(s_at + 16 * k, keep);
-            if (j > 0) rescale_outputs<D>(o_at, keep);
+            for (int k = q & 2; k < q; ++k) rescale_weights(s_at + 16 * k, keep);
+            if (j > 0 || q >= 2) rescale_outputs<D>(o_at, keep);
           }
           const uint64_t f2v = f2(factor, factor), m2 = f2(-m, -m);
           uint64_t sum = f2(0.0f, 0.0f);
@@ -474,10 +483,12 @@ attention_prefill_kernel(const AttentionArgs a, const KvCache c) {
           float l0, l1;
           f2_split(sum, l0, l1);
           l += l0 + l1;
+          if (q & 1) {  // the products of the first half of the positions need not wait for the second
+            tmem_stored();
+            fence_before();
+            mbar_arrive(p_full(t, q >> 1));
+          }
         }
-        tmem_stored();
-        fence_before();
-        mbar_arrive(p_full(t));
       }
       if (n > 0 && ok) {
         ok = wait_for(o_full, 0, abort_flag);
@@ -712,12 +723,13 @@ attention_prefill_kernel(const AttentionArgs a, const KvCache c) {
         }
         __syncwarp();
       };
-      auto outputs = [&](int t, int b, bool add) {  // O += P V
+      auto outputs = [&](int t, int b, int half, bool add) {  // O += P V for half of the positions
         if (elected()) {
-          const uint32_t d = acc + 2 * kTile + t * D, p = acc + t * kTile, v = v_op + b * kTileOp;
+          const uint32_t d = acc + 2 * kTile + t * D, p = acc + t * kTile + 32 * half;
+          const uint32_t v = v_op + b * kTileOp + half * ((D * 128) >> 4);
 #pragma unroll
-          for (int i = 0; i < kTile / 16; ++i)
-            mma_tmem(d, p + 8 * i, v + (((i / 4) * D * 128 + (i % 4) * 32) >> 4), idesc(D, 1), i > 0 || add);
+          for (int i = 0; i < 4; ++i) mma_tmem(d, p + 8 * i, v + ((i * 32) >> 4), idesc(D, 1), i > 0 || add);
+          if (half == 0) mma_commit(half_done(t));
         }
         __syncwarp();
       };
@@ -740,10 +752,14 @@ attention_prefill_kernel(const AttentionArgs a, const KvCache c) {
       for (int j = 0; ok && j < n; ++j) {
         const int b = j & 1, nb = b ^ 1;
         const bool more = j + 1 < n;
-        ok = wait_all(v_full(b), (j >> 1) & 1) && wait_all(p_full(0), j & 1);
+        ok = wait_all(v_full(b), (j >> 1) & 1) && wait_all(p_full(0, 0), j & 1);
         if (!ok) break;
         fence_after();
-        outputs(0, b, j > 0);
+        outputs(0, b, 0, j > 0);
+        ok = wait_all(p_full(0, 1), j & 1);
+        if (!ok) break;
+        fence_after();
+        outputs(0, b, 1, true);
         if (more) {
           ok = wait_all(k_full(nb), ((j + 1) >> 1) & 1);
           if (!ok) break;
@@ -751,10 +767,14 @@ attention_prefill_kernel(const AttentionArgs a, const KvCache c) {
           scores(0, nb);
         }
         if (two) {
-          ok = wait_all(p_full(1), j & 1);
+          ok = wait_all(p_full(1, 0), j & 1);
           if (!ok) break;
           fence_after();
-          outputs(1, b, j > 0);
+          outputs(1, b, 0, j > 0);
+          ok = wait_all(p_full(1, 1), j & 1);
+          if (!ok) break;
+          fence_after();
+          outputs(1, b, 1, true);
         }
         commit(v_free(b));
         if (more) {

@@ -256,3 +256,14 @@ def test_keys_of_any_size(factor, q_scale):
                 else:
                     b.put(r, p, np.zeros((2, 128)), b.rng.normal(0, 1, (2, 128)))
         run(b, q_scale=q_scale)
+
+
+@pytest.mark.parametrize("at", [0, 20, 40, 70, 100, 127, 130, 200, 255])
+def test_scores_that_leap(at):
+    """One key far above all others, met in each part of a tile, after rows of ordinary scores."""
+    b = Batch([120], [256], 4, 2, 128, 16, seed=at, k_mean=0.0)
+    q = b.rows(4)
+    q[:] = q.abs() + 0.5
+    b.put(0, at, np.full((2, 128), 20.0) + b.rng.normal(0, 1, (2, 128)), b.rng.normal(0, 1, (2, 128)))
+    out = attend(b, q, scale=1.0)
+    check(out, *oracle.attention(bits(q), b.cache, b.table, b.qsl, b.lens, 1.0))

@@ -62,7 +62,7 @@ struct Prefill {
   static constexpr int kAtMasks = kAtV + 2 * kQ;             // [ring][4][4] present; V not finite; K has a factor; any such
   static constexpr int kAtFactors = kAtMasks + kMaskRing * 16 * 4;  // [ring][128] of K rows
   static constexpr int kAtBars = kAtFactors + kMaskRing * kTile * 4;
-  static constexpr int kAtWords = kAtBars + 20 * 8;
+  static constexpr int kAtWords = kAtBars + 16 * 8;
   static constexpr int kSmem = kAtWords + 64 + 1024;         // and alignment
 };
 
@@ -163,6 +163,13 @@ __device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity, const vo
   }
 }
 
+// One arrival a warp, for what all its lanes have done: 32 arrivals at one
+// barrier are taken one after the other.
+__device__ __forceinline__ void warp_arrive(uint32_t bar) {
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
+}
+
 // Byte of 16-byte chunk `chunk` of row `row` in an operand tile of `rows` rows.
 __device__ __forceinline__ uint32_t chunk_at(int rows, int row, int chunk) {
   return static_cast<uint32_t>((chunk >> 3) * rows * 128 + row * 128 + (((chunk & 7) ^ (row & 7)) << 4));
@@ -260,8 +267,7 @@ attention_prefill_kernel(const AttentionArgs a, const KvCache c) {
   auto v_full = [&](int b) { return bar0 + 48 + 8u * b; };
   auto v_free = [&](int b) { return bar0 + 64 + 8u * b; };
   auto s_full = [&](int t) { return bar0 + 80 + 8u * t; };
-  auto p_full = [&](int t, int half) { return bar0 + 96 + 16u * half + 8u * t; };
-  auto half_done = [&](int t) { return bar0 + 128 + 8u * t; };
+  auto p_full = [&](int t) { return bar0 + 96 + 8u * t; };
   uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kAtWords);
   volatile int* const abort_flag = reinterpret_cast<volatile int*>(smem + L::kAtWords + 4);
   Job* const job = reinterpret_cast<Job*>(smem + L::kAtWords + 8);
@@ -270,17 +276,15 @@ attention_prefill_kernel(const AttentionArgs a, const KvCache c) {
   const int G = a.num_heads / c.num_kv_heads, hk = c.num_kv_heads;
 
   if (threadIdx.x == 0) {
-    mbar_init(q_full, 2 * kGroupThreads);
+    mbar_init(q_full, 8);  // warps
     mbar_init(o_full, 1);
     for (int b = 0; b < 2; ++b) {
-      mbar_init(k_full(b), kGroupThreads);
+      mbar_init(k_full(b), 4);
       mbar_init(k_free(b), 1);
-      mbar_init(v_full(b), kGroupThreads);
+      mbar_init(v_full(b), 4);
       mbar_init(v_free(b), 1);
       mbar_init(s_full(b), 1);
-      mbar_init(p_full(b, 0), kGroupThreads);
-      mbar_init(p_full(b, 1), kGroupThreads);
-      mbar_init(half_done(b), 1);
+      mbar_init(p_full(b), 4);
     }
     mbar_fence_init();
     *abort_flag = 0;
@@ -395,7 +399,7 @@ attention_prefill_kernel(const AttentionArgs a, const KvCache c) {
       }
     }
     fence_operands();
-    mbar_arrive(q_full);
+    warp_arrive(q_full);
     const int last = !live ? -1 : a.causal ? x.len - x.n + token : x.len - 1;
     const int from = a.window > 0 && last - a.window + 1 > 0 ? last - a.window + 1 : 0;
     // what every live row of the warp sees
@@ -410,8 +414,7 @@ attention_prefill_kernel(const AttentionArgs a, const KvCache c) {
 #pragma unroll 1
       for (int j = 0; j < n; ++j) {
         ok = wait_for(s_full(t), j & 1, abort_flag);
-        ok = !gave_up(__all_sync(0xffffffffu, ok));
-        if (!ok) break;
+        if (gave_up(__all_sync(0xffffffffu, ok))) { ok = false; break; }
         fence_after();
         const int p0 = (x.first + j) * kTile;
         const uint32_t* mask = masks + (j % kMaskRing) * 16;
@@ -425,9 +428,10 @@ attention_prefill_kernel(const AttentionArgs a, const KvCache c) {
           // S(j) done means that the products of tile j - 1, issued before it, are done
           if (j > 0) rescale_outputs<D>(o_at, keep);
         }
-        // a quarter of the row at a time, in a loop: what the roles run side
-        // by side has to fit the instruction caches
-#pragma unroll 1
+        // a quarter of the row at a time, two to a turn of the loop: what the
+        // roles run side by side has to fit the instruction caches (four to a
+        // turn took half as long again)
+#pragma unroll 2
         for (int q = 0; q < 4; ++q) {
           float v[32];
           tmem_load(s_at + 32 * q, v);
@@ -460,12 +464,9 @@ attention_prefill_kernel(const AttentionArgs a, const KvCache c) {
             m = next;
             l *= keep;
             tmem_stored();
-            // the first half's weights may be in the products already: then they are in O
-            if (q >= 2) ok = wait_for(half_done(t), j & 1, abort_flag);
-            fence_after();
 #pragma unroll 1
-            for (int k = q & 2; k < q; ++k) rescale_weights(s_at + 16 * k, keep);
-            if (j > 0 || q >= 2) rescale_outputs<D>(o_at, keep);
+            for (int k = 0; k < q; ++k) rescale_weights(s_at + 16 * k, keep);
+            if (j > 0) rescale_outputs<D>(o_at, keep);
           }
           const uint64_t f2v = f2(factor, factor), m2 = f2(-m, -m);
           uint64_t sum = f2(0.0f, 0.0f);
@@ -483,12 +484,10 @@ attention_prefill_kernel(const AttentionArgs a, const KvCache c) {
           float l0, l1;
           f2_split(sum, l0, l1);
           l += l0 + l1;
-          if (q & 1) {  // the products of the first half of the positions need not wait for the second
-            tmem_stored();
-            fence_before();
-            mbar_arrive(p_full(t, q >> 1));
-          }
         }
+        tmem_stored();
+        fence_before();
+        warp_arrive(p_full(t));
       }
       if (n > 0 && ok) {
         ok = wait_for(o_full, 0, abort_flag);
@@ -610,7 +609,7 @@ attention_prefill_kernel(const AttentionArgs a, const KvCache c) {
           }
         }
         fence_operands();
-        mbar_arrive(k_full(b));
+        warp_arrive(k_full(b));
       }
     } else {
       // V: eight positions and D / 64 words of them a thread; neighbouring
@@ -700,7 +699,7 @@ attention_prefill_kernel(const AttentionArgs a, const KvCache c) {
             }
           }
         fence_operands();
-        mbar_arrive(v_full(b));
+        warp_arrive(v_full(b));
       }
     }
   } else if (x.r >= 0) {
@@ -723,13 +722,12 @@ attention_prefill_kernel(const AttentionArgs a, const KvCache c) {
         }
         __syncwarp();
       };
-      auto outputs = [&](int t, int b, int half, bool add) {  // O += P V for half of the positions
+      auto outputs = [&](int t, int b, bool add) {  // O += P V
         if (elected()) {
-          const uint32_t d = acc + 2 * kTile + t * D, p = acc + t * kTile + 32 * half;
-          const uint32_t v = v_op + b * kTileOp + half * ((D * 128) >> 4);
+          const uint32_t d = acc + 2 * kTile + t * D, p = acc + t * kTile, v = v_op + b * kTileOp;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) mma_tmem(d, p + 8 * i, v + ((i * 32) >> 4), idesc(D, 1), i > 0 || add);
-          if (half == 0) mma_commit(half_done(t));
+          for (int i = 0; i < kTile / 16; ++i)
+            mma_tmem(d, p + 8 * i, v + (((i / 4) * D * 128 + (i % 4) * 32) >> 4), idesc(D, 1), i > 0 || add);
         }
         __syncwarp();
       };
@@ -752,14 +750,10 @@ attention_prefill_kernel(const AttentionArgs a, const KvCache c) {
       for (int j = 0; ok && j < n; ++j) {
         const int b = j & 1, nb = b ^ 1;
         const bool more = j + 1 < n;
-        ok = wait_all(v_full(b), (j >> 1) & 1) && wait_all(p_full(0, 0), j & 1);
+        ok = wait_all(v_full(b), (j >> 1) & 1) && wait_all(p_full(0), j & 1);
         if (!ok) break;
         fence_after();
-        outputs(0, b, 0, j > 0);
-        ok = wait_all(p_full(0, 1), j & 1);
-        if (!ok) break;
-        fence_after();
-        outputs(0, b, 1, true);
+        outputs(0, b, j > 0);
         if (more) {
           ok = wait_all(k_full(nb), ((j + 1) >> 1) & 1);
           if (!ok) break;
@@ -767,14 +761,10 @@ attention_prefill_kernel(const AttentionArgs a, const KvCache c) {
           scores(0, nb);
         }
         if (two) {
-          ok = wait_all(p_full(1, 0), j & 1);
+          ok = wait_all(p_full(1), j & 1);
           if (!ok) break;
           fence_after();
-          outputs(1, b, 0, j > 0);
-          ok = wait_all(p_full(1, 1), j & 1);
-          if (!ok) break;
-          fence_after();
-          outputs(1, b, 1, true);
+          outputs(1, b, j > 0);
         }
         commit(v_free(b));
         if (more) {

@@ -106,9 +106,7 @@ __device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1
 
 // A pair of bf16 subnormals times 2^100.
 __device__ __forceinline__ uint32_t times_2_100(uint32_t x) {
-  uint32_t y;
-  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(y) : "r"(x), "r"(0x71807180u));
-  return y;
+  return bf2_mul(x, 0x71807180u);
 }
 
 __device__ __forceinline__ uint64_t f2_add(uint64_t a, uint64_t b) {

@@ -2,6 +2,7 @@
 // query rows (kv_attention.cu), one for requests of many (kv_prefill.cu).
 #pragma once
 
+#include "codes.cuh"
 #include "kv_cache.cuh"
 
 namespace ple {
@@ -27,12 +28,6 @@ __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
-}
-
-// Codes i and i + 4 of a word (i = 0..3) where they stand: read as f16 pair,
-// c 2^-24 for even i and c 2^-20 for odd i; read as bf16, c 2^-133 and c 2^-129.
-__device__ __forceinline__ uint32_t code_bits(uint32_t word, int i) {
-  return (i < 2 ? word : word >> 8) & (i % 2 == 0 ? 0x000F000Fu : 0x00F000F0u);
 }
 
 }  // namespace ple

@@ -35,6 +35,7 @@
 // enters as zeros, and a value that is not finite is left out of V and makes
 // NaN of the rows that see it, instead of all rows of its tile.
 #include "kv_attention.cuh"
+#include "tensor_core.cuh"
 
 #include <cuda_fp16.h>
 
@@ -65,126 +66,6 @@ struct Prefill {
   static constexpr int kAtWords = kAtBars + 16 * 8;
   static constexpr int kSmem = kAtWords + 64 + 1024;         // and alignment
 };
-
-// Instruction descriptor, kind::f16: f32 sums, f16 (0) or bf16 (1) operands,
-// both K-major, M = 128.
-constexpr uint32_t idesc(int n, uint32_t type) {
-  return (1u << 4) | (type << 7) | (type << 10) | (uint32_t(n >> 3) << 17) | (uint32_t(kTile >> 4) << 24);
-}
-
-// Descriptor of a K-major operand with 128-byte swizzle: rows of 128 bytes,
-// groups of 8 rows 1024 bytes apart. The low word holds the address and is
-// all that changes.
-constexpr uint32_t kOperandHigh = (1024u >> 4) | (1u << 14) | (2u << 29);
-__device__ __forceinline__ uint32_t operand(uint32_t saddr) { return ((saddr & 0x3FFFFu) >> 4) | (1u << 16); }
-
-template <bool kAdd>
-__device__ __forceinline__ void mma_smem(uint32_t d, uint32_t a, uint32_t b, uint32_t desc) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t.reg .b64 x, y;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "mov.b64 x, {%1, %5};\n\t"
-      "mov.b64 y, {%2, %5};\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n\t}" ::"r"(d), "r"(a), "r"(b), "r"(desc),
-      "n"(kAdd ? 1 : 0), "n"(kOperandHigh)
-      : "memory");
-}
-
-// The A operand in tensor memory: two elements a column.
-__device__ __forceinline__ void mma_tmem(uint32_t d, uint32_t a, uint32_t b, uint32_t desc, bool add) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t.reg .b64 y;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "mov.b64 y, {%2, %5};\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %3, p;\n\t}" ::"r"(d), "r"(a), "r"(b), "r"(desc),
-      "r"(static_cast<uint32_t>(add)), "n"(kOperandHigh)
-      : "memory");
-}
-
-// One lane of a converged warp: the products are issued by it, in code that
-// the whole warp runs (their operands are uniform registers).
-__device__ __forceinline__ bool elected() {
-  uint32_t r;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "elect.sync _|p, 0xffffffff;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(r));
-  return r != 0;
-}
-
-__device__ __forceinline__ void mma_commit(uint32_t bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
-}
-
-__device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void fence_operands() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
-
-// 32 columns of this thread's row.
-__device__ __forceinline__ void tmem_load(uint32_t at, float (&r)[32]) {
-  uint32_t* u = reinterpret_cast<uint32_t*>(r);
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
-      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];\n\t"
-      "tcgen05.wait::ld.sync.aligned;"
-      : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]), "=r"(u[7]),
-        "=r"(u[8]), "=r"(u[9]), "=r"(u[10]), "=r"(u[11]), "=r"(u[12]), "=r"(u[13]), "=r"(u[14]), "=r"(u[15]),
-        "=r"(u[16]), "=r"(u[17]), "=r"(u[18]), "=r"(u[19]), "=r"(u[20]), "=r"(u[21]), "=r"(u[22]), "=r"(u[23]),
-        "=r"(u[24]), "=r"(u[25]), "=r"(u[26]), "=r"(u[27]), "=r"(u[28]), "=r"(u[29]), "=r"(u[30]), "=r"(u[31])
-      : "r"(at)
-      : "memory");
-}
-
-__device__ __forceinline__ void tmem_store16(uint32_t at, const uint32_t (&u)[16]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15};" ::"r"(u[0]), "r"(u[1]), "r"(u[2]), "r"(u[3]), "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7]), "r"(u[8]), "r"(u[9]), "r"(u[10]), "r"(u[11]), "r"(u[12]), "r"(u[13]), "r"(u[14]), "r"(u[15]), "r"(at)
-      : "memory");
-}
-
-__device__ __forceinline__ void tmem_store32(uint32_t at, const uint32_t (&u)[32]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31};" ::"r"(u[0]), "r"(u[1]), "r"(u[2]), "r"(u[3]), "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7]), "r"(u[8]), "r"(u[9]), "r"(u[10]), "r"(u[11]), "r"(u[12]), "r"(u[13]), "r"(u[14]), "r"(u[15]), "r"(u[16]), "r"(u[17]), "r"(u[18]), "r"(u[19]), "r"(u[20]), "r"(u[21]), "r"(u[22]), "r"(u[23]), "r"(u[24]), "r"(u[25]), "r"(u[26]), "r"(u[27]), "r"(u[28]), "r"(u[29]), "r"(u[30]), "r"(u[31]), "r"(at)
-      : "memory");
-}
-
-__device__ __forceinline__ void tmem_stored() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-
-// mbar_wait, in line: the roles' register shares leave no room for calls.
-__device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity, const volatile int* abort_flag) {
-  if (mbar_try_wait(bar, parity)) return true;
-  const uint64_t t0 = global_ns();
-  for (;;) {
-#pragma unroll 1
-    for (int i = 0; i < 32; ++i)
-      if (mbar_try_wait(bar, parity)) return true;
-    if ((abort_flag != nullptr && *abort_flag) || global_ns() - t0 > kWaitLimitNs) return false;
-  }
-}
-
-// One arrival a warp, for what all its lanes have done: 32 arrivals at one
-// barrier are taken one after the other.
-__device__ __forceinline__ void warp_arrive(uint32_t bar) {
-  __syncwarp();
-  if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
-}
-
-// Byte of 16-byte chunk `chunk` of row `row` in an operand tile of `rows` rows.
-__device__ __forceinline__ uint32_t chunk_at(int rows, int row, int chunk) {
-  return static_cast<uint32_t>((chunk >> 3) * rows * 128 + row * 128 + (((chunk & 7) ^ (row & 7)) << 4));
-}
-
-__device__ __forceinline__ uint32_t bf2_mul(uint32_t a, uint32_t b) {
-  uint32_t y;
-  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(y) : "r"(a), "r"(b));
-  return y;
-}
-__device__ __forceinline__ uint32_t bf2_mad(uint32_t a, uint32_t b, uint32_t c) {
-  uint32_t y;
-  asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(y) : "r"(a), "r"(b), "r"(c));
-  return y;
-}
 
 __device__ __forceinline__ uint32_t f16_mul(uint32_t a, uint32_t b) {
   uint32_t y;

@@ -14,11 +14,12 @@
 // of 128, 64 or 32 columns, four lanes together a group of a row - and the
 // x of the same columns, 16 bytes a word of codes.
 //
-// A CTA takes 16 MT output rows and all columns; its warps take blocks of 128
+// A CTA takes 16 output rows and all columns; its warps take blocks of 128
 // columns in turn, each with the next blocks' codes in flight, and add their
 // sums up in shared memory, in the warps' order. All codes of a small weight
 // are thus asked for at once, by as many SMs as there are.
-#include "common.cuh"
+#include "codes.cuh"
+#include "tensor_core.cuh"
 
 namespace ple {
 namespace {
@@ -38,13 +39,11 @@ struct ProjArgs {
 
 template <int NT>
 struct Proj {
-  static constexpr int kMT = NT >= 4 ? 2 : 1;      // tiles of 16 rows
   static constexpr int kWarps = 8;
-  static constexpr int kDepth = NT >= 4 ? 2 : 4;   // blocks of codes in flight
-  static constexpr int kRows = 16 * kMT;
+  static constexpr int kDepth = 4;                 // blocks of codes in flight
+  static constexpr int kRows = 16;
   static constexpr int kPitch = 8 * NT + 1;        // floats of a row's sums, padded
-  static constexpr int kJoin = NT == 8 ? kWarps / 2 : kWarps;  // warps whose sums are held at a time
-  static constexpr int kSmem = kJoin * kRows * kPitch * 4;
+  static constexpr int kSmem = kWarps * kRows * kPitch * 4;
 };
 
 __device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -57,10 +56,7 @@ __device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], 
 
 // Codes i and i + 4 of a word as (c - z) / 64, with z64 a pair of -z / 64.
 __device__ __forceinline__ uint32_t code_pair(uint32_t word, int i, uint32_t z64) {
-  const uint32_t c = (i < 2 ? word : word >> 8) & (i % 2 == 0 ? 0x000F000Fu : 0x00F000F0u);
-  uint32_t y;  // 2^127, or 2^123
-  asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(y) : "r"(c), "r"(i % 2 == 0 ? 0x7F007F00u : 0x7D007D00u), "r"(z64));
-  return y;
+  return bf2_mad(code_bits(word, i), i % 2 == 0 ? 0x7F007F00u /* 2^127 */ : 0x7D007D00u /* 2^123 */, z64);
 }
 
 // Column of a lane's word w in a block: four lanes share a group's columns.
@@ -96,10 +92,10 @@ __device__ __forceinline__ void load_codes(uint32_t (&w)[4], const uint8_t* row,
 }
 
 template <int kGroup, int NT>
-__global__ void __launch_bounds__(Proj<NT>::kWarps * 32, NT >= 4 ? 1 : 2)
+__global__ void __launch_bounds__(Proj<NT>::kWarps * 32, 2)
 proj_w4_kernel(const ProjArgs a) {
   using L = Proj<NT>;
-  constexpr int MT = L::kMT, kWarps = L::kWarps, kDepth = L::kDepth;
+  constexpr int kWarps = L::kWarps, kDepth = L::kDepth;
   constexpr int kGroups = kColumns / kGroup;  // of a block
   constexpr int kWords = kGroup / 32;
   extern __shared__ float join[];  // [warp][row][token]
@@ -112,31 +108,25 @@ proj_w4_kernel(const ProjArgs a) {
   const int tokens = static_cast<int>(min(a.T - t0, int64_t(8 * NT)));
   const int groups = a.E / kGroup;
   const int blocks = (a.E + kColumns - 1) / kColumns;
-  // this lane's rows: g and g + 8 of each tile; past the last: the last again
-  const uint8_t* codes[MT][2];
-  int64_t at_group[MT][2];
+  // this lane's rows: g and g + 8; past the last: the last again
+  const uint8_t* codes[2];
+  int64_t at_group[2];
 #pragma unroll
-  for (int m = 0; m < MT; ++m)
+  for (int h = 0; h < 2; ++h) {
+    const int64_t n = min(n0 + h * 8 + g, a.N - 1);
+    codes[h] = a.codes + n * (a.E / 2);
+    at_group[h] = n * groups;
+  }
+  float total[NT][4];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int64_t n = min(n0 + m * 16 + h * 8 + g, a.N - 1);
-      codes[m][h] = a.codes + n * (a.E / 2);
-      at_group[m][h] = n * groups;
-    }
-  float total[MT][NT][4];
+  for (int t = 0; t < NT; ++t)
 #pragma unroll
-  for (int m = 0; m < MT; ++m)
-#pragma unroll
-    for (int t = 0; t < NT; ++t)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) total[m][t][i] = 0.0f;
+    for (int i = 0; i < 4; ++i) total[t][i] = 0.0f;
 
-  uint32_t w[kDepth][MT][2][4];
-  auto load = [&](uint32_t (&to)[MT][2][4], int block) {
+  uint32_t w[kDepth][2][4];
+  auto load = [&](uint32_t (&to)[2][4], int block) {
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
-#pragma unroll
-      for (int h = 0; h < 2; ++h) load_codes<kGroup>(to[m][h], codes[m][h], block * kColumns, a.E, j);
+    for (int h = 0; h < 2; ++h) load_codes<kGroup>(to[h], codes[h], block * kColumns, a.E, j);
   };
 #pragma unroll
   for (int d = 0; d < kDepth; ++d)
@@ -151,96 +141,58 @@ proj_w4_kernel(const ProjArgs a) {
       for (int q = 0; q < kGroups; ++q) {
         const int group = block * kGroups + q;
         if (group >= groups) break;
-        float scale[MT][2];
-        uint32_t z64[MT][2];
+        float scale[2];
+        uint32_t z64[2];
 #pragma unroll
-        for (int m = 0; m < MT; ++m)
+        for (int h = 0; h < 2; ++h) {
+          scale[h] = 64.0f * bf_lo(__ldg(a.scales + at_group[h] + group));
+          const float z = a.zeros != nullptr ? static_cast<float>(__ldg(a.zeros + at_group[h] + group)) : 8.0f;
+          z64[h] = pack2(z * -0.015625f, z * -0.015625f);
+        }
+        float acc[NT][4];
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            scale[m][h] = 64.0f * bf_lo(__ldg(a.scales + at_group[m][h] + group));
-            const float z = a.zeros != nullptr ? static_cast<float>(__ldg(a.zeros + at_group[m][h] + group)) : 8.0f;
-            z64[m][h] = pack2(z * -0.015625f, z * -0.015625f);
-          }
-        float acc[MT][NT][4];
+        for (int t = 0; t < NT; ++t)
 #pragma unroll
-        for (int m = 0; m < MT; ++m)
-#pragma unroll
-          for (int t = 0; t < NT; ++t)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) acc[m][t][i] = 0.0f;
+          for (int i = 0; i < 4; ++i) acc[t][i] = 0.0f;
 #pragma unroll
         for (int v = 0; v < kWords; ++v) {
           const int i = q * kWords + v;
           const int e = block * kColumns + column_of<kGroup>(i, j);
-          uint32_t c[MT][2][4];  // [tile][k step][operand register]
+          uint32_t c[2][4];  // [k step][operand register]
 #pragma unroll
-          for (int m = 0; m < MT; ++m)
+          for (int k = 0; k < 2; ++k)
 #pragma unroll
-            for (int k = 0; k < 2; ++k)
-#pragma unroll
-              for (int r = 0; r < 4; ++r)
-                c[m][k][r] = code_pair(w[d][m][r & 1][i], 2 * k + (r >> 1), z64[m][r & 1]);
+            for (int r = 0; r < 4; ++r) c[k][r] = code_pair(w[d][r & 1][i], 2 * k + (r >> 1), z64[r & 1]);
 #pragma unroll
           for (int t = 0; t < NT; ++t) {
             uint4 x = make_uint4(0, 0, 0, 0);
             if (t * 8 + g < tokens) x = ldg16(a.x + (t0 + t * 8 + g) * a.x_stride + e);
-            const uint32_t x0 = __byte_perm(x.x, x.z, 0x5410), x1 = __byte_perm(x.x, x.z, 0x7632);
-            const uint32_t x2 = __byte_perm(x.y, x.w, 0x5410), x3 = __byte_perm(x.y, x.w, 0x7632);
-#pragma unroll
-            for (int m = 0; m < MT; ++m) {
-              mma_bf16(acc[m][t], c[m][0], x0, x1);
-              mma_bf16(acc[m][t], c[m][1], x2, x3);
-            }
+            mma_bf16(acc[t], c[0], __byte_perm(x.x, x.z, 0x5410), __byte_perm(x.x, x.z, 0x7632));
+            mma_bf16(acc[t], c[1], __byte_perm(x.y, x.w, 0x5410), __byte_perm(x.y, x.w, 0x7632));
           }
         }
 #pragma unroll
-        for (int m = 0; m < MT; ++m)
+        for (int t = 0; t < NT; ++t)
 #pragma unroll
-          for (int t = 0; t < NT; ++t)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) total[m][t][i] = fmaf(scale[m][i >> 1], acc[m][t][i], total[m][t][i]);
+          for (int i = 0; i < 4; ++i) total[t][i] = fmaf(scale[i >> 1], acc[t][i], total[t][i]);
       }
       if (block + kDepth * kWarps < blocks) load(w[d], block + kDepth * kWarps);
     }
   }
 
   // the warps' sums, in their order
-  auto place = [&](int slot, int m, int t, int i) -> float& {
-    return join[(slot * L::kRows + m * 16 + (i >> 1) * 8 + g) * L::kPitch + t * 8 + 2 * j + (i & 1)];
-  };
-  if constexpr (L::kJoin < kWarps) {  // the upper half of the warps hands over first
-    if (warp >= L::kJoin) {
 #pragma unroll
-      for (int m = 0; m < MT; ++m)
+  for (int t = 0; t < NT; ++t)
 #pragma unroll
-        for (int t = 0; t < NT; ++t)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) place(warp - L::kJoin, m, t, i) = total[m][t][i];
-    }
-    __syncthreads();
-    if (warp < L::kJoin) {
-#pragma unroll
-      for (int m = 0; m < MT; ++m)
-#pragma unroll
-        for (int t = 0; t < NT; ++t)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) place(warp, m, t, i) = total[m][t][i] + place(warp, m, t, i);
-    }
-  } else {
-#pragma unroll
-    for (int m = 0; m < MT; ++m)
-#pragma unroll
-      for (int t = 0; t < NT; ++t)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) place(warp, m, t, i) = total[m][t][i];
-  }
+    for (int i = 0; i < 4; ++i)
+      join[(warp * L::kRows + (i >> 1) * 8 + g) * L::kPitch + t * 8 + 2 * j + (i & 1)] = total[t][i];
   __syncthreads();
   for (int i = threadIdx.x; i < L::kRows * tokens; i += kWarps * 32) {
     const int row = i % L::kRows, t = i / L::kRows;
     if (n0 + row >= a.N) continue;
     float sum = 0.0f;
 #pragma unroll
-    for (int k = 0; k < L::kJoin; ++k) sum += join[(k * L::kRows + row) * L::kPitch + t];
+    for (int k = 0; k < kWarps; ++k) sum += join[(k * L::kRows + row) * L::kPitch + t];
     a.out[(t0 + t) * a.N + n0 + row] = static_cast<ple_bf16_t>(pack2(sum, 0.0f) & 0xffffu);
   }
 }
@@ -255,12 +207,377 @@ cudaError_t launch(const ProjArgs& a, cudaStream_t stream) {
   return launch_kernel(kernel, grid, dim3(L::kWarps * 32), L::kSmem, stream, 1, a);
 }
 
-// As many tiles of 8 tokens as the step has, up to 8: the codes are read once
-// for each 64 tokens.
+// ---------------------------------------------------------------------------
+// 17 to 64 tokens at a time: the 5th-generation tensor cores
+// ---------------------------------------------------------------------------
+// With this many tokens the warp-wide instructions would be the bound (a
+// quarter of the rate, and every warp reading every x). A CTA takes 128 rows
+// of W as the first operand, (c - z) / 64 in bf16 (exact), against the tokens,
+// 128 columns to a stage. W goes through registers into tensor memory and x
+// as it is into shared memory: with both laid out in shared memory its
+// bandwidth was the bound (16384 x 4096, 64 tokens: 32 us).
+// The sums of each group of columns get tensor-memory columns of their own,
+// four sets in turn, and eight warps take them out, a row a thread, and add
+// them up times the group's scale in float32.
+// Where the rows alone would leave SMs without work, a cluster of CTAs shares
+// a row tile: each takes part of the columns, and their sums meet through
+// distributed shared memory, in the order of the CTAs.
+//
+// Warps: 0-15 lay out, 16 issues the products, 17-19 fetch scales and zero
+// points, 20-27 take the sums, half of the tokens each four.
+constexpr int kWideRows = 128;
+constexpr int kLayWarps = 16, kSumWarps = 8;
+constexpr int kWideThreads = (kLayWarps + 4 + kSumWarps) * 32;
+constexpr int kSets = 4;  // of sums in tensor memory
+constexpr int kParamSets = 4, kParamGroups = 4;  // groups' scales and zero points, a few groups at a time
+
+template <int kTokens>
+struct Wide {
+  static constexpr int kX = kTokens * kColumns * 2;  // bytes of a stage's tokens
+  static constexpr int kStages = 4;                  // of weights in tensor memory
+  static constexpr int kXStages = 12;                // of tokens in shared memory
+  static constexpr int kAhead = kXStages - kStages;  // as many stages ahead tokens are asked for
+  static constexpr int kTmemW = kSets * kTokens;     // weights stand behind the sums
+  static constexpr int kTmem = 512;                  // columns
+  static constexpr int kAtParams = kXStages * kX;
+  static constexpr int kAtBars = kAtParams + kParamSets * kParamGroups * kWideRows * 4;
+  static constexpr int kAtWords = kAtBars + (2 * kStages + 2 * kSets + 2 * kParamSets + 1) * 8;
+  static constexpr int kSmem = kAtWords + 16 + 1024;   // and alignment
+  static_assert(kTmemW + kStages * kColumns / 2 <= kTmem, "tensor memory");
+  static_assert(kTokens * kWideRows * 4 <= kXStages * kX, "the sums of a tile fit where the tokens were");
+};
+
+__device__ __forceinline__ void cluster_barrier() {
+  __syncwarp();
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// 16 bytes to shared memory, or as many zeros.
+__device__ __forceinline__ void copy16(uint32_t to, const void* from, bool there) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(there ? 16 : 0)
+               : "memory");
+}
+
+__device__ __forceinline__ float read_cluster(uint32_t at, uint32_t rank) {
+  uint32_t there;
+  float v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(there) : "r"(at), "r"(rank));
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(there) : "memory");
+  return v;
+}
+
+template <int kGroup, int kTokens>
+__global__ void __launch_bounds__(kWideThreads, 1)
+proj_w4_wide_kernel(const ProjArgs a, int parts, int32_t* dev_err) {
+  using L = Wide<kTokens>;
+  constexpr int kGroups = kColumns / kGroup;            // of a stage
+  constexpr int kParamStages = kParamGroups / kGroups;  // of a set of scales and zero points
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* const smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t base = smem_u32(smem), bar0 = base + L::kAtBars;
+  auto full = [&](int s) { return bar0 + 8u * s; };
+  auto free = [&](int s) { return bar0 + 8u * (L::kStages + s); };
+  auto sums_full = [&](int s) { return bar0 + 8u * (2 * L::kStages + s); };
+  auto sums_free = [&](int s) { return bar0 + 8u * (2 * L::kStages + kSets + s); };
+  auto params_full = [&](int s) { return bar0 + 8u * (2 * L::kStages + 2 * kSets + s); };
+  auto params_free = [&](int s) { return bar0 + 8u * (2 * L::kStages + 2 * kSets + kParamSets + s); };
+  const uint32_t done = bar0 + 8u * (2 * L::kStages + 2 * kSets + 2 * kParamSets);
+  uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kAtWords);
+  volatile int* const abort_flag = reinterpret_cast<volatile int*>(smem + L::kAtWords + 4);
+  const int warp = threadIdx.x / 32;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < L::kStages; ++s) {
+      mbar_init(full(s), kLayWarps / 2);
+      mbar_init(free(s), 1);
+    }
+    for (int s = 0; s < kSets; ++s) {
+      mbar_init(sums_full(s), 1);
+      mbar_init(sums_free(s), kSumWarps);
+    }
+    for (int s = 0; s < kParamSets; ++s) {
+      mbar_init(params_full(s), 1);
+      mbar_init(params_free(s), (kParamStages == 1 ? kLayWarps / 2 : kLayWarps) + kSumWarps);
+    }
+    mbar_init(done, 1);
+    mbar_fence_init();
+    *abort_flag = 0;
+  }
+  if (warp == kLayWarps) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)), "n"(L::kTmem) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  fence_before();
+  __syncthreads();
+  fence_after();
+  pdl_wait();
+  pdl_trigger();
+  const uint32_t tmem = *tmem_slot;
+  const int part = blockIdx.x % parts;
+  const int n0 = blockIdx.x / parts * kWideRows;
+  const int64_t t0 = int64_t(blockIdx.y) * kTokens;
+  const int tokens = static_cast<int>(min(a.T - t0, int64_t(kTokens)));
+  const int groups = a.E / kGroup;
+  // this part's stages of columns, cut between sets of scales
+  const int stages = (a.E + kColumns - 1) / kColumns, cuts = (stages + kParamStages - 1) / kParamStages;
+  const int first = static_cast<int>(int64_t(part) * cuts / parts) * kParamStages;
+  const int last = min(static_cast<int>(int64_t(part + 1) * cuts / parts) * kParamStages, stages);
+  auto gave_up = [&](bool ok) {
+    if (!ok) {
+      *abort_flag = 1;
+      set_dev_err(dev_err, PLE_DEVERR_TIMEOUT);
+    }
+    return !ok;
+  };
+  uint32_t* const params = reinterpret_cast<uint32_t*>(smem + L::kAtParams);  // [set][group][row]: scale, -z / 64
+  float* const mine = reinterpret_cast<float*>(smem);  // a part's sums, [token][row]: where the operands were
+
+  if (warp < kLayWarps) {
+    // ---------------- operands ----------------
+    // Two teams of eight warps, every other stage each. W: half of a row's
+    // columns a thread, through registers into tensor memory. x: a chunk of 8
+    // columns of every 16th token, copied to where the products read it.
+    // Nothing is read past a row's end, nor of tokens that are not there:
+    // zeros stand for both.
+    const int team = warp / 8, row = threadIdx.x % kWideRows, half = threadIdx.x / kWideRows % 2;
+    const uint8_t* const codes = a.codes + min(n0 + row, a.N - 1) * int64_t(a.E / 2) + half * 32;
+    const uint32_t to_w = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + L::kTmemW + half * 32;
+    const int chunk = threadIdx.x % 16, token0 = threadIdx.x / 16 % 16;
+    const ple_bf16_t* const x = a.x + (t0 + token0) * a.x_stride + chunk * 8;
+    auto fetch_w = [&](uint4 (&w)[2], int stage) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        w[i] = make_uint4(0, 0, 0, 0);
+        if (stage < last && stage * kColumns + half * 64 + i * 32 < a.E)
+          w[i] = __ldg(reinterpret_cast<const uint4*>(codes + int64_t(stage) * (kColumns / 2)) + i);
+      }
+    };
+    auto fetch_x = [&](int stage) {
+      if (stage < last) {
+        const uint32_t to = base + (stage - first) % L::kXStages * L::kX + chunk_at(kTokens, token0, chunk);
+        const ple_bf16_t* from = x + int64_t(stage) * kColumns;
+        const bool in_row = stage * kColumns + chunk * 8 < a.E;
+#pragma unroll
+        for (int i = 0; i < kTokens / 16; ++i) {
+          const bool there = token0 + 16 * i < tokens && in_row;
+          copy16(to + i * 16 * 128, there ? from : a.x, there);
+          from += 16 * a.x_stride;
+        }
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    uint4 w[2][2];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) fetch_w(w[u], first + team + 2 * u);
+    for (int k = first + team; k < first + L::kAhead; k += 2) fetch_x(k);
+    bool ok = true;
+#pragma unroll 1
+    for (int k0 = first + team, round = 0; ok && k0 < last; k0 += L::kStages, ++round) {
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int k = k0 + 2 * u, s = team + 2 * u;
+        if (k >= last) break;
+        const int rel = (k - first) * kGroups, chunk_no = rel / kParamGroups;
+        ok = wait_for(params_full(chunk_no % kParamSets), chunk_no / kParamSets & 1, abort_flag);
+        // the products of kStages ago: their weights' place, and the tokens' that are asked for next
+        ok = __all_sync(0xffffffffu, ok && wait_for(free(s), (round & 1) ^ 1u, abort_flag));
+        if (!ok) break;
+        fetch_x(k + L::kAhead);
+        fence_after();
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int group = (rel + (half * 64 + i * 32) / kGroup) % (kParamSets * kParamGroups);
+          const uint32_t z64 = __byte_perm(params[group * kWideRows + row], 0, 0x1010);
+          const uint32_t words[4] = {w[u][i].x, w[u][i].y, w[u][i].z, w[u][i].w};
+          uint32_t v[16];
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            uint32_t pair[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) pair[j] = code_pair(words[q], j, z64);
+            v[4 * q] = __byte_perm(pair[0], pair[1], 0x5410);
+            v[4 * q + 1] = __byte_perm(pair[2], pair[3], 0x5410);
+            v[4 * q + 2] = __byte_perm(pair[0], pair[1], 0x7632);
+            v[4 * q + 3] = __byte_perm(pair[2], pair[3], 0x7632);
+          }
+          tmem_store16(to_w + s * (kColumns / 2) + i * 16, v);
+        }
+        fetch_w(w[u], k + L::kStages);
+        asm volatile("cp.async.wait_group %0;" ::"n"(L::kAhead / 2) : "memory");
+        tmem_stored();
+        fence_before();
+        fence_operands();
+        warp_arrive(full(s));
+        // the last of a team's stages with these scales and zero points
+        if (kParamStages == 1 || (k - first) % kParamStages >= kParamStages - 2) warp_arrive(params_free(chunk_no % kParamSets));
+      }
+    }
+    gave_up(ok);
+    asm volatile("cp.async.wait_all;" ::: "memory");
+  } else if (warp == kLayWarps) {
+    // ---------------- products ----------------
+    const uint32_t acc = __shfl_sync(0xffffffffu, tmem, 0);
+    const uint32_t x_op = operand(base);
+    int set = 0;
+    uint32_t set_parity = 1;
+    bool ok = true;
+#pragma unroll 1
+    for (int k = first; ok && k < last; ++k) {
+      const int s = (k - first) % L::kStages, round = (k - first) / L::kStages;
+      ok = __all_sync(0xffffffffu, wait_for(full(s), round & 1, abort_flag));
+      if (!ok) break;
+#pragma unroll
+      for (int g = 0; g < kGroups; ++g) {
+        if (k * kGroups + g >= groups) break;
+        ok = __all_sync(0xffffffffu, wait_for(sums_free(set), set_parity, abort_flag));
+        if (!ok) break;
+        fence_after();
+        if (elected()) {
+          const uint32_t d = acc + set * kTokens, w = acc + L::kTmemW + s * (kColumns / 2), xm = x_op + (k - first) % L::kXStages * (L::kX >> 4);
+#pragma unroll
+          for (int i = 0; i < kGroup / 16; ++i) {
+            const int step = g * (kGroup / 16) + i;
+            mma_tmem(d, w + 8 * step, xm + (((step / 4) * kTokens * 128 + (step % 4) * 32) >> 4), idesc(kTokens, 1), i > 0);
+          }
+          mma_commit(sums_full(set));
+        }
+        __syncwarp();
+        if (++set == kSets) { set = 0; set_parity ^= 1u; }
+      }
+      if (!ok) break;
+      if (elected()) mma_commit(free(s));
+      __syncwarp();
+    }
+    // however the loop ended, no product reads or writes after this
+    if (elected()) mma_commit(done);
+    __syncwarp();
+    ok = wait_for(done, 0, nullptr) && ok;
+    gave_up(ok);
+  } else if (warp < kLayWarps + 4) {
+    // ---------------- scales and zero points ----------------
+    // A few bytes of every row: three warps take turns at fetching them
+    // ahead, four groups of a row in one piece where that is aligned.
+    const int chunks = ((last - first) * kGroups + kParamGroups - 1) / kParamGroups;
+    const bool whole = groups % kParamGroups == 0 && (reinterpret_cast<uintptr_t>(a.scales) & 7) == 0 &&
+                       (reinterpret_cast<uintptr_t>(a.zeros) & 3) == 0;
+#pragma unroll 1
+    for (int c = warp - (kLayWarps + 1); c < chunks; c += 3) {
+      const int group0 = first * kGroups + c * kParamGroups;  // a multiple of kParamGroups
+      uint2 scales[kWideRows / 32];
+      uint32_t zeros[kWideRows / 32];
+#pragma unroll
+      for (int i = 0; i < kWideRows / 32; ++i) {
+        const int64_t at = min(int64_t(n0) + i * 32 + (threadIdx.x & 31), int64_t(a.N - 1)) * groups;
+        zeros[i] = 0x08080808u;
+        if (whole) {
+          scales[i] = __ldg(reinterpret_cast<const uint2*>(a.scales + at + group0));
+          if (a.zeros != nullptr) zeros[i] = __ldg(reinterpret_cast<const uint32_t*>(a.zeros + at + group0));
+        } else {
+          uint32_t v[kParamGroups], z[kParamGroups];
+#pragma unroll
+          for (int g = 0; g < kParamGroups; ++g) {
+            const int64_t from = at + min(group0 + g, groups - 1);
+            v[g] = __ldg(a.scales + from);
+            z[g] = a.zeros != nullptr ? __ldg(a.zeros + from) : 8;
+          }
+          scales[i] = make_uint2(v[0] | v[1] << 16, v[2] | v[3] << 16);
+          zeros[i] = z[0] | z[1] << 8 | z[2] << 16 | z[3] << 24;
+        }
+      }
+      if (gave_up(__all_sync(0xffffffffu, wait_for(params_free(c % kParamSets), c / kParamSets & 1 ^ 1, abort_flag)))) break;
+#pragma unroll
+      for (int i = 0; i < kWideRows / 32; ++i)
+#pragma unroll
+        for (int g = 0; g < kParamGroups; ++g) {
+          const uint32_t two = g < 2 ? scales[i].x : scales[i].y;
+          params[(c % kParamSets * kParamGroups + g) * kWideRows + i * 32 + (threadIdx.x & 31)] =
+              (g % 2 == 0 ? two << 16 : two & 0xffff0000u) | pack2(static_cast<float>(zeros[i] >> (8 * g) & 0xff) * -0.015625f, 0.0f);
+        }
+      warp_arrive(params_full(c % kParamSets));
+    }
+  } else {
+    // ---------------- sums: a row and half of the tokens a thread ----------------
+    constexpr int kMine = kTokens / 2;
+    const int t_first = (warp - kLayWarps - 4) / 4 * kMine;
+    const int row = threadIdx.x % kWideRows;
+    const int64_t n = min(n0 + row, a.N - 1);
+    const int g0 = first * kGroups, g1 = min(last * kGroups, groups);
+    const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    float total[kMine];
+#pragma unroll
+    for (int t = 0; t < kMine; ++t) total[t] = 0.0f;
+#pragma unroll 1
+    for (int g = g0; g < g1; ++g) {
+      const int set = (g - g0) % kSets, round = (g - g0) / kSets;
+      const int chunk_no = (g - g0) / kParamGroups;
+      if ((g - g0) % kParamGroups == 0 &&
+          gave_up(__all_sync(0xffffffffu, wait_for(params_full(chunk_no % kParamSets), chunk_no / kParamSets & 1, abort_flag)))) break;
+      const float scale = 64.0f * bf_hi(params[(g - g0) % (kParamSets * kParamGroups) * kWideRows + row]);
+      if (gave_up(__all_sync(0xffffffffu, wait_for(sums_full(set), round & 1, abort_flag)))) break;
+      fence_after();
+#pragma unroll
+      for (int q = 0; q < kMine / 16; ++q) {
+        float v[16];
+        tmem_load16(tmem + lanes + set * kTokens + t_first + 16 * q, v);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) total[16 * q + i] = fmaf(scale, v[i], total[16 * q + i]);
+      }
+      fence_before();
+      warp_arrive(sums_free(set));
+      if ((g - g0 + 1) % kParamGroups == 0) warp_arrive(params_free(chunk_no % kParamSets));
+    }
+    // all products are done, so their operands may be written over
+    if (parts > 1) {
+#pragma unroll
+      for (int t = 0; t < kMine; ++t) mine[(t_first + t) * kWideRows + row] = total[t];
+    } else if (n0 + row < a.N) {
+#pragma unroll
+      for (int t = 0; t < kMine; ++t)
+        if (t_first + t < tokens) a.out[(t0 + t_first + t) * a.N + n] = static_cast<ple_bf16_t>(pack2(total[t], 0.0f) & 0xffffu);
+    }
+  }
+  fence_before();
+  __syncthreads();
+  if (warp == kLayWarps) {
+    fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(L::kTmem) : "memory");
+  }
+  if (parts == 1) return;
+  // the parts' sums, in their order, tokens shared out
+  cluster_barrier();
+  const int n = n0 + threadIdx.x % kWideRows;
+  if (n < a.N) {
+    for (int t = part + threadIdx.x / kWideRows * parts; t < tokens; t += kWideThreads / kWideRows * parts) {
+      const uint32_t at = base + (t * kWideRows + threadIdx.x % kWideRows) * 4;
+      float sum = 0.0f;
+      for (int r = 0; r < parts; ++r) sum += read_cluster(at, r);
+      a.out[(t0 + t) * a.N + n] = static_cast<ple_bf16_t>(pack2(sum, 0.0f) & 0xffffu);
+    }
+  }
+  cluster_barrier();  // no CTA leaves while its sums are read
+}
+
+template <int kGroup, int kTokens>
+cudaError_t launch_wide(const ProjArgs& a, int32_t* dev_err, cudaStream_t stream) {
+  using L = Wide<kTokens>;
+  const auto kernel = proj_w4_wide_kernel<kGroup, kTokens>;
+  const cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kSmem);
+  if (err != cudaSuccess) return err;
+  const int tiles = (a.N + kWideRows - 1) / kWideRows, stages = (a.E + kColumns - 1) / kColumns;
+  const int blocks = static_cast<int>((a.T + kTokens - 1) / kTokens);
+  // parts of the columns, as long as all CTAs are on SMs at once and have some stages each
+  int parts = 1;
+  while (parts < 8 && int64_t(tiles) * blocks * parts * 2 <= num_sms() && stages >= parts * 2 * kParamGroups) parts *= 2;
+  const dim3 grid(static_cast<unsigned>(tiles * parts), static_cast<unsigned>(blocks));
+  return launch_kernel(kernel, grid, dim3(kWideThreads), L::kSmem, stream, static_cast<unsigned>(parts), a, parts, dev_err);
+}
+
+// Up to 16 tokens, in tiles of 8, on warp-wide instructions; more on the
+// tensor cores, 32 or 64 to a pass over the codes.
 template <int kGroup>
-cudaError_t launch_tiles(const ProjArgs& a, cudaStream_t stream) {
+cudaError_t launch_tiles(const ProjArgs& a, int32_t* dev_err, cudaStream_t stream) {
   return a.T <= 8 ? launch<kGroup, 1>(a, stream) : a.T <= 16 ? launch<kGroup, 2>(a, stream)
-       : a.T <= 32 ? launch<kGroup, 4>(a, stream) : launch<kGroup, 8>(a, stream);
+       : a.T <= 32 ? launch_wide<kGroup, 32>(a, dev_err, stream) : launch_wide<kGroup, 64>(a, dev_err, stream);
 }
 
 }  // namespace
@@ -273,7 +590,6 @@ PLE_EXPORT ple_status ple_proj_w4(const ple_bf16_t* x, int64_t x_stride, int64_t
                                   const ple_bf16_t* scales, const uint8_t* zeros, int32_t group,
                                   ple_bf16_t* out, int32_t* dev_err, cudaStream_t stream) {
   const char* name = "ple_proj_w4";
-  (void)dev_err;
   if (num_tokens < 0 || num_tokens > INT32_MAX || in_dim < 1 || out_dim < 1)
     return fail(PLE_ERR_INVALID_ARG, "%s: num_tokens %lld, in_dim %d, out_dim %d", name,
                 static_cast<long long>(num_tokens), in_dim, out_dim);
@@ -289,6 +605,6 @@ PLE_EXPORT ple_status ple_proj_w4(const ple_bf16_t* x, int64_t x_stride, int64_t
   if (!aligned16(x) || !aligned16(codes) || x_stride % 8 != 0)
     return fail(PLE_ERR_INVALID_ARG, "%s: x and codes must be 16-byte aligned, x_stride a multiple of 8", name);
   const ProjArgs a{x, x_stride, num_tokens, in_dim, out_dim, codes, scales, zeros, out};
-  return check_cuda(group == 128 ? launch_tiles<128>(a, stream) : group == 64 ? launch_tiles<64>(a, stream)
-                                                                             : launch_tiles<32>(a, stream), name);
+  return check_cuda(group == 128 ? launch_tiles<128>(a, dev_err, stream) : group == 64 ? launch_tiles<64>(a, dev_err, stream)
+                                                                             : launch_tiles<32>(a, dev_err, stream), name);
 }

@@ -208,14 +208,16 @@ cudaError_t launch(const ProjArgs& a, cudaStream_t stream) {
 }
 
 // ---------------------------------------------------------------------------
-// 17 to 64 tokens at a time: the 5th-generation tensor cores
+// Up to 64 tokens at a time: the 5th-generation tensor cores
 // ---------------------------------------------------------------------------
 // With this many tokens the warp-wide instructions would be the bound (a
 // quarter of the rate, and every warp reading every x). A CTA takes 128 rows
 // of W as the first operand, (c - z) / 64 in bf16 (exact), against the tokens,
 // 128 columns to a stage. W goes through registers into tensor memory and x
 // as it is into shared memory: with both laid out in shared memory its
-// bandwidth was the bound (16384 x 4096, 64 tokens: 32 us).
+// bandwidth was the bound (4096 x 16384, 64 tokens: 32 us). Now 24 us, 1.5
+// TB/s; what bounds it is the unpacking, 13 instructions for 8 weights in
+// every stage's chain of waiting, unpacking, storing and handing over.
 // The sums of each group of columns get tensor-memory columns of their own,
 // four sets in turn, and eight warps take them out, a row a thread, and add
 // them up times the group's scale in float32.
@@ -228,6 +230,7 @@ cudaError_t launch(const ProjArgs& a, cudaStream_t stream) {
 constexpr int kWideRows = 128;
 constexpr int kLayWarps = 16, kSumWarps = 8;
 constexpr int kWideThreads = (kLayWarps + 4 + kSumWarps) * 32;
+constexpr int kMaxParts = 4;
 constexpr int kSets = 4;  // of sums in tensor memory
 constexpr int kParamSets = 4, kParamGroups = 4;  // groups' scales and zero points, a few groups at a time
 
@@ -258,11 +261,12 @@ __device__ __forceinline__ void copy16(uint32_t to, const void* from, bool there
                : "memory");
 }
 
-__device__ __forceinline__ float read_cluster(uint32_t at, uint32_t rank) {
+__device__ __forceinline__ float4 read_cluster(uint32_t at, uint32_t rank) {
   uint32_t there;
-  float v;
+  float4 v;
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(there) : "r"(at), "r"(rank));
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(there) : "memory");
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(there) : "memory");
   return v;
 }
 
@@ -318,10 +322,11 @@ proj_w4_wide_kernel(const ProjArgs a, int parts, int32_t* dev_err) {
   const int64_t t0 = int64_t(blockIdx.y) * kTokens;
   const int tokens = static_cast<int>(min(a.T - t0, int64_t(kTokens)));
   const int groups = a.E / kGroup;
-  // this part's stages of columns, cut between sets of scales
-  const int stages = (a.E + kColumns - 1) / kColumns, cuts = (stages + kParamStages - 1) / kParamStages;
-  const int first = static_cast<int>(int64_t(part) * cuts / parts) * kParamStages;
-  const int last = min(static_cast<int>(int64_t(part + 1) * cuts / parts) * kParamStages, stages);
+  // this part's stages of columns, cut between sets of scales where there are enough
+  const int stages = (a.E + kColumns - 1) / kColumns, unit = stages >= parts * kParamStages ? kParamStages : 1;
+  const int cuts = (stages + unit - 1) / unit;
+  const int first = static_cast<int>(int64_t(part) * cuts / parts) * unit;
+  const int last = min(static_cast<int>(int64_t(part + 1) * cuts / parts) * unit, stages);
   auto gave_up = [&](bool ok) {
     if (!ok) {
       *abort_flag = 1;
@@ -458,11 +463,11 @@ proj_w4_wide_kernel(const ProjArgs a, int parts, int32_t* dev_err) {
     // A few bytes of every row: three warps take turns at fetching them
     // ahead, four groups of a row in one piece where that is aligned.
     const int chunks = ((last - first) * kGroups + kParamGroups - 1) / kParamGroups;
-    const bool whole = groups % kParamGroups == 0 && (reinterpret_cast<uintptr_t>(a.scales) & 7) == 0 &&
+    const bool whole = groups % kParamGroups == 0 && first * kGroups % kParamGroups == 0 && (reinterpret_cast<uintptr_t>(a.scales) & 7) == 0 &&
                        (reinterpret_cast<uintptr_t>(a.zeros) & 3) == 0;
 #pragma unroll 1
     for (int c = warp - (kLayWarps + 1); c < chunks; c += 3) {
-      const int group0 = first * kGroups + c * kParamGroups;  // a multiple of kParamGroups
+      const int group0 = first * kGroups + c * kParamGroups;
       uint2 scales[kWideRows / 32];
       uint32_t zeros[kWideRows / 32];
 #pragma unroll
@@ -545,14 +550,21 @@ proj_w4_wide_kernel(const ProjArgs a, int parts, int32_t* dev_err) {
   if (parts == 1) return;
   // the parts' sums, in their order, tokens shared out
   cluster_barrier();
-  const int n = n0 + threadIdx.x % kWideRows;
-  if (n < a.N) {
-    for (int t = part + threadIdx.x / kWideRows * parts; t < tokens; t += kWideThreads / kWideRows * parts) {
-      const uint32_t at = base + (t * kWideRows + threadIdx.x % kWideRows) * 4;
-      float sum = 0.0f;
-      for (int r = 0; r < parts; ++r) sum += read_cluster(at, r);
-      a.out[(t0 + t) * a.N + n] = static_cast<ple_bf16_t>(pack2(sum, 0.0f) & 0xffffu);
-    }
+  for (int i = threadIdx.x; part + i / (kWideRows / 4) * parts < tokens; i += kWideThreads) {
+    const int t = part + i / (kWideRows / 4) * parts, row = i % (kWideRows / 4) * 4;
+    float4 v[kMaxParts];
+#pragma unroll
+    for (int r = 0; r < kMaxParts; ++r)
+      if (r < parts) v[r] = read_cluster(base + (t * kWideRows + row) * 4, r);
+    float sum[4] = {};
+#pragma unroll
+    for (int r = 0; r < kMaxParts; ++r)
+      if (r < parts) {
+        sum[0] += v[r].x; sum[1] += v[r].y; sum[2] += v[r].z; sum[3] += v[r].w;
+      }
+#pragma unroll
+    for (int m = 0; m < 4; ++m)
+      if (n0 + row + m < a.N) a.out[(t0 + t) * a.N + n0 + row + m] = static_cast<ple_bf16_t>(pack2(sum[m], 0.0f) & 0xffffu);
   }
   cluster_barrier();  // no CTA leaves while its sums are read
 }
@@ -567,17 +579,29 @@ cudaError_t launch_wide(const ProjArgs& a, int32_t* dev_err, cudaStream_t stream
   const int blocks = static_cast<int>((a.T + kTokens - 1) / kTokens);
   // parts of the columns, as long as all CTAs are on SMs at once and have some stages each
   int parts = 1;
-  while (parts < 8 && int64_t(tiles) * blocks * parts * 2 <= num_sms() && stages >= parts * 2 * kParamGroups) parts *= 2;
+  while (parts < kMaxParts && int64_t(tiles) * blocks * parts * 2 <= num_sms() && stages >= parts * 2 * 2) parts *= 2;
   const dim3 grid(static_cast<unsigned>(tiles * parts), static_cast<unsigned>(blocks));
   return launch_kernel(kernel, grid, dim3(kWideThreads), L::kSmem, stream, static_cast<unsigned>(parts), a, parts, dev_err);
 }
 
-// Up to 16 tokens, in tiles of 8, on warp-wide instructions; more on the
-// tensor cores, 32 or 64 to a pass over the codes.
+// Warp-wide instructions or the tensor cores of the 5th generation. The former
+// are slower per token, the latter cost 6 us before the first sum is out (both
+// operands laid out, tensor memory, the parts' sums). What decides is how many
+// tokens there are and how often the first kernel's CTAs, 16 rows each, two an
+// SM, fill the GPU. Measured, warp-wide / tensor cores, us, tokens over
+// columns x rows:
+//   16   4096 x 4096  7.0 / 11.6   8192 x 8192  25.1 / 26.6   4096 x 16384  25.9 / 20.5
+//   24   2048 x 2048  4.3 /  8.4   4096 x 4096   9.2 / 11.5   4096 x  6144  16.9 / 16.3
+//   64   2048 x 2048  8.7 /  9.6   4096 x 4096  20.4 / 12.9
+// Hence up to 8 tokens always the first, up to 16 if its CTAs fill the GPU
+// three times at most, up to 32 once at most, and more never.
 template <int kGroup>
 cudaError_t launch_tiles(const ProjArgs& a, int32_t* dev_err, cudaStream_t stream) {
-  return a.T <= 8 ? launch<kGroup, 1>(a, stream) : a.T <= 16 ? launch<kGroup, 2>(a, stream)
-       : a.T <= 32 ? launch_wide<kGroup, 32>(a, dev_err, stream) : launch_wide<kGroup, 64>(a, dev_err, stream);
+  const int fills = (a.N - 1) / (Proj<1>::kRows * 2 * num_sms());  // beyond the first
+  if (a.T <= 8) return launch<kGroup, 1>(a, stream);
+  if (a.T <= 16 && fills < 3) return launch<kGroup, 2>(a, stream);
+  if (a.T <= 32) return fills < 1 ? launch<kGroup, 4>(a, stream) : launch_wide<kGroup, 32>(a, dev_err, stream);
+  return launch_wide<kGroup, 64>(a, dev_err, stream);
 }
 
 }  // namespace

@@ -51,6 +51,17 @@ def test_against_float64(T, E, group, with_zeros):
     check(project(x.cuda(), codes, scales, zeros), x, codes, scales, zeros, group)
 
 
+# many rows: every way the columns are shared out between CTAs, and none
+@pytest.mark.parametrize("T,N,E,group", [(16, 14601, 160, 32), (17, 5000, 96, 32), (24, 4870, 2176, 128), (32, 9001, 1088, 64),
+                                         (33, 700, 4096, 128), (64, 2500, 832, 64), (48, 9999, 640, 128), (64, 20001, 352, 32),
+                                         (129, 6000, 1152, 128)])
+@pytest.mark.parametrize("with_zeros", [False, True])
+def test_many_rows(T, N, E, group, with_zeros):
+    codes, scales, zeros = weight(N, E, group, with_zeros, seed=N + E)
+    x = torch.randn(T, E, generator=torch.Generator().manual_seed(T)).to(torch.bfloat16)
+    check(project(x.cuda(), codes, scales, zeros), x, codes, scales, zeros, group)
+
+
 @pytest.mark.parametrize("N", [1, 2, 15, 16, 17, 4099])
 def test_output_sizes(N):
     codes, scales, zeros = weight(N, 512, 128, True, seed=N)

@@ -4,7 +4,8 @@ The compute path is libple.so (hand-written CUDA for sm_103a, C ABI in
 include/ple.h); this package holds its build script, a ctypes binding with
 the C names, the PLELayer convenience wrapper (and PLEHostPipeline, which
 runs it over pinned host buffers with transfers overlapping compute; PLEChain,
-several layers with the next layers' lookups prefetched), the sharded lookups
+several layers with the next layers' lookups prefetched), PLEAttention (the
+attention block between two layers, its cache and weights in 4 bits), the sharded lookups
 over a group of ranks (HeadShardedLookup, RowShardedLookup) and the seeded
 synthetic workloads used by the tests and the benchmark.
 """
@@ -39,5 +40,6 @@ from ._lib import (  # noqa: F401
     PLE_SHARD_HEADS,
     PLE_SHARD_ROWS,
 )
+from .attention import PLEAttention, pack_w4  # noqa: F401
 from .layer import PLELayer, PLEHostPipeline, PLEChain  # noqa: F401
 from .sharded import HeadShardedLookup, RowShardedLookup  # noqa: F401

@@ -7,17 +7,23 @@
 // long requests come first, so that the last CTAs are short ones.
 //
 // Mathematics. For each tile of positions, S = Q K^T (f16 operands, f32 in
-// tensor memory), P = exp2(f S - m) rounded to bf16 over S in tensor memory,
-// O += P V (bf16 operands, f32 in tensor memory). m need not be the largest
+// tensor memory), P = exp2(f S - m) rounded to f16 over S in tensor memory,
+// O += P V (f16 operands, f32 in tensor memory). m need not be the largest
 // score for that, only near it: weights and sums are floating point. So a
 // tile's weights are taken with the m there is while its maximum is being
-// found, and m is raised (and O scaled) between tiles, when a score passed it
-// by 2^8. Only a score 2^64 above m - a row's first, mostly - raises it at once.
+// found, and m is raised (and O scaled) between tiles, when a weight passed
+// 2^11. Only a weight above 2^15, which f16 could not hold - a row's first,
+// mostly - raises it at once. A raise leaves the largest weight at 2^4, so that
+// what f16 cannot tell from nothing, 2^-25, is 2^-29 of it.
 // Roundings: a key enters as f16(code * scale + offset), because a score of
 // hundreds must not move by a bf16's 2^-8 of it; rows of Q are scaled to
 // [1, 2) by a power of two (in the row's f), and a key row outside
 // [2^-6, 512) by one of its own, which is multiplied back on a path of its
-// own. Values and weights enter as bf16, and their errors only ever average.
+// own. Values and weights enter as f16 too (with bf16 the result's error was
+// 0.0028 of it, now it is its own rounding's, 0.0017). A value row outside
+// [2^-6, 512) is divided by a power of two, 2^k, and k added to its scores in
+// log2 units: the weights that meet V, and m, are those of the shifted scores,
+// the sum that divides them is that of the true ones.
 //
 // Roles (20 warps): warps 0-3 and 4-7 each own a tile of rows, a row a
 // thread: they read S, write P, scale O and write the result. Warps 8-11 turn
@@ -29,7 +35,7 @@
 // 6, 3, 7), as two masks of a word of codes give them.
 //
 // A code masked out where it stands is a subnormal number: one product makes
-// c / 512 (f16) or c / 64 (bf16) of it, one multiply-add code * scale + offset.
+// c / 512 of it, one multiply-add code * scale + offset.
 //
 // What is masked never meets what it must not: a position outside the cache
 // enters as zeros, and a value that is not finite is left out of V and makes
@@ -54,15 +60,19 @@ static_assert(kRowRegisters >= kRegisters && kCodeRegisters <= kRegisters && kPr
               "rows ask for more than they start with, the others give back");
 static_assert(2 * kRowRegisters + 2 * kCodeRegisters + kProductRegisters <= 5 * kRegisters, "more would never be had");
 constexpr int kMaskRing = 4;      // tiles whose masks are kept
+constexpr int kMaskWords = 20;
+// In log2 of a weight: where a raise puts the largest, when it is due, when it cannot wait.
+constexpr float kRaised = 4.0f, kRaise = 11.0f, kRaiseNow = 15.0f;
 
 template <int D>
 struct Prefill {
   static constexpr int kQ = kTile * D * 2;       // bytes of an operand tile
   static constexpr int kAtK = 2 * kQ;
   static constexpr int kAtV = kAtK + 2 * kQ;
-  static constexpr int kAtMasks = kAtV + 2 * kQ;             // [ring][4][4] present; V not finite; K has a factor; any such
-  static constexpr int kAtFactors = kAtMasks + kMaskRing * 16 * 4;  // [ring][128] of K rows
-  static constexpr int kAtBars = kAtFactors + kMaskRing * kTile * 4;
+  static constexpr int kAtMasks = kAtV + 2 * kQ;  // [ring][5][4] present; V not finite; K has a factor; any such; V is shifted
+  static constexpr int kAtFactors = kAtMasks + kMaskRing * kMaskWords * 4;  // [ring][128] of K rows
+  static constexpr int kAtShifts = kAtFactors + kMaskRing * kTile * 4;      // [ring][128] of V rows, in log2
+  static constexpr int kAtBars = kAtShifts + kMaskRing * kTile * 4;
   static constexpr int kAtWords = kAtBars + 16 * 8;
   static constexpr int kSmem = kAtWords + 64 + 1024;         // and alignment
 };
@@ -87,9 +97,16 @@ __device__ __forceinline__ uint32_t code_512ths(uint32_t word, int i) {
   return f16_mul(code_bits(word, i), i % 2 == 0 ? 0x78007800u /* 2^15 */ : 0x68006800u /* 2^11 */);
 }
 
-// Codes i and i + 4 of a word as bf16 pair c / 64.
-__device__ __forceinline__ uint32_t code_64ths(uint32_t word, int i) {
-  return bf2_mul(code_bits(word, i), i % 2 == 0 ? 0x7F007F00u : 0x7D007D00u);
+// log2 of what a value row of these (scale, offset) is divided by to lie in
+// f16's range: 0 if its largest magnitude is in [2^-6, 512), or if it is zero
+// or not finite. Not below -90, so that a true weight stays below 2^128 (of
+// rows smaller than 2^-96 bits are lost).
+__device__ __forceinline__ int value_shift(uint32_t pair) {
+  const float s = bf_lo(pair), m = bf_hi(pair);
+  const float most = fmaxf(fabsf(m), fabsf(fmaf(15.0f, s, m)));
+  const bool inside = most >= 0.015625f && most < 512.0f;
+  const int k = min(max(static_cast<int>(__float_as_uint(most) >> 23) - 127, -90), 119);
+  return inside || most == 0.0f || !(fabsf(s) < INFINITY && fabsf(m) < INFINITY) ? 0 : k;
 }
 
 __device__ __forceinline__ uint64_t f2_add(uint64_t a, uint64_t b) {
@@ -114,12 +131,12 @@ __device__ __forceinline__ void rescale_outputs(uint32_t at, float keep) {
 
 // 32 weights of a row, already in tensor memory, times `keep` (a power of two). Rare.
 __device__ __forceinline__ void rescale_weights(uint32_t at, float keep) {
-  float w[32];
+  float w[16];
   uint32_t u[16];
-  const uint32_t keep2 = pack2(keep, keep);
-  tmem_load(at, w);
+  const uint32_t keep2 = f16_pair(keep, keep);
+  tmem_load16(at, w);
 #pragma unroll
-  for (int i = 0; i < 16; ++i) u[i] = bf2_mul(__float_as_uint(w[i]), keep2);
+  for (int i = 0; i < 16; ++i) u[i] = f16_mul(__float_as_uint(w[i]), keep2);
   tmem_store16(at, u);
 }
 
@@ -298,11 +315,11 @@ attention_prefill_kernel(const AttentionArgs a, const KvCache c) {
         if (gave_up(__all_sync(0xffffffffu, ok))) { ok = false; break; }
         fence_after();
         const int p0 = (x.first + j) * kTile;
-        const uint32_t* mask = masks + (j % kMaskRing) * 16;
+        const uint32_t* mask = masks + (j % kMaskRing) * kMaskWords;
         const uint4 any = *reinterpret_cast<const uint4*>(mask + 12);
         const bool special = p0 < all_from || p0 + kTile - 1 > all_to || (any.x | any.y | any.z | any.w) != 0;
-        if (__any_sync(0xffffffffu, top > m + 8.0f)) {
-          const float next = fmaxf(m, top);
+        if (__any_sync(0xffffffffu, top > m + kRaise)) {
+          const float next = fmaxf(m, top - kRaised);
           const float keep = ex2(m - next);
           m = next;
           l *= keep;
@@ -312,10 +329,11 @@ attention_prefill_kernel(const AttentionArgs a, const KvCache c) {
         // a quarter of the row at a time, two to a turn of the loop: what the
         // roles run side by side has to fit the instruction caches (four to a
         // turn took half as long again)
-#pragma unroll 2
-        for (int q = 0; q < 4; ++q) {
+        auto quarter = [&](int q, auto shifted) {
           float v[32];
           tmem_load(s_at + 32 * q, v);
+          float to_log2 = factor;
+          const float* shifts = reinterpret_cast<const float*>(smem + L::kAtShifts) + (j % kMaskRing) * kTile + 32 * q;
           if (special) {
             const float* factors = reinterpret_cast<const float*>(smem + L::kAtFactors) + (j % kMaskRing) * kTile + 32 * q;
             // bits of the columns that the row may see
@@ -328,6 +346,11 @@ attention_prefill_kernel(const AttentionArgs a, const KvCache c) {
 #pragma unroll
               for (int i = 0; i < 32; ++i) v[i] *= factors[i];
             }
+            if constexpr (shifted.value) {
+              to_log2 = 1.0f;
+#pragma unroll
+              for (int i = 0; i < 32; ++i) v[i] = fmaf(v[i], factor, shifts[i]);
+            }
 #pragma unroll
             for (int i = 0; i < 32; ++i)
               if (!((see >> i) & 1u)) v[i] = -INFINITY;
@@ -338,9 +361,9 @@ attention_prefill_kernel(const AttentionArgs a, const KvCache c) {
             tops[0] = fmaxf(tops[0], v[i]);
             tops[1] = fmaxf(tops[1], v[i + 1]);
           }
-          top = fmaxf(top, factor * fmaxf(tops[0], tops[1]));
-          if (__any_sync(0xffffffffu, top > m + 64.0f)) {  // at once, by a power of two: what is scaled is scaled exactly
-            const float next = top > m ? (m == -FLT_MAX ? ceilf(top) : m + ceilf(top - m)) : m;
+          top = fmaxf(top, to_log2 * fmaxf(tops[0], tops[1]));
+          if (__any_sync(0xffffffffu, top > m + kRaiseNow)) {  // by a power of two: weights are scaled exactly
+            const float next = !(top > m + kRaised) ? m : m == -FLT_MAX ? ceilf(top) - kRaised : m + ceilf(top - m) - kRaised;
             const float keep = ex2(m - next);
             m = next;
             l *= keep;
@@ -349,7 +372,11 @@ attention_prefill_kernel(const AttentionArgs a, const KvCache c) {
             for (int k = 0; k < q; ++k) rescale_weights(s_at + 16 * k, keep);
             if (j > 0) rescale_outputs<D>(o_at, keep);
           }
-          const uint64_t f2v = f2(factor, factor), m2 = f2(-m, -m);
+          const uint64_t f2v = f2(to_log2, to_log2), m2 = f2(-m, -m);
+          if constexpr (shifted.value) {  // the true weights' sum
+#pragma unroll
+            for (int i = 0; i < 32; ++i) l += ex2(v[i] - shifts[i] - m);
+          }
           uint64_t sum = f2(0.0f, 0.0f);
           uint32_t p[16];
 #pragma unroll
@@ -359,12 +386,19 @@ attention_prefill_kernel(const AttentionArgs a, const KvCache c) {
             e0 = ex2(e0);
             e1 = ex2(e1);
             sum = f2_add(sum, f2(e0, e1));
-            p[i >> 1] = pack2(e0, e1);
+            p[i >> 1] = f16_pair(e0, e1);
           }
           tmem_store16(s_at + 16 * q, p);  // over columns already read
           float l0, l1;
           f2_split(sum, l0, l1);
-          l += l0 + l1;
+          if constexpr (!shifted.value) l += l0 + l1;
+        };
+        if (special && (mask[16] | mask[17] | mask[18] | mask[19]) != 0) {
+#pragma unroll 1
+          for (int q = 0; q < 4; ++q) quarter(q, std::true_type{});
+        } else {
+#pragma unroll 2
+          for (int q = 0; q < 4; ++q) quarter(q, std::false_type{});
         }
         tmem_stored();
         fence_before();
@@ -456,6 +490,8 @@ attention_prefill_kernel(const AttentionArgs a, const KvCache c) {
         const uint32_t present = __ballot_sync(0xffffffffu, here);
         const uint32_t broken = __ballot_sync(0xffffffffu, !finite);
         const uint32_t scaled = __ballot_sync(0xffffffffu, odd);
+        const int shift = value_shift(vp);
+        const uint32_t shifted = __ballot_sync(0xffffffffu, shift != 0);
         ok = wait_for(k_free(b), ((j >> 1) & 1) ^ 1u, abort_flag);
         if (gave_up(__all_sync(0xffffffffu, ok))) break;
         float* factors = reinterpret_cast<float*>(smem + L::kAtFactors) + (j % kMaskRing) * kTile;
@@ -467,12 +503,14 @@ attention_prefill_kernel(const AttentionArgs a, const KvCache c) {
         } else {
           factors[id] = 1.0f;
         }
+        reinterpret_cast<float*>(smem + L::kAtShifts)[(j % kMaskRing) * kTile + id] = static_cast<float>(shift);
         if (lane == 0) {
-          uint32_t* mask = masks + (j % kMaskRing) * 16 + dw;
+          uint32_t* mask = masks + (j % kMaskRing) * kMaskWords + dw;
           mask[0] = present;
           mask[4] = broken;
           mask[8] = scaled;
-          mask[12] = ~present | broken | scaled;
+          mask[12] = ~present | broken | scaled | shifted;
+          mask[16] = shifted;
         }
         const uint32_t s512 = f16_pair(512.0f * ks, 512.0f * ks), off = f16_pair(km, km);
         uint8_t* dst = smem + L::kAtK + b * L::kQ;
@@ -500,16 +538,18 @@ attention_prefill_kernel(const AttentionArgs a, const KvCache c) {
       const int word = ((lane >> 3) + 4 * (dw & 1)) * kPer;
       int block;
       uint32_t next[8][kPer];
-      uint4 next_pairs[2];
+      uint2 next_pairs;  // of two of the eight positions, this lane's to prepare
       auto find = [&](int j) { block = j < n ? block_at((x.first + j) * (kTile / kBlockTokens) + eights / 2) : -1; };
       auto fetch = [&](int j) {
-        next_pairs[0] = next_pairs[1] = make_uint4(0, 0, 0, 0);
+        next_pairs = make_uint2(0, 0);
         const int left = x.len - ((x.first + j) * kTile + eights * 8);  // positions of these in the cache
         if (block >= 0 && left > 0) {
           const uint8_t* p = cache + static_cast<int64_t>(block) * B::kBytes;
           const int slot = (eights & 1) * 8;
-          next_pairs[0] = __ldg(reinterpret_cast<const uint4*>(p + B::kVPairs + slot * 4));
-          next_pairs[1] = __ldg(reinterpret_cast<const uint4*>(p + B::kVPairs + slot * 4) + 1);
+          next_pairs = __ldg(reinterpret_cast<const uint2*>(p + B::kVPairs + slot * 4) + (lane >> 3));
+          // what lies behind the last position enters as zeros
+          if (left <= (lane >> 3) * 2) next_pairs.x = 0;
+          if (left <= (lane >> 3) * 2 + 1) next_pairs.y = 0;
           p += B::kV + slot * B::kRow + word * 4;
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
@@ -520,12 +560,6 @@ attention_prefill_kernel(const AttentionArgs a, const KvCache c) {
             } else {
               next[i][0] = __ldg(reinterpret_cast<const uint32_t*>(p + i * B::kRow));
             }
-          }
-          if (left < 8) {  // what lies behind the last position enters as zeros
-            uint32_t* pair = reinterpret_cast<uint32_t*>(next_pairs);
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-              if (i >= left) pair[i] = 0;
           }
         }
       };
@@ -544,17 +578,24 @@ attention_prefill_kernel(const AttentionArgs a, const KvCache c) {
         for (int i = 0; i < 8; ++i)
 #pragma unroll
           for (int k = 0; k < kPer; ++k) codes[i][k] = next[i][k];
-        uint32_t s64[4], off[4];
+        // (512 scale, offset) of two positions a lane, then of all eight
+        uint32_t s512[4], off[4];
         {
-          uint32_t pair[8] = {next_pairs[0].x, next_pairs[0].y, next_pairs[0].z, next_pairs[0].w,
-                              next_pairs[1].x, next_pairs[1].y, next_pairs[1].z, next_pairs[1].w};
+          uint32_t pair[2] = {next_pairs.x, next_pairs.y};
+          float step[2], low[2];
 #pragma unroll
-          for (int i = 0; i < 8; ++i)  // not finite: the rows that see it become NaN by the mask
+          for (int i = 0; i < 2; ++i) {
+            // not finite: the rows that see it become NaN by the mask
             if ((pair[i] & 0x7F80u) == 0x7F80u || (pair[i] & 0x7F800000u) == 0x7F800000u) pair[i] = 0;
+            const float down = __uint_as_float(static_cast<uint32_t>(127 - value_shift(pair[i])) << 23);
+            step[i] = 512.0f * (bf_lo(pair[i]) * down);
+            low[i] = bf_hi(pair[i]) * down;
+          }
+          const uint32_t steps = f16_pair(step[0], step[1]), lows = f16_pair(low[0], low[1]);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            s64[i] = bf2_mul(__byte_perm(pair[2 * i], pair[2 * i + 1], 0x5410), 0x42804280u);
-            off[i] = __byte_perm(pair[2 * i], pair[2 * i + 1], 0x7632);
+            s512[i] = __shfl_sync(0xffffffffu, steps, (lane & 7) + 8 * i);
+            off[i] = __shfl_sync(0xffffffffu, lows, (lane & 7) + 8 * i);
           }
         }
         fetch(j + 1);
@@ -572,10 +613,10 @@ attention_prefill_kernel(const AttentionArgs a, const KvCache c) {
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
               uint4 v;
-              v.x = bf2_mad(code_64ths(y[0], q), s64[0], off[0]);
-              v.y = bf2_mad(code_64ths(y[1], q), s64[1], off[1]);
-              v.z = bf2_mad(code_64ths(y[2], q), s64[2], off[2]);
-              v.w = bf2_mad(code_64ths(y[3], q), s64[3], off[3]);
+              v.x = f16_mad(code_512ths(y[0], q), s512[0], off[0]);
+              v.y = f16_mad(code_512ths(y[1], q), s512[1], off[1]);
+              v.z = f16_mad(code_512ths(y[2], q), s512[2], off[2]);
+              v.w = f16_mad(code_512ths(y[3], q), s512[3], off[3]);
               *reinterpret_cast<uint4*>(dst + chunk_at(D, (word + k) * 8 + half * 4 + q, eights)) = v;
             }
           }
@@ -608,7 +649,7 @@ attention_prefill_kernel(const AttentionArgs a, const KvCache c) {
           const uint32_t d = acc + 2 * kTile + t * D, p = acc + t * kTile, v = v_op + b * kTileOp;
 #pragma unroll
           for (int i = 0; i < kTile / 16; ++i)
-            mma_tmem(d, p + 8 * i, v + (((i / 4) * D * 128 + (i % 4) * 32) >> 4), idesc(D, 1), i > 0 || add);
+            mma_tmem(d, p + 8 * i, v + (((i / 4) * D * 128 + (i % 4) * 32) >> 4), idesc(D, 0), i > 0 || add);
         }
         __syncwarp();
       };

@@ -244,6 +244,17 @@ def test_values_of_any_size(factor):
         run(b)
 
 
+@pytest.mark.parametrize("even,odd", [(1e-25, 1e-25), (1e30, 1e30), (1e30, 1e-12), (1e-3, 600.0)])
+def test_values_all_beyond_one(even, odd):
+    """No value of ordinary size among them; a long request, so that tiles of both kinds follow one another."""
+    for queries, lens in (([2, 100], [40, 150]), ([150], [700])):
+        b = Batch(queries, lens, 8, 2, 64, 32, seed=71)
+        for r, n in enumerate(lens):
+            for p in range(n):
+                b.put(r, p, b.rng.normal(0, 1, (2, 64)), b.rng.normal(0, odd if p % 2 or p > 300 else even, (2, 64)))
+        run(b)
+
+
 @pytest.mark.parametrize("factor,q_scale", [(1e-4, 1e3), (1e3, 1e-2), (1e12, 1e-12), (1e-20, 1e18)])
 def test_keys_of_any_size(factor, q_scale):
     """Keys far below and above one, among ordinary ones, and queries to match."""

@@ -967,7 +967,8 @@ PLE_EXPORT ple_status ple_kv_attention(const ple_bf16_t* q, int64_t q_stride, in
   unsigned* counters = static_cast<unsigned*>(workspace);
   float* partial = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + counter_bytes());
   cudaError_t err = cudaSuccess;
-  if (rows >= many) err = launch_prefill(a, c, head_dim, stream);
+  // both kernels' partial results may lie in one place: one runs after the other
+  if (rows >= many) err = launch_prefill(a, c, head_dim, partial, need - counter_bytes(), stream);
   if (err != cudaSuccess) return check_cuda(err, name);
   if (head_dim == 64)
     err = rows <= 8 ? launch_split<64, 1>(a, c, counters, partial, stream)

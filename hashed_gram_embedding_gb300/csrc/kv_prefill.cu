@@ -4,7 +4,10 @@
 // Work. A CTA takes 256 query rows of one request and kv head (rows are
 // (token, head of the group), so a group's heads share every key) as two
 // tiles of 128, and walks the positions they see in tiles of 128. Rows of
-// long requests come first, so that the last CTAs are short ones.
+// long requests come first, so that the last CTAs are short ones. Where these
+// would not fill the GPU, several CTAs share the positions of one such piece of
+// rows, and a second kernel joins their outputs, each with its rows' m and l,
+// in the order of the positions.
 //
 // Mathematics. For each tile of positions, S = Q K^T (f16 operands, f32 in
 // tensor memory), P = exp2(f S - m) rounded to f16 over S in tensor memory,
@@ -45,6 +48,7 @@
 
 #include <cuda_fp16.h>
 
+#include <algorithm>
 #include <cfloat>
 #include <cmath>
 
@@ -74,7 +78,7 @@ struct Prefill {
   static constexpr int kAtShifts = kAtFactors + kMaskRing * kTile * 4;      // [ring][128] of V rows, in log2
   static constexpr int kAtBars = kAtShifts + kMaskRing * kTile * 4;
   static constexpr int kAtWords = kAtBars + 16 * 8;
-  static constexpr int kSmem = kAtWords + 64 + 1024;         // and alignment
+  static constexpr int kSmem = kAtWords + 80 + 1024;         // and alignment
 };
 
 __device__ __forceinline__ uint32_t f16_mul(uint32_t a, uint32_t b) {
@@ -138,6 +142,17 @@ __device__ __forceinline__ void rescale_weights(uint32_t at, float keep) {
   tmem_store16(at, u);
 }
 
+// Where pieces of rows are shared: what a piece became, and its parts' results.
+struct Parts {
+  int most;        // parts of a piece at most; 1: none is shared
+  int4* pieces;    // [pieces][2] parts (0: no such piece), rows, tile, head; first token
+  float2* sums;    // [pieces][most][256] m, l
+  float* outputs;  // [pieces][most][256][D]
+};
+
+// Tiles of positions to a part at least: a CTA's start and end cost as much as some tiles.
+constexpr int kPartTiles = 4;
+
 // A CTA's share of the work.
 struct Job {
   int r, tile, h;     // request, 256-row tile, kv head
@@ -145,12 +160,13 @@ struct Job {
   int rows;           // in the tile
   int first, tiles;   // first position tile, and how many
   int block0, block_end;
+  int parts;          // CTAs that share its rows
   bool clipped;
 };
 
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
-attention_prefill_kernel(const AttentionArgs a, const KvCache c) {
+attention_prefill_kernel(const AttentionArgs a, const KvCache c, const Parts parts) {
   using L = Prefill<D>;
   using B = KvBlock<D>;
   extern __shared__ uint8_t smem_raw[];
@@ -167,7 +183,7 @@ attention_prefill_kernel(const AttentionArgs a, const KvCache c) {
   uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kAtWords);
   volatile int* const abort_flag = reinterpret_cast<volatile int*>(smem + L::kAtWords + 4);
   Job* const job = reinterpret_cast<Job*>(smem + L::kAtWords + 8);
-  static_assert(sizeof(Job) <= 56, "room in shared memory");
+  static_assert(sizeof(Job) <= 60, "room in shared memory");
   const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
   const int G = a.num_heads / c.num_kv_heads, hk = c.num_kv_heads;
 
@@ -188,7 +204,8 @@ attention_prefill_kernel(const AttentionArgs a, const KvCache c) {
   pdl_wait();
   pdl_trigger();
   if (warp == 0) {  // this CTA's share: tiles of a request from the last one on, its heads side by side
-    int left = blockIdx.x, r0 = 0;
+    const int piece = blockIdx.x / parts.most, part = blockIdx.x - piece * parts.most;
+    int left = piece, r0 = 0;
     Job x;
     x.r = -1;
     while (r0 < c.num_reqs) {
@@ -226,6 +243,15 @@ attention_prefill_kernel(const AttentionArgs a, const KvCache c) {
           x.tiles = hi > lo ? static_cast<int>((hi + kTile - 1) / kTile) - x.first : 0;
           x.block0 = static_cast<int>(lo / kBlockTokens);
           x.block_end = hi > 0 ? static_cast<int>((hi + kBlockTokens - 1) / kBlockTokens) : 0;
+          x.parts = max(1, min(parts.most, x.tiles / kPartTiles));
+          if (parts.most > 1 && part == 0) {
+            parts.pieces[2 * piece] = make_int4(x.parts, x.rows, x.tile, x.h);
+            parts.pieces[2 * piece + 1] = make_int4(x.t0, 0, 0, 0);
+          }
+          const int lo_tile = static_cast<int>(int64_t(x.tiles) * part / x.parts);
+          x.tiles = static_cast<int>(int64_t(x.tiles) * (part + 1) / x.parts) - lo_tile;
+          x.first += lo_tile;
+          if (part >= x.parts) x.r = -1;
           *job = x;
         }
         break;
@@ -233,7 +259,10 @@ attention_prefill_kernel(const AttentionArgs a, const KvCache c) {
       left -= __shfl_sync(0xffffffffu, sum, 31);
       r0 += 32;
     }
-    if (r0 >= c.num_reqs && lane == 0) job->r = -1;
+    if (r0 >= c.num_reqs && lane == 0) {
+      job->r = -1;
+      if (parts.most > 1 && part == 0) parts.pieces[2 * piece] = make_int4(0, 0, 0, 0);
+    }
     __syncwarp();
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(tmem_slot)) : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
@@ -407,6 +436,8 @@ attention_prefill_kernel(const AttentionArgs a, const KvCache c) {
         ok = !gave_up(__all_sync(0xffffffffu, ok));
         fence_after();
       }
+      const int64_t slot = static_cast<int64_t>(blockIdx.x) * (2 * kTile) + in_tile;
+      if (x.parts > 1) parts.sums[slot] = make_float2(m, l);
       const float inv = l == 0.0f ? 0.0f : 1.0f / l;
       ple_bf16_t* dst = a.out + static_cast<int64_t>(x.t0 + token) * a.out_stride + head;
 #pragma unroll 1
@@ -417,7 +448,11 @@ attention_prefill_kernel(const AttentionArgs a, const KvCache c) {
 #pragma unroll
           for (int i = 0; i < 32; ++i) o[i] = 0.0f;
         }
-        if (live) {
+        if (x.parts > 1) {
+#pragma unroll
+          for (int i = 0; i < 32; i += 4)
+            *reinterpret_cast<float4*>(parts.outputs + slot * D + 32 * q + i) = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+        } else if (live) {
 #pragma unroll
           for (int i = 0; i < 32; i += 8)
             *reinterpret_cast<uint4*>(dst + 32 * q + i) =
@@ -707,23 +742,103 @@ attention_prefill_kernel(const AttentionArgs a, const KvCache c) {
   }
 }
 
+// A row a warp: the parts' outputs, weighted by how far each one's m is below
+// the largest.
+constexpr int kJoinWarps = 8, kJoinRows = 32;  // rows of a CTA
+
 template <int D>
-cudaError_t launch(const AttentionArgs& a, const KvCache& c, cudaStream_t stream) {
+__global__ void __launch_bounds__(kJoinWarps * 32)
+attention_join_kernel(const AttentionArgs a, const KvCache c, const Parts parts) {
+  pdl_wait();
+  pdl_trigger();
+  const int piece = blockIdx.x / (2 * kTile / kJoinRows), row0 = blockIdx.x % (2 * kTile / kJoinRows) * kJoinRows;
+  const int4 x = parts.pieces[2 * piece];
+  const int count = x.x, rows = x.y, t0 = parts.pieces[2 * piece + 1].x;
+  if (count <= 1) return;
+  const int lane = threadIdx.x & 31, G = a.num_heads / c.num_kv_heads;
+  constexpr int kMine = D / 32;  // columns of a lane
+  for (int row = row0 + threadIdx.x / 32; row < min(row0 + kJoinRows, rows); row += kJoinWarps) {
+    const int64_t slot = static_cast<int64_t>(piece) * parts.most * (2 * kTile) + row;
+    float2 ml = make_float2(-FLT_MAX, 0.0f);
+    if (lane < count) ml = parts.sums[slot + lane * (2 * kTile)];
+    float most = ml.x;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
+    const float w = ex2(ml.x - most);
+    float sum = w * ml.y;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    float acc[kMine] = {};
+#pragma unroll 4
+    for (int i = 0; i < count; ++i) {
+      const float* from = parts.outputs + (slot + i * (2 * kTile)) * D + lane * kMine;
+      const float wi = __shfl_sync(0xffffffffu, w, i);
+      if constexpr (kMine == 4) {
+        const float4 v = *reinterpret_cast<const float4*>(from);
+        acc[0] = fmaf(wi, v.x, acc[0]);
+        acc[1] = fmaf(wi, v.y, acc[1]);
+        acc[2] = fmaf(wi, v.z, acc[2]);
+        acc[3] = fmaf(wi, v.w, acc[3]);
+      } else {
+        const float2 v = *reinterpret_cast<const float2*>(from);
+        acc[0] = fmaf(wi, v.x, acc[0]);
+        acc[1] = fmaf(wi, v.y, acc[1]);
+      }
+    }
+    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+    const int flat = x.z * 2 * kTile + row, token = flat / G;
+    ple_bf16_t* dst = a.out + static_cast<int64_t>(t0 + token) * a.out_stride +
+                      static_cast<int64_t>(x.w * G + (flat - token * G)) * D + lane * kMine;
+#pragma unroll
+    for (int i = 0; i < kMine; i += 2) *reinterpret_cast<uint32_t*>(dst + i) = pack2(acc[i] * inv, acc[i + 1] * inv);
+  }
+}
+
+template <int D>
+cudaError_t launch(const AttentionArgs& a, const KvCache& c, uint8_t* room, size_t room_bytes, cudaStream_t stream) {
   const auto kernel = attention_prefill_kernel<D>;
   const cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Prefill<D>::kSmem);
   if (err != cudaSuccess) return err;
-  // no more tiles than this: every request's last one may be short
-  const int64_t rows = a.T * (a.num_heads / c.num_kv_heads);
+  // no more pieces than this: every request's last one may be short
+  const int group = a.num_heads / c.num_kv_heads;
+  const int64_t rows = a.T * group;
   const int64_t requests = rows / a.many_rows < c.num_reqs ? rows / a.many_rows : c.num_reqs;
-  const int64_t tiles = rows / (2 * kTile) + requests;
-  return launch_kernel(kernel, dim3(static_cast<unsigned>(tiles * c.num_kv_heads)), dim3(kThreads), Prefill<D>::kSmem,
-                       stream, 1, a, c);
+  const int64_t pieces = (requests == 1 ? (rows + 2 * kTile - 1) / (2 * kTile) : rows / (2 * kTile) + requests) * c.num_kv_heads;
+  // Parts: what makes the fullest turns of all SMs, in tiles of the longest
+  // context that the table has room for; a CTA's start and end cost some 6 tiles.
+  constexpr size_t kPartBytes = 2 * kTile * (D * sizeof(float) + sizeof(float2));
+  const int64_t cap = static_cast<int64_t>((room_bytes - 1024) / (kPartBytes + 2 * sizeof(int4)));
+  int64_t seen = static_cast<int64_t>(c.max_pages) * c.page_size;
+  if (a.window > 0) seen = std::min(seen, static_cast<int64_t>(a.window) + 2 * kTile / group + 1);
+  const int64_t tiles = seen / kTile + 1;
+  int most = 1;
+  int64_t least = INT64_MAX;
+  for (int n = 1; n <= 32 && (n == 1 || (pieces * n <= cap && n * kPartTiles <= tiles)); ++n) {
+    const int64_t turns = (pieces * n + num_sms() - 1) / num_sms(), cost = turns * ((tiles + n - 1) / n + 6);
+    if (cost < least) {
+      least = cost;
+      most = n;
+    }
+  }
+  Parts parts{most, nullptr, nullptr, nullptr};
+  if (most > 1) {
+    parts.pieces = reinterpret_cast<int4*>(room);
+    parts.sums = reinterpret_cast<float2*>(room + (pieces * 2 * sizeof(int4) + 255) / 256 * 256);
+    parts.outputs = reinterpret_cast<float*>(parts.sums + pieces * most * 2 * kTile);
+  }
+  const cudaError_t run = launch_kernel(kernel, dim3(static_cast<unsigned>(pieces * most)), dim3(kThreads),
+                                        Prefill<D>::kSmem, stream, 1, a, c, parts);
+  if (run != cudaSuccess || most == 1) return run;
+  return launch_kernel(attention_join_kernel<D>, dim3(static_cast<unsigned>(pieces * (2 * kTile / kJoinRows))),
+                       dim3(kJoinWarps * 32), 0, stream, 1, a, c, parts);
 }
 
 }  // namespace
 
-cudaError_t launch_prefill(const AttentionArgs& a, const KvCache& c, int head_dim, cudaStream_t stream) {
-  return head_dim == 64 ? launch<64>(a, c, stream) : launch<128>(a, c, stream);
+cudaError_t launch_prefill(const AttentionArgs& a, const KvCache& c, int head_dim, void* room, size_t room_bytes,
+                           cudaStream_t stream) {
+  uint8_t* at = static_cast<uint8_t*>(room);
+  return head_dim == 64 ? launch<64>(a, c, at, room_bytes, stream) : launch<128>(a, c, at, room_bytes, stream);
 }
 
 }  // namespace ple

@@ -244,6 +244,29 @@ def test_values_of_any_size(factor):
         run(b)
 
 
+@pytest.mark.parametrize("queries,lens,H,Hk,D,page,causal,window", [
+    ([30], [5000], 4, 1, 128, 64, True, 0),
+    ([100, 2, 40, 300], [2500, 900, 4100, 300], 4, 1, 64, 16, True, 0),
+    ([70, 33], [3001, 2049], 8, 2, 128, 112, False, 0),
+    ([300], [2800], 2, 2, 64, 32, True, 1100),
+    ([128, 64], [0, 1700], 6, 2, 128, 16, True, 0),
+    ([512], [4096], 3, 1, 128, 128, True, 1),
+])
+def test_few_rows_on_long_contexts(queries, lens, H, Hk, D, page, causal, window):
+    """The positions of the same rows are shared out between CTAs and the results joined."""
+    b = Batch(queries, lens, H, Hk, D, page, seed=sum(queries), pad=3)
+    run(b, causal=causal, window=window)
+
+
+def test_shared_positions_then_single_tokens_in_one_workspace():
+    """Calls of every kind after one another leave each other nothing."""
+    ws = torch.zeros(_lib.ple_kv_attention_workspace(8, 2, 128), dtype=torch.uint8, device="cuda")
+    for queries, lens in (([40], [2600]), ([1] * 5, [700, 3, 40, 1500, 90]), ([40, 1, 3], [1500, 2000, 77]), ([1], [2500])):
+        b = Batch(queries, lens, 8, 2, 128, 32, seed=len(lens))
+        q = b.rows(8)
+        check(attend(b, q, ws=ws), *oracle.attention(bits(q), b.cache, b.table, b.qsl, b.lens, 128 ** -0.5))
+
+
 @pytest.mark.parametrize("even,odd", [(1e-25, 1e-25), (1e30, 1e30), (1e30, 1e-12), (1e-3, 600.0)])
 def test_values_all_beyond_one(even, odd):
     """No value of ordinary size among them; a long request, so that tiles of both kinds follow one another."""

@@ -877,9 +877,19 @@ attention_split_kernel(const AttentionArgs a, const KvCache c, unsigned* __restr
     if ((armed >> s) & 1u) mbar_wait(bar0 + 8 * s, (phases >> s) & 1u, nullptr);
 }
 
-// From this many rows on a request's cache is read for 256 rows at a time, by
-// the 5th-generation tensor cores.
-constexpr int kManyRows = 96;
+// From how many rows (query tokens times heads of a group) on a request's
+// cache is read for 256 rows at a time, by the 5th-generation tensor cores.
+// This file's kernel takes up to 32 rows in one pass over the cache and is
+// bound by the cache's bytes; the other's time does not depend on the rows up
+// to 256 and is bound by turning codes into operands. Measured at 8 kv heads,
+// 2048 positions unless stated, this kernel / the other, us:
+//   16 rows,  4 requests  28 /  26;  1 request, 64k positions  52 /  82
+//   32 rows,  4 requests  48 /  30;  1 request, 64k positions  91 /  91
+//            16 requests  62 /  47;  32 requests  77 / 95;  64 requests  128 / 185
+//   48 rows, 16 requests  69 /  47;  32 requests 112 / 95;  64 requests  228 / 186
+// So 33 rows always go to the other, and 17 to 32 do where a CTA for each
+// request and kv head finds an SM of its own.
+int many_rows(int num_reqs, int num_kv_heads) { return int64_t(num_reqs) * num_kv_heads <= num_sms() ? 17 : 33; }
 
 constexpr int kMaxWarps = 16;  // of an SM, of any variant
 constexpr int kLevels = 4;   // of joining: more than 8^4 warps there are not
@@ -959,7 +969,7 @@ PLE_EXPORT ple_status ple_kv_attention(const ple_bf16_t* q, int64_t q_stride, in
   // the rows of a request and kv head, at most
   const int64_t tokens = max_query_len > 0 && max_query_len < num_tokens ? max_query_len : num_tokens;
   const int64_t rows = tokens * (num_heads / num_kv_heads);
-  const int many = head_dim <= 128 ? kManyRows : INT32_MAX;
+  const int many = head_dim <= 128 ? many_rows(num_reqs, num_kv_heads) : INT32_MAX;
   const AttentionArgs a{q, q_stride, num_tokens, num_heads, scale * 1.4426950408889634f, causal != 0,
                         window, out, out_stride, dev_err, many};
   const KvCache c{const_cast<uint8_t*>(static_cast<const uint8_t*>(cache)), num_pages, page_size,

@@ -969,7 +969,7 @@ PLE_EXPORT ple_status ple_kv_attention(const ple_bf16_t* q, int64_t q_stride, in
   // the rows of a request and kv head, at most
   const int64_t tokens = max_query_len > 0 && max_query_len < num_tokens ? max_query_len : num_tokens;
   const int64_t rows = tokens * (num_heads / num_kv_heads);
-  const int many = head_dim <= 128 ? many_rows(num_reqs, num_kv_heads) : INT32_MAX;
+  const int many = many_rows(num_reqs, num_kv_heads);
   const AttentionArgs a{q, q_stride, num_tokens, num_heads, scale * 1.4426950408889634f, causal != 0,
                         window, out, out_stride, dev_err, many};
   const KvCache c{const_cast<uint8_t*>(static_cast<const uint8_t*>(cache)), num_pages, page_size,

@@ -21,7 +21,7 @@ struct AttentionArgs {
   int many_rows;     // requests with this many query rows a kv head or more go to the second kernel
 };
 
-// Attention of the requests with many rows, for head_dim 64 and 128. room:
+// Attention of the requests with many rows. room:
 // device memory for the results of shared rows, 256-byte aligned, of any content.
 cudaError_t launch_prefill(const AttentionArgs& a, const KvCache& c, int head_dim, void* room, size_t room_bytes,
                            cudaStream_t stream);

@@ -70,14 +70,19 @@ constexpr float kRaised = 4.0f, kRaise = 11.0f, kRaiseNow = 15.0f;
 
 template <int D>
 struct Prefill {
+  // Two tiles of rows and two buffers of K and V; heads of 256 fill shared and
+  // tensor memory with one of each.
+  static constexpr int kRowTiles = D <= 128 ? 2 : 1, kBuffers = D <= 128 ? 2 : 1;
+  static constexpr int kRows = kRowTiles * kTile;
   static constexpr int kQ = kTile * D * 2;       // bytes of an operand tile
-  static constexpr int kAtK = 2 * kQ;
-  static constexpr int kAtV = kAtK + 2 * kQ;
-  static constexpr int kAtMasks = kAtV + 2 * kQ;  // [ring][5][4] present; V not finite; K has a factor; any such; V is shifted
+  static constexpr int kAtK = kRowTiles * kQ;
+  static constexpr int kAtV = kAtK + kBuffers * kQ;
+  static constexpr int kAtMasks = kAtV + kBuffers * kQ;  // [ring][5][4] present; V not finite; K has a factor; any such; V is shifted
   static constexpr int kAtFactors = kAtMasks + kMaskRing * kMaskWords * 4;  // [ring][128] of K rows
   static constexpr int kAtShifts = kAtFactors + kMaskRing * kTile * 4;      // [ring][128] of V rows, in log2
   static constexpr int kAtBars = kAtShifts + kMaskRing * kTile * 4;
   static constexpr int kAtWords = kAtBars + 16 * 8;
+  static_assert(2 * kTile + kRowTiles * D <= 512, "tensor memory");
   static constexpr int kSmem = kAtWords + 80 + 1024;         // and alignment
 };
 
@@ -146,8 +151,8 @@ __device__ __forceinline__ void rescale_weights(uint32_t at, float keep) {
 struct Parts {
   int most;        // parts of a piece at most; 1: none is shared
   int4* pieces;    // [pieces][2] parts (0: no such piece), rows, tile, head; first token
-  float2* sums;    // [pieces][most][256] m, l
-  float* outputs;  // [pieces][most][256][D]
+  float2* sums;    // [pieces][most][rows] m, l
+  float* outputs;  // [pieces][most][rows][D]
 };
 
 // Tiles of positions to a part at least: a CTA's start and end cost as much as some tiles.
@@ -213,7 +218,7 @@ attention_prefill_kernel(const AttentionArgs a, const KvCache c, const Parts par
       int64_t t0 = 0, end = 0;
       if (r < c.num_reqs) request_span(c.qsl, c.num_reqs + 1, a.T, r, &t0, &end);
       const int rows = static_cast<int>(end - t0) * G;
-      const int tiles = rows >= a.many_rows ? (rows + 2 * kTile - 1) / (2 * kTile) : 0;
+      const int tiles = rows >= a.many_rows ? (rows + L::kRows - 1) / L::kRows : 0;
       int sum = tiles * hk;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -230,9 +235,9 @@ attention_prefill_kernel(const AttentionArgs a, const KvCache c, const Parts par
           x.t0 = static_cast<int>(t0);
           x.n = static_cast<int>(end - t0);
           x.len = max(__ldg(c.kv_lens + r), 0);
-          x.rows = min(2 * kTile, rows - x.tile * 2 * kTile);
+          x.rows = min(L::kRows, rows - x.tile * L::kRows);
           // the positions that its rows see
-          const int tok0 = x.tile * 2 * kTile / G, tok1 = (x.tile * 2 * kTile + x.rows - 1) / G;
+          const int tok0 = x.tile * L::kRows / G, tok1 = (x.tile * L::kRows + x.rows - 1) / G;
           const int64_t room = static_cast<int64_t>(c.max_pages) * c.page_size;
           int64_t hi = a.causal ? int64_t(x.len) - x.n + tok1 + 1 : x.len;
           x.clipped = hi > room;
@@ -289,7 +294,7 @@ attention_prefill_kernel(const AttentionArgs a, const KvCache c, const Parts par
     const int t = warp / 4;                       // tile of rows
     const int row = threadIdx.x % kGroupThreads;
     const int in_tile = t * kTile + row;
-    const int flat = x.tile * 2 * kTile + in_tile;
+    const int flat = x.tile * L::kRows + in_tile;
     const bool live = in_tile < x.rows;
     const int token = flat / G;
     const int64_t head = static_cast<int64_t>(x.h * G + (flat - token * G)) * D;
@@ -436,7 +441,7 @@ attention_prefill_kernel(const AttentionArgs a, const KvCache c, const Parts par
         ok = !gave_up(__all_sync(0xffffffffu, ok));
         fence_after();
       }
-      const int64_t slot = static_cast<int64_t>(blockIdx.x) * (2 * kTile) + in_tile;
+      const int64_t slot = static_cast<int64_t>(blockIdx.x) * L::kRows + in_tile;
       if (x.parts > 1) parts.sums[slot] = make_float2(m, l);
       const float inv = l == 0.0f ? 0.0f : 1.0f / l;
       ple_bf16_t* dst = a.out + static_cast<int64_t>(x.t0 + token) * a.out_stride + head;
@@ -507,7 +512,7 @@ attention_prefill_kernel(const AttentionArgs a, const KvCache c, const Parts par
       find(1);
 #pragma unroll 1
       for (int j = 0; j < n; ++j) {
-        const int b = j & 1;
+        const int b = j % L::kBuffers;
         uint4 codes[kWords / 4];
 #pragma unroll
         for (int i = 0; i < kWords / 4; ++i) codes[i] = next[i];
@@ -525,7 +530,7 @@ attention_prefill_kernel(const AttentionArgs a, const KvCache c, const Parts par
         const uint32_t scaled = __ballot_sync(0xffffffffu, odd);
         const int shift = value_shift(vp);
         const uint32_t shifted = __ballot_sync(0xffffffffu, shift != 0);
-        ok = wait_for(k_free(b), ((j >> 1) & 1) ^ 1u, abort_flag);
+        ok = wait_for(k_free(b), ((j / L::kBuffers) & 1) ^ 1u, abort_flag);
         if (gave_up(__all_sync(0xffffffffu, ok))) break;
         float* factors = reinterpret_cast<float*>(smem + L::kAtFactors) + (j % kMaskRing) * kTile;
         if (scaled != 0) {
@@ -586,7 +591,13 @@ attention_prefill_kernel(const AttentionArgs a, const KvCache c, const Parts par
           p += B::kV + slot * B::kRow + word * 4;
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
-            if constexpr (kPer == 2) {
+            if constexpr (kPer == 4) {
+              const uint4 v = __ldg(reinterpret_cast<const uint4*>(p + i * B::kRow));
+              next[i][0] = v.x;
+              next[i][1] = v.y;
+              next[i][2] = v.z;
+              next[i][3] = v.w;
+            } else if constexpr (kPer == 2) {
               const uint2 v = __ldg(reinterpret_cast<const uint2*>(p + i * B::kRow));
               next[i][0] = v.x;
               next[i][1] = v.y;
@@ -605,7 +616,7 @@ attention_prefill_kernel(const AttentionArgs a, const KvCache c, const Parts par
       find(1);
 #pragma unroll 1
       for (int j = 0; j < n; ++j) {
-        const int b = j & 1;
+        const int b = j % L::kBuffers;
         uint32_t codes[8][kPer];
 #pragma unroll
         for (int i = 0; i < 8; ++i)
@@ -633,7 +644,7 @@ attention_prefill_kernel(const AttentionArgs a, const KvCache c, const Parts par
         }
         fetch(j + 1);
         find(j + 2);
-        ok = wait_for(v_free(b), ((j >> 1) & 1) ^ 1u, abort_flag);
+        ok = wait_for(v_free(b), ((j / L::kBuffers) & 1) ^ 1u, abort_flag);
         if (gave_up(__all_sync(0xffffffffu, ok))) break;
         uint8_t* dst = smem + L::kAtV + b * L::kQ;
 #pragma unroll
@@ -703,14 +714,15 @@ attention_prefill_kernel(const AttentionArgs a, const KvCache c, const Parts par
       }
 #pragma unroll 1
       for (int j = 0; ok && j < n; ++j) {
-        const int b = j & 1, nb = b ^ 1;
+        const int b = j % L::kBuffers, nb = (j + 1) % L::kBuffers;
         const bool more = j + 1 < n;
-        ok = wait_all(v_full(b), (j >> 1) & 1) && wait_all(p_full(0), j & 1);
+        ok = wait_all(v_full(b), (j / L::kBuffers) & 1) && wait_all(p_full(0), j & 1);
         if (!ok) break;
         fence_after();
         outputs(0, b, j > 0);
+        if constexpr (L::kRowTiles == 1) commit(v_free(b));
         if (more) {
-          ok = wait_all(k_full(nb), ((j + 1) >> 1) & 1);
+          ok = wait_all(k_full(nb), ((j + 1) / L::kBuffers) & 1);
           if (!ok) break;
           fence_after();
           scores(0, nb);
@@ -721,7 +733,7 @@ attention_prefill_kernel(const AttentionArgs a, const KvCache c, const Parts par
           fence_after();
           outputs(1, b, j > 0);
         }
-        commit(v_free(b));
+        if constexpr (L::kRowTiles == 2) commit(v_free(b));
         if (more) {
           if (two) scores(1, nb);
           commit(k_free(nb));
@@ -751,16 +763,17 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
 attention_join_kernel(const AttentionArgs a, const KvCache c, const Parts parts) {
   pdl_wait();
   pdl_trigger();
-  const int piece = blockIdx.x / (2 * kTile / kJoinRows), row0 = blockIdx.x % (2 * kTile / kJoinRows) * kJoinRows;
+  constexpr int kRows = Prefill<D>::kRows;
+  const int piece = blockIdx.x / (kRows / kJoinRows), row0 = blockIdx.x % (kRows / kJoinRows) * kJoinRows;
   const int4 x = parts.pieces[2 * piece];
   const int count = x.x, rows = x.y, t0 = parts.pieces[2 * piece + 1].x;
   if (count <= 1) return;
   const int lane = threadIdx.x & 31, G = a.num_heads / c.num_kv_heads;
   constexpr int kMine = D / 32;  // columns of a lane
   for (int row = row0 + threadIdx.x / 32; row < min(row0 + kJoinRows, rows); row += kJoinWarps) {
-    const int64_t slot = static_cast<int64_t>(piece) * parts.most * (2 * kTile) + row;
+    const int64_t slot = static_cast<int64_t>(piece) * parts.most * kRows + row;
     float2 ml = make_float2(-FLT_MAX, 0.0f);
-    if (lane < count) ml = parts.sums[slot + lane * (2 * kTile)];
+    if (lane < count) ml = parts.sums[slot + lane * kRows];
     float most = ml.x;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
@@ -771,22 +784,17 @@ attention_join_kernel(const AttentionArgs a, const KvCache c, const Parts parts)
     float acc[kMine] = {};
 #pragma unroll 4
     for (int i = 0; i < count; ++i) {
-      const float* from = parts.outputs + (slot + i * (2 * kTile)) * D + lane * kMine;
+      const float* from = parts.outputs + (slot + i * kRows) * D + lane * kMine;
       const float wi = __shfl_sync(0xffffffffu, w, i);
-      if constexpr (kMine == 4) {
-        const float4 v = *reinterpret_cast<const float4*>(from);
-        acc[0] = fmaf(wi, v.x, acc[0]);
-        acc[1] = fmaf(wi, v.y, acc[1]);
-        acc[2] = fmaf(wi, v.z, acc[2]);
-        acc[3] = fmaf(wi, v.w, acc[3]);
-      } else {
-        const float2 v = *reinterpret_cast<const float2*>(from);
-        acc[0] = fmaf(wi, v.x, acc[0]);
-        acc[1] = fmaf(wi, v.y, acc[1]);
+#pragma unroll
+      for (int k = 0; k < kMine; k += 2) {
+        const float2 v = *reinterpret_cast<const float2*>(from + k);
+        acc[k] = fmaf(wi, v.x, acc[k]);
+        acc[k + 1] = fmaf(wi, v.y, acc[k + 1]);
       }
     }
     const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-    const int flat = x.z * 2 * kTile + row, token = flat / G;
+    const int flat = x.z * kRows + row, token = flat / G;
     ple_bf16_t* dst = a.out + static_cast<int64_t>(t0 + token) * a.out_stride +
                       static_cast<int64_t>(x.w * G + (flat - token * G)) * D + lane * kMine;
 #pragma unroll
@@ -796,6 +804,7 @@ attention_join_kernel(const AttentionArgs a, const KvCache c, const Parts parts)
 
 template <int D>
 cudaError_t launch(const AttentionArgs& a, const KvCache& c, uint8_t* room, size_t room_bytes, cudaStream_t stream) {
+  constexpr int kRows = Prefill<D>::kRows;
   const auto kernel = attention_prefill_kernel<D>;
   const cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Prefill<D>::kSmem);
   if (err != cudaSuccess) return err;
@@ -803,13 +812,13 @@ cudaError_t launch(const AttentionArgs& a, const KvCache& c, uint8_t* room, size
   const int group = a.num_heads / c.num_kv_heads;
   const int64_t rows = a.T * group;
   const int64_t requests = rows / a.many_rows < c.num_reqs ? rows / a.many_rows : c.num_reqs;
-  const int64_t pieces = (requests == 1 ? (rows + 2 * kTile - 1) / (2 * kTile) : rows / (2 * kTile) + requests) * c.num_kv_heads;
+  const int64_t pieces = (requests == 1 ? (rows + kRows - 1) / kRows : rows / kRows + requests) * c.num_kv_heads;
   // Parts: what makes the fullest turns of all SMs, in tiles of the longest
   // context that the table has room for; a CTA's start and end cost some 6 tiles.
-  constexpr size_t kPartBytes = 2 * kTile * (D * sizeof(float) + sizeof(float2));
+  constexpr size_t kPartBytes = kRows * (D * sizeof(float) + sizeof(float2));
   const int64_t cap = static_cast<int64_t>((room_bytes - 1024) / (kPartBytes + 2 * sizeof(int4)));
   int64_t seen = static_cast<int64_t>(c.max_pages) * c.page_size;
-  if (a.window > 0) seen = std::min(seen, static_cast<int64_t>(a.window) + 2 * kTile / group + 1);
+  if (a.window > 0) seen = std::min(seen, static_cast<int64_t>(a.window) + kRows / group + 1);
   const int64_t tiles = seen / kTile + 1;
   int most = 1;
   int64_t least = INT64_MAX;
@@ -824,12 +833,12 @@ cudaError_t launch(const AttentionArgs& a, const KvCache& c, uint8_t* room, size
   if (most > 1) {
     parts.pieces = reinterpret_cast<int4*>(room);
     parts.sums = reinterpret_cast<float2*>(room + (pieces * 2 * sizeof(int4) + 255) / 256 * 256);
-    parts.outputs = reinterpret_cast<float*>(parts.sums + pieces * most * 2 * kTile);
+    parts.outputs = reinterpret_cast<float*>(parts.sums + pieces * most * kRows);
   }
   const cudaError_t run = launch_kernel(kernel, dim3(static_cast<unsigned>(pieces * most)), dim3(kThreads),
                                         Prefill<D>::kSmem, stream, 1, a, c, parts);
   if (run != cudaSuccess || most == 1) return run;
-  return launch_kernel(attention_join_kernel<D>, dim3(static_cast<unsigned>(pieces * (2 * kTile / kJoinRows))),
+  return launch_kernel(attention_join_kernel<D>, dim3(static_cast<unsigned>(pieces * (kRows / kJoinRows))),
                        dim3(kJoinWarps * 32), 0, stream, 1, a, c, parts);
 }
 
@@ -838,7 +847,9 @@ cudaError_t launch(const AttentionArgs& a, const KvCache& c, uint8_t* room, size
 cudaError_t launch_prefill(const AttentionArgs& a, const KvCache& c, int head_dim, void* room, size_t room_bytes,
                            cudaStream_t stream) {
   uint8_t* at = static_cast<uint8_t*>(room);
-  return head_dim == 64 ? launch<64>(a, c, at, room_bytes, stream) : launch<128>(a, c, at, room_bytes, stream);
+  return head_dim == 64    ? launch<64>(a, c, at, room_bytes, stream)
+         : head_dim == 128 ? launch<128>(a, c, at, room_bytes, stream)
+                           : launch<256>(a, c, at, room_bytes, stream);
 }
 
 }  // namespace ple

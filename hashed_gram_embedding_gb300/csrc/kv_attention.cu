@@ -888,8 +888,13 @@ attention_split_kernel(const AttentionArgs a, const KvCache c, unsigned* __restr
 //            16 requests  62 /  47;  32 requests  77 / 95;  64 requests  128 / 185
 //   48 rows, 16 requests  69 /  47;  32 requests 112 / 95;  64 requests  228 / 186
 // So 33 rows always go to the other, and 17 to 32 do where a CTA for each
-// request and kv head finds an SM of its own.
-int many_rows(int num_reqs, int num_kv_heads) { return int64_t(num_reqs) * num_kv_heads <= num_sms() ? 17 : 33; }
+// request and kv head finds an SM of its own. Heads of 256 (16 rows a pass
+// here, half the buffers there) meet later; 2 kv heads:
+//   64 rows,  1 request  37 / 43;  64 requests  89 / 86
+//  128 rows,  1 request  38 / 45;  64 requests 154 / 90
+int many_rows(int num_reqs, int num_kv_heads, int head_dim) {
+  return head_dim == 256 ? 96 : int64_t(num_reqs) * num_kv_heads <= num_sms() ? 17 : 33;
+}
 
 constexpr int kMaxWarps = 16;  // of an SM, of any variant
 constexpr int kLevels = 4;   // of joining: more than 8^4 warps there are not
@@ -969,7 +974,7 @@ PLE_EXPORT ple_status ple_kv_attention(const ple_bf16_t* q, int64_t q_stride, in
   // the rows of a request and kv head, at most
   const int64_t tokens = max_query_len > 0 && max_query_len < num_tokens ? max_query_len : num_tokens;
   const int64_t rows = tokens * (num_heads / num_kv_heads);
-  const int many = many_rows(num_reqs, num_kv_heads);
+  const int many = many_rows(num_reqs, num_kv_heads, head_dim);
   const AttentionArgs a{q, q_stride, num_tokens, num_heads, scale * 1.4426950408889634f, causal != 0,
                         window, out, out_stride, dev_err, many};
   const KvCache c{const_cast<uint8_t*>(static_cast<const uint8_t*>(cache)), num_pages, page_size,

@@ -258,6 +258,11 @@ def test_few_rows_on_long_contexts(queries, lens, H, Hk, D, page, causal, window
     run(b, causal=causal, window=window)
 
 
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_a_hint_too_small_loses_no_rows(dim):
+    run(Batch([1, 60, 5], [90, 100, 5], 4, 2, dim, 16, seed=73), hint=1)
+
+
 def test_shared_positions_then_single_tokens_in_one_workspace():
     """Calls of every kind after one another leave each other nothing."""
     ws = torch.zeros(_lib.ple_kv_attention_workspace(8, 2, 128), dtype=torch.uint8, device="cuda")

@@ -36,7 +36,7 @@ namespace {
 // positions, a token each, 230 us = 5.8 TB/s; 4 tokens each on up to 4096
 // positions 167 us = 3.8 TB/s (16 rows: twice the products for the same
 // bytes); one token on 131071 positions 49 us = 2.9 TB/s (start,
-// lookups and three levels of joining, which on 700 positions take 15.5 us). Bound by issue (56 % of the slots, 25 % of
+// lookups and three levels of joining, which on 700 positions take 12.4 us). Bound by issue (56 % of the slots, 25 % of
 // the matrix pipe) and by latency at the ends, with 58 % of the memory's time
 // in use on a cold cache.
 //
@@ -178,8 +178,10 @@ __device__ __forceinline__ int64_t weight_of(const Span& s, int hk) {
   return static_cast<int64_t>(s.tiles) * hk * units_of(s);
 }
 
-// Pieces of the line, one a warp; none so short that starting it is most of it.
-constexpr int kMinPiece = 8;
+// Pieces of the line, one a warp; none so short that starting and joining it
+// is most of it. One token on 700 positions, with pieces of at least 8, 4, 3, 2
+// steps: 15.6, 13.5, 12.4, 14.6 us; 4 and 16 requests of as many alike.
+constexpr int kMinPiece = 3;
 __device__ __forceinline__ int pieces_of(int64_t W, int warps) {
   const int64_t p = (W + kMinPiece - 1) / kMinPiece;
   return p < warps ? static_cast<int>(p) : warps;

@@ -62,6 +62,26 @@ def test_many_rows(T, N, E, group, with_zeros):
     check(project(x.cuda(), codes, scales, zeros), x, codes, scales, zeros, group)
 
 
+@pytest.mark.parametrize("T", [20, 40])
+@pytest.mark.parametrize("shift", [1, 3])
+def test_many_rows_strided_and_unaligned(T, shift):
+    """Rows of x far apart, scales and zero points at odd addresses, on another stream."""
+    codes, scales, zeros = weight(5001, 512, 32, True, seed=T)
+    wide = torch.randn(T, 512 + 64, generator=torch.Generator().manual_seed(T)).to(torch.bfloat16)
+    x = wide.cuda()[:, 32:32 + 512]
+    held = torch.empty(scales.numel() + shift, dtype=torch.bfloat16, device="cuda")
+    held_z = torch.empty(scales.numel() + shift, dtype=torch.uint8, device="cuda")
+    s, z = held[shift:].view(scales.shape), held_z[shift:].view(scales.shape)
+    s.copy_(scales)
+    z.copy_(torch.from_numpy(zeros))
+    out = torch.empty(T, 5001, dtype=torch.bfloat16, device="cuda")
+    stream = torch.cuda.Stream()
+    stream.wait_stream(torch.cuda.current_stream())
+    _lib.ple_proj_w4(x, torch.from_numpy(codes).cuda(), s, out, zeros=z, stream=stream)
+    torch.cuda.synchronize()
+    check(out, wide[:, 32:32 + 512], codes, scales, zeros, 32)
+
+
 @pytest.mark.parametrize("N", [1, 2, 15, 16, 17, 4099])
 def test_output_sizes(N):
     codes, scales, zeros = weight(N, 512, 128, True, seed=N)

@@ -378,18 +378,22 @@ def ple_gated_conv(kv, gate, query_start_loc, w, dilation, out, conv_state=None,
 # so their checks read each attribute once and pointers go to ctypes as plain
 # integers.
 
+_U8, _I32, _F32, _BF16 = torch.uint8, torch.int32, torch.float32, torch.bfloat16
+
+
 def _raw_stream(stream, t):
     if stream is not None:
         return stream.cuda_stream
-    return torch._C._cuda_getCurrentRawStream(t.device.index)
+    return torch._C._cuda_getCurrentRawStream(t.get_device())
 
 
 def _heads(name, t, head_dim=None):
     """Row stride and shape of [T, heads, head_dim] bf16 rows: the heads of a
     row lie together, the rows any distance apart."""
-    if t.dtype is not torch.bfloat16 or not t.is_cuda or t.dim() != 3:
+    shape = t.shape
+    if t.dtype is not _BF16 or not t.is_cuda or len(shape) != 3:
         raise ValueError(f"{name}: a CUDA bf16 tensor [T, heads, head_dim] is needed")
-    T, H, D = t.shape
+    T, H, D = shape
     stride, per_head, one = t.stride()
     if (one != 1 and D > 1) or (per_head != D and H > 1) or (head_dim is not None and D != head_dim):
         raise ValueError(f"{name}: heads of {head_dim or D} elements must lie together in a row")
@@ -404,19 +408,22 @@ def _whole(name, t, dtype, dims):
 
 def _cache_args(cache, block_table, query_start_loc, kv_lens, head_dim):
     """Kv heads, and the arguments shared by the cache's calls."""
-    at = _whole("cache", cache, torch.uint8, 4)
-    table = _whole("block_table", block_table, torch.int32, 2)
-    qsl = _whole("query_start_loc", query_start_loc, torch.int32, 1)
-    lens = _whole("kv_lens", kv_lens, torch.int32, 1)
-    pages, hk, sub, nbytes = cache.shape
-    R = kv_lens.shape[0]
-    rows, max_pages = block_table.shape
+    if (cache.dtype is not _U8 or block_table.dtype is not _I32 or query_start_loc.dtype is not _I32
+            or kv_lens.dtype is not _I32
+            or not (cache.is_contiguous() and block_table.is_contiguous() and query_start_loc.is_contiguous()
+                    and kv_lens.is_contiguous())
+            or not (cache.is_cuda and block_table.is_cuda and query_start_loc.is_cuda and kv_lens.is_cuda)):
+        raise ValueError("contiguous CUDA tensors are needed: cache uint8, block_table, query_start_loc and "
+                         "kv_lens int32")
+    pages, hk, sub, nbytes = cache.shape  # a ValueError, too, where there are more dimensions or fewer
+    (rows, max_pages), (bounds,), (R,) = block_table.shape, query_start_loc.shape, kv_lens.shape
     if nbytes != 16 * (head_dim + 8):
         raise ValueError(f"cache: blocks of {nbytes} bytes, not {16 * (head_dim + 8)} (head_dim {head_dim})")
-    if rows != R or query_start_loc.shape[0] != R + 1:
+    if rows != R or bounds != R + 1:
         raise ValueError(f"block_table must have a row, and query_start_loc an entry and one more, for "
                          f"each of the {R} requests of kv_lens")
-    return hk, (at, pages, sub * 16, table, max_pages, qsl, R, lens)
+    return hk, (cache.data_ptr(), pages, sub * 16, block_table.data_ptr(), max_pages, query_start_loc.data_ptr(), R,
+                kv_lens.data_ptr())
 
 
 def ple_kv_block_bytes(head_dim):
@@ -447,11 +454,11 @@ def ple_kv_append(q, k, v, cos_sin, cache, block_table, query_start_loc, kv_lens
         raise ValueError("q, k, v and the cache differ in tokens or kv heads")
     cs, entries, rot = None, 0, 0
     if cos_sin is not None:
-        cs = _whole("cos_sin", cos_sin, torch.float32, 2)
+        cs = _whole("cos_sin", cos_sin, _F32, 2)
         entries, rot = cos_sin.shape
     at = None
     if positions is not None:
-        at = _whole("positions", positions, torch.int32, 1)
+        at = _whole("positions", positions, _I32, 1)
         if positions.shape[0] != T:
             raise ValueError("positions must have one entry for each token")
     status = lib().ple_kv_append(
@@ -468,8 +475,8 @@ def ple_kv_read(cache, block_table, query_start_loc, kv_lens, k_out, v_out, dev_
     some = k_out if k_out is not None else v_out
     if some is None:
         raise ValueError("k_out or v_out is needed")
-    k_at = None if k_out is None else _whole("k_out", k_out, torch.bfloat16, 3)
-    v_at = None if v_out is None else _whole("v_out", v_out, torch.bfloat16, 3)
+    k_at = None if k_out is None else _whole("k_out", k_out, _BF16, 3)
+    v_at = None if v_out is None else _whole("v_out", v_out, _BF16, 3)
     if k_at is not None and v_at is not None and k_out.shape != v_out.shape:
         raise ValueError("k_out and v_out differ in shape")
     T, Hk, D = some.shape
@@ -498,7 +505,7 @@ def ple_kv_attention(q, cache, block_table, query_start_loc, kv_lens, out, works
     if To != T or Ho != H:
         raise ValueError("out must have q's shape")
     hk, c = _cache_args(cache, block_table, query_start_loc, kv_lens, D)
-    room = _whole("workspace", workspace, torch.uint8, 1)
+    room = _whole("workspace", workspace, _U8, 1)
     status = lib().ple_kv_attention(
         q.data_ptr(), q_stride, T, H, hk, D, *c, max_query_len, D ** -0.5 if scale is None else scale,
         1 if causal else 0, window, out.data_ptr(), o_stride, room, workspace.shape[0],
@@ -510,28 +517,26 @@ def ple_proj_w4(x, codes, scales, out, zeros=None, dev_err=None, stream=None):
     """out [T, N] bf16 = x [T, E] bf16 times the transpose of a 4-bit weight:
     codes uint8 [N, E / 2], scales bf16 [N, E / group], zeros uint8 like
     scales, or None for 8 everywhere."""
-    code_at = _whole("codes", codes, torch.uint8, 2)
-    scale_at = _whole("scales", scales, torch.bfloat16, 2)
-    out_at = _whole("out", out, torch.bfloat16, 2)
-    if x.dtype is not torch.bfloat16 or not x.is_cuda or x.dim() != 2:
-        raise ValueError("x: a CUDA bf16 tensor [T, E] is needed")
-    T, E = x.shape
-    N, groups = scales.shape
+    if (x.dtype is not _BF16 or codes.dtype is not _U8 or scales.dtype is not _BF16 or out.dtype is not _BF16
+            or not (codes.is_contiguous() and scales.is_contiguous() and out.is_contiguous())
+            or not (x.is_cuda and codes.is_cuda and scales.is_cuda and out.is_cuda)):
+        raise ValueError("CUDA tensors are needed: x bf16; contiguous codes uint8, scales and out bf16")
+    # a ValueError, too, where one has more dimensions or fewer
+    (T, E), (Nc, half), (N, groups), (To, No) = x.shape, codes.shape, scales.shape, out.shape
     stride, one = x.stride()
     if one != 1 and E > 1:
         raise ValueError("x: the columns of a row must lie together")
-    Nc, half = codes.shape
-    To, No = out.shape
     if Nc != N or half * 2 != E or To != T or No != N or groups < 1 or E % groups != 0:
         raise ValueError(f"x {tuple(x.shape)}, codes {tuple(codes.shape)}, scales "
                          f"{tuple(scales.shape)} and out {tuple(out.shape)} do not fit")
     zero_at = None
     if zeros is not None:
-        zero_at = _whole("zeros", zeros, torch.uint8, 2)
+        zero_at = _whole("zeros", zeros, _U8, 2)
         if zeros.shape != scales.shape:
             raise ValueError("zeros must have the shape of scales")
     status = lib().ple_proj_w4(
-        x.data_ptr(), stride if T > 1 else E, T, E, N, code_at, scale_at, zero_at, E // groups, out_at,
+        x.data_ptr(), stride if T > 1 else E, T, E, N, codes.data_ptr(), scales.data_ptr(), zero_at,
+        E // groups, out.data_ptr(),
         None if dev_err is None else dev_err.data_ptr(), _raw_stream(stream, x))
     return status if status == PLE_OK else _check("ple_proj_w4", status)
 

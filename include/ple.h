@@ -742,7 +742,8 @@ ple_status ple_kv_read(const void* cache, int64_t num_pages, int32_t page_size,
  *   scale         finite, > 0 (usually 1 / sqrt(head_dim)).
  *   window        >= 0; not 0 only with causal.
  *   max_query_len the largest n_r, if the host knows it; 0 if not. It picks
- *                 the kernel; results do not depend on it.
+ *                 kernels, whose roundings differ; no token depends on its
+ *                 being right.
  *   out           bf16 rows like q's, out_stride apart, 16-byte aligned.
  *   workspace     device scratch of ple_kv_attention_workspace(...) bytes or
  *                 more, 256-byte aligned, ZERO-FILLED before its first use;

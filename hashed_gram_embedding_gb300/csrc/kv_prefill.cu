@@ -26,7 +26,10 @@
 // 0.0028 of it, now it is its own rounding's, 0.0017). A value row outside
 // [2^-6, 512) is divided by a power of two, 2^k, and k added to its scores in
 // log2 units: the weights that meet V, and m, are those of the shifted scores,
-// the sum that divides them is that of the true ones.
+// the sum that divides them is that of the true ones. It is kept in units of
+// 2^m while that loses nothing: with shifts in [-24, 32] m stays within 40 of
+// the true scores' maximum, far inside float32's exponents. From the first
+// tile on with a shift outside, it has a maximum of its own.
 //
 // Roles (20 warps): warps 0-3 and 4-7 each own a tile of rows, a row a
 // thread: they read S, write P, scale O and write the result. Warps 8-11 turn
@@ -124,6 +127,8 @@ __device__ __forceinline__ int value_shift(uint32_t pair) {
   const int e = static_cast<int>(__float_as_uint(fmaxf(fabsf(m), fabsf(fmaf(15.0f, s, m)))) >> 23);
   return static_cast<unsigned>(e - 121) < 15u || e == 0 ? 0 : min(max(e - 127, -90), 119);
 }
+// Shifts that the sum of a row's weights cannot follow in the units of m.
+__device__ __forceinline__ bool far_shift(float shift) { return shift < -24.0f || shift > 32.0f; }
 
 __device__ __forceinline__ uint64_t f2_add(uint64_t a, uint64_t b) {
   uint64_t d;
@@ -160,7 +165,7 @@ __device__ __forceinline__ void rescale_weights(uint32_t at, float keep) {
 struct Parts {
   int most;        // parts of a piece at most; 1: none is shared
   int4* pieces;    // [pieces][2] parts (0: no such piece), rows, tile, head; first token
-  float2* sums;    // [pieces][most][rows] m, l
+  float4* sums;    // [pieces][most][rows] m; l, and the log2 of its unit
   float* outputs;  // [pieces][most][rows][D]
 };
 
@@ -348,111 +353,134 @@ attention_prefill_kernel(const AttentionArgs a, const KvCache c, const Parts par
     const uint32_t s_at = tmem + lanes + t * kTile;
     const uint32_t o_at = tmem + lanes + 2 * kTile + t * D;
     float m = -FLT_MAX, l = 0.0f, top = -FLT_MAX;
+    float lm = 0.0f;                              // once the sum has a unit of its own: l is in units of 2^lm
     bool ok = true;
     if (t == 0 || two) {
+      int j = 0;
+      // Tiles from j on; without `apart` up to the first that needs it, which
+      // keeps what is rare out of the loop that is not.
+      auto walk = [&](auto apart) {
+        constexpr bool kApart = decltype(apart)::value;
 #pragma unroll 1
-      for (int j = 0; j < n; ++j) {
-        ok = wait_for(s_full(t), j & 1, abort_flag);
-        if (gave_up(__all_sync(0xffffffffu, ok))) { ok = false; break; }
-        fence_after();
-        const int p0 = (x.first + j) * kTile;
-        const uint32_t* mask = masks + (j % kMaskRing) * kMaskWords;
-        const uint4 any = *reinterpret_cast<const uint4*>(mask + 12);
-        const bool special = p0 < all_from || p0 + kTile - 1 > all_to || (any.x | any.y | any.z | any.w) != 0;
-        if (__any_sync(0xffffffffu, top > m + kRaise)) {
-          const float next = fmaxf(m, top - kRaised);
-          const float keep = ex2(m - next);
-          m = next;
-          l *= keep;
-          // S(j) done means that the products of tile j - 1, issued before it, are done
-          if (j > 0) rescale_outputs<D>(o_at, keep);
-        }
-        // a quarter of the row at a time, in a rolled loop: what the roles run
-        // side by side has to fit the instruction caches (2048 rows of 32 heads
-        // on 16k positions: 540 us, two quarters to a turn 553, four half as long again)
-        auto quarter = [&](int q, auto shifted) {
-          float v[32];
-          tmem_load(s_at + 32 * q, v);
-          float to_log2 = factor;
-          const float* shifts = reinterpret_cast<const float*>(smem + L::kAtShifts) + (j % kMaskRing) * kTile + 32 * q;
-          if (special) {
-            const float* factors = reinterpret_cast<const float*>(smem + L::kAtFactors) + (j % kMaskRing) * kTile + 32 * q;
-            // bits of the columns that the row may see
-            const int hi = last - p0 - 32 * q, lo = from - p0 - 32 * q;  // lo..hi
-            uint32_t see = hi < 0 ? 0u : hi >= 31 ? 0xffffffffu : (2u << hi) - 1u;
-            if (lo > 0) see &= lo >= 32 ? 0u : 0xffffffffu << lo;
-            see &= mask[q];
-            if ((see & mask[4 + q]) != 0) l = NAN;
-            if (mask[8 + q] != 0) {
-#pragma unroll
-              for (int i = 0; i < 32; ++i) v[i] *= factors[i];
-            }
-            if constexpr (shifted.value) {
-              to_log2 = 1.0f;
-#pragma unroll
-              for (int i = 0; i < 32; ++i) v[i] = fmaf(v[i], factor, shifts[i]);
-            }
-#pragma unroll
-            for (int i = 0; i < 32; ++i)
-              if (!((see >> i) & 1u)) v[i] = -INFINITY;
-          }
-          float tops[2] = {v[0], v[1]};
-#pragma unroll
-          for (int i = 2; i < 32; i += 2) {
-            tops[0] = fmaxf(tops[0], v[i]);
-            tops[1] = fmaxf(tops[1], v[i + 1]);
-          }
-          top = fmaxf(top, to_log2 * fmaxf(tops[0], tops[1]));
-          if (__any_sync(0xffffffffu, top > m + kRaiseNow)) {  // by a power of two: weights are scaled exactly
-            const float next = !(top > m + kRaised) ? m : m == -FLT_MAX ? ceilf(top) - kRaised : m + ceilf(top - m) - kRaised;
+        for (; j < n; ++j) {
+          ok = wait_for(s_full(t), j & 1, abort_flag);
+          if (gave_up(__all_sync(0xffffffffu, ok))) { ok = false; break; }
+          fence_after();
+          const int p0 = (x.first + j) * kTile;
+          const uint32_t* mask = masks + (j % kMaskRing) * kMaskWords;
+          const uint4 any = *reinterpret_cast<const uint4*>(mask + 12);
+          const bool special = p0 < all_from || p0 + kTile - 1 > all_to || (any.x | any.y | any.z | any.w) != 0;
+          if (__any_sync(0xffffffffu, top > m + kRaise)) {
+            const float next = fmaxf(m, top - kRaised);
             const float keep = ex2(m - next);
             m = next;
-            l *= keep;
-            tmem_stored();
-#pragma unroll 1
-            for (int k = 0; k < q; ++k) rescale_weights(s_at + 16 * k, keep);
+            if constexpr (!kApart) l *= keep;
+            // S(j) done means that the products of tile j - 1, issued before it, are done
             if (j > 0) rescale_outputs<D>(o_at, keep);
           }
-          const uint64_t f2v = f2(to_log2, to_log2), m2 = f2(-m, -m);
-          if constexpr (shifted.value) {  // the true weights' sum
+          // a quarter of the row at a time, in a rolled loop: what the roles run
+          // side by side has to fit the instruction caches (2048 rows of 32 heads
+          // on 16k positions: 540 us, two quarters to a turn 553, four half as long again)
+          auto quarter = [&](int q, auto shifted) {
+            float v[32];
+            tmem_load(s_at + 32 * q, v);
+            float to_log2 = factor;
+            const float* shifts = reinterpret_cast<const float*>(smem + L::kAtShifts) + (j % kMaskRing) * kTile + 32 * q;
+            if (shifted.value || special) {
+              const float* factors = reinterpret_cast<const float*>(smem + L::kAtFactors) + (j % kMaskRing) * kTile + 32 * q;
+              // bits of the columns that the row may see
+              const int hi = last - p0 - 32 * q, lo = from - p0 - 32 * q;  // lo..hi
+              uint32_t see = hi < 0 ? 0u : hi >= 31 ? 0xffffffffu : (2u << hi) - 1u;
+              if (lo > 0) see &= lo >= 32 ? 0u : 0xffffffffu << lo;
+              see &= mask[q];
+              if ((see & mask[4 + q]) != 0) l = NAN;
+              if (mask[8 + q] != 0) {
 #pragma unroll
-            for (int i = 0; i < 32; ++i) l += ex2(v[i] - shifts[i] - m);
-          }
-          uint64_t sum = f2(0.0f, 0.0f);
-          uint32_t p[16];
+                for (int i = 0; i < 32; ++i) v[i] *= factors[i];
+              }
+              if constexpr (shifted.value) {
+                to_log2 = 1.0f;
 #pragma unroll
-          for (int i = 0; i < 32; i += 2) {
-            float e0, e1;
-            f2_split(f2_fma(f2(v[i], v[i + 1]), f2v, m2), e0, e1);
-            e0 = ex2(e0);
-            e1 = ex2(e1);
-            sum = f2_add(sum, f2(e0, e1));
-            p[i >> 1] = f16_pair(e0, e1);
+                for (int i = 0; i < 32; ++i) v[i] = fmaf(v[i], factor, shifts[i]);
+              }
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                if (!((see >> i) & 1u)) v[i] = -INFINITY;
+            }
+            float tops[2] = {v[0], v[1]};
+#pragma unroll
+            for (int i = 2; i < 32; i += 2) {
+              tops[0] = fmaxf(tops[0], v[i]);
+              tops[1] = fmaxf(tops[1], v[i + 1]);
+            }
+            top = fmaxf(top, to_log2 * fmaxf(tops[0], tops[1]));
+            if (__any_sync(0xffffffffu, top > m + kRaiseNow)) {  // by a power of two: weights are scaled exactly
+              const float next = !(top > m + kRaised) ? m : m == -FLT_MAX ? ceilf(top) - kRaised : m + ceilf(top - m) - kRaised;
+              const float keep = ex2(m - next);
+              m = next;
+              if constexpr (!kApart) l *= keep;
+              tmem_stored();
+#pragma unroll 1
+              for (int k = 0; k < q; ++k) rescale_weights(s_at + 16 * k, keep);
+              if (j > 0) rescale_outputs<D>(o_at, keep);
+            }
+            const uint64_t f2v = f2(to_log2, to_log2), m2 = f2(-m, -m);
+            if constexpr (shifted.value) {  // the true weights' sum
+              if constexpr (kApart) {
+                float most = lm;
+#pragma unroll
+                for (int i = 0; i < 32; ++i) most = fmaxf(most, v[i] - shifts[i]);
+                l *= ex2(lm - most);
+                lm = most;
+              }
+              const float unit = kApart ? lm : m;
+#pragma unroll
+              for (int i = 0; i < 32; ++i) l += ex2(v[i] - shifts[i] - unit);
+            }
+            uint64_t sum = f2(0.0f, 0.0f);
+            uint32_t p[16];
+#pragma unroll
+            for (int i = 0; i < 32; i += 2) {
+              float e0, e1;
+              f2_split(f2_fma(f2(v[i], v[i + 1]), f2v, m2), e0, e1);
+              e0 = ex2(e0);
+              e1 = ex2(e1);
+              sum = f2_add(sum, f2(e0, e1));
+              p[i >> 1] = f16_pair(e0, e1);
+            }
+            tmem_store16(s_at + 16 * q, p);  // over columns already read
+            float l0, l1;
+            f2_split(sum, l0, l1);
+            if constexpr (!shifted.value) l += l0 + l1;
+          };
+          if (kApart || (special && (mask[16] | mask[17] | mask[18] | mask[19]) != 0)) {
+            if constexpr (!kApart) {
+              // looked at here, where it is rare: four more words of masks cost 5 %
+              const float4 sh = reinterpret_cast<const float4*>(smem + L::kAtShifts)[(j % kMaskRing) * (kTile / 4) + lane];
+              if (__any_sync(0xffffffffu, far_shift(sh.x) || far_shift(sh.y) || far_shift(sh.z) || far_shift(sh.w))) return;
+            }
+#pragma unroll 1
+            for (int q = 0; q < 4; ++q) quarter(q, std::true_type{});
+          } else if constexpr (!kApart) {
+#pragma unroll 1
+            for (int q = 0; q < 4; ++q) quarter(q, std::false_type{});
           }
-          tmem_store16(s_at + 16 * q, p);  // over columns already read
-          float l0, l1;
-          f2_split(sum, l0, l1);
-          if constexpr (!shifted.value) l += l0 + l1;
-        };
-        if (special && (mask[16] | mask[17] | mask[18] | mask[19]) != 0) {
-#pragma unroll 1
-          for (int q = 0; q < 4; ++q) quarter(q, std::true_type{});
-        } else {
-#pragma unroll 1
-          for (int q = 0; q < 4; ++q) quarter(q, std::false_type{});
+          tmem_stored();
+          fence_before();
+          warp_arrive(p_full(t));
         }
-        tmem_stored();
-        fence_before();
-        warp_arrive(p_full(t));
-      }
+      };
+      walk(std::false_type{});
+      lm = m;
+      if (ok && j < n) walk(std::true_type{});
       if (n > 0 && ok) {
         ok = wait_for(o_full, 0, abort_flag);
         ok = !gave_up(__all_sync(0xffffffffu, ok));
         fence_after();
       }
       const int64_t slot = static_cast<int64_t>(blockIdx.x) * L::kRows + in_tile;
-      if (x.parts > 1) parts.sums[slot] = make_float2(m, l);
-      const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+      if (x.parts > 1) parts.sums[slot] = make_float4(m, l, lm, 0.0f);
+      const float inv = l == 0.0f ? 0.0f : 1.0f / l * ex2(m - lm);
       ple_bf16_t* dst = a.out + static_cast<int64_t>(x.t0 + token) * a.out_stride + head;
 #pragma unroll 1
       for (int q = 0; q < D / 32; ++q) {
@@ -764,7 +792,7 @@ attention_prefill_kernel(const AttentionArgs a, const KvCache c, const Parts par
 }
 
 // A row a warp: the parts' outputs, weighted by how far each one's m is below
-// the largest.
+// the largest, and their sums by their own units.
 constexpr int kJoinWarps = 8, kJoinRows = 32;  // rows of a CTA
 
 template <int D>
@@ -781,13 +809,16 @@ attention_join_kernel(const AttentionArgs a, const KvCache c, const Parts parts)
   constexpr int kMine = D / 32;  // columns of a lane
   for (int row = row0 + threadIdx.x / 32; row < min(row0 + kJoinRows, rows); row += kJoinWarps) {
     const int64_t slot = static_cast<int64_t>(piece) * parts.most * kRows + row;
-    float2 ml = make_float2(-FLT_MAX, 0.0f);
+    float4 ml = make_float4(-FLT_MAX, 0.0f, -FLT_MAX, 0.0f);
     if (lane < count) ml = parts.sums[slot + lane * kRows];
-    float most = ml.x;
+    float most = ml.x, unit = ml.z;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
+    for (int o = 16; o > 0; o >>= 1) {
+      most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
+      unit = fmaxf(unit, __shfl_xor_sync(0xffffffffu, unit, o));
+    }
     const float w = ex2(ml.x - most);
-    float sum = w * ml.y;
+    float sum = ex2(ml.z - unit) * ml.y;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     float acc[kMine] = {};
@@ -802,7 +833,7 @@ attention_join_kernel(const AttentionArgs a, const KvCache c, const Parts parts)
         acc[k + 1] = fmaf(wi, v.y, acc[k + 1]);
       }
     }
-    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum * ex2(most - unit);
     const int flat = x.z * kRows + row, token = flat / G;
     ple_bf16_t* dst = a.out + static_cast<int64_t>(t0 + token) * a.out_stride +
                       static_cast<int64_t>(x.w * G + (flat - token * G)) * D + lane * kMine;
@@ -824,7 +855,7 @@ cudaError_t launch(const AttentionArgs& a, const KvCache& c, uint8_t* room, size
   const int64_t pieces = (requests == 1 ? (rows + kRows - 1) / kRows : rows / kRows + requests) * c.num_kv_heads;
   // Parts: what makes the fullest turns of all SMs, in tiles of the longest
   // context that the table has room for; a CTA's start and end cost some 6 tiles.
-  constexpr size_t kPartBytes = kRows * (D * sizeof(float) + sizeof(float2));
+  constexpr size_t kPartBytes = kRows * (D * sizeof(float) + sizeof(float4));
   const int64_t cap = static_cast<int64_t>((room_bytes - 1024) / (kPartBytes + 2 * sizeof(int4)));
   int64_t seen = static_cast<int64_t>(c.max_pages) * c.page_size;
   if (a.window > 0) seen = std::min(seen, static_cast<int64_t>(a.window) + kRows / group + 1);
@@ -841,7 +872,7 @@ cudaError_t launch(const AttentionArgs& a, const KvCache& c, uint8_t* room, size
   Parts parts{most, nullptr, nullptr, nullptr};
   if (most > 1) {
     parts.pieces = reinterpret_cast<int4*>(room);
-    parts.sums = reinterpret_cast<float2*>(room + (pieces * 2 * sizeof(int4) + 255) / 256 * 256);
+    parts.sums = reinterpret_cast<float4*>(room + (pieces * 2 * sizeof(int4) + 255) / 256 * 256);
     parts.outputs = reinterpret_cast<float*>(parts.sums + pieces * most * kRows);
   }
   const cudaError_t run = launch_kernel(kernel, dim3(static_cast<unsigned>(pieces * most)), dim3(kThreads),

@@ -1,0 +1,46 @@
+"""ple_kv_attention on the GPU where values, keys and queries lie far from one: what float32 holds of the
+float64 result, row by row (the bounds are those of _rows.py)."""
+
+import numpy as np
+import pytest
+import torch
+
+from _four_bit import Batch, bits
+from _helpers import bf16_values, dev_err_word
+from _rows import faults, reference
+from test_gpu_kv_attention import attend
+
+pytestmark = pytest.mark.gpu
+
+
+def run(b, q, scale=None, **kw):
+    err = dev_err_word()
+    out = attend(b, q, scale=scale, err=err, **kw)
+    assert int(err.item()) == 0
+    got = faults(bf16_values(bits(out)), *reference(b, bits(q), scale))
+    assert not got, got
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("queries,length", [(120, 256), (40, 2600)])
+@pytest.mark.parametrize("first,then", [(1e-12, 1e30), (1e30, 1e-12), (1e-6, 1e4), (1e-25, 1e25)])
+def test_values_that_leap(dim, queries, length, first, then):
+    """Values of one size for half of the positions, of another for the rest: the sum of the weights outlives
+    what the outputs are scaled by."""
+    b = Batch([queries], [length], 4, 1, dim, 16, seed=3, k_mean=0.0)
+    for p in range(length):
+        b.put(0, p, b.rng.normal(0, 1, (1, dim)), b.rng.normal(0, first if p < length // 2 else then, (1, dim)))
+    run(b, b.rows(4))
+
+
+@pytest.mark.parametrize("queries,length", [(60, 2600), (300, 1500)])
+@pytest.mark.parametrize("at", [0, 700, 1300])
+def test_one_huge_value_among_many_small_weights(queries, length, at):
+    """A value of 2e36 takes a weight 2^12 times those of the others, which together weigh as much."""
+    b = Batch([queries], [length], 4, 1, 128, 16, seed=5)
+    for p in range(length):
+        b.put(0, p, np.zeros((1, 128)), b.rng.normal(0, 1, (1, 128)))
+    b.put(0, at, np.full((1, 128), 0.55), b.rng.uniform(0.5, 1, (1, 128)) * 2e36)
+    q = b.rows(4)
+    q[:] = q.abs() + 0.5
+    run(b, q)

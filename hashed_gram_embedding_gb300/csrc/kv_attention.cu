@@ -43,7 +43,7 @@ namespace {
 // Products, on warp-wide matrix instructions (16 x 8 x 16, f32 sums; reading
 // the cache and unpacking it, not their rate, is the bound):
 //   S^T = K Q^T     16 tokens x 8 query rows, f16
-//   O^T = V^T P^T   16 elements x 8 query rows, bf16
+//   O^T = V^T P^T   16 elements x 8 query rows, f16
 // so that a group of up to 8 query heads fills a tile, and the codes are the
 // A operand of both. Unpacking a word of 8 codes:
 //   Masked out where they stand, a byte's codes are subnormal numbers that no
@@ -52,20 +52,21 @@ namespace {
 //   four masks and one shift by a byte.
 //   K: f16 subnormals multiply as they are; the query elements that meet the
 //     second kind are divided by 16, and 2^24 goes into the rows' factors.
-//   V: bf16 subnormals as they are, too: the weights carry a factor of 2^100
-//     that brings the products back among the normal numbers (2^-33 of the
-//     result, 2^-29 for the second kind). Weights that 2^100 might carry out
-//     of range - a value's scale above 2^18 - meet codes multiplied by 2^100
-//     instead, on a path of their own.
+//   V: f16 subnormals as they are, too; the sums are multiplied by 2^24, or
+//     2^20, at the end. Where a step has scales outside [2^-9, 2^10), whose
+//     weights f16 would not hold or lose bits of, weights are bf16, and so are
+//     codes, multiplied by 2^115 to meet them among the normal numbers.
 // Query rows are scaled to [1, 2) by a power of two each, which keeps f16
 // exact for bf16 queries (elements below 2^-14 of the row's largest round at
 // 2^-24 of it). Scale and offset of a token meet the float32 sums instead of
 // its elements:
 //   <q, K_t> = s_t sum_d q_d c_td + m_t sum_d q_d
-//   sum_t p_t V_t = sum_t p'_t c_t - 8 sum_t p'_t + sum_t p_t (m_t + 8 s_t),  p' = bf16(p s)
-// p' is the only rounding to fewer bits, and it meets codes centred on 8, so
-// that an offset far from zero costs no precision; sum p' is one more row of
-// the product, by constants.
+//   sum_t p_t V_t = sum_t p'_t c_t - 8 sum_t p'_t + sum_t p_t (m_t + 8 s_t),  p' = f16(p s)
+// p' is the only rounding to fewer bits (2^-11 of it, or 2^-25; bf16: 2^-8 of
+// it, with which the result's error was 0.0024 of it throughout, now it is its
+// own rounding's, 0.0017). It meets codes centred on 8, so that an offset far
+// from zero costs no precision; sum p' is one more row of the product, by
+// constants. p is at most 2^6.
 // The contraction index of a product may run in any order: a lane's 16 bytes
 // of a K row are 32 neighbouring elements, and the query's fragments follow
 // that order; two tokens' V bytes are interleaved with one permute a word.
@@ -112,9 +113,9 @@ __device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// A pair of bf16 subnormals times 2^100.
-__device__ __forceinline__ uint32_t times_2_100(uint32_t x) {
-  return bf2_mul(x, 0x71807180u);
+// A pair of bf16 subnormals times 2^115.
+__device__ __forceinline__ uint32_t times_2_115(uint32_t x) {
+  return bf2_mul(x, 0x79007900u);
 }
 
 __device__ __forceinline__ uint64_t f2_add(uint64_t a, uint64_t b) {
@@ -674,7 +675,7 @@ attention_split_kernel(const AttentionArgs a, const KvCache c, unsigned* __restr
         // scores in units of log2: scale and offset, then the mask; two rows at a time
         float vs[2][2], vm[2][2];  // the values' scale, and offset + 8 scales
         uint32_t unseen = 0;       // bit (query tile, block, token, row)
-        bool large = false;        // a scale that 2^100 would carry out of range
+        float most = 0.0f;         // of the scales that the lane's rows see
 #pragma unroll
         for (int b = 0; b < 2; ++b)
 #pragma unroll
@@ -685,7 +686,6 @@ attention_split_kernel(const AttentionArgs a, const KvCache c, unsigned* __restr
             const uint64_t ks = f2(bf_lo(kp), bf_lo(kp)), km = f2(bf_hi(kp), bf_hi(kp));
             vs[b][e] = bf_lo(vp);
             vm[b][e] = fmaf(8.0f, bf_lo(vp), bf_hi(vp));
-            large |= !(vs[b][e] <= 262144.0f);
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
               const uint64_t f = *reinterpret_cast<const uint64_t*>(row_info + n * 8 + 2 * j);
@@ -708,10 +708,14 @@ attention_split_kernel(const AttentionArgs a, const KvCache c, unsigned* __restr
                   }
                 }
               }
+              constexpr uint32_t kRowBits = 0x03030303u >> (8 * (4 - NT));
+              if ((~unseen & (kRowBits << (b * 4 + e * 2))) != 0) most = fmaxf(most, fabsf(vs[b][e]));
+            } else {
+              most = fmaxf(most, fabsf(vs[b][e]));
             }
           }
-        // The running maximum is raised only when a score passes it by 2^8:
-        // weights of up to 256 cost no precision in float32 or bf16, and a
+        // The running maximum is raised only when a score passes it by 2^6:
+        // weights of up to 64 cost no precision in float32 or f16, and a
         // step without a raise needs no exchange between lanes.
         bool raise = false;
         float top[2 * NT];
@@ -721,7 +725,7 @@ attention_split_kernel(const AttentionArgs a, const KvCache c, unsigned* __restr
           for (int i = 0; i < 2; ++i) {
             const float t = fmaxf(fmaxf(s[n][0][i], s[n][0][2 + i]), fmaxf(s[n][1][i], s[n][1][2 + i]));
             top[2 * n + i] = t;
-            raise |= t > m[2 * n + i] + 8.0f;
+            raise |= t > m[2 * n + i] + 6.0f;
           }
         if (__any_sync(0xffffffffu, raise)) {
 #pragma unroll
@@ -743,14 +747,14 @@ attention_split_kernel(const AttentionArgs a, const KvCache c, unsigned* __restr
             for (int u = 0; u < D / 16; ++u) { o[n][u][e] *= keep; o[n][u][2 + e] *= keep; }
           }
         }
-        large = __any_sync(0xffffffffu, large);
-        uint32_t pt[NT][2][2];  // weights times the values' scale (times 2^100), bf16, as B fragments
+        const bool wide = __any_sync(0xffffffffu, !(most < 1024.0f) || (most < 0x1p-9f && most > 0.0f));
+        uint32_t pt[NT][2][2];  // weights times the values' scale as B fragments: f16, or bf16 times 2^-6
         auto weights = [&](auto with_mask) {
 #pragma unroll
           for (int b = 0; b < 2; ++b)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              const float by = large ? vs[b][e] : vs[b][e] * 0x1p100f;
+              const float by = wide ? vs[b][e] * 0x1p-6f : vs[b][e];
               const uint64_t by2 = f2(by, by), vm2 = f2(vm[b][e], vm[b][e]);
 #pragma unroll
               for (int n = 0; n < NT; ++n) {
@@ -773,13 +777,13 @@ attention_split_kernel(const AttentionArgs a, const KvCache c, unsigned* __restr
                   next = f2(now[0], now[1]);
                 }
                 off2[n] = next;
-                pt[n][b][e] = transpose8x8(pack2(w[0], w[1]));
+                pt[n][b][e] = transpose8x8(wide ? pack2(w[0], w[1]) : pack_f16(w[0], w[1]));
               }
             }
         };
         if (masked) weights(std::true_type{});
         else weights(std::false_type{});
-        auto values = [&](auto scaled) {  // scaled: 2^100 is in the codes, not in the weights
+        auto values = [&](auto in_bf16) {
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
           const uint8_t* vb = st + b * B::kBytes + B::kV + g * (D / 16);
@@ -792,10 +796,15 @@ attention_split_kernel(const AttentionArgs a, const KvCache c, unsigned* __restr
             else if constexpr (kVWords == 2) *reinterpret_cast<uint2*>(v[i]) = *reinterpret_cast<const uint2*>(p);
             else v[i][0] = *reinterpret_cast<const uint32_t*>(p);
           }
-          constexpr uint32_t kOne = decltype(scaled)::value ? 0x3F803F80u : 0x0D800D80u;  // 1, or 2^-100
+          constexpr bool kBf16 = decltype(in_bf16)::value;
+          constexpr uint32_t kOne = kBf16 ? 0x42804280u : 0x3C003C00u;  // 2^6, or 1
+          auto product = [](float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+            if constexpr (kBf16) mma_bf16(c, a0, a1, a2, a3, b0, b1);
+            else mma_f16(c, a0, a1, a2, a3, b0, b1);
+          };
 #pragma unroll
-          for (int n = 0; n < NT; ++n) mma_bf16(sum[n], kOne, kOne, kOne, kOne, pt[n][b][0], pt[n][b][1]);
-          auto code = [](uint32_t x, int i) { return decltype(scaled)::value ? times_2_100(code_bits(x, i)) : code_bits(x, i); };
+          for (int n = 0; n < NT; ++n) product(sum[n], kOne, kOne, kOne, kOne, pt[n][b][0], pt[n][b][1]);
+          auto code = [](uint32_t x, int i) { return kBf16 ? times_2_115(code_bits(x, i)) : code_bits(x, i); };
 #pragma unroll
           for (int w = 0; w < kVWords; ++w)
 #pragma unroll
@@ -808,12 +817,12 @@ attention_split_kernel(const AttentionArgs a, const KvCache c, unsigned* __restr
                 const uint32_t a2 = code(x1, 2 * k), a3 = code(x1, 2 * k + 1);
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
-                  mma_bf16(o[n][w * 4 + half * 2 + k], a0, a1, a2, a3, pt[n][b][0], pt[n][b][1]);
+                  product(o[n][w * 4 + half * 2 + k], a0, a1, a2, a3, pt[n][b][0], pt[n][b][1]);
               }
             }
         }
         };
-        if (large) values(std::true_type{});
+        if (wide) values(std::true_type{});
         else values(std::false_type{});
       }
       __syncwarp();  // every lane has read the stage
@@ -840,8 +849,8 @@ attention_split_kernel(const AttentionArgs a, const KvCache c, unsigned* __restr
         off[e] = fmaf(-8.0f, sum[n][e], off[e]);
 #pragma unroll
         for (int u = 0; u < D / 16; ++u) {
-          o[n][u][e] = fmaf(0x1p33f, o[n][u][e], off[e]);
-          o[n][u][2 + e] = fmaf(0x1p29f, o[n][u][2 + e], off[e]);
+          o[n][u][e] = fmaf(0x1p24f, o[n][u][e], off[e]);
+          o[n][u][2 + e] = fmaf(0x1p20f, o[n][u][2 + e], off[e]);
         }
       }
     }

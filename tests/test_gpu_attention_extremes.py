@@ -7,22 +7,22 @@ import torch
 
 from _four_bit import Batch, bits
 from _helpers import bf16_values, dev_err_word
-from _rows import faults, reference
+from _rows import F16, U, faults, reference
 from test_gpu_kv_attention import attend
 
 pytestmark = pytest.mark.gpu
 
 
-def run(b, q, scale=None, **kw):
+def run(b, q, scale=None, weights=F16, **kw):
     err = dev_err_word()
     out = attend(b, q, scale=scale, err=err, **kw)
     assert int(err.item()) == 0
-    got = faults(bf16_values(bits(out)), *reference(b, bits(q), scale))
+    got = faults(bf16_values(bits(out)), *reference(b, bits(q), scale), weights=weights)
     assert not got, got
 
 
 @pytest.mark.parametrize("dim", [64, 128, 256])
-@pytest.mark.parametrize("queries,length", [(120, 256), (40, 2600)])
+@pytest.mark.parametrize("queries,length", [(120, 256), (40, 2600), (3, 300)])
 @pytest.mark.parametrize("first,then", [(1e-12, 1e30), (1e30, 1e-12), (1e-6, 1e4), (1e-25, 1e25)])
 def test_values_that_leap(dim, queries, length, first, then):
     """Values of one size for half of the positions, of another for the rest: the sum of the weights outlives
@@ -30,7 +30,7 @@ def test_values_that_leap(dim, queries, length, first, then):
     b = Batch([queries], [length], 4, 1, dim, 16, seed=3, k_mean=0.0)
     for p in range(length):
         b.put(0, p, b.rng.normal(0, 1, (1, dim)), b.rng.normal(0, first if p < length // 2 else then, (1, dim)))
-    run(b, b.rows(4))
+    run(b, b.rows(4), weights=U if queries == 3 else F16)
 
 
 @pytest.mark.parametrize("queries,length", [(60, 2600), (300, 1500)])

@@ -51,15 +51,16 @@ namespace {
 //   as bf16), bits 4-7 sixteen times that. So a word of eight codes takes
 //   four masks and one shift by a byte.
 //   K: f16 subnormals multiply as they are; the query elements that meet the
-//     second kind are divided by 16, and 2^24 goes into the rows' factors.
+//     second kind are divided by 16, and of 2^24 what the query rows leave
+//     goes into the rows' factors and the keys' scales.
 //   V: f16 subnormals as they are, too; the sums are multiplied by 2^24, or
 //     2^20, at the end. Where a step has scales outside [2^-9, 2^10), whose
 //     weights f16 would not hold or lose bits of, weights are bf16, and so are
 //     codes, multiplied by 2^115 to meet them among the normal numbers.
-// Query rows are scaled to [1, 2) by a power of two each, which keeps f16
-// exact for bf16 queries (elements below 2^-14 of the row's largest round at
-// 2^-24 of it). Scale and offset of a token meet the float32 sums instead of
-// its elements:
+// Query rows are scaled to [2^15, 2^16) by a power of two each, which keeps f16
+// exact for bf16 queries: elements below 2^-28 of the row's largest, or 2^-24
+// where they are divided by 16, lose bits. Scale and offset of a token meet
+// the float32 sums instead of its elements:
 //   <q, K_t> = s_t sum_d q_d c_td + m_t sum_d q_d
 //   sum_t p_t V_t = sum_t p'_t c_t - 8 sum_t p'_t + sum_t p_t (m_t + 8 s_t),  p' = f16(p s)
 // p' is the only rounding to fewer bits (2^-11 of it, or 2^-25; bf16: 2^-8 of
@@ -550,9 +551,9 @@ attention_split_kernel(const AttentionArgs a, const KvCache c, unsigned* __restr
       }
       top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
       top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-      // 2^k <= top < 2^(k + 1)
-      const int k = top > 0.0f && top < INFINITY ? max(ilogbf(top), -126) : 0;
-      const float down = ldexpf(1.0f, -k);
+      // 2^k <= top < 2^(k + 1), or below
+      const int k = top > 0.0f && top < INFINITY ? max(ilogbf(top), -100) : 0;
+      const float down = ldexpf(1.0f, 15 - k);
       float even = 0.0f, odd = 0.0f;  // sums of the elements; the odd ones' are of sixteenths
 #pragma unroll
       for (int w = 0; w < kWords; ++w) {
@@ -581,8 +582,10 @@ attention_split_kernel(const AttentionArgs a, const KvCache c, unsigned* __restr
         odd += __shfl_xor_sync(0xffffffffu, odd, x2);
       }
       if (j == 0) {
-        row_info[rr] = ldexpf(a.scale_log2, k + 24);
-        row_info[kRows + rr] = ldexpf(fmaf(16.0f, odd, even), -24);
+        // 2^(24 + k - 15) is to come: 2^6 of it with the keys' scales, so that
+        // neither is infinite for a row of bf16's largest queries, or keys
+        row_info[rr] = ldexpf(a.scale_log2, k + 3);
+        row_info[kRows + rr] = ldexpf(fmaf(16.0f, odd, even), -18);
         const int last = a.causal ? it->len - it->n + token : it->len - 1;
         row_last[rr] = rr < rows ? last : -1;
         row_out[rr] = static_cast<int64_t>(it->t0 + token) * a.out_stride + head;
@@ -681,7 +684,8 @@ attention_split_kernel(const AttentionArgs a, const KvCache c, unsigned* __restr
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             const int tok = r0 + 8 * e;
-            const uint32_t kp = *reinterpret_cast<const uint32_t*>(st + b * B::kBytes + B::kPairs + tok * 4);
+            const uint32_t kp = bf2_mul(*reinterpret_cast<const uint32_t*>(st + b * B::kBytes + B::kPairs + tok * 4),
+                                        0x3F804280u);  // the scale times 2^6
             const uint32_t vp = *reinterpret_cast<const uint32_t*>(st + b * B::kBytes + B::kVPairs + tok * 4);
             const uint64_t ks = f2(bf_lo(kp), bf_lo(kp)), km = f2(bf_hi(kp), bf_hi(kp));
             vs[b][e] = bf_lo(vp);

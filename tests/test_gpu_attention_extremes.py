@@ -44,3 +44,30 @@ def test_one_huge_value_among_many_small_weights(queries, length, at):
     q = b.rows(4)
     q[:] = q.abs() + 0.5
     run(b, q)
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("queries", [2, 100])
+@pytest.mark.parametrize("exponent", [-115, 95, 104, 122])
+def test_queries_of_any_size(dim, queries, exponent):
+    """Every kernel takes the queries that the others take: rows near both ends of bf16's range, keys to match."""
+    b = Batch([queries], [150], 4, 1, dim, 16, seed=7, k_mean=0.0)
+    for p in range(150):
+        b.put(0, p, b.rng.normal(0, 2.0 ** min(-exponent, 100), (1, dim)), b.rng.normal(0, 1, (1, dim)))
+    q = b.rows(4, 2.0 ** exponent)
+    q[0, 1] = 0.0
+    run(b, q)
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("queries", [2, 100])
+def test_small_elements_of_a_query_count(dim, queries):
+    """One element of a query row 2^12 times the others, met by zeros in the keys."""
+    b = Batch([queries], [150], 4, 1, dim, 16, seed=9)
+    for p in range(150):
+        k = np.abs(b.rng.normal(0, 1, (1, dim)))
+        k[:, 3] = 0.0
+        b.put(0, p, k, b.rng.normal(0, 1, (1, dim)))
+    q = b.rows(4)
+    q[:, :, 3] = 4096.0
+    run(b, q)

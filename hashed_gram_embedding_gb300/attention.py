@@ -74,6 +74,8 @@ class PLEAttention:
         self.qkv = torch.empty((self.max_tokens, rows), dtype=torch.bfloat16, device=device)
         self.mixed = torch.empty((self.max_tokens, self.num_heads, self.head_dim), dtype=torch.bfloat16,
                                  device=device)
+        # the fills above are on this stream, and a first step may be on any
+        torch.cuda.current_stream(device).synchronize()
 
     def forward(self, hidden, block_table, query_start_loc, kv_lens, positions=None, max_query_len=0,
                 dev_err=None, stream=None, out=None):
@@ -82,14 +84,17 @@ class PLEAttention:
         query_start_loc int32 [R + 1], kv_lens int32 [R] (this step's tokens
         included); positions int32 [T] or None for the places in the cache;
         max_query_len: the most tokens of a request, if known. The steps of one
-        block run one after another (they share its buffers)."""
+        block run one after another (they share its buffers): a step on another
+        stream than the last one's has to wait for it. A result that has no
+        place given is a tensor of the stream that the step runs on."""
         T = hidden.shape[0]
         if T > self.max_tokens:
             raise ValueError(f"{T} tokens, and buffers for {self.max_tokens}")
         H, Hk, D = self.num_heads, self.num_kv_heads, self.head_dim
         qkv, mixed = self.qkv[:T], self.mixed[:T]
         if out is None:
-            out = torch.empty((T, self.hidden), dtype=torch.bfloat16, device=hidden.device)
+            with torch.cuda.stream(stream):  # where its memory may be written at once (None: the current one)
+                out = torch.empty((T, self.hidden), dtype=torch.bfloat16, device=hidden.device)
         codes, scales, zeros = self.w_qkv
         _lib.ple_proj_w4(hidden, codes, scales, qkv, zeros=zeros, dev_err=dev_err, stream=stream)
         q, k, v = qkv.view(T, H + 2 * Hk, D).split((H, Hk, Hk), dim=1)

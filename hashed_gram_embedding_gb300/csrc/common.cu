@@ -26,6 +26,33 @@ ple_status fail(ple_status status, const char* fmt, ...) {
   return status;
 }
 
+bool rows_overlap(RowSpan a, RowSpan b) {
+  using wide = __int128;  // strides are the caller's
+  wide at[2] = {static_cast<wide>(reinterpret_cast<uintptr_t>(a.base)), static_cast<wide>(reinterpret_cast<uintptr_t>(b.base))};
+  RowSpan* const rows[2] = {&a, &b};
+  for (int i = 0; i < 2; ++i) {
+    RowSpan& r = *rows[i];
+    if (r.count <= 0 || r.width <= 0) return false;
+    if (r.stride < 0) {
+      at[i] += static_cast<wide>(r.stride) * (r.count - 1);
+      r.stride = -r.stride;
+    }
+    if (r.stride == 0) r.count = 1;
+    if (r.stride == r.width) {  // one piece
+      r.width *= r.count;
+      r.count = 1;
+    }
+  }
+  const wide d = at[1] - at[0];
+  if (a.count > 1 && b.count > 1 && a.stride != b.stride)
+    return d < static_cast<wide>(a.stride) * (a.count - 1) + a.width && -d < static_cast<wide>(b.stride) * (b.count - 1) + b.width;
+  const wide s = a.count > 1 ? a.stride : b.count > 1 ? b.stride : 1;
+  // row i of a and row j of b meet where -b.width < d + (j - i) s < a.width
+  auto floor_div = [](wide x, wide y) { return x / y - (x % y != 0 && x < 0); };
+  const wide low = floor_div(-b.width - d, s) + 1, high = -floor_div(d - a.width, s) - 1;
+  return (low > 1 - a.count ? low : 1 - a.count) <= (high < b.count - 1 ? high : b.count - 1);
+}
+
 ple_status check_cuda(cudaError_t err, const char* what) {
   if (err == cudaSuccess) return PLE_OK;
   return fail(PLE_ERR_CUDA, "%s: %s (%s)", what, cudaGetErrorName(err),

@@ -26,6 +26,15 @@ inline bool overlaps(const void* a, size_t na, const void* b, size_t nb) {
   auto pb = reinterpret_cast<uintptr_t>(b);
   return pa < pb + nb && pb < pa + na;
 }
+// Rows of `width` bytes, `stride` bytes apart.
+struct RowSpan {
+  const void* base;
+  int64_t count, stride, width;
+};
+// True if a row of a and a row of b share a byte. Exact for rows that lie as
+// far apart in both (columns of one wide tensor) or where one of the two is a
+// single piece; else by the bytes from the first row to the last.
+bool rows_overlap(RowSpan a, RowSpan b);
 inline bool aligned16(const void* p) {
   return (reinterpret_cast<uintptr_t>(p) & 15u) == 0;
 }

@@ -986,6 +986,10 @@ PLE_EXPORT ple_status ple_kv_attention(const ple_bf16_t* q, int64_t q_stride, in
     return fail(PLE_ERR_INVALID_ARG, "%s: %d heads over %d kv heads", name, num_heads, num_kv_heads);
   if (q == nullptr || out == nullptr || !aligned16(q) || !aligned16(out) || q_stride % 8 != 0 || out_stride % 8 != 0)
     return fail(PLE_ERR_INVALID_ARG, "%s: q and out must be 16-byte aligned, their strides multiples of 8", name);
+  const int64_t row = int64_t(num_heads) * head_dim * 2;
+  if (!(q == out && q_stride == out_stride) &&
+      rows_overlap({out, num_tokens, out_stride * 2, row}, {q, num_tokens, q_stride * 2, row}))
+    return fail(PLE_ERR_INVALID_ARG, "%s: out overlaps q without being it", name);
   if (!(scale > 0.0f) || !std::isfinite(scale))
     return fail(PLE_ERR_INVALID_ARG, "%s: scale %g", name, scale);
   if (max_query_len < 0 || window < 0 || (window > 0 && !causal))

@@ -385,6 +385,13 @@ PLE_EXPORT ple_status ple_kv_append(const ple_bf16_t* q, int64_t q_stride, const
     return fail(PLE_ERR_INVALID_ARG, "%s: row strides must be multiples of 8", name);
   if (cos_sin != nullptr && (rotary_dim <= 0 || rotary_dim % 16 != 0 || rotary_dim > head_dim))
     return fail(PLE_ERR_UNSUPPORTED, "%s: rotary_dim %d (a multiple of 16, at most head_dim)", name, rotary_dim);
+  if (q != nullptr) {
+    const int64_t wide = int64_t(num_heads) * head_dim * 2, narrow = int64_t(num_kv_heads) * head_dim * 2;
+    const RowSpan to{q_out, num_tokens, q_out_stride * 2, wide};
+    if ((!(q == q_out && q_stride == q_out_stride) && rows_overlap(to, {q, num_tokens, q_stride * 2, wide})) ||
+        rows_overlap(to, {k, num_tokens, k_stride * 2, narrow}) || rows_overlap(to, {v, num_tokens, v_stride * 2, narrow}))
+      return fail(PLE_ERR_INVALID_ARG, "%s: q_out overlaps k, v, or q without being it", name);
+  }
   if (cos_sin != nullptr && num_positions < 0)
     return fail(PLE_ERR_INVALID_ARG, "%s: num_positions %lld", name, static_cast<long long>(num_positions));
   const AppendArgs a{q, k, v, q_out, q_stride, k_stride, v_stride, q_out_stride, num_tokens, num_heads,

@@ -627,6 +627,8 @@ PLE_EXPORT ple_status ple_proj_w4(const ple_bf16_t* x, int64_t x_stride, int64_t
     return fail(PLE_ERR_UNSUPPORTED, "%s: %lld tokens", name, static_cast<long long>(num_tokens));
   if (x == nullptr || codes == nullptr || scales == nullptr || out == nullptr)
     return fail(PLE_ERR_INVALID_ARG, "%s: null x, codes, scales or out", name);
+  if (rows_overlap({out, 1, 0, num_tokens * out_dim * 2}, {x, num_tokens, x_stride * 2, int64_t(in_dim) * 2}))
+    return fail(PLE_ERR_INVALID_ARG, "%s: out overlaps x", name);
   if (!aligned16(x) || !aligned16(codes) || x_stride % 8 != 0)
     return fail(PLE_ERR_INVALID_ARG, "%s: x and codes must be 16-byte aligned, x_stride a multiple of 8", name);
   const ProjArgs a{x, x_stride, num_tokens, in_dim, out_dim, codes, scales, zeros, out};

@@ -700,7 +700,8 @@ size_t ple_kv_block_bytes(int32_t head_dim);
  *                 [0, num_positions) raises PLE_DEVERR_BOUNDS: the token is
  *                 not stored and its row of q_out is zeros.
  *   q_out         bf16 rows like q's, q_out_stride apart; may be q itself
- *                 (same pointer and stride), rotated in place.
+ *                 (same pointer and stride), rotated in place. Any other
+ *                 overlap with q, k or v is PLE_ERR_INVALID_ARG.
  * Keys are quantised from the rotated float32 values. Two tokens of one call
  * must not fall on the same slot.
  */
@@ -744,7 +745,9 @@ ple_status ple_kv_read(const void* cache, int64_t num_pages, int32_t page_size,
  *   max_query_len the largest n_r, if the host knows it; 0 if not. It picks
  *                 kernels, whose roundings differ; no token depends on its
  *                 being right.
- *   out           bf16 rows like q's, out_stride apart, 16-byte aligned.
+ *   out           bf16 rows like q's, out_stride apart, 16-byte aligned; may
+ *                 be q itself (same pointer and stride). Any other overlap
+ *                 with q is PLE_ERR_INVALID_ARG.
  *   workspace     device scratch of ple_kv_attention_workspace(...) bytes or
  *                 more, 256-byte aligned, ZERO-FILLED before its first use;
  *                 each completed call leaves its counters zero, so it is
@@ -776,7 +779,7 @@ ple_status ple_kv_attention(const ple_bf16_t* q, int64_t q_stride, int64_t num_t
  *   zeros    [out_dim][in_dim / group] uint8, or NULL for 8 everywhere.
  *   group    32, 64 or 128; in_dim a multiple of it (else
  *            PLE_ERR_UNSUPPORTED).
- *   out      [num_tokens][out_dim] bf16.
+ *   out      [num_tokens][out_dim] bf16, no part of it x's.
  */
 ple_status ple_proj_w4(const ple_bf16_t* x, int64_t x_stride, int64_t num_tokens, int32_t in_dim,
                        int32_t out_dim, const uint8_t* codes, const ple_bf16_t* scales,

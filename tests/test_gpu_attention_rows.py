@@ -4,6 +4,8 @@ _rows.py, which are those of f16 weights, values and keys and one rounding of th
 import pytest
 import torch
 
+from hashed_gram_embedding_gb300 import _lib
+
 from _four_bit import Batch, bits
 from _helpers import bf16_values, dev_err_word
 from _rows import faults, reference
@@ -84,3 +86,18 @@ def test_bytes_that_no_token_sees_change_no_bit(queries, lens):
         outs.append(attend(b, q).cpu().view(torch.int16))
     for other in outs[1:]:
         assert torch.equal(outs[0], other)
+
+
+@pytest.mark.parametrize("queries,lens", [([1] * 5, [700, 3, 90, 1500, 1]), ([4, 2], [900, 40]), ([200, 1], [300, 60]),
+                                          ([40], [2600])])
+def test_in_place(queries, lens):
+    """The result in q's own memory: the same bits."""
+    b = Batch(queries, lens, 8, 2, 128, 16, seed=43, pad=2)
+    q = b.rows(8)
+    want = attend(b, q)
+    cache, table, qsl, lens_d = b.device()
+    ws = torch.zeros(_lib.ple_kv_attention_workspace(8, 2, 128), dtype=torch.uint8, device="cuda")
+    for _ in range(3):
+        x = q.cuda()
+        _lib.ple_kv_attention(x, cache, table, qsl, lens_d, x, ws)
+        assert torch.equal(x.view(torch.int16), want.view(torch.int16))

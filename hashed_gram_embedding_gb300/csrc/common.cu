@@ -44,8 +44,9 @@ bool rows_overlap(RowSpan a, RowSpan b) {
     }
   }
   const wide d = at[1] - at[0];
-  if (a.count > 1 && b.count > 1 && a.stride != b.stride)
-    return d < static_cast<wide>(a.stride) * (a.count - 1) + a.width && -d < static_cast<wide>(b.stride) * (b.count - 1) + b.width;
+  if (d >= static_cast<wide>(a.stride) * (a.count - 1) + a.width || -d >= static_cast<wide>(b.stride) * (b.count - 1) + b.width)
+    return false;
+  if (a.count > 1 && b.count > 1 && a.stride != b.stride) return true;
   const wide s = a.count > 1 ? a.stride : b.count > 1 ? b.stride : 1;
   // row i of a and row j of b meet where -b.width < d + (j - i) s < a.width
   auto floor_div = [](wide x, wide y) { return x / y - (x % y != 0 && x < 0); };

@@ -381,6 +381,29 @@ def ple_gated_conv(kv, gate, query_start_loc, w, dilation, out, conv_state=None,
 _U8, _I32, _F32, _BF16 = torch.uint8, torch.int32, torch.float32, torch.bfloat16
 
 
+_one_gpu = None  # whether the process sees no more than one; None: not asked yet
+
+
+def _same_gpu(*tensors):
+    """ValueError unless the tensors (or None) are on the current GPU, where a
+    call's kernels go. Called unless there is one GPU, which is_cuda tells as well."""
+    global _one_gpu
+    if _one_gpu is None:
+        _one_gpu = torch.cuda.device_count() <= 1
+        if _one_gpu:
+            return
+    current = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.get_device() != current:
+            raise ValueError(f"all tensors must be on the current device, cuda:{current}; one is on {t.device}")
+
+
+def _err_word(t):
+    if t.dtype is not _I32 or not t.is_cuda or t.numel() < 1:
+        raise ValueError("dev_err: a CUDA int32 word is needed")
+    return t.data_ptr()
+
+
 def _raw_stream(stream, t):
     if stream is not None:
         return stream.cuda_stream
@@ -452,6 +475,8 @@ def ple_kv_append(q, k, v, cos_sin, cache, block_table, query_start_loc, kv_lens
         q_at, o_at = q.data_ptr(), q_out.data_ptr()
     if Hk != hk or Hv != hk or Tv != T or Tq != T:
         raise ValueError("q, k, v and the cache differ in tokens or kv heads")
+    if not _one_gpu:
+        _same_gpu(q, k, v, cos_sin, cache, block_table, query_start_loc, kv_lens, q_out, positions, dev_err)
     cs, entries, rot = None, 0, 0
     if cos_sin is not None:
         cs = _whole("cos_sin", cos_sin, _F32, 2)
@@ -463,7 +488,7 @@ def ple_kv_append(q, k, v, cos_sin, cache, block_table, query_start_loc, kv_lens
             raise ValueError("positions must have one entry for each token")
     status = lib().ple_kv_append(
         q_at, q_stride, k.data_ptr(), k_stride, v.data_ptr(), v_stride, T, H, hk, D, cs, entries, rot,
-        1 if interleaved else 0, at, *c, o_at, o_stride, None if dev_err is None else dev_err.data_ptr(),
+        1 if interleaved else 0, at, *c, o_at, o_stride, None if dev_err is None else _err_word(dev_err),
         _raw_stream(stream, k))
     return status if status == PLE_OK else _check("ple_kv_append", status)
 
@@ -483,7 +508,9 @@ def ple_kv_read(cache, block_table, query_start_loc, kv_lens, k_out, v_out, dev_
     hk, c = _cache_args(cache, block_table, query_start_loc, kv_lens, D)
     if Hk != hk:
         raise ValueError(f"{Hk} kv heads, and {hk} in the cache")
-    status = lib().ple_kv_read(*c, T, hk, D, k_at, v_at, None if dev_err is None else dev_err.data_ptr(),
+    if not _one_gpu:
+        _same_gpu(cache, block_table, query_start_loc, kv_lens, k_out, v_out, dev_err)
+    status = lib().ple_kv_read(*c, T, hk, D, k_at, v_at, None if dev_err is None else _err_word(dev_err),
                                _raw_stream(stream, some))
     return status if status == PLE_OK else _check("ple_kv_read", status)
 
@@ -506,10 +533,12 @@ def ple_kv_attention(q, cache, block_table, query_start_loc, kv_lens, out, works
         raise ValueError("out must have q's shape")
     hk, c = _cache_args(cache, block_table, query_start_loc, kv_lens, D)
     room = _whole("workspace", workspace, _U8, 1)
+    if not _one_gpu:
+        _same_gpu(q, cache, block_table, query_start_loc, kv_lens, out, workspace, dev_err)
     status = lib().ple_kv_attention(
         q.data_ptr(), q_stride, T, H, hk, D, *c, max_query_len, D ** -0.5 if scale is None else scale,
         1 if causal else 0, window, out.data_ptr(), o_stride, room, workspace.shape[0],
-        None if dev_err is None else dev_err.data_ptr(), _raw_stream(stream, q))
+        None if dev_err is None else _err_word(dev_err), _raw_stream(stream, q))
     return status if status == PLE_OK else _check("ple_kv_attention", status)
 
 
@@ -529,6 +558,8 @@ def ple_proj_w4(x, codes, scales, out, zeros=None, dev_err=None, stream=None):
     if Nc != N or half * 2 != E or To != T or No != N or groups < 1 or E % groups != 0:
         raise ValueError(f"x {tuple(x.shape)}, codes {tuple(codes.shape)}, scales "
                          f"{tuple(scales.shape)} and out {tuple(out.shape)} do not fit")
+    if not _one_gpu:
+        _same_gpu(x, codes, scales, out, zeros, dev_err)
     zero_at = None
     if zeros is not None:
         zero_at = _whole("zeros", zeros, _U8, 2)
@@ -537,7 +568,7 @@ def ple_proj_w4(x, codes, scales, out, zeros=None, dev_err=None, stream=None):
     status = lib().ple_proj_w4(
         x.data_ptr(), stride if T > 1 else E, T, E, N, codes.data_ptr(), scales.data_ptr(), zero_at,
         E // groups, out.data_ptr(),
-        None if dev_err is None else dev_err.data_ptr(), _raw_stream(stream, x))
+        None if dev_err is None else _err_word(dev_err), _raw_stream(stream, x))
     return status if status == PLE_OK else _check("ple_proj_w4", status)
 
 

@@ -418,7 +418,7 @@ def _heads(name, t, head_dim=None):
         raise ValueError(f"{name}: a CUDA bf16 tensor [T, heads, head_dim] is needed")
     T, H, D = shape
     stride, per_head, one = t.stride()
-    if (one != 1 and D > 1) or (per_head != D and H > 1) or (head_dim is not None and D != head_dim):
+    if (T > 0 and ((one != 1 and D > 1) or (per_head != D and H > 1))) or (head_dim is not None and D != head_dim):
         raise ValueError(f"{name}: heads of {head_dim or D} elements must lie together in a row")
     return (stride if T > 1 else H * D), T, H, D
 
@@ -553,7 +553,7 @@ def ple_proj_w4(x, codes, scales, out, zeros=None, dev_err=None, stream=None):
     # a ValueError, too, where one has more dimensions or fewer
     (T, E), (Nc, half), (N, groups), (To, No) = x.shape, codes.shape, scales.shape, out.shape
     stride, one = x.stride()
-    if one != 1 and E > 1:
+    if one != 1 and E > 1 and T > 0:
         raise ValueError("x: the columns of a row must lie together")
     if Nc != N or half * 2 != E or To != T or No != N or groups < 1 or E % groups != 0:
         raise ValueError(f"x {tuple(x.shape)}, codes {tuple(codes.shape)}, scales "

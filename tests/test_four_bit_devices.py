@@ -121,3 +121,20 @@ def test_one_gpu_is_asked_for_once(library, monkeypatch):
         args[first].on(-1)
         with pytest.raises(ValueError):
             getattr(_lib, name)(**args, stream=Stream())
+
+
+def test_no_tokens_in_tensors_of_any_strides(library):
+    """An empty tensor's strides say nothing (NumPy's and a slice's differ from a fresh tensor's)."""
+    def empty(*shape):
+        t = Stand(BF16, *shape)
+        t._t = torch.empty_strided(shape, tuple(range(1, len(shape) + 1)), dtype=BF16)
+        return t
+
+    _lib.ple_kv_append(empty(0, 4, 128), empty(0, 2, 128), empty(0, 2, 128), None, **cache(), q_out=empty(0, 4, 128),
+                       stream=Stream())
+    _lib.ple_kv_attention(empty(0, 4, 128), **cache(), out=empty(0, 4, 128), workspace=Stand(U8, 512), stream=Stream())
+    _lib.ple_proj_w4(empty(0, 256), Stand(U8, 8, 128), Stand(BF16, 8, 2), Stand(BF16, 0, 8), stream=Stream())
+    assert library.calls == ["ple_kv_append", "ple_kv_attention", "ple_proj_w4"]
+    with pytest.raises(ValueError):
+        _lib.ple_kv_append(empty(0, 4, 128), empty(0, 2, 128), empty(0, 2, 64), None, **cache(), q_out=empty(0, 4, 128),
+                           stream=Stream())

@@ -7,8 +7,9 @@
 // memory again: masked out of its word where it stands, a pair of codes is a
 // pair of bf16 subnormals (c 2^-133, or c 2^-129 for the upper half of a
 // byte), and one fused multiply-add makes (c - z) / 64 of it, exactly. The
-// scale meets the float32 sum once per group:
-//   out[t][n] = sum_g 64 s_ng sum_{e in g} x_te (c_ne - z_ng) / 64.
+// scale meets the float32 sum once per group, and 64 the whole sum (with the
+// scale it would be infinite for scales that are not):
+//   out[t][n] = 64 sum_g s_ng sum_{e in g} x_te (c_ne - z_ng) / 64.
 // The contraction index may run in any order, so a lane reads codes in the
 // widest pieces that lie in one group - 16, 8 or 4 bytes of a row for groups
 // of 128, 64 or 32 columns, four lanes together a group of a row - and the
@@ -147,7 +148,7 @@ proj_w4_kernel(const ProjArgs a) {
         uint32_t z64[2];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          scale[h] = 64.0f * bf_lo(__ldg(a.scales + at_group[h] + group));
+          scale[h] = bf_lo(__ldg(a.scales + at_group[h] + group));
           const float z = a.zeros != nullptr ? static_cast<float>(__ldg(a.zeros + at_group[h] + group)) : 8.0f;
           z64[h] = pack2(z * -0.015625f, z * -0.015625f);
         }
@@ -195,7 +196,7 @@ proj_w4_kernel(const ProjArgs a) {
     float sum = 0.0f;
 #pragma unroll
     for (int k = 0; k < kWarps; ++k) sum += join[(k * L::kRows + row) * L::kPitch + t];
-    a.out[(t0 + t) * a.N + n0 + row] = static_cast<ple_bf16_t>(pack2(sum, 0.0f) & 0xffffu);
+    a.out[(t0 + t) * a.N + n0 + row] = static_cast<ple_bf16_t>(pack2(64.0f * sum, 0.0f) & 0xffffu);
   }
 }
 
@@ -518,7 +519,7 @@ proj_w4_wide_kernel(const ProjArgs a, int parts, int32_t* dev_err) {
       const int chunk_no = (g - g0) / kParamGroups;
       if ((g - g0) % kParamGroups == 0 &&
           gave_up(__all_sync(0xffffffffu, wait_for(params_full(chunk_no % kParamSets), chunk_no / kParamSets & 1, abort_flag)))) break;
-      const float scale = 64.0f * bf_hi(params[(g - g0) % (kParamSets * kParamGroups) * kWideRows + row]);
+      const float scale = bf_hi(params[(g - g0) % (kParamSets * kParamGroups) * kWideRows + row]);
       if (gave_up(__all_sync(0xffffffffu, wait_for(sums_full(set), round & 1, abort_flag)))) break;
       fence_after();
 #pragma unroll
@@ -539,7 +540,7 @@ proj_w4_wide_kernel(const ProjArgs a, int parts, int32_t* dev_err) {
     } else if (n0 + row < a.N) {
 #pragma unroll
       for (int t = 0; t < kMine; ++t)
-        if (t_first + t < tokens) a.out[(t0 + t_first + t) * a.N + n] = static_cast<ple_bf16_t>(pack2(total[t], 0.0f) & 0xffffu);
+        if (t_first + t < tokens) a.out[(t0 + t_first + t) * a.N + n] = static_cast<ple_bf16_t>(pack2(64.0f * total[t], 0.0f) & 0xffffu);
     }
   }
   fence_before();
@@ -565,7 +566,7 @@ proj_w4_wide_kernel(const ProjArgs a, int parts, int32_t* dev_err) {
       }
 #pragma unroll
     for (int m = 0; m < 4; ++m)
-      if (n0 + row + m < a.N) a.out[(t0 + t) * a.N + n0 + row + m] = static_cast<ple_bf16_t>(pack2(sum[m], 0.0f) & 0xffffu);
+      if (n0 + row + m < a.N) a.out[(t0 + t) * a.N + n0 + row + m] = static_cast<ple_bf16_t>(pack2(64.0f * sum[m], 0.0f) & 0xffffu);
   }
   cluster_barrier();  // no CTA leaves while its sums are read
 }

@@ -50,3 +50,17 @@ def test_zero_points_of_any_byte_and_large_inputs(T):
     out = project(x.cuda(), codes, scales, zeros)
     got = faults(bf16_values(bits(out)), *oracle.proj_w4(bits(x), codes, bits(scales), zeros, 64), 1024, 64)
     assert not got, got
+
+
+@pytest.mark.parametrize("T,N", [(1, 600), (12, 600), (40, 600), (64, 40000)])
+def test_scales_near_the_largest(T, N):
+    """Scales of 2^122 to 2^127 on inputs small enough for a finite result, and on zeros."""
+    E, group = 512, 128
+    codes, scales, zeros = weight(N, E, group, True, seed=T)
+    scales = (scales.float() / 0.02 * 2.0 ** 127).to(torch.bfloat16)
+    x = (torch.randn(T, E, generator=torch.Generator().manual_seed(T)) * 2.0 ** -20).to(torch.bfloat16)
+    x[T // 2:, :] = 0.0 if T > 1 else x[0]
+    out = project(x.cuda(), codes, scales, zeros)
+    want, total = oracle.proj_w4(bits(x), codes, bits(scales), zeros, group)
+    got = faults(bf16_values(bits(out)), want, total, E, group)
+    assert not got, got

@@ -526,7 +526,8 @@ def ple_kv_attention(q, cache, block_table, query_start_loc, kv_lens, out, works
     out [T, H, D] bf16. workspace: a device uint8 tensor of at least
     ple_kv_attention_workspace(H, Hk, D) bytes, zero-filled before its first
     use. scale: 1 / sqrt(D) by default; max_query_len: the most query tokens
-    of a request, if known. Other arguments as in ple_kv_append."""
+    of a request, if known (0: not known, which costs batches of single tokens
+    several times as long); out may be q. Other arguments as in ple_kv_append."""
     q_stride, T, H, D = _heads("q", q)
     o_stride, To, Ho, _ = _heads("out", out, D)
     if To != T or Ho != H:

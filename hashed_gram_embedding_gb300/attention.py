@@ -83,7 +83,8 @@ class PLEAttention:
         tokens and both in one batch. block_table int32 [R, max_pages],
         query_start_loc int32 [R + 1], kv_lens int32 [R] (this step's tokens
         included); positions int32 [T] or None for the places in the cache;
-        max_query_len: the most tokens of a request, if known. The steps of one
+        max_query_len: the most tokens of a request, if known (0 costs steps of
+        single tokens several times the attention's time). The steps of one
         block run one after another (they share its buffers): a step on another
         stream than the last one's has to wait for it. A result that has no
         place given is a tensor of the stream that the step runs on."""

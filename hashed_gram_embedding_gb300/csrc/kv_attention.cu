@@ -33,12 +33,13 @@ namespace {
 // below: steps handed out in turn are held up by the slowest.)
 //
 // Measured, 32 heads on 8 kv heads of 128: 256 ragged requests of up to 8192
-// positions, a token each, 230 us = 5.8 TB/s; 4 tokens each on up to 4096
-// positions 167 us = 3.8 TB/s (16 rows: twice the products for the same
-// bytes); one token on 131071 positions 49 us = 2.9 TB/s (start,
-// lookups and three levels of joining, which on 700 positions take 12.4 us). Bound by issue (56 % of the slots, 25 % of
-// the matrix pipe) and by latency at the ends, with 58 % of the memory's time
-// in use on a cold cache.
+// positions, a token each, 235 us = 5.7 TB/s; 4 tokens each on up to 4096
+// positions 169 us = 3.7 TB/s (16 rows: twice the products for the same
+// bytes); one token on 131071 positions 50 us = 2.8 TB/s (start, lookups and
+// three levels of joining, which on 700 positions take 12.8 us). Bound by
+// issue and by latency: on up to 2048 positions and a cold cache 56 % of the
+// issue slots, 25 % of the matrix pipe and 57 % of the memory's time are in
+// use with a token a request, 48, 35 and 42 % with four.
 //
 // Products, on warp-wide matrix instructions (16 x 8 x 16, f32 sums; reading
 // the cache and unpacking it, not their rate, is the bound):

@@ -45,12 +45,14 @@
 //
 // Bound by latency: a tile's chain of S, weights, P V and the next S, about
 // 4900 cycles for both tiles, of which their products are 2048 and their
-// exponentials another 2048, side by side only in part; registers and
-// instruction caches leave no room for a third tile. Measured, 32 heads on 8
-// kv heads of 128: 2048 tokens of a request on 16k positions 550 us = 935
-// TFLOP/s, a ragged prefill of 8192 tokens behind 2000 positions 338 us = 614
-// (its last CTAs run alone); 64 tokens on 65k positions 112 us. Heads of 256:
-// 2 x 1024 tokens of 16 heads on 4k positions 310 us = 500 TFLOP/s.
+// exponentials another 2048, side by side only in part: a tile's weights stand
+// over its scores, so its next scores wait for P V (scores of 64 positions at a
+// time, in two pieces, would find room; registers and instruction caches leave
+// none for a third tile of rows). Measured, 32 heads on 8 kv heads of 128:
+// 2048 tokens of a request on 16k positions 557 us = 926 TFLOP/s, a ragged
+// prefill of 8192 tokens behind 2000 positions 339 us = 611 (its last CTAs run
+// alone); 64 tokens on 65k positions 126 us. Heads of 256: 2 x 1024 tokens of
+// 16 heads on 4k positions 310 us = 500 TFLOP/s.
 //
 // What is masked never meets what it must not: a position outside the cache
 // enters as zeros, and a value that is not finite is left out of V and makes
@@ -380,7 +382,8 @@ attention_prefill_kernel(const AttentionArgs a, const KvCache c, const Parts par
           }
           // a quarter of the row at a time, in a rolled loop: what the roles run
           // side by side has to fit the instruction caches (2048 rows of 32 heads
-          // on 16k positions: 540 us, two quarters to a turn 553, four half as long again)
+          // on 16k positions, when this was chosen: 540 us, two quarters to a turn
+          // 553, four half as long again)
           auto quarter = [&](int q, auto shifted) {
             float v[32];
             tmem_load(s_at + 32 * q, v);

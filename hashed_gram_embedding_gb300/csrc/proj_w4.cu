@@ -217,9 +217,11 @@ cudaError_t launch(const ProjArgs& a, cudaStream_t stream) {
 // of W as the first operand, (c - z) / 64 in bf16 (exact), against the tokens,
 // 128 columns to a stage. W goes through registers into tensor memory and x
 // as it is into shared memory: with both laid out in shared memory its
-// bandwidth was the bound (4096 x 16384, 64 tokens: 32 us). Now 24 us, 1.5
-// TB/s; what bounds it is the unpacking, 13 instructions for 8 weights in
-// every stage's chain of waiting, unpacking, storing and handing over.
+// bandwidth was the bound (4096 x 16384, 64 tokens: 32 us). Now 24.5 us, 1.5
+// TB/s. What bounds it is a stage's chain of waiting, unpacking, storing and
+// handing over, at 53 % of the issue slots: of 13.3 M warp instructions a
+// quarter unpacks (13 for 8 weights), the others copy x by 16 bytes, take out
+// sums and wait.
 // The sums of each group of columns get tensor-memory columns of their own,
 // four sets in turn, and eight warps take them out, a row a thread, and add
 // them up times the group's scale in float32.

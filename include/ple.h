@@ -670,9 +670,11 @@ ple_status ple_step(cudaStream_t copy_in, cudaStream_t compute, cudaStream_t cop
  *   block_table   [num_reqs][max_pages] int32 device.
  *   query_start_loc, kv_lens  [num_reqs + 1] and [num_reqs] int32 device.
  *   head_dim      64, 128 or 256 (else PLE_ERR_UNSUPPORTED).
- * A position that is negative, past max_pages * page_size, or in a page
- * outside [0, num_pages) raises PLE_DEVERR_BOUNDS: it is not written, reads
- * as zeros, and no query sees it.
+ * A position past max_pages * page_size, or in a page outside
+ * [0, num_pages), raises PLE_DEVERR_BOUNDS: it is not written, reads as
+ * zeros, and no query sees it. So does a token before position 0 (n_r above
+ * kv_lens[r]) in ple_kv_append and ple_kv_read; in ple_kv_attention it is a
+ * token that sees nothing.
  */
 
 /* Bytes of a block of 16 tokens: 16 * (head_dim + 8); 0 for a head_dim that
@@ -736,15 +738,30 @@ ple_status ple_kv_read(const void* cache, int64_t num_pages, int32_t page_size,
  * last = kv_lens[r] - 1), over the positions p with
  * max(0, last - window + 1) <= p <= last (window 0: from 0):
  *   out[t][h] = sum_p softmax_p(scale * <q[t][h], K[p]>) V[p].
- * A token that sees no position gets zeros. Whatever lies in the cache past
- * what a token sees has no influence on it.
+ * A token that sees no position gets zeros. What lies in the cache behind a
+ * request's positions, or in pages that none of its tokens sees, has no
+ * influence on it; a value that is not finite makes NaN of the tokens that
+ * see it, and of no other.
+ * Arithmetic: scores, maxima, sums and outputs are float32, and the result is
+ * rounded once. Rounded before that, each row or token by a power of two of
+ * its own (2^-11 of an element): with few query rows (tokens times heads of a
+ * group) weights in f16, against exact codes - in bf16 (2^-8) where a step of
+ * the cache has value scales outside [2^-9, 2^10); with many rows queries,
+ * keys, values and weights in f16. Both leave the result within its own
+ * rounding's 0.0017 (2-norm) of float64 on normal inputs. Values up to about
+ * 2^100 keep the sums finite, those below 2^-96 lose bits; scale times a
+ * query's elements has to stay below 2^126.
  *   q             bf16 rows of num_heads heads, q_stride elements apart,
  *                 16-byte aligned, stride a multiple of 8.
  *   scale         finite, > 0 (usually 1 / sqrt(head_dim)).
  *   window        >= 0; not 0 only with causal.
  *   max_query_len the largest n_r, if the host knows it; 0 if not. It picks
  *                 kernels, whose roundings differ; no token depends on its
- *                 being right.
+ *                 being right. 0 counts the whole batch as one request's:
+ *                 256 single tokens of 32 heads on 8 kv heads take 3.6 times
+ *                 as long without it (841 us against 235 on up to 8192
+ *                 positions). A batch with one long prompt in it takes its
+ *                 single tokens by the wide kernels likewise.
  *   out           bf16 rows like q's, out_stride apart, 16-byte aligned; may
  *                 be q itself (same pointer and stride). Any other overlap
  *                 with q is PLE_ERR_INVALID_ARG.
@@ -770,7 +787,8 @@ ple_status ple_kv_attention(const ple_bf16_t* q, int64_t q_stride, int64_t num_t
  * ple_proj_w4 -- out = x W^T for a weight held in 4 bits, for steps of few
  * tokens (the weight is read once for every 64 tokens).
  *   W[n][e] = scales[n][e / group] * (code[n][e] - zeros[n][e / group]),
- *   float32 accumulation, bf16 result.
+ *   float32 accumulation, bf16 result. A group's products x (code - zero) are
+ *   added up before the scale meets the sum, which has to be finite as well.
  *   x        bf16 rows of in_dim, x_stride elements apart, 16-byte aligned,
  *            stride a multiple of 8.
  *   codes    [out_dim][in_dim / 2] bytes, 16-byte aligned; column e is the

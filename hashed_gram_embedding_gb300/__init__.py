@@ -5,9 +5,10 @@ include/ple.h); this package holds its build script, a ctypes binding with
 the C names, the PLELayer convenience wrapper (and PLEHostPipeline, which
 runs it over pinned host buffers with transfers overlapping compute; PLEChain,
 several layers with the next layers' lookups prefetched), PLEAttention (the
-attention block between two layers, its cache and weights in 4 bits), the sharded lookups
-over a group of ranks (HeadShardedLookup, RowShardedLookup) and the seeded
-synthetic workloads used by the tests and the benchmark.
+attention block between two layers, its cache and weights in 4 bits),
+PLEFeedForward (the gated feed-forward block behind it, in 8 bits), the
+sharded lookups over a group of ranks (HeadShardedLookup, RowShardedLookup)
+and the seeded synthetic workloads used by the tests and the benchmark.
 """
 
 from ._lib import (  # noqa: F401
@@ -31,15 +32,23 @@ from ._lib import (  # noqa: F401
     ple_kv_block_bytes,
     ple_kv_read,
     ple_proj_w4,
+    ple_gated_mx8,
+    ple_mx8_read,
+    ple_mx8_scale_bytes,
+    ple_norm_mx8,
+    ple_proj_mx8,
     ple_version,
     PLE_DEVERR_BOUNDS,
     PLE_DEVERR_QSL,
     PLE_DEVERR_TIMEOUT,
+    PLE_GELU,
     PLE_HBM,
     PLE_HOST_UVA,
     PLE_SHARD_HEADS,
     PLE_SHARD_ROWS,
+    PLE_SILU,
 )
 from .attention import PLEAttention, pack_w4  # noqa: F401
+from .feed_forward import PLEFeedForward, pack_mx8  # noqa: F401
 from .layer import PLELayer, PLEHostPipeline, PLEChain  # noqa: F401
 from .sharded import HeadShardedLookup, RowShardedLookup  # noqa: F401

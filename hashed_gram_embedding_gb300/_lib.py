@@ -35,6 +35,8 @@ PLE_HOST_UVA = 1
 PLE_SHARD_HEADS = 0
 PLE_SHARD_ROWS = 1
 PLE_HOST_TABLE_REGISTER = 1
+PLE_SILU = 0
+PLE_GELU = 1
 
 # Every entry point of include/ple.h with its ctypes signature.
 _P = ctypes.c_void_p
@@ -96,6 +98,11 @@ SIGNATURES = {
     "ple_kv_attention": [_P, _I64, _I64, _I32, _I32, _I32, _P, _I64, _I32, _P, _I32, _P, _I32, _P,
                          _I32, _F32, _I32, _I32, _P, _I64, _P, ctypes.c_size_t, _P, _P],
     "ple_proj_w4": [_P, _I64, _I64, _I32, _I32, _P, _P, _P, _I32, _P, _P, _P],
+    "ple_mx8_scale_bytes": [_I64, _I32],
+    "ple_mx8_read": [_P, _P, _I64, _I32, _P, _P],
+    "ple_norm_mx8": [_P, _I64, _P, _I64, _P, _F32, _I64, _I32, _P, _I64, _P, _P, _P],
+    "ple_gated_mx8": [_P, _P, _I64, _I32, _P, _P, _I32, _I32, _P, _P, _P, _P],
+    "ple_proj_mx8": [_P, _P, _I64, _I32, _P, _P, _I32, _P, _I64, _P, _P, _P],
     "ple_last_error": [],
     "ple_version": [],
 }
@@ -571,6 +578,116 @@ def ple_proj_w4(x, codes, scales, out, zeros=None, dev_err=None, stream=None):
         E // groups, out.data_ptr(),
         None if dev_err is None else _err_word(dev_err), _raw_stream(stream, x))
     return status if status == PLE_OK else _check("ple_proj_w4", status)
+
+
+# ---- the 8-bit step of the feed-forward block: norm, gated products, projection ----
+
+_ACTIVATIONS = {"silu": PLE_SILU, "gelu": PLE_GELU}
+
+
+def ple_mx8_scale_bytes(rows, columns):
+    """Bytes of the scales of an 8-bit tensor [rows, columns] (0: sizes that
+    have none)."""
+    return int(lib().ple_mx8_scale_bytes(int(rows), int(columns)))
+
+
+def _mx8(name, codes, scales):
+    """Shape of an 8-bit tensor: codes uint8 [R, C], scales uint8, their bytes
+    in one dimension, as many as ple_mx8_scale_bytes says or more."""
+    if (codes.dtype is not _U8 or scales.dtype is not _U8 or not (codes.is_contiguous() and scales.is_contiguous())
+            or not (codes.is_cuda and scales.is_cuda)):
+        raise ValueError(f"{name}: contiguous CUDA uint8 tensors are needed")
+    (R, C), (n,) = codes.shape, scales.shape  # a ValueError, too, where there are more dimensions or fewer
+    if C % 128 != 0 or n < (R + 127) // 128 * (C * 4):
+        raise ValueError(f"{name}: codes {R} x {C} (columns: a multiple of 128) need "
+                         f"{(R + 127) // 128 * (C * 4)} bytes of scales, not {n}")
+    return R, C
+
+
+def _rows_of(name, t, rows, columns):
+    """Address and row stride of bf16 rows any distance apart."""
+    if t.dtype is not _BF16 or not t.is_cuda or t.shape != (rows, columns):
+        raise ValueError(f"{name}: a CUDA bf16 tensor [{rows}, {columns}] is needed")
+    stride, one = t.stride()
+    if one != 1 and columns > 1 and rows > 0:
+        raise ValueError(f"{name}: the columns of a row must lie together")
+    return t.data_ptr(), stride if rows > 1 else columns
+
+
+def ple_mx8_read(codes, scales, out, stream=None):
+    """out [R, C] bf16: the values of an 8-bit tensor, codes uint8 [R, C] and
+    scales uint8 [ple_mx8_scale_bytes(R, C)]."""
+    R, C = _mx8("codes, scales", codes, scales)
+    at = _whole("out", out, _BF16, 2)
+    if out.shape != codes.shape:
+        raise ValueError("out must have the shape of codes")
+    if not _one_gpu:
+        _same_gpu(codes, scales, out)
+    status = lib().ple_mx8_read(codes.data_ptr(), scales.data_ptr(), R, C, at, _raw_stream(stream, codes))
+    return status if status == PLE_OK else _check("ple_mx8_read", status)
+
+
+def ple_norm_mx8(x, gamma, codes, scales, residual=None, sum_out=None, eps=1e-6, stream=None):
+    """codes uint8 [T, C] and scales uint8 [ple_mx8_scale_bytes(T, C)]: the
+    root-mean-square norm of x + residual, in 8 bits; sum_out: the sum. x,
+    residual and sum_out bf16 [T, C], columns of a wider tensor will do;
+    sum_out may be x or residual itself. gamma bf16 [C], or None for 1."""
+    T, C = _mx8("codes, scales", codes, scales)
+    x_at, x_stride = _rows_of("x", x, T, C)
+    r_at, r_stride, s_at, s_stride, g_at = None, C, None, C, None
+    if residual is not None:
+        r_at, r_stride = _rows_of("residual", residual, T, C)
+    if sum_out is not None:
+        s_at, s_stride = _rows_of("sum_out", sum_out, T, C)
+    if gamma is not None:
+        g_at = _whole("gamma", gamma, _BF16, 1)
+        if gamma.shape[0] != C:
+            raise ValueError(f"gamma must have {C} entries")
+    if not _one_gpu:
+        _same_gpu(x, gamma, codes, scales, residual, sum_out)
+    status = lib().ple_norm_mx8(x_at, x_stride, r_at, r_stride, g_at, eps, T, C, s_at, s_stride, codes.data_ptr(),
+                                scales.data_ptr(), _raw_stream(stream, x))
+    return status if status == PLE_OK else _check("ple_norm_mx8", status)
+
+
+def ple_gated_mx8(x, x_scales, w, w_scales, codes, scales, activation="silu", dev_err=None, stream=None):
+    """codes, scales: act(x Wg^T) * (x Wu^T) in 8 bits [T, I], for x in 8 bits
+    [T, C] and w in 8 bits [2 I, C], Wg's rows before Wu's. activation: "silu"
+    or "gelu" (its tanh form)."""
+    T, C = _mx8("x", x, x_scales)
+    rows, Cw = _mx8("w", w, w_scales)
+    To, I = _mx8("codes, scales", codes, scales)
+    if Cw != C or rows != 2 * I or To != T:
+        raise ValueError(f"x {tuple(x.shape)}, w {tuple(w.shape)} and codes {tuple(codes.shape)} do not fit")
+    act = _ACTIVATIONS.get(activation)
+    if act is None:
+        raise ValueError(f"activation {activation!r}: one of {', '.join(_ACTIVATIONS)} is needed")
+    if not _one_gpu:
+        _same_gpu(x, x_scales, w, w_scales, codes, scales, dev_err)
+    status = lib().ple_gated_mx8(
+        x.data_ptr(), x_scales.data_ptr(), T, C, w.data_ptr(), w_scales.data_ptr(), I, act, codes.data_ptr(),
+        scales.data_ptr(), None if dev_err is None else _err_word(dev_err), _raw_stream(stream, x))
+    return status if status == PLE_OK else _check("ple_gated_mx8", status)
+
+
+def ple_proj_mx8(x, x_scales, w, w_scales, out, residual=None, dev_err=None, stream=None):
+    """out [T, N] bf16 = residual + x W^T, for x in 8 bits [T, E] and w in 8
+    bits [N, E]. residual bf16 [T, N], columns of a wider tensor will do; it
+    may be out itself."""
+    T, E = _mx8("x", x, x_scales)
+    N, Ew = _mx8("w", w, w_scales)
+    at = _whole("out", out, _BF16, 2)
+    if Ew != E or out.shape != (T, N):
+        raise ValueError(f"x {tuple(x.shape)}, w {tuple(w.shape)} and out {tuple(out.shape)} do not fit")
+    r_at, r_stride = None, N
+    if residual is not None:
+        r_at, r_stride = _rows_of("residual", residual, T, N)
+    if not _one_gpu:
+        _same_gpu(x, x_scales, w, w_scales, out, residual, dev_err)
+    status = lib().ple_proj_mx8(
+        x.data_ptr(), x_scales.data_ptr(), T, E, w.data_ptr(), w_scales.data_ptr(), N, r_at, r_stride, at,
+        None if dev_err is None else _err_word(dev_err), _raw_stream(stream, x))
+    return status if status == PLE_OK else _check("ple_proj_mx8", status)
 
 
 def ple_version():

@@ -1,0 +1,251 @@
+// ple_norm_mx8: the residual's addition and the root-mean-square norm with
+// its result in 8 bits, one pass over the data; ple_mx8_read: values of an
+// 8-bit tensor.
+//
+//   s = x + residual, n = s / sqrt(mean(s^2) + eps) * gamma, mx8(n)
+//
+// Bound by memory: 2 bytes each of x, the residual and the sum, and 33 / 32
+// of the result. A CTA takes a row and holds it in registers as float32, 8
+// neighbouring elements a thread and turn, so that loads and stores are wide;
+// four lanes hold a block of 32 and agree on its scale by two shuffles. The
+// norm is taken of the float32 sum, not of the bf16 that sum_out gets.
+#include "mx8.cuh"
+
+#include <cmath>
+
+namespace ple {
+namespace {
+
+struct NormArgs {
+  const ple_bf16_t *x, *residual, *gamma;
+  int64_t x_stride, residual_stride, sum_stride;
+  int C;
+  float eps;
+  ple_bf16_t* sum_out;
+  uint8_t *codes, *scales;
+};
+
+// A value for the whole CTA, the warps' in their order.
+template <typename T, typename F>
+__device__ __forceinline__ T over_block(T v, T* room, F join) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v = join(v, __shfl_xor_sync(0xffffffffu, v, o));
+  const int warp = threadIdx.x / 32, warps = blockDim.x / 32;
+  if (warps == 1) return v;
+  if (threadIdx.x % 32 == 0) room[warp] = v;
+  __syncthreads();
+  v = room[0];
+  for (int i = 1; i < warps; ++i) v = join(v, room[i]);
+  return v;
+}
+
+__device__ __forceinline__ float square_sum(const float (&v)[8]) {
+  float a = 0.0f, b = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 8; i += 2) {
+    a = fmaf(v[i], v[i], a);
+    b = fmaf(v[i + 1], v[i + 1], b);
+  }
+  return a + b;
+}
+
+template <int kTurns>
+__global__ void __launch_bounds__(kTurns == 1 ? 512 : 1024)
+norm_mx8_kernel(const NormArgs a) {
+  __shared__ float sums[32];
+  __shared__ uint32_t tops[32];
+  __shared__ float again[32];
+  pdl_wait();
+  pdl_trigger();
+  const int64_t row = blockIdx.x;
+  const ple_bf16_t* const x = a.x + row * a.x_stride;
+  const ple_bf16_t* const residual = a.residual == nullptr ? nullptr : a.residual + row * a.residual_stride;
+  float v[kTurns][8];
+  uint4 add[kTurns];
+  // columns are a multiple of 128: whole groups of 16 lanes take part
+#pragma unroll
+  for (int t = 0; t < kTurns; ++t) {
+    const int c = (t * blockDim.x + threadIdx.x) * 8;
+    uint4 w = make_uint4(0, 0, 0, 0);
+    add[t] = w;
+    if (c < a.C) {
+      w = *reinterpret_cast<const uint4*>(x + c);
+      if (residual != nullptr) add[t] = *reinterpret_cast<const uint4*>(residual + c);
+    }
+    unpack8(w, v[t]);
+  }
+  float sum = 0.0f;
+#pragma unroll
+  for (int t = 0; t < kTurns; ++t) {
+    if (residual != nullptr) {
+      float r[8];
+      unpack8(add[t], r);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[t][i] += r[i];
+    }
+    const int c = (t * blockDim.x + threadIdx.x) * 8;
+    if (a.sum_out != nullptr && c < a.C)
+      *reinterpret_cast<uint4*>(a.sum_out + row * a.sum_stride + c) =
+          make_uint4(pack2(v[t][0], v[t][1]), pack2(v[t][2], v[t][3]), pack2(v[t][4], v[t][5]), pack2(v[t][6], v[t][7]));
+    sum += square_sum(v[t]);
+  }
+  const auto plus = [](float p, float q) { return p + q; };
+  sum = over_block(sum, sums, plus);
+  float by = 1.0f / sqrtf(sum / static_cast<float>(a.C) + a.eps);
+  if (!(sum < 1e38f) || (sum < 1e-28f && a.eps < 1e-18f)) {
+    // squares that leave float32: the row in units of a power of two near its
+    // largest value (infinities and NaN stay what they are)
+    uint32_t top = 0;
+#pragma unroll
+    for (int t = 0; t < kTurns; ++t)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) top = max(top, abs_bits(v[t][i]));
+    top = over_block(top, tops, [](uint32_t p, uint32_t q) { return max(p, q); });
+    if (top < 0x7F800000u && top > 0) {
+      const float unit = __uint_as_float(min(max(254 - static_cast<int>(top >> 23), 1), 253) << 23);
+      sum = 0.0f;
+#pragma unroll
+      for (int t = 0; t < kTurns; ++t) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[t][i] *= unit;
+        sum += square_sum(v[t]);
+      }
+      sum = over_block(sum, again, plus);
+      by = static_cast<float>(1.0 / sqrt(static_cast<double>(sum) / a.C + static_cast<double>(a.eps) * unit * unit));
+    }
+  }
+#pragma unroll
+  for (int t = 0; t < kTurns; ++t) {
+    const int c = (t * blockDim.x + threadIdx.x) * 8;
+    if (a.gamma != nullptr) {
+      float g[8];
+      unpack8(c < a.C ? ldg16(a.gamma + c) : make_uint4(0, 0, 0, 0), g);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[t][i] = v[t][i] * by * g[i];
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[t][i] *= by;
+    }
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) top = max(top, abs_bits(v[t][i]));
+    top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+    top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+    const uint32_t b = mx_scale_byte(top);
+    const float m = mx_inverse(b);
+    // the bytes of the four blocks of a piece, in its first lane
+    uint32_t word = b << (threadIdx.x / 4 % 4 * 8);
+    word |= __shfl_xor_sync(0xffffffffu, word, 4);
+    word |= __shfl_xor_sync(0xffffffffu, word, 8);
+    if (c < a.C) {
+      *reinterpret_cast<uint2*>(a.codes + row * a.C + c) =
+          make_uint2(mx_codes4(v[t][0] * m, v[t][1] * m, v[t][2] * m, v[t][3] * m),
+                     mx_codes4(v[t][4] * m, v[t][5] * m, v[t][6] * m, v[t][7] * m));
+      if (threadIdx.x % 16 == 0) *reinterpret_cast<uint32_t*>(a.scales + mx_scale_at(row, c / kMxBlock, a.C)) = word;
+    }
+  }
+}
+
+template <int kTurns>
+cudaError_t launch_norm(const NormArgs& a, int64_t rows, cudaStream_t stream) {
+  const int threads = ((a.C / 8 + kTurns - 1) / kTurns + 31) / 32 * 32;
+  return launch_kernel(norm_mx8_kernel<kTurns>, dim3(static_cast<unsigned>(rows)), dim3(threads), 0, stream, 1, a);
+}
+
+// 16 codes a thread.
+__global__ void __launch_bounds__(256) mx8_read_kernel(const uint8_t* codes, const uint8_t* scales, int64_t rows,
+                                                       int columns, ple_bf16_t* out) {
+  pdl_wait();
+  pdl_trigger();
+  const int per_row = columns / 16;
+  const int64_t all = rows * per_row, step = int64_t(gridDim.x) * blockDim.x;
+  for (int64_t i = int64_t(blockIdx.x) * blockDim.x + threadIdx.x; i < all; i += step) {
+    const int64_t row = i / per_row;
+    const int c = static_cast<int>(i % per_row) * 16;
+    const uint4 w = __ldg(reinterpret_cast<const uint4*>(codes + row * columns + c));
+    const float power = mx_power(__ldg(scales + mx_scale_at(row, c / kMxBlock, columns)));
+    const uint32_t words[4] = {w.x, w.y, w.z, w.w};
+    uint32_t v[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const float2 f = mx_values2(words[k / 2] >> (k % 2 * 16) & 0xffff);
+      v[k] = pack2(f.x * power, f.y * power);
+    }
+    uint4* to = reinterpret_cast<uint4*>(out + row * columns + c);
+    to[0] = make_uint4(v[0], v[1], v[2], v[3]);
+    to[1] = make_uint4(v[4], v[5], v[6], v[7]);
+  }
+}
+
+constexpr int kMaxNorm = 16384;  // columns: two turns of 1024 threads
+
+}  // namespace
+}  // namespace ple
+
+using namespace ple;
+
+PLE_EXPORT size_t ple_mx8_scale_bytes(int64_t rows, int32_t columns) {
+  const int64_t n = mx_scale_size(rows, columns);
+  return n > 0 ? static_cast<size_t>(n) : 0;
+}
+
+PLE_EXPORT ple_status ple_norm_mx8(const ple_bf16_t* x, int64_t x_stride, const ple_bf16_t* residual,
+                                   int64_t residual_stride, const ple_bf16_t* gamma, float eps,
+                                   int64_t num_tokens, int32_t hidden, ple_bf16_t* sum_out,
+                                   int64_t sum_stride, uint8_t* codes, uint8_t* scales,
+                                   cudaStream_t stream) {
+  const char* name = "ple_norm_mx8";
+  if (num_tokens < 0 || num_tokens > INT32_MAX || hidden < 1 || !(eps > 0.0f) || !std::isfinite(eps))
+    return fail(PLE_ERR_INVALID_ARG, "%s: num_tokens %lld, hidden %d, eps %g", name,
+                static_cast<long long>(num_tokens), hidden, static_cast<double>(eps));
+  if (hidden % kMxTile != 0 || hidden > kMaxNorm)
+    return fail(PLE_ERR_UNSUPPORTED, "%s: hidden %d (a multiple of %d up to %d)", name, hidden, kMxTile, kMaxNorm);
+  if (num_tokens == 0) return PLE_OK;
+  if (x == nullptr || codes == nullptr || scales == nullptr)
+    return fail(PLE_ERR_INVALID_ARG, "%s: null x, codes or scales", name);
+  if (!aligned16(x) || !aligned16(residual) || !aligned16(gamma) || !aligned16(sum_out) || !aligned16(codes) ||
+      !aligned16(scales) || x_stride % 8 != 0 || residual_stride % 8 != 0 || sum_stride % 8 != 0)
+    return fail(PLE_ERR_INVALID_ARG, "%s: buffers must be 16-byte aligned, strides multiples of 8", name);
+  const int64_t width = int64_t(hidden) * 2;
+  const RowSpan in[] = {{x, num_tokens, x_stride * 2, width},
+                        {residual, residual == nullptr ? 0 : num_tokens, residual_stride * 2, width},
+                        {gamma, gamma == nullptr ? 0 : 1, 0, width}};
+  const RowSpan out[] = {{codes, 1, 0, num_tokens * hidden},
+                         {scales, 1, 0, mx_scale_size(num_tokens, hidden)},
+                         {sum_out, sum_out == nullptr ? 0 : num_tokens, sum_stride * 2, width}};
+  for (int o = 0; o < 3; ++o) {
+    for (int i = 0; i < 3; ++i) {
+      // a row is read whole before its place is written
+      const bool itself = o == 2 && i < 2 && out[o].base == in[i].base && out[o].stride == in[i].stride;
+      if (!itself && rows_overlap(out[o], in[i]))
+        return fail(PLE_ERR_INVALID_ARG, "%s: an output overlaps an input", name);
+    }
+    for (int i = 0; i < o; ++i)
+      if (rows_overlap(out[o], out[i])) return fail(PLE_ERR_INVALID_ARG, "%s: two outputs overlap", name);
+  }
+  if (sum_out != nullptr && num_tokens > 1 && (sum_stride < 0 ? -sum_stride : sum_stride) < hidden)
+    return fail(PLE_ERR_INVALID_ARG, "%s: rows of sum_out overlap", name);
+  const NormArgs a{x, residual, gamma, x_stride, residual_stride, sum_stride, hidden, eps, sum_out, codes, scales};
+  return check_cuda(hidden <= 4096 ? launch_norm<1>(a, num_tokens, stream) : launch_norm<2>(a, num_tokens, stream), name);
+}
+
+PLE_EXPORT ple_status ple_mx8_read(const uint8_t* codes, const uint8_t* scales, int64_t rows, int32_t columns,
+                                   ple_bf16_t* out, cudaStream_t stream) {
+  const char* name = "ple_mx8_read";
+  if (rows < 0 || rows > INT32_MAX || columns < 1)
+    return fail(PLE_ERR_INVALID_ARG, "%s: rows %lld, columns %d", name, static_cast<long long>(rows), columns);
+  if (columns % kMxTile != 0)
+    return fail(PLE_ERR_UNSUPPORTED, "%s: columns %d (a multiple of %d)", name, columns, kMxTile);
+  if (rows == 0) return PLE_OK;
+  if (codes == nullptr || scales == nullptr || out == nullptr)
+    return fail(PLE_ERR_INVALID_ARG, "%s: null codes, scales or out", name);
+  if (!aligned16(codes) || !aligned16(scales) || !aligned16(out))
+    return fail(PLE_ERR_INVALID_ARG, "%s: buffers must be 16-byte aligned", name);
+  const size_t n = static_cast<size_t>(rows) * columns;
+  if (overlaps(out, 2 * n, codes, n) || overlaps(out, 2 * n, scales, mx_scale_size(rows, columns)))
+    return fail(PLE_ERR_INVALID_ARG, "%s: out overlaps codes or scales", name);
+  const int64_t need = (static_cast<int64_t>(n / 16) + 255) / 256;
+  const int64_t most = int64_t(num_sms()) * 8;
+  return check_cuda(launch_kernel(mx8_read_kernel, dim3(static_cast<unsigned>(need < most ? need : most)), dim3(256), 0,
+                                  stream, 1, codes, scales, rows, columns, out), name);
+}

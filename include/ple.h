@@ -17,7 +17,9 @@
  *   ple_gated_conv    short conv of u = g * v   -> y   [T][C] bf16
  * Beside the layer, the 4-bit step of its attention block (near the end of
  * this file): ple_kv_append / ple_kv_read / ple_kv_attention over a paged
- * key/value cache in 4 bits, and ple_proj_w4, a projection with 4-bit weights.
+ * key/value cache in 4 bits, and ple_proj_w4, a projection with 4-bit weights;
+ * and the 8-bit step of its feed-forward block (after it): ple_norm_mx8,
+ * ple_gated_mx8, ple_proj_mx8 and ple_mx8_read.
  *
  * Sources (page titles abbreviated):
  *   PR#54517 report "[Qwen3.8-Flash-Next] Fuse Qwen4Exp PLE kernels":
@@ -803,6 +805,87 @@ ple_status ple_proj_w4(const ple_bf16_t* x, int64_t x_stride, int64_t num_tokens
                        int32_t out_dim, const uint8_t* codes, const ple_bf16_t* scales,
                        const uint8_t* zeros, int32_t group, ple_bf16_t* out, int32_t* dev_err,
                        cudaStream_t stream);
+
+/*
+ * The 8-bit step of the feed-forward block beside the layer: the norm with
+ * the residual's addition (ple_norm_mx8), the gated block's two projections
+ * with activation and product (ple_gated_mx8), the projection back
+ * (ple_proj_mx8), and an 8-bit tensor's values (ple_mx8_read).
+ *
+ * 8-bit tensors ("mx8"). codes [rows][columns] are e4m3 bytes, columns a
+ * multiple of 128 (else PLE_ERR_UNSUPPORTED), rows `columns` bytes apart.
+ * Each 32 columns of a row (a block) share a scale byte b: a code stands for
+ * e4m3(code) * 2^(b - 127), and for NaN where b is 255. A block x is
+ * quantised with the least b >= 0 for which max |x| <= 448 * 2^(b - 127),
+ *   code = e4m3_rn(x * 2^(127 - b));
+ * a block with a NaN or an infinity in it has b = 255: its 32 values read as
+ * NaN. Scales lie in pieces of 512 bytes for 128 rows and 128 columns:
+ *   byte ((r / 128) * (columns / 128) + j / 4) * 512
+ *        + (r % 32) * 16 + (r % 128 / 32) * 4 + j % 4
+ * is row r's of block j. ple_mx8_scale_bytes(rows, columns) is their size,
+ * whole pieces; bytes of rows that do not exist are neither used nor written.
+ * Codes and scales are 16-byte aligned device memory.
+ */
+size_t ple_mx8_scale_bytes(int64_t rows, int32_t columns);
+
+/* Values of an 8-bit tensor: out [rows][columns] bf16, 16-byte aligned, each
+ * bf16_rn(e4m3(code) * 2^(b - 127)), which rounds only below 2^-126. */
+ple_status ple_mx8_read(const uint8_t* codes, const uint8_t* scales, int64_t rows,
+                        int32_t columns, ple_bf16_t* out, cudaStream_t stream);
+
+/*
+ * ple_norm_mx8 -- s = x + residual; sum_out = bf16(s);
+ * (codes, scales) = mx8(s / sqrt(mean(s^2) + eps) * gamma), in float32: the
+ * norm is of the sum before it is rounded.
+ *   x, residual  bf16 rows of hidden, x_stride (residual_stride) elements
+ *                apart, 16-byte aligned, strides multiples of 8. residual may
+ *                be NULL (nothing is added).
+ *   gamma        [hidden] bf16, 16-byte aligned, or NULL for 1.
+ *   eps          finite, > 0.
+ *   hidden       a multiple of 128 up to 16384 (else PLE_ERR_UNSUPPORTED).
+ *   sum_out      bf16 rows, sum_stride apart, or NULL; may be x or residual
+ *                itself (same pointer and stride). Any other overlap of an
+ *                output is PLE_ERR_INVALID_ARG.
+ *   codes, scales  [num_tokens][hidden], as above.
+ * Rows up to bf16's largest and down to its least are normalised as any other.
+ */
+ple_status ple_norm_mx8(const ple_bf16_t* x, int64_t x_stride, const ple_bf16_t* residual,
+                        int64_t residual_stride, const ple_bf16_t* gamma, float eps,
+                        int64_t num_tokens, int32_t hidden, ple_bf16_t* sum_out,
+                        int64_t sum_stride, uint8_t* codes, uint8_t* scales,
+                        cudaStream_t stream);
+
+/* Activations of ple_gated_mx8: x / (1 + exp(-x)); gelu in its tanh form,
+ * x / (1 + exp(-2 sqrt(2 / pi) (x + 0.044715 x^3))). */
+typedef enum { PLE_SILU = 0, PLE_GELU = 1 } ple_activation;
+
+/*
+ * ple_gated_mx8 -- the first half of a gated feed-forward block,
+ *   h = act(x Wg^T) * (x Wu^T), (codes, scales) = mx8(h).
+ * Float32 sums; h is not rounded before it is quantised.
+ *   x, x_scales  mx8 [num_tokens][hidden].
+ *   w, w_scales  mx8 [2 * inner][hidden]: Wg's rows, then Wu's.
+ *   inner        a multiple of 128 (else PLE_ERR_UNSUPPORTED).
+ *   codes, scales  mx8 [num_tokens][inner], no part of them an operand's.
+ */
+ple_status ple_gated_mx8(const uint8_t* x, const uint8_t* x_scales, int64_t num_tokens,
+                         int32_t hidden, const uint8_t* w, const uint8_t* w_scales,
+                         int32_t inner, int32_t activation, uint8_t* codes, uint8_t* scales,
+                         int32_t* dev_err, cudaStream_t stream);
+
+/*
+ * ple_proj_mx8 -- out = residual + x W^T, float32 sums, rounded once.
+ *   x, x_scales  mx8 [num_tokens][in_dim].
+ *   w, w_scales  mx8 [out_dim][in_dim].
+ *   residual     bf16 rows of out_dim, residual_stride elements apart, or
+ *                NULL; may be out itself (residual_stride = out_dim). Any
+ *                other overlap with out is PLE_ERR_INVALID_ARG.
+ *   out          [num_tokens][out_dim] bf16, no part of it an operand's.
+ */
+ple_status ple_proj_mx8(const uint8_t* x, const uint8_t* x_scales, int64_t num_tokens,
+                        int32_t in_dim, const uint8_t* w, const uint8_t* w_scales,
+                        int32_t out_dim, const ple_bf16_t* residual, int64_t residual_stride,
+                        ple_bf16_t* out, int32_t* dev_err, cudaStream_t stream);
 
 /* Text of the last non-OK status on this host thread ("" if none). */
 const char* ple_last_error(void);

@@ -1,12 +1,17 @@
-// ple_proj_mx8 and ple_gated_mx8: products of 8-bit tensors (mx8.cuh).
+// ple_proj_mx8 and ple_gated_mx8: products of 8-bit tensors (mx8.cuh) on the
+// 5th-generation tensor cores, which take the blocks' scales with the codes.
 //
 //   ple_proj_mx8    out = residual + x W^T, rounded once to bf16
 //   ple_gated_mx8   h = act(x Wg^T) * (x Wu^T), quantised as it is computed
 //
-// One thread block takes 64 tokens and 64 rows of W (gated: 32 of the gate's
-// and the 32 of the other half that meet them) and a block of 32 columns at a
-// time, its values in shared memory as float32.
-#include "mx8.cuh"
+// Two kernels: for many tokens a pair of CTAs takes 256 tokens against 256
+// rows of W (bound by the tensor cores); for few a CTA takes 128 rows of W
+// against all tokens, its columns shared out in a cluster (bound by reading
+// W).
+#include "mx8_tensor.cuh"
+
+#include <algorithm>
+#include <atomic>
 
 namespace ple {
 namespace {
@@ -16,6 +21,7 @@ struct ProductArgs {
   int64_t T;
   int E, N;  // columns; rows of the result: of W, or half as many
   int gelu;
+  int wide;  // rows of out and the residual may be taken 16 bytes at a time
   const ple_bf16_t* residual;
   int64_t residual_stride;
   ple_bf16_t* out;
@@ -27,79 +33,563 @@ __device__ __forceinline__ float activation(float g, int gelu) {
   return g / (1.0f + expf(-turn));
 }
 
+// ---------------------------------------------------------------------------
+// Many tokens: a pair of CTAs, 256 tokens x 256 rows of W
+// ---------------------------------------------------------------------------
+// Each CTA stages its own 128 tokens and half of the tile's W rows (gated:
+// one the gate's 128 rows, the other the 128 rows of the other half that meet
+// them, so that a thread of the epilogue finds both in its row), and the
+// scales of its tokens and of all W rows. A stage holds 256 columns; its
+// scales go to tensor memory in front of its products.
+// The sums take 256 of the 512 columns of tensor memory and the scales some
+// of the rest, so there is one set of sums: the epilogue's eight warps take
+// them into registers (128 a thread) and give the place back before they do
+// anything with them.
+// Tiles are walked in groups of 2048 tokens, tokens first: W is read once for
+// each group, and the group's tokens stay in L2.
+//
+// Warps: 0 copies, 1 issues, 2-9 the epilogue: two for each quarter of the
+// rows, half of the columns each.
+constexpr int kPairStages = 3;
+constexpr int kPairAtoms = 2;                              // 128 columns each, of a stage
+constexpr int kAtom = 128 * 128;                           // bytes of 128 rows' codes of 128 columns
+constexpr int kPairScales = kPairAtoms * 3 * kMxPiece;     // bytes of a stage's scales: x, two of W
+constexpr int kPairStage = kPairAtoms * 2 * kAtom + kPairScales;
+constexpr int kAtScales = kPairStages * kPairAtoms * 2 * kAtom;
+constexpr int kAtRoom = kAtScales + kPairStages * kPairScales;
+constexpr int kRoomPitch = 17;                             // floats of a row of the epilogue's room
+constexpr int kRoom = 32 * kRoomPitch * 4;                 // bytes of it for a warp
+constexpr int kPairEpilogue = 8;                           // warps
+constexpr int kAtBars = kAtRoom + kPairEpilogue * kRoom;
+constexpr int kPairBars = 2 * kPairStages + 3;
+constexpr int kPairSmem = kAtBars + kPairBars * 8 + 16 + 1024;  // and alignment
+constexpr int kPairThreads = 64 + 32 * kPairEpilogue;
+constexpr int kGroupTiles = 8;                             // of 256 tokens
+constexpr int kScaleCols = 256;                            // scales stand behind the sums
+constexpr int kAtomCols = 12;                              // 4 of x, 8 of W
+static_assert(kScaleCols + kPairStages * kPairAtoms * kAtomCols <= 512, "tensor memory");
+static_assert(kPairSmem <= 227 << 10, "shared memory");
+
+struct PairTile {
+  int m, n;  // first token; first row of the result
+};
+
+__device__ __forceinline__ PairTile pair_tile(int u, int m_tiles, int n_tiles, int rows) {
+  const int group = u / (kGroupTiles * n_tiles), first = group * kGroupTiles;
+  const int height = min(m_tiles - first, kGroupTiles), r = u - first * n_tiles;
+  return {(first + r % height) * 256, r / height * rows};
+}
+
 template <bool kGated>
-__global__ void __launch_bounds__(256) product_kernel(const ProductArgs a) {
-  __shared__ float xs[32][65], ws[32][65];
-  const int64_t t0 = int64_t(blockIdx.y) * 64;
-  const int n0 = blockIdx.x * (kGated ? 32 : 64);
-  const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
-  float acc[4][4] = {};
-  // this thread's 8 codes of x and of W
-  const int r = threadIdx.x / 4, c = threadIdx.x % 4 * 8;
-  const int64_t t = t0 + r;
-  const int64_t n = kGated ? int64_t(r / 32) * a.N + n0 + r % 32 : n0 + r;
-  const bool t_in = t < a.T, n_in = kGated || n < a.N;
-  for (int e0 = 0; e0 < a.E; e0 += 32) {
-    uint2 cx = make_uint2(0, 0), cw = cx;
-    float px = 0.0f, pw = 0.0f;
-    if (t_in) {
-      cx = __ldg(reinterpret_cast<const uint2*>(a.x + t * a.E + e0 + c));
-      px = mx_power(a.x_scales[mx_scale_at(t, e0 / 32, a.E)]);
+__global__ void __launch_bounds__(kPairThreads, 1)
+product_pair_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_w,
+                    const __grid_constant__ CUtensorMap map_xs, const __grid_constant__ CUtensorMap map_ws,
+                    const ProductArgs a, int32_t* dev_err) {
+  constexpr int kRows = kGated ? 128 : 256;  // of the result in a tile
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* const smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t base = smem_u32(smem), bar0 = base + kAtBars;
+  auto full = [&](int s) { return bar0 + 8u * s; };
+  auto free = [&](int s) { return bar0 + 8u * (kPairStages + s); };
+  const uint32_t sums_full = bar0 + 8u * (2 * kPairStages), sums_free = sums_full + 8, done = sums_full + 16;
+  uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(smem + kAtBars + kPairBars * 8);
+  volatile int* const abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const uint32_t rank = cluster_rank();
+  const int m_tiles = static_cast<int>((a.T + 255) / 256), n_tiles = (a.N + kRows - 1) / kRows;
+  const int units = m_tiles * n_tiles;
+  const int atoms = a.E / 128, stages = (atoms + kPairAtoms - 1) / kPairAtoms;
+  const int pair = blockIdx.x / 2, pairs = gridDim.x / 2;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kPairStages; ++s) {
+      mbar_init(full(s), 1);  // the even CTA's expect_tx; bytes of both
+      mbar_init(free(s), 1);
     }
-    if (n_in) {
-      cw = __ldg(reinterpret_cast<const uint2*>(a.w + n * a.E + e0 + c));
-      pw = mx_power(a.w_scales[mx_scale_at(n, e0 / 32, a.E)]);
+    mbar_init(sums_full, 1);
+    mbar_init(sums_free, 2 * kPairEpilogue);
+    mbar_init(done, 1);
+    mbar_fence_init();
+    *abort_flag = 0;
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(tmem_slot)) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  }
+  fence_before();
+  __syncthreads();
+  cluster_barrier();  // both CTAs' barriers and tensor memory are there
+  fence_after();
+  const uint32_t tmem = *tmem_slot;
+  pdl_wait();
+  pdl_trigger();
+
+  if (warp == 0 && lane == 0) {
+    // ---------------- copies (both CTAs) ----------------
+    prefetch_map(&map_x);
+    prefetch_map(&map_w);
+    prefetch_map(&map_xs);
+    prefetch_map(&map_ws);
+    int s = 0;
+    uint32_t phase = 0, armed = 0, armed_parity = 0;
+    bool ok = true;
+    for (int u = pair; ok && u < units; u += pairs) {
+      const PairTile t = pair_tile(u, m_tiles, n_tiles, kRows);
+      const int m = t.m + static_cast<int>(rank) * 128;
+      const int n = kGated ? static_cast<int>(rank) * a.N + t.n : t.n + static_cast<int>(rank) * 128;  // this CTA's W rows
+      const int n2[2] = {t.n, kGated ? a.N + t.n : t.n + 128};  // all of them, for their scales
+      for (int k = 0; k < stages; ++k) {
+        if (!mbar_wait(free(s), phase ^ 1u, abort_flag)) { ok = false; break; }
+        const uint32_t bar = at_rank(full(s), 0);
+        if (rank == 0) {
+          mbar_arrive_expect_tx(full(s), 2 * kPairStage);
+          armed |= 1u << s;
+          armed_parity = (armed_parity & ~(1u << s)) | (phase << s);
+        }
+        // past the last column (an odd number of atoms) zeros come
+        for (int i = 0; i < kPairAtoms; ++i) {
+          const int x = (k * kPairAtoms + i) * 128;
+          tma_load_pair(base + (s * kPairAtoms + i) * 2 * kAtom, &map_x, bar, x, m);
+          tma_load_pair(base + (s * kPairAtoms + i) * 2 * kAtom + kAtom, &map_w, bar, x, n);
+        }
+        const uint32_t to = base + kAtScales + s * kPairScales;
+        tma_load_pair(to, &map_xs, bar, 0, m / 128 * atoms + k * kPairAtoms);
+        for (int h = 0; h < 2; ++h)
+          tma_load_pair(to + (1 + h) * kPairAtoms * kMxPiece, &map_ws, bar, 0, n2[h] / 128 * atoms + k * kPairAtoms);
+        if (++s == kPairStages) { s = 0; phase ^= 1u; }
+      }
     }
-    __syncthreads();
+    if (!ok) { *abort_flag = 1; set_dev_err(dev_err, PLE_DEVERR_TIMEOUT); }
+    // no leaving with copies in flight
+    for (int i = 0; i < kPairStages; ++i)
+      if (armed & (1u << i)) mbar_wait(full(i), (armed_parity >> i) & 1u, nullptr);
+  } else if (warp == 1) {
+    if (rank == 0 && lane == 0) {
+      // ---------------- products (the even CTA, for both) ----------------
+      int s = 0;
+      uint32_t phase = 0, tile_phase = 0;
+      bool ok = true;
+      for (int u = pair; ok && u < units; u += pairs, tile_phase ^= 1u) {
+        if (!mbar_wait(sums_free, tile_phase ^ 1u, abort_flag)) { ok = false; break; }
+        fence_after();
+        for (int k = 0; k < stages; ++k) {
+          if (!mbar_wait(full(s), phase, abort_flag)) { ok = false; break; }
+          fence_after();
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 fx = mx_values2((i < 2 ? cx.x : cx.y) >> (i % 2 * 16) & 0xffff);
-      const float2 fw = mx_values2((i < 2 ? cw.x : cw.y) >> (i % 2 * 16) & 0xffff);
-      xs[c + 2 * i][r] = fx.x * px;
-      xs[c + 2 * i + 1][r] = fx.y * px;
-      ws[c + 2 * i][r] = fw.x * pw;
-      ws[c + 2 * i + 1][r] = fw.y * pw;
+          for (int i = 0; i < kPairAtoms; ++i) {
+            if (k * kPairAtoms + i >= atoms) break;  // its scales are another row's
+            const uint32_t scales = tmem + kScaleCols + (s * kPairAtoms + i) * kAtomCols;
+            const uint32_t from = base + kAtScales + s * kPairScales + i * kMxPiece;
+#pragma unroll
+            for (int j = 0; j < 3; ++j) scales_to_tmem<2>(scales + 4 * j, from + j * kPairAtoms * kMxPiece);
+            const uint64_t x = codes_operand(base + (s * kPairAtoms + i) * 2 * kAtom);
+            const uint64_t w = codes_operand(base + (s * kPairAtoms + i) * 2 * kAtom + kAtom);
+#pragma unroll
+            for (int b = 0; b < 4; ++b)
+              mma_mx8<2>(tmem, x + 2 * b, w + 2 * b, mx_idesc(256, 256) | mx_block(b), scales, scales + 4, (k | i | b) != 0);
+          }
+          mma_commit_pair(free(s));
+          if (++s == kPairStages) { s = 0; phase ^= 1u; }
+        }
+        if (!ok) break;
+        mma_commit_pair(sums_full);
+      }
+      if (!ok) { *abort_flag = 1; set_dev_err(dev_err, PLE_DEVERR_TIMEOUT); }
+      asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(done) : "memory");
+      mbar_wait(done, 0, nullptr);
     }
-    __syncthreads();
-#pragma unroll 8
-    for (int k = 0; k < 32; ++k) {
-      float p[4], q[4];
+    __syncwarp();
+  } else if (warp >= 2) {
+    // ---------------- epilogue (both CTAs) ----------------
+    const int quad = warp & 3, half = (warp - 2) >> 2;
+    const uint32_t lanes = tmem + (static_cast<uint32_t>(quad * 32) << 16);
+    uint32_t tile_phase = 0;
+    for (int u = pair; u < units; u += pairs, tile_phase ^= 1u) {
+      const PairTile t = pair_tile(u, m_tiles, n_tiles, kRows);
+      if (!__all_sync(0xffffffffu, mbar_wait(sums_full, tile_phase, abort_flag))) {
+        if (lane == 0) { *abort_flag = 1; set_dev_err(dev_err, PLE_DEVERR_TIMEOUT); }
+        break;
+      }
+      fence_after();
+      float v[4][32];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        // gated: 64 columns of the gate and the 64 that meet them
+        const int col = kGated ? c / 2 * 128 + half * 64 + c % 2 * 32 : half * 128 + c * 32;
+        tmem_load(lanes + col, v[c]);
+      }
+      fence_before();
+      __syncwarp();
+      if (lane == 0) arrive_cluster(at_rank(sums_free, 0));
+      const int64_t m0 = t.m + static_cast<int64_t>(rank) * 128 + quad * 32;
+      if constexpr (kGated) {
+        const int64_t m = m0 + lane;
+        uint32_t word = 0;
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          uint32_t top = 0;
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            v[c][i] = activation(v[c][i], a.gelu) * v[c + 2][i];
+            top = max(top, abs_bits(v[c][i]));
+          }
+          const uint32_t b = mx_scale_byte(top);
+          const float by = mx_inverse(b);
+          word |= b << (8 * c);
+          uint32_t codes[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            codes[i] = mx_codes4(v[c][4 * i] * by, v[c][4 * i + 1] * by, v[c][4 * i + 2] * by, v[c][4 * i + 3] * by);
+          if (m < a.T) {
+            uint4* to = reinterpret_cast<uint4*>(a.codes + m * a.N + t.n + half * 64 + c * 32);
+            to[0] = make_uint4(codes[0], codes[1], codes[2], codes[3]);
+            to[1] = make_uint4(codes[4], codes[5], codes[6], codes[7]);
+          }
+        }
+        if (m < a.T) *reinterpret_cast<uint16_t*>(a.scales + mx_scale_at(m, (t.n + half * 64) / 32, a.N)) = static_cast<uint16_t>(word);
+      } else {
+        const int n0 = t.n + half * 128;
+        if (a.wide) {
+          const int64_t m = m0 + lane;
+          if (m < a.T) {
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+#pragma unroll
+              for (int q = 0; q < 4; ++q) {
+                const int n = n0 + c * 32 + q * 8;
+                if (n >= a.N) continue;
+                float* y = v[c] + 8 * q;
+                if (a.residual != nullptr) {
+                  float r[8];
+                  unpack8(*reinterpret_cast<const uint4*>(a.residual + m * a.residual_stride + n), r);
+#pragma unroll
+                  for (int i = 0; i < 8; ++i) y[i] += r[i];
+                }
+                *reinterpret_cast<uint4*>(a.out + m * a.N + n) =
+                    make_uint4(pack2(y[0], y[1]), pack2(y[2], y[3]), pack2(y[4], y[5]), pack2(y[6], y[7]));
+              }
+          }
+        } else {
+          // rows at any address: 16 columns of two rows at a time
+          float* const mine = reinterpret_cast<float*>(smem + kAtRoom) + (warp - 2) * 32 * kRoomPitch;
+#pragma unroll
+          for (int c = 0; c < 8; ++c) {
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < 16; ++i) mine[lane * kRoomPitch + i] = v[c / 2][c % 2 * 16 + i];
+            __syncwarp();
+            const int n = n0 + c * 16 + lane % 16;
+            for (int r = lane / 16; r < 32; r += 2) {
+              const int64_t m = m0 + r;
+              if (m >= a.T || n >= a.N) break;
+              float y = mine[r * kRoomPitch + lane % 16];
+              if (a.residual != nullptr) y += bf_lo(a.residual[m * a.residual_stride + n]);
+              a.out[m * a.N + n] = static_cast<ple_bf16_t>(pack2(y, 0.0f) & 0xffffu);
+            }
+          }
+        }
+      }
+    }
+  }
+  fence_before();
+  __syncthreads();
+  cluster_barrier();  // no CTA leaves while the other's products read its memory
+  if (warp == 1) {
+    fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+  }
+}
+
+// Pairs of CTAs that can be on the GPU at once (a GPC may not hold a whole
+// number of pairs), of a kernel on the current device.
+template <bool kGated>
+int resident_pairs() {
+  constexpr int kDevices = 64;
+  static std::atomic<int> known[kDevices];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 1;
+  if (dev >= 0 && dev < kDevices && known[dev].load() > 0) return known[dev].load();
+  int pairs = num_sms() / 2, active = 0;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(pairs) * 2);
+  cfg.blockDim = dim3(kPairThreads);
+  cfg.dynamicSmemBytes = kPairSmem;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaOccupancyMaxActiveClusters(&active, product_pair_kernel<kGated>, &cfg) == cudaSuccess && active > 0)
+    pairs = active < pairs ? active : pairs;
+  else
+    cudaGetLastError();  // a failed query leaves the SMs' bound
+  if (dev >= 0 && dev < kDevices) known[dev].store(pairs);
+  return pairs;
+}
+
+template <bool kGated>
+ple_status launch_pair(const ProductArgs& a, int32_t* dev_err, cudaStream_t stream, const char* name) {
+  const int64_t w_rows = kGated ? 2 * int64_t(a.N) : a.N;
+  CUtensorMap x, w, xs, ws;
+  ple_status s = mx_codes_map(&x, a.x, a.T, a.E, 128, name);
+  if (s == PLE_OK) s = mx_codes_map(&w, a.w, w_rows, a.E, 128, name);
+  if (s == PLE_OK) s = mx_scales_map(&xs, a.x_scales, a.T, a.E, kPairAtoms, name);
+  if (s == PLE_OK) s = mx_scales_map(&ws, a.w_scales, w_rows, a.E, kPairAtoms, name);
+  if (s != PLE_OK) return s;
+  const auto kernel = product_pair_kernel<kGated>;
+  cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kPairSmem);
+  if (err != cudaSuccess) return check_cuda(err, name);
+  const int64_t units = (a.T + 255) / 256 * ((a.N + (kGated ? 127 : 255)) / (kGated ? 128 : 256));
+  if (units > INT32_MAX / 2) return fail(PLE_ERR_UNSUPPORTED, "%s: %lld tokens", name, static_cast<long long>(a.T));
+  const int64_t pairs = std::min<int64_t>(units, resident_pairs<kGated>());
+  return check_cuda(launch_kernel(kernel, dim3(static_cast<unsigned>(2 * pairs)), dim3(kPairThreads), kPairSmem, stream, 2,
+                                  x, w, xs, ws, a, dev_err), name);
+}
+
+// ---------------------------------------------------------------------------
+// Few tokens: a CTA takes 128 rows of W
+// ---------------------------------------------------------------------------
+// W is the first operand (128 rows fill the tensor cores' lanes), the tokens
+// the second: 16 to 256 of them. Gated, a CTA takes 128 rows of the gate and
+// the 128 that meet them, into sums of their own. Where the rows alone would
+// leave SMs without work, a cluster of CTAs shares them: each takes a part of
+// the columns, and their sums meet through distributed shared memory, in the
+// order of the CTAs, each joining (and finishing) a share of the tokens.
+//
+// Warps: 0 copies, 1 issues, 2-5 take the sums out; all join.
+constexpr int kFewThreads = 192;
+constexpr int kMaxParts = 8;
+
+template <bool kGated, int kTokens>
+struct Few {
+  static constexpr int kSides = kGated ? 2 : 1;  // of W
+  static constexpr int kXPieces = kTokens > 128 ? 2 : 1;
+  static constexpr int kCodes = kSides * kAtom + kTokens * 128;  // bytes of a stage
+  static constexpr int kScales = (kSides + kXPieces) * kMxPiece;
+  static constexpr int kResident = kTokens <= 32 ? 2 : 1;        // CTAs an SM
+  static constexpr int kBudget = kResident == 2 ? 110 << 10 : 220 << 10;
+  static constexpr int kFit = kBudget / (kCodes + kScales);
+  static constexpr int kStages = kFit > 8 ? 8 : kFit;
+  static constexpr int kAtScales = kStages * kCodes;
+  static constexpr int kAtBars = kAtScales + kStages * kScales;
+  static constexpr int kSmem = kAtBars + (2 * kStages + 2) * 8 + 16 + 1024;  // and alignment
+  static constexpr int kCols = kSides * kTokens;                 // of sums
+  static constexpr int kStageCols = 4 * (kSides + kXPieces);     // of scales
+  static constexpr int kNeed = kCols + kStages * kStageCols;
+  static constexpr int kTmem = kNeed <= 64 ? 64 : kNeed <= 128 ? 128 : kNeed <= 256 ? 256 : 512;
+  static_assert(kNeed <= 512 / kResident && kTmem <= 512 / kResident, "tensor memory");
+  static_assert(kTokens * kSides * 128 * 4 <= kAtScales, "the sums fit where the codes were");
+  static_assert(kStages >= 2, "stages");
+};
+
+template <bool kGated, int kTokens>
+__global__ void __launch_bounds__(kFewThreads, Few<kGated, kTokens>::kResident)
+product_few_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_w,
+                   const ProductArgs a, int parts, int32_t* dev_err) {
+  using L = Few<kGated, kTokens>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* const smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t base = smem_u32(smem), bar0 = base + L::kAtBars;
+  auto full = [&](int s) { return bar0 + 8u * s; };
+  auto free = [&](int s) { return bar0 + 8u * (L::kStages + s); };
+  const uint32_t sums_full = bar0 + 8u * (2 * L::kStages);
+  uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kAtBars + (2 * L::kStages + 2) * 8);
+  volatile int* const abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int part = blockIdx.x % parts, n0 = blockIdx.x / parts * 128;
+  const int64_t t0 = int64_t(blockIdx.y) * kTokens;
+  const int tokens = static_cast<int>(min(a.T - t0, int64_t(kTokens)));
+  const int atoms = a.E / 128;
+  const int first = static_cast<int>(int64_t(part) * atoms / parts), last = static_cast<int>(int64_t(part + 1) * atoms / parts);
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < L::kStages; ++s) {
+      mbar_init(full(s), 1);
+      mbar_init(free(s), 1);
+    }
+    mbar_init(sums_full, 1);
+    mbar_fence_init();
+    *abort_flag = 0;
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)), "n"(L::kTmem) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  fence_before();
+  __syncthreads();
+  fence_after();
+  const uint32_t tmem = *tmem_slot;
+  pdl_wait();
+  pdl_trigger();
+
+  if (warp == 0) {
+    if (lane == 0) {
+      // ---------------- copies ----------------
+      uint32_t armed = 0, armed_parity = 0;
+      bool ok = true;
+      const uint8_t* const xs = a.x_scales + t0 / 128 * atoms * kMxPiece;
+      const uint8_t* ws[2];
+      for (int i = 0; i < L::kSides; ++i) ws[i] = a.w_scales + (int64_t(i) * a.N + n0) / 128 * atoms * kMxPiece;
+      // the second 128 tokens' scales, where there are such tokens
+      const bool more = L::kXPieces == 2 && tokens > 128;
+      for (int k = first; k < last; ++k) {
+        const int s = (k - first) % L::kStages;
+        const uint32_t phase = (k - first) / L::kStages & 1;
+        if (!mbar_wait(free(s), phase ^ 1u, abort_flag)) { ok = false; break; }
+        mbar_arrive_expect_tx(full(s), L::kCodes + L::kScales - (L::kXPieces == 2 && !more ? kMxPiece : 0));
+        armed |= 1u << s;
+        armed_parity = (armed_parity & ~(1u << s)) | (phase << s);
+        const uint32_t to = base + s * L::kCodes, scales = base + L::kAtScales + s * L::kScales;
+        for (int i = 0; i < L::kSides; ++i) {
+          tma_load_2d(to + i * kAtom, &map_w, full(s), k * 128, i * a.N + n0);
+          bulk_copy_g2s(scales + i * kMxPiece, ws[i] + int64_t(k) * kMxPiece, kMxPiece, full(s));
+        }
+        tma_load_2d(to + L::kSides * kAtom, &map_x, full(s), k * 128, static_cast<int>(t0));
+        bulk_copy_g2s(scales + L::kSides * kMxPiece, xs + int64_t(k) * kMxPiece, kMxPiece, full(s));
+        if (more)
+          bulk_copy_g2s(scales + (L::kSides + 1) * kMxPiece, xs + int64_t(atoms + k) * kMxPiece, kMxPiece, full(s));
+      }
+      if (!ok) { *abort_flag = 1; set_dev_err(dev_err, PLE_DEVERR_TIMEOUT); }
+      for (int i = 0; i < L::kStages; ++i)
+        if (armed & (1u << i)) mbar_wait(full(i), (armed_parity >> i) & 1u, nullptr);
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    if (lane == 0) {
+      // ---------------- products ----------------
+      bool ok = true;
+      for (int k = first; k < last; ++k) {
+        const int s = (k - first) % L::kStages;
+        if (!mbar_wait(full(s), (k - first) / L::kStages & 1, abort_flag)) { ok = false; break; }
+        fence_after();
+        const uint32_t scales = tmem + L::kCols + s * L::kStageCols, from = base + L::kAtScales + s * L::kScales;
+#pragma unroll
+        for (int i = 0; i < L::kSides + L::kXPieces; ++i) scales_to_tmem<1>(scales + 4 * i, from + i * kMxPiece);
+        const uint64_t x = codes_operand(base + s * L::kCodes + L::kSides * kAtom);
+#pragma unroll
+        for (int i = 0; i < L::kSides; ++i) {
+          const uint64_t w = codes_operand(base + s * L::kCodes + i * kAtom);
+#pragma unroll
+          for (int b = 0; b < 4; ++b)
+            mma_mx8<1>(tmem + i * kTokens, w + 2 * b, x + 2 * b, mx_idesc(128, kTokens) | mx_block(b), scales + 4 * i,
+                       scales + 4 * L::kSides, k > first || b > 0);
+        }
+        mma_commit(free(s));
+      }
+      if (!ok) { *abort_flag = 1; set_dev_err(dev_err, PLE_DEVERR_TIMEOUT); }
+      // however the loop ended, no product reads or writes after this
+      mma_commit(sums_full);
+      mbar_wait(sums_full, 0, nullptr);
+    }
+    __syncwarp();
+  } else {
+    // ---------------- sums, where the codes were: [token][side][row] ----------------
+    const bool ok = __all_sync(0xffffffffu, mbar_wait(sums_full, 0, nullptr)) && *abort_flag == 0;
+    fence_after();
+    if (ok) {
+      const int row = (warp & 3) * 32 + lane;
+      const uint32_t lanes = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+      float* const mine = reinterpret_cast<float*>(smem);
+#pragma unroll
+      for (int i = 0; i < L::kSides; ++i)
+#pragma unroll 1
+        for (int c = 0; c < kTokens && c < tokens; c += 16) {
+          float v[16];
+          tmem_load16(lanes + i * kTokens + c, v);
+#pragma unroll
+          for (int j = 0; j < 16; ++j)
+            if (c + j < tokens) mine[((c + j) * L::kSides + i) * 128 + row] = v[j];
+        }
+    }
+  }
+  fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(L::kTmem) : "memory");
+  }
+  if (parts > 1) cluster_barrier();
+  // ---------------- the parts' sums, in their order: a warp takes a token, a lane 4 rows ----------------
+  for (int t = part + warp * parts; t < tokens; t += parts * (kFewThreads / 32)) {
+    float v[L::kSides][4] = {};
+    for (int p = 0; p < parts; ++p)
+#pragma unroll
+      for (int i = 0; i < L::kSides; ++i) {
+        const float4 f = read_cluster4(base + ((t * L::kSides + i) * 128 + lane * 4) * 4, p);
+        v[i][0] += f.x; v[i][1] += f.y; v[i][2] += f.z; v[i][3] += f.w;
+      }
+    const int64_t m = t0 + t;
+    if constexpr (kGated) {
+      uint32_t top = 0;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        p[i] = xs[k][ty * 4 + i];
-        q[i] = ws[k][tx + 16 * i];
+        v[0][i] = activation(v[0][i], a.gelu) * v[1][i];
+        top = max(top, abs_bits(v[0][i]));
       }
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(p[i], q[j], acc[i][j]);
-    }
-  }
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int64_t token = t0 + ty * 4 + i;
-    if constexpr (kGated) {
-      const float h0 = activation(acc[i][0], a.gelu) * acc[i][2], h1 = activation(acc[i][1], a.gelu) * acc[i][3];
-      uint32_t top = max(abs_bits(h0), abs_bits(h1));
-#pragma unroll
-      for (int o = 8; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+      for (int o = 4; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
       const uint32_t b = mx_scale_byte(top);
-      if (token < a.T) {
-        a.codes[token * a.N + n0 + tx] = static_cast<uint8_t>(mx_codes2(h0 * mx_inverse(b), 0.0f));
-        a.codes[token * a.N + n0 + tx + 16] = static_cast<uint8_t>(mx_codes2(h1 * mx_inverse(b), 0.0f));
-        if (tx == 0) a.scales[mx_scale_at(token, n0 / 32, a.N)] = static_cast<uint8_t>(b);
-      }
-    } else if (token < a.T) {
+      const float by = mx_inverse(b);
+      *reinterpret_cast<uint32_t*>(a.codes + m * a.N + n0 + lane * 4) = mx_codes4(v[0][0] * by, v[0][1] * by, v[0][2] * by, v[0][3] * by);
+      uint32_t word = b << (lane / 8 * 8);
+      word |= __shfl_xor_sync(0xffffffffu, word, 8);
+      word |= __shfl_xor_sync(0xffffffffu, word, 16);
+      if (lane == 0) *reinterpret_cast<uint32_t*>(a.scales + mx_scale_at(m, n0 / 32, a.N)) = word;
+    } else {
+      const int n = n0 + lane * 4;
+      ple_bf16_t* const to = a.out + m * a.N + n;
+      const ple_bf16_t* const r = a.residual == nullptr ? nullptr : a.residual + m * a.residual_stride + n;
+      if (a.wide) {
+        if (n < a.N) {
+          if (r != nullptr) {
+            const uint2 w = *reinterpret_cast<const uint2*>(r);
+            v[0][0] += bf_lo(w.x); v[0][1] += bf_hi(w.x); v[0][2] += bf_lo(w.y); v[0][3] += bf_hi(w.y);
+          }
+          *reinterpret_cast<uint2*>(to) = make_uint2(pack2(v[0][0], v[0][1]), pack2(v[0][2], v[0][3]));
+        }
+      } else {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int row = n0 + tx + 16 * j;
-        if (row >= a.N) continue;
-        float y = acc[i][j];
-        if (a.residual != nullptr) y += bf_lo(a.residual[token * a.residual_stride + row]);
-        a.out[token * a.N + row] = static_cast<ple_bf16_t>(pack2(y, 0.0f) & 0xffffu);
+        for (int i = 0; i < 4; ++i)
+          if (n + i < a.N) {
+            if (r != nullptr) v[0][i] += bf_lo(r[i]);
+            to[i] = static_cast<ple_bf16_t>(pack2(v[0][i], 0.0f) & 0xffffu);
+          }
       }
     }
   }
+  if (parts > 1) cluster_barrier();  // no CTA leaves while its sums are read
+}
+
+template <bool kGated, int kTokens>
+ple_status launch_few(const ProductArgs& a, int32_t* dev_err, cudaStream_t stream, const char* name) {
+  using L = Few<kGated, kTokens>;
+  CUtensorMap x, w;
+  ple_status s = mx_codes_map(&x, a.x, a.T, a.E, kTokens, name);
+  if (s == PLE_OK) s = mx_codes_map(&w, a.w, kGated ? 2 * int64_t(a.N) : a.N, a.E, 128, name);
+  if (s != PLE_OK) return s;
+  const auto kernel = product_few_kernel<kGated, kTokens>;
+  const cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kSmem);
+  if (err != cudaSuccess) return check_cuda(err, name);
+  const int tiles = (a.N + 127) / 128, blocks = static_cast<int>((a.T + kTokens - 1) / kTokens), atoms = a.E / 128;
+  // parts of the columns, as long as all CTAs are on SMs at once and have some stages each
+  int parts = 1;
+  while (parts < kMaxParts && int64_t(tiles) * blocks * parts * 2 <= int64_t(num_sms()) * L::kResident && atoms >= parts * 2 * 4)
+    parts *= 2;
+  const dim3 grid(static_cast<unsigned>(tiles * parts), static_cast<unsigned>(blocks));
+  return check_cuda(launch_kernel(kernel, grid, dim3(kFewThreads), L::kSmem, stream, static_cast<unsigned>(parts), x, w, a,
+                                  parts, dev_err), name);
+}
+
+template <bool kGated>
+ple_status launch_product(const ProductArgs& a, int32_t* dev_err, cudaStream_t stream, const char* name) {
+  if (a.T <= 16) return launch_few<kGated, 16>(a, dev_err, stream, name);
+  if (a.T <= 32) return launch_few<kGated, 32>(a, dev_err, stream, name);
+  if (a.T <= 64) return launch_few<kGated, 64>(a, dev_err, stream, name);
+  if (a.T <= 128) return launch_few<kGated, 128>(a, dev_err, stream, name);
+  if constexpr (!kGated)
+    if (a.T <= 256) return launch_few<false, 256>(a, dev_err, stream, name);
+  return launch_pair<kGated>(a, dev_err, stream, name);
 }
 
 ple_status check_product(const char* name, const uint8_t* x, const uint8_t* x_scales, int64_t num_tokens, int32_t in_dim,
@@ -125,6 +615,30 @@ bool meets_operands(const void* to, size_t n, const ProductArgs& a, int64_t w_ro
 }
 
 }  // namespace
+
+ple_status encode_map(CUtensorMap* map, CUtensorMapDataType type, const void* at, int64_t columns, int64_t rows,
+                      int64_t row_bytes, int box_columns, int box_rows, CUtensorMapSwizzle swizzle, const char* name) {
+  const auto encode = tensor_map_encoder();
+  if (encode == nullptr) return fail(PLE_ERR_CUDA, "%s: cuTensorMapEncodeTiled unavailable", name);
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(columns), static_cast<cuuint64_t>(rows)};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(row_bytes)};
+  const cuuint32_t box[2] = {static_cast<cuuint32_t>(box_columns), static_cast<cuuint32_t>(box_rows)};
+  const cuuint32_t steps[2] = {1, 1};
+  const CUresult r = encode(map, type, 2, const_cast<void*>(at), dims, strides, box, steps, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                            swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? PLE_OK : fail(PLE_ERR_CUDA, "%s: cuTensorMapEncodeTiled failed (%d)", name, static_cast<int>(r));
+}
+
+ple_status mx_codes_map(CUtensorMap* map, const void* codes, int64_t rows, int columns, int box_rows, const char* name) {
+  return encode_map(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, codes, columns, rows, columns, 128, box_rows,
+                    CU_TENSOR_MAP_SWIZZLE_128B, name);
+}
+
+ple_status mx_scales_map(CUtensorMap* map, const void* scales, int64_t rows, int columns, int box_pieces, const char* name) {
+  return encode_map(map, CU_TENSOR_MAP_DATA_TYPE_UINT32, scales, kMxPiece / 4, mx_scale_size(rows, columns) / kMxPiece,
+                    kMxPiece, kMxPiece / 4, box_pieces, CU_TENSOR_MAP_SWIZZLE_NONE, name);
+}
+
 }  // namespace ple
 
 using namespace ple;
@@ -143,13 +657,12 @@ PLE_EXPORT ple_status ple_gated_mx8(const uint8_t* x, const uint8_t* x_scales, i
   if (codes == nullptr || scales == nullptr) return fail(PLE_ERR_INVALID_ARG, "%s: null codes or scales", name);
   if (!aligned16(codes) || !aligned16(scales))
     return fail(PLE_ERR_INVALID_ARG, "%s: codes and scales must be 16-byte aligned", name);
-  const ProductArgs a{x, x_scales, w, w_scales, num_tokens, hidden, inner, activation == PLE_GELU, nullptr, 0, nullptr,
-                      codes, scales};
+  const ProductArgs a{x, x_scales, w, w_scales, num_tokens, hidden, inner, activation == PLE_GELU, 0, nullptr, 0,
+                      nullptr, codes, scales};
   const size_t n = static_cast<size_t>(num_tokens) * inner, m = mx_scale_size(num_tokens, inner);
   if (meets_operands(codes, n, a, 2LL * inner) || meets_operands(scales, m, a, 2LL * inner) || overlaps(codes, n, scales, m))
     return fail(PLE_ERR_INVALID_ARG, "%s: an output overlaps an operand or the other output", name);
-  const dim3 grid(inner / 32, static_cast<unsigned>((num_tokens + 63) / 64));
-  return check_cuda(launch_kernel_pdl(false, product_kernel<true>, grid, dim3(256), 0, stream, 1, a), name);
+  return launch_product<true>(a, dev_err, stream, name);
 }
 
 PLE_EXPORT ple_status ple_proj_mx8(const uint8_t* x, const uint8_t* x_scales, int64_t num_tokens, int32_t in_dim,
@@ -160,13 +673,13 @@ PLE_EXPORT ple_status ple_proj_mx8(const uint8_t* x, const uint8_t* x_scales, in
   const ple_status s = check_product(name, x, x_scales, num_tokens, in_dim, w, w_scales, out_dim);
   if (s != PLE_OK || num_tokens == 0) return s;
   if (out == nullptr) return fail(PLE_ERR_INVALID_ARG, "%s: null out", name);
-  const ProductArgs a{x, x_scales, w, w_scales, num_tokens, in_dim, out_dim, 0, residual, residual_stride, out,
+  const bool wide = out_dim % 8 == 0 && aligned16(out) && (residual == nullptr || (aligned16(residual) && residual_stride % 8 == 0));
+  const ProductArgs a{x, x_scales, w, w_scales, num_tokens, in_dim, out_dim, 0, wide, residual, residual_stride, out,
                       nullptr, nullptr};
   const size_t n = static_cast<size_t>(num_tokens) * out_dim * 2;
   if (meets_operands(out, n, a, out_dim)) return fail(PLE_ERR_INVALID_ARG, "%s: out overlaps an operand", name);
   if (residual != nullptr && !(residual == out && (residual_stride == out_dim || num_tokens == 1)) &&
       rows_overlap({out, 1, 0, static_cast<int64_t>(n)}, {residual, num_tokens, residual_stride * 2, int64_t(out_dim) * 2}))
     return fail(PLE_ERR_INVALID_ARG, "%s: out overlaps the residual and is not the residual", name);
-  const dim3 grid((out_dim + 63) / 64, static_cast<unsigned>((num_tokens + 63) / 64));
-  return check_cuda(launch_kernel_pdl(false, product_kernel<false>, grid, dim3(256), 0, stream, 1, a), name);
+  return launch_product<false>(a, dev_err, stream, name);
 }

@@ -30,7 +30,7 @@ struct ProductArgs {
 
 __device__ __forceinline__ float activation(float g, int gelu) {
   const float turn = gelu ? 1.5957691216057308f * (g + 0.044715f * g * g * g) : g;  // 2 sqrt(2 / pi)
-  return g / (1.0f + expf(-turn));
+  return __fdividef(g, 1.0f + __expf(-turn));
 }
 
 // ---------------------------------------------------------------------------
@@ -176,12 +176,15 @@ product_pair_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_cons
           if (!mbar_wait(full(s), phase, abort_flag)) { ok = false; break; }
           fence_after();
 #pragma unroll
+          for (int i = 0; i < kPairAtoms; ++i)
+#pragma unroll
+            for (int j = 0; j < 3; ++j)
+              scales_to_tmem<2>(tmem + kScaleCols + (s * kPairAtoms + i) * kAtomCols + 4 * j,
+                                base + kAtScales + s * kPairScales + (j * kPairAtoms + i) * kMxPiece);
+#pragma unroll
           for (int i = 0; i < kPairAtoms; ++i) {
             if (k * kPairAtoms + i >= atoms) break;  // its scales are another row's
             const uint32_t scales = tmem + kScaleCols + (s * kPairAtoms + i) * kAtomCols;
-            const uint32_t from = base + kAtScales + s * kPairScales + i * kMxPiece;
-#pragma unroll
-            for (int j = 0; j < 3; ++j) scales_to_tmem<2>(scales + 4 * j, from + j * kPairAtoms * kMxPiece);
             const uint64_t x = codes_operand(base + (s * kPairAtoms + i) * 2 * kAtom);
             const uint64_t w = codes_operand(base + (s * kPairAtoms + i) * 2 * kAtom + kAtom);
 #pragma unroll
@@ -211,13 +214,11 @@ product_pair_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_cons
         break;
       }
       fence_after();
+      // gated: 64 columns of the gate and the 64 that meet them
       float v[4][32];
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        // gated: 64 columns of the gate and the 64 that meet them
-        const int col = kGated ? c / 2 * 128 + half * 64 + c % 2 * 32 : half * 128 + c * 32;
-        tmem_load(lanes + col, v[c]);
-      }
+      for (int c = 0; c < 4; ++c) tmem_ask(lanes + (kGated ? c / 2 * 128 + half * 64 + c % 2 * 32 : half * 128 + c * 32), v[c]);
+      tmem_wait(v);
       fence_before();
       __syncwarp();
       if (lane == 0) arrive_cluster(at_rank(sums_free, 0));

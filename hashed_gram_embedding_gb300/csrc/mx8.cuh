@@ -61,6 +61,20 @@ __device__ __forceinline__ float2 mx_values2(uint32_t codes) {
 
 __device__ __forceinline__ uint32_t abs_bits(float x) { return __float_as_uint(x) & 0x7FFFFFFFu; }
 
+// 32 bytes in one store, where the address is a multiple of 32 (a whole sector
+// at a time), or two.
+__device__ __forceinline__ void store32(void* to, const uint32_t (&v)[8]) {
+  if ((reinterpret_cast<uintptr_t>(to) & 31) == 0) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+                 "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+  } else {
+    uint4* const p = static_cast<uint4*>(to);
+    p[0] = make_uint4(v[0], v[1], v[2], v[3]);
+    p[1] = make_uint4(v[4], v[5], v[6], v[7]);
+  }
+}
+
 // Bytes of a tensor's scales, or -1 for sizes that have none.
 inline int64_t mx_scale_size(int64_t rows, int64_t columns) {
   if (rows < 0 || rows > INT32_MAX || columns < kMxTile || columns % kMxTile != 0 || columns > INT32_MAX) return -1;

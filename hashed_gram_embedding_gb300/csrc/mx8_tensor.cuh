@@ -69,8 +69,30 @@ __device__ __forceinline__ uint32_t at_rank(uint32_t saddr, uint32_t rank) {
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(saddr), "r"(rank));
   return r;
 }
-// A copy into this CTA's shared memory, counted on a barrier of either CTA.
-__device__ __forceinline__ void tma_load_pair(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y) {
+// Copies into this CTA's shared memory, counted on a barrier of either CTA:
+// codes of some rows, from an atom (128 columns) on, each atom [row][128];
+// pieces of scales.
+__device__ __forceinline__ void tma_load_pair(uint32_t dst, const CUtensorMap* map, uint32_t bar, int atom, int row) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2"
+      " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(row), "r"(atom), "r"(bar)
+      : "memory");
+}
+// The same codes for a CTA by itself, and only as far as L2.
+__device__ __forceinline__ void tma_load_atoms(uint32_t dst, const CUtensorMap* map, uint32_t bar, int atom, int row) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(row), "r"(atom), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void prefetch_atoms(const CUtensorMap* map, int atom, int row) {
+  asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];" ::"l"(reinterpret_cast<uint64_t>(map)),
+               "r"(0), "r"(row), "r"(atom)
+               : "memory");
+}
+__device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y) {
   asm volatile(
       "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2"
       " [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
@@ -116,9 +138,10 @@ __device__ __forceinline__ void tmem_wait(float (&v)[kLoads][32]) {
     for (int i = 0; i < 32; ++i) asm volatile("" : "+f"(v[c][i]));
 }
 
-// Maps of an 8-bit tensor: its codes in boxes of 128 columns, its scales as
-// rows of 512 bytes, one a piece.
-ple_status mx_codes_map(CUtensorMap* map, const void* codes, int64_t rows, int columns, int box_rows, const char* name);
+// Maps of an 8-bit tensor: its codes as [atom][row][128], its scales as rows
+// of 512 bytes, one a piece.
+ple_status mx_codes_map(CUtensorMap* map, const void* codes, int64_t rows, int columns, int box_rows, int box_atoms,
+                        const char* name);
 ple_status mx_scales_map(CUtensorMap* map, const void* scales, int64_t rows, int columns, int box_pieces,
                          const char* name);
 

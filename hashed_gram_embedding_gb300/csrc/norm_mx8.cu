@@ -25,18 +25,20 @@ struct NormArgs {
   uint8_t *codes, *scales;
 };
 
-// A value for the whole CTA, the warps' in their order.
+// A value for the whole CTA, in an order that its size alone decides; `none`
+// changes nothing in a join.
 template <typename T, typename F>
-__device__ __forceinline__ T over_block(T v, T* room, F join) {
+__device__ __forceinline__ T over_block(T v, T* room, T none, F join) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v = join(v, __shfl_xor_sync(0xffffffffu, v, o));
-  const int warp = threadIdx.x / 32, warps = blockDim.x / 32;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, warps = blockDim.x / 32;
   if (warps == 1) return v;
-  if (threadIdx.x % 32 == 0) room[warp] = v;
+  if (lane == 0) room[warp] = v;
   __syncthreads();
-  v = room[0];
-  for (int i = 1; i < warps; ++i) v = join(v, room[i]);
-  return v;
+  v = lane < warps ? room[lane] : none;
+  for (int o = warps > 8 ? 8 : warps > 4 ? 4 : warps > 2 ? 2 : 1; o > 0; o >>= 1)
+    v = join(v, __shfl_xor_sync(0xffffffffu, v, o));
+  return __shfl_sync(0xffffffffu, v, 0);
 }
 
 __device__ __forceinline__ float square_sum(const float (&v)[8]) {
@@ -50,7 +52,7 @@ __device__ __forceinline__ float square_sum(const float (&v)[8]) {
 }
 
 template <int kTurns>
-__global__ void __launch_bounds__(kTurns == 1 ? 512 : 1024)
+__global__ void __launch_bounds__(512)
 norm_mx8_kernel(const NormArgs a) {
   __shared__ float sums[32];
   __shared__ uint32_t tops[32];
@@ -90,7 +92,7 @@ norm_mx8_kernel(const NormArgs a) {
     sum += square_sum(v[t]);
   }
   const auto plus = [](float p, float q) { return p + q; };
-  sum = over_block(sum, sums, plus);
+  sum = over_block(sum, sums, 0.0f, plus);
   float by = 1.0f / sqrtf(sum / static_cast<float>(a.C) + a.eps);
   if (!(sum < 1e38f) || (sum < 1e-28f && a.eps < 1e-18f)) {
     // squares that leave float32: the row in units of a power of two near its
@@ -100,7 +102,7 @@ norm_mx8_kernel(const NormArgs a) {
     for (int t = 0; t < kTurns; ++t)
 #pragma unroll
       for (int i = 0; i < 8; ++i) top = max(top, abs_bits(v[t][i]));
-    top = over_block(top, tops, [](uint32_t p, uint32_t q) { return max(p, q); });
+    top = over_block(top, tops, 0u, [](uint32_t p, uint32_t q) { return max(p, q); });
     if (top < 0x7F800000u && top > 0) {
       const float unit = __uint_as_float(min(max(254 - static_cast<int>(top >> 23), 1), 253) << 23);
       sum = 0.0f;
@@ -110,7 +112,7 @@ norm_mx8_kernel(const NormArgs a) {
         for (int i = 0; i < 8; ++i) v[t][i] *= unit;
         sum += square_sum(v[t]);
       }
-      sum = over_block(sum, again, plus);
+      sum = over_block(sum, again, 0.0f, plus);
       by = static_cast<float>(1.0 / sqrt(static_cast<double>(sum) / a.C + static_cast<double>(a.eps) * unit * unit));
     }
   }
@@ -152,32 +154,40 @@ cudaError_t launch_norm(const NormArgs& a, int64_t rows, cudaStream_t stream) {
   return launch_kernel(norm_mx8_kernel<kTurns>, dim3(static_cast<unsigned>(rows)), dim3(threads), 0, stream, 1, a);
 }
 
-// 16 codes a thread.
-__global__ void __launch_bounds__(256) mx8_read_kernel(const uint8_t* codes, const uint8_t* scales, int64_t rows,
-                                                       int columns, ple_bf16_t* out) {
+// 16 codes a thread and row, of two rows at a time: a CTA takes 4096 columns.
+__global__ void __launch_bounds__(256) mx8_read_kernel(const uint8_t* codes, const uint8_t* scales, int rows, int columns,
+                                                       ple_bf16_t* out) {
   pdl_wait();
   pdl_trigger();
-  const int per_row = columns / 16;
-  const int64_t all = rows * per_row, step = int64_t(gridDim.x) * blockDim.x;
-  for (int64_t i = int64_t(blockIdx.x) * blockDim.x + threadIdx.x; i < all; i += step) {
-    const int64_t row = i / per_row;
-    const int c = static_cast<int>(i % per_row) * 16;
-    const uint4 w = __ldg(reinterpret_cast<const uint4*>(codes + row * columns + c));
-    const float power = mx_power(__ldg(scales + mx_scale_at(row, c / kMxBlock, columns)));
-    const uint32_t words[4] = {w.x, w.y, w.z, w.w};
-    uint32_t v[8];
+  const int c = (blockIdx.y * 256 + threadIdx.x) * 16;
+  if (c >= columns) return;
+  constexpr int kRows = 2;
+  for (int64_t r0 = int64_t(blockIdx.x) * kRows; r0 < rows; r0 += int64_t(gridDim.x) * kRows) {
+    uint4 w[kRows];
+    uint32_t b[kRows];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const float2 f = mx_values2(words[k / 2] >> (k % 2 * 16) & 0xffff);
-      v[k] = pack2(f.x * power, f.y * power);
-    }
-    uint4* to = reinterpret_cast<uint4*>(out + row * columns + c);
-    to[0] = make_uint4(v[0], v[1], v[2], v[3]);
-    to[1] = make_uint4(v[4], v[5], v[6], v[7]);
+    for (int i = 0; i < kRows; ++i)
+      if (r0 + i < rows) {
+        w[i] = __ldg(reinterpret_cast<const uint4*>(codes + (r0 + i) * columns + c));
+        b[i] = __ldg(scales + mx_scale_at(r0 + i, c / kMxBlock, columns));
+      }
+#pragma unroll
+    for (int i = 0; i < kRows; ++i)
+      if (r0 + i < rows) {
+        const float power = mx_power(b[i]);
+        const uint32_t words[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+        uint32_t v[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const float2 f = mx_values2(words[k / 2] >> (k % 2 * 16) & 0xffff);
+          v[k] = pack2(f.x * power, f.y * power);
+        }
+        store32(out + (r0 + i) * columns + c, v);
+      }
   }
 }
 
-constexpr int kMaxNorm = 16384;  // columns: two turns of 1024 threads
+constexpr int kMaxNorm = 16384;  // columns: four turns of 512 threads
 
 }  // namespace
 }  // namespace ple
@@ -226,7 +236,7 @@ PLE_EXPORT ple_status ple_norm_mx8(const ple_bf16_t* x, int64_t x_stride, const 
   if (sum_out != nullptr && num_tokens > 1 && (sum_stride < 0 ? -sum_stride : sum_stride) < hidden)
     return fail(PLE_ERR_INVALID_ARG, "%s: rows of sum_out overlap", name);
   const NormArgs a{x, residual, gamma, x_stride, residual_stride, sum_stride, hidden, eps, sum_out, codes, scales};
-  return check_cuda(hidden <= 4096 ? launch_norm<1>(a, num_tokens, stream) : launch_norm<2>(a, num_tokens, stream), name);
+  return check_cuda(hidden <= 8192 ? launch_norm<2>(a, num_tokens, stream) : launch_norm<4>(a, num_tokens, stream), name);
 }
 
 PLE_EXPORT ple_status ple_mx8_read(const uint8_t* codes, const uint8_t* scales, int64_t rows, int32_t columns,
@@ -234,7 +244,7 @@ PLE_EXPORT ple_status ple_mx8_read(const uint8_t* codes, const uint8_t* scales, 
   const char* name = "ple_mx8_read";
   if (rows < 0 || rows > INT32_MAX || columns < 1)
     return fail(PLE_ERR_INVALID_ARG, "%s: rows %lld, columns %d", name, static_cast<long long>(rows), columns);
-  if (columns % kMxTile != 0)
+  if (columns % kMxTile != 0 || columns > 65535 * 4096)  // the grid's second dimension
     return fail(PLE_ERR_UNSUPPORTED, "%s: columns %d (a multiple of %d)", name, columns, kMxTile);
   if (rows == 0) return PLE_OK;
   if (codes == nullptr || scales == nullptr || out == nullptr)
@@ -244,8 +254,8 @@ PLE_EXPORT ple_status ple_mx8_read(const uint8_t* codes, const uint8_t* scales, 
   const size_t n = static_cast<size_t>(rows) * columns;
   if (overlaps(out, 2 * n, codes, n) || overlaps(out, 2 * n, scales, mx_scale_size(rows, columns)))
     return fail(PLE_ERR_INVALID_ARG, "%s: out overlaps codes or scales", name);
-  const int64_t need = (static_cast<int64_t>(n / 16) + 255) / 256;
-  const int64_t most = int64_t(num_sms()) * 8;
-  return check_cuda(launch_kernel(mx8_read_kernel, dim3(static_cast<unsigned>(need < most ? need : most)), dim3(256), 0,
-                                  stream, 1, codes, scales, rows, columns, out), name);
+  const int across = (columns + 4095) / 4096;
+  const int64_t most = (int64_t(num_sms()) * 32 + across - 1) / across, need = (rows + 1) / 2;
+  return check_cuda(launch_kernel(mx8_read_kernel, dim3(static_cast<unsigned>(need < most ? need : most), across), dim3(256), 0,
+                                  stream, 1, codes, scales, static_cast<int>(rows), columns, out), name);
 }

@@ -70,6 +70,21 @@ constexpr int kAtomCols = 12;                              // 4 of x, 8 of W
 static_assert(kScaleCols + kPairStages * kPairAtoms * kAtomCols <= 512, "tensor memory");
 static_assert(kPairSmem <= 227 << 10, "shared memory");
 
+// A place in a ring of buffers, the parity of its round, and which copies
+// were last asked for.
+template <int kPlaces>
+struct Ring {
+  int at = 0;
+  uint32_t phase = 0, armed = 0, armed_parity = 0;
+  __device__ __forceinline__ void next() {
+    if (++at == kPlaces) { at = 0; phase ^= 1u; }
+  }
+  __device__ __forceinline__ void arm() {
+    armed |= 1u << at;
+    armed_parity = (armed_parity & ~(1u << at)) | phase << at;
+  }
+};
+
 struct PairTile {
   int m, n;  // first token; first row of the result
 };
@@ -137,7 +152,7 @@ product_pair_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_cons
       const PairTile t = pair_tile(u, m_tiles, n_tiles, kRows);
       const int m = t.m + static_cast<int>(rank) * 128;
       const int n = kGated ? static_cast<int>(rank) * a.N + t.n : t.n + static_cast<int>(rank) * 128;  // this CTA's W rows
-      const int n2[2] = {t.n, kGated ? a.N + t.n : t.n + 128};  // all of them, for their scales
+      const int piece[3] = {m / 128 * atoms, t.n / 128 * atoms, (kGated ? a.N + t.n : t.n + 128) / 128 * atoms};  // scales: of all W rows
       for (int k = 0; k < stages; ++k) {
         if (!mbar_wait(free(s), phase ^ 1u, abort_flag)) { ok = false; break; }
         const uint32_t bar = at_rank(full(s), 0);
@@ -147,15 +162,12 @@ product_pair_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_cons
           armed_parity = (armed_parity & ~(1u << s)) | (phase << s);
         }
         // past the last column (an odd number of atoms) zeros come
-        for (int i = 0; i < kPairAtoms; ++i) {
-          const int x = (k * kPairAtoms + i) * 128;
-          tma_load_pair(base + (s * kPairAtoms + i) * 2 * kAtom, &map_x, bar, x, m);
-          tma_load_pair(base + (s * kPairAtoms + i) * 2 * kAtom + kAtom, &map_w, bar, x, n);
-        }
+        tma_load_pair(base + s * 2 * kPairAtoms * kAtom, &map_x, bar, k * kPairAtoms, m);
+        tma_load_pair(base + (s * 2 + 1) * kPairAtoms * kAtom, &map_w, bar, k * kPairAtoms, n);
         const uint32_t to = base + kAtScales + s * kPairScales;
-        tma_load_pair(to, &map_xs, bar, 0, m / 128 * atoms + k * kPairAtoms);
+        tma_load_2d_pair(to, &map_xs, bar, 0, piece[0] + k * kPairAtoms);
         for (int h = 0; h < 2; ++h)
-          tma_load_pair(to + (1 + h) * kPairAtoms * kMxPiece, &map_ws, bar, 0, n2[h] / 128 * atoms + k * kPairAtoms);
+          tma_load_2d_pair(to + (1 + h) * kPairAtoms * kMxPiece, &map_ws, bar, 0, piece[1 + h] + k * kPairAtoms);
         if (++s == kPairStages) { s = 0; phase ^= 1u; }
       }
     }
@@ -185,8 +197,8 @@ product_pair_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_cons
           for (int i = 0; i < kPairAtoms; ++i) {
             if (k * kPairAtoms + i >= atoms) break;  // its scales are another row's
             const uint32_t scales = tmem + kScaleCols + (s * kPairAtoms + i) * kAtomCols;
-            const uint64_t x = codes_operand(base + (s * kPairAtoms + i) * 2 * kAtom);
-            const uint64_t w = codes_operand(base + (s * kPairAtoms + i) * 2 * kAtom + kAtom);
+            const uint64_t x = codes_operand(base + (s * 2 * kPairAtoms + i) * kAtom);
+            const uint64_t w = codes_operand(base + ((s * 2 + 1) * kPairAtoms + i) * kAtom);
 #pragma unroll
             for (int b = 0; b < 4; ++b)
               mma_mx8<2>(tmem, x + 2 * b, w + 2 * b, mx_idesc(256, 256) | mx_block(b), scales, scales + 4, (k | i | b) != 0);
@@ -241,11 +253,7 @@ product_pair_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_cons
 #pragma unroll
           for (int i = 0; i < 8; ++i)
             codes[i] = mx_codes4(v[c][4 * i] * by, v[c][4 * i + 1] * by, v[c][4 * i + 2] * by, v[c][4 * i + 3] * by);
-          if (m < a.T) {
-            uint4* to = reinterpret_cast<uint4*>(a.codes + m * a.N + t.n + half * 64 + c * 32);
-            to[0] = make_uint4(codes[0], codes[1], codes[2], codes[3]);
-            to[1] = make_uint4(codes[4], codes[5], codes[6], codes[7]);
-          }
+          if (m < a.T) store32(a.codes + m * a.N + t.n + half * 64 + c * 32, codes);
         }
         if (m < a.T) *reinterpret_cast<uint16_t*>(a.scales + mx_scale_at(m, (t.n + half * 64) / 32, a.N)) = static_cast<uint16_t>(word);
       } else {
@@ -256,18 +264,25 @@ product_pair_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_cons
 #pragma unroll
             for (int c = 0; c < 4; ++c)
 #pragma unroll
-              for (int q = 0; q < 4; ++q) {
-                const int n = n0 + c * 32 + q * 8;
+              for (int q = 0; q < 2; ++q) {
+                const int n = n0 + c * 32 + q * 16;
                 if (n >= a.N) continue;
-                float* y = v[c] + 8 * q;
+                float* y = v[c] + 16 * q;
                 if (a.residual != nullptr) {
+                  const uint4* from = reinterpret_cast<const uint4*>(a.residual + m * a.residual_stride + n);
+                  const uint4 w[2] = {from[0], from[1]};
                   float r[8];
-                  unpack8(*reinterpret_cast<const uint4*>(a.residual + m * a.residual_stride + n), r);
 #pragma unroll
-                  for (int i = 0; i < 8; ++i) y[i] += r[i];
+                  for (int h = 0; h < 2; ++h) {
+                    unpack8(w[h], r);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) y[8 * h + i] += r[i];
+                  }
                 }
-                *reinterpret_cast<uint4*>(a.out + m * a.N + n) =
-                    make_uint4(pack2(y[0], y[1]), pack2(y[2], y[3]), pack2(y[4], y[5]), pack2(y[6], y[7]));
+                uint32_t packed[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) packed[i] = pack2(y[2 * i], y[2 * i + 1]);
+                store32(a.out + m * a.N + n, packed);
               }
           }
         } else {
@@ -333,8 +348,8 @@ template <bool kGated>
 ple_status launch_pair(const ProductArgs& a, int32_t* dev_err, cudaStream_t stream, const char* name) {
   const int64_t w_rows = kGated ? 2 * int64_t(a.N) : a.N;
   CUtensorMap x, w, xs, ws;
-  ple_status s = mx_codes_map(&x, a.x, a.T, a.E, 128, name);
-  if (s == PLE_OK) s = mx_codes_map(&w, a.w, w_rows, a.E, 128, name);
+  ple_status s = mx_codes_map(&x, a.x, a.T, a.E, 128, kPairAtoms, name);
+  if (s == PLE_OK) s = mx_codes_map(&w, a.w, w_rows, a.E, 128, kPairAtoms, name);
   if (s == PLE_OK) s = mx_scales_map(&xs, a.x_scales, a.T, a.E, kPairAtoms, name);
   if (s == PLE_OK) s = mx_scales_map(&ws, a.w_scales, w_rows, a.E, kPairAtoms, name);
   if (s != PLE_OK) return s;
@@ -358,25 +373,29 @@ ple_status launch_pair(const ProductArgs& a, int32_t* dev_err, cudaStream_t stre
 // the columns, and their sums meet through distributed shared memory, in the
 // order of the CTAs, each joining (and finishing) a share of the tokens.
 //
-// Warps: 0 copies, 1 issues, 2-5 take the sums out; all join.
-constexpr int kFewThreads = 192;
-constexpr int kMaxParts = 8;
+// Warps: 0 copies, 1 issues, 2-5 take the sums out; all eight join.
+constexpr int kFewThreads = 256;
 
 template <bool kGated, int kTokens>
 struct Few {
   static constexpr int kSides = kGated ? 2 : 1;  // of W
   static constexpr int kXPieces = kTokens > 128 ? 2 : 1;
-  static constexpr int kCodes = kSides * kAtom + kTokens * 128;  // bytes of a stage
-  static constexpr int kScales = (kSides + kXPieces) * kMxPiece;
-  static constexpr int kResident = kTokens <= 32 ? 2 : 1;        // CTAs an SM
+  static constexpr int kResident = kTokens <= 64 ? 2 : 1;        // CTAs an SM
+  static constexpr int kMaxParts = kResident == 2 ? 8 : 4;       // CTAs that share the columns
+  static constexpr int kStep = 1;                                // atoms of a stage
+  static constexpr int kCodes = kStep * (kSides * kAtom + kTokens * 128);  // bytes of a stage
+  static constexpr int kScales = kStep * (kSides + kXPieces) * kMxPiece;
   static constexpr int kBudget = kResident == 2 ? 110 << 10 : 220 << 10;
   static constexpr int kFit = kBudget / (kCodes + kScales);
   static constexpr int kStages = kFit > 8 ? 8 : kFit;
   static constexpr int kAtScales = kStages * kCodes;
   static constexpr int kAtBars = kAtScales + kStages * kScales;
   static constexpr int kSmem = kAtBars + (2 * kStages + 2) * 8 + 16 + 1024;  // and alignment
+  static constexpr int kAsk = kTokens < 32 ? 16 : 32;            // tokens a thread takes out at once
+  static constexpr int kBatch = 16 / (kMaxParts * kSides);       // tokens a warp joins at once
   static constexpr int kCols = kSides * kTokens;                 // of sums
-  static constexpr int kStageCols = 4 * (kSides + kXPieces);     // of scales
+  static constexpr int kAtomCols = 4 * (kSides + kXPieces);      // of scales
+  static constexpr int kStageCols = kStep * kAtomCols;
   static constexpr int kNeed = kCols + kStages * kStageCols;
   static constexpr int kTmem = kNeed <= 64 ? 64 : kNeed <= 128 ? 128 : kNeed <= 256 ? 256 : 512;
   static_assert(kNeed <= 512 / kResident && kTmem <= 512 / kResident, "tensor memory");
@@ -421,60 +440,77 @@ product_few_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_const
   __syncthreads();
   fence_after();
   const uint32_t tmem = *tmem_slot;
+  if (warp == 0 && lane == 0) {
+    // W into L2 while the kernel before this one ends: nothing is read of it
+    prefetch_map(&map_w);
+    prefetch_map(&map_x);
+    for (int k = first; k < last && k < first + L::kStages * L::kStep; k += L::kStep)
+      for (int i = 0; i < L::kSides; ++i) prefetch_atoms(&map_w, k, i * a.N + n0);
+  }
   pdl_wait();
   pdl_trigger();
 
   if (warp == 0) {
     if (lane == 0) {
       // ---------------- copies ----------------
-      uint32_t armed = 0, armed_parity = 0;
+      Ring<L::kStages> ring;
       bool ok = true;
       const uint8_t* const xs = a.x_scales + t0 / 128 * atoms * kMxPiece;
       const uint8_t* ws[2];
       for (int i = 0; i < L::kSides; ++i) ws[i] = a.w_scales + (int64_t(i) * a.N + n0) / 128 * atoms * kMxPiece;
       // the second 128 tokens' scales, where there are such tokens
       const bool more = L::kXPieces == 2 && tokens > 128;
-      for (int k = first; k < last; ++k) {
-        const int s = (k - first) % L::kStages;
-        const uint32_t phase = (k - first) / L::kStages & 1;
-        if (!mbar_wait(free(s), phase ^ 1u, abort_flag)) { ok = false; break; }
-        mbar_arrive_expect_tx(full(s), L::kCodes + L::kScales - (L::kXPieces == 2 && !more ? kMxPiece : 0));
-        armed |= 1u << s;
-        armed_parity = (armed_parity & ~(1u << s)) | (phase << s);
+      for (int k = first; k < last; k += L::kStep, ring.next()) {
+        const int s = ring.at;
+        if (!(ok = mbar_wait(free(s), ring.phase ^ 1u, abort_flag))) break;
+        const uint32_t bytes = static_cast<uint32_t>(min(L::kStep, last - k)) * kMxPiece;  // of scales; codes come whole
+        mbar_arrive_expect_tx(full(s), L::kCodes + bytes * (L::kSides + (more ? 2 : 1)));
+        ring.arm();
         const uint32_t to = base + s * L::kCodes, scales = base + L::kAtScales + s * L::kScales;
         for (int i = 0; i < L::kSides; ++i) {
-          tma_load_2d(to + i * kAtom, &map_w, full(s), k * 128, i * a.N + n0);
-          bulk_copy_g2s(scales + i * kMxPiece, ws[i] + int64_t(k) * kMxPiece, kMxPiece, full(s));
+          tma_load_atoms(to + i * L::kStep * kAtom, &map_w, full(s), k, i * a.N + n0);
+          bulk_copy_g2s(scales + i * L::kStep * kMxPiece, ws[i] + int64_t(k) * kMxPiece, bytes, full(s));
         }
-        tma_load_2d(to + L::kSides * kAtom, &map_x, full(s), k * 128, static_cast<int>(t0));
-        bulk_copy_g2s(scales + L::kSides * kMxPiece, xs + int64_t(k) * kMxPiece, kMxPiece, full(s));
+        tma_load_atoms(to + L::kSides * L::kStep * kAtom, &map_x, full(s), k, static_cast<int>(t0));
+        bulk_copy_g2s(scales + L::kSides * L::kStep * kMxPiece, xs + int64_t(k) * kMxPiece, bytes, full(s));
         if (more)
-          bulk_copy_g2s(scales + (L::kSides + 1) * kMxPiece, xs + int64_t(atoms + k) * kMxPiece, kMxPiece, full(s));
+          bulk_copy_g2s(scales + (L::kSides + 1) * L::kStep * kMxPiece, xs + int64_t(atoms + k) * kMxPiece, bytes, full(s));
       }
       if (!ok) { *abort_flag = 1; set_dev_err(dev_err, PLE_DEVERR_TIMEOUT); }
       for (int i = 0; i < L::kStages; ++i)
-        if (armed & (1u << i)) mbar_wait(full(i), (armed_parity >> i) & 1u, nullptr);
+        if (ring.armed >> i & 1u) mbar_wait(full(i), ring.armed_parity >> i & 1u, nullptr);
     }
     __syncwarp();
   } else if (warp == 1) {
     if (lane == 0) {
       // ---------------- products ----------------
+      Ring<L::kStages> ring;
       bool ok = true;
-      for (int k = first; k < last; ++k) {
-        const int s = (k - first) % L::kStages;
-        if (!mbar_wait(full(s), (k - first) / L::kStages & 1, abort_flag)) { ok = false; break; }
+      for (int k = first; k < last; k += L::kStep, ring.next()) {
+        const int s = ring.at;
+        if (!(ok = mbar_wait(full(s), ring.phase, abort_flag))) break;
         fence_after();
-        const uint32_t scales = tmem + L::kCols + s * L::kStageCols, from = base + L::kAtScales + s * L::kScales;
+        const uint32_t from = base + L::kAtScales + s * L::kScales;
 #pragma unroll
-        for (int i = 0; i < L::kSides + L::kXPieces; ++i) scales_to_tmem<1>(scales + 4 * i, from + i * kMxPiece);
-        const uint64_t x = codes_operand(base + s * L::kCodes + L::kSides * kAtom);
+        for (int j = 0; j < L::kStep; ++j) {
+          if (k + j >= last) break;
+          const uint32_t scales = tmem + L::kCols + s * L::kStageCols + j * L::kAtomCols;
 #pragma unroll
-        for (int i = 0; i < L::kSides; ++i) {
-          const uint64_t w = codes_operand(base + s * L::kCodes + i * kAtom);
+          for (int i = 0; i < L::kSides + L::kXPieces; ++i) scales_to_tmem<1>(scales + 4 * i, from + (i * L::kStep + j) * kMxPiece);
+        }
 #pragma unroll
-          for (int b = 0; b < 4; ++b)
-            mma_mx8<1>(tmem + i * kTokens, w + 2 * b, x + 2 * b, mx_idesc(128, kTokens) | mx_block(b), scales + 4 * i,
-                       scales + 4 * L::kSides, k > first || b > 0);
+        for (int j = 0; j < L::kStep; ++j) {
+          if (k + j >= last) break;
+          const uint32_t scales = tmem + L::kCols + s * L::kStageCols + j * L::kAtomCols;
+          const uint64_t x = codes_operand(base + s * L::kCodes + L::kSides * L::kStep * kAtom + j * kTokens * 128);
+#pragma unroll
+          for (int i = 0; i < L::kSides; ++i) {
+            const uint64_t w = codes_operand(base + s * L::kCodes + (i * L::kStep + j) * kAtom);
+#pragma unroll
+            for (int b = 0; b < 4; ++b)
+              mma_mx8<1>(tmem + i * kTokens, w + 2 * b, x + 2 * b, mx_idesc(128, kTokens) | mx_block(b), scales + 4 * i,
+                         scales + 4 * L::kSides, k + j > first || b > 0);
+          }
         }
         mma_commit(free(s));
       }
@@ -484,7 +520,7 @@ product_few_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_const
       mbar_wait(sums_full, 0, nullptr);
     }
     __syncwarp();
-  } else {
+  } else if (warp < 6) {
     // ---------------- sums, where the codes were: [token][side][row] ----------------
     const bool ok = __all_sync(0xffffffffu, mbar_wait(sums_full, 0, nullptr)) && *abort_flag == 0;
     fence_after();
@@ -495,11 +531,12 @@ product_few_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_const
 #pragma unroll
       for (int i = 0; i < L::kSides; ++i)
 #pragma unroll 1
-        for (int c = 0; c < kTokens && c < tokens; c += 16) {
-          float v[16];
-          tmem_load16(lanes + i * kTokens + c, v);
+        for (int c = 0; c < tokens; c += L::kAsk) {
+          float v[L::kAsk];
+          if constexpr (L::kAsk == 16) tmem_load16(lanes + i * kTokens + c, v);
+          else tmem_load(lanes + i * kTokens + c, v);
 #pragma unroll
-          for (int j = 0; j < 16; ++j)
+          for (int j = 0; j < L::kAsk; ++j)
             if (c + j < tokens) mine[((c + j) * L::kSides + i) * 128 + row] = v[j];
         }
     }
@@ -512,49 +549,66 @@ product_few_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_const
   }
   if (parts > 1) cluster_barrier();
   // ---------------- the parts' sums, in their order: a warp takes a token, a lane 4 rows ----------------
-  for (int t = part + warp * parts; t < tokens; t += parts * (kFewThreads / 32)) {
-    float v[L::kSides][4] = {};
-    for (int p = 0; p < parts; ++p)
+  // (a few tokens at once: what is far away is asked for together)
+  const int n = n0 + lane * 4;
+  constexpr int kStride = kFewThreads / 32;
+  for (int i0 = warp; part + i0 * parts < tokens; i0 += kStride * L::kBatch) {
+    float4 f[L::kBatch][L::kMaxParts][L::kSides];
+    uint2 more[L::kBatch];
+    auto token = [&](int q) { return part + (i0 + q * kStride) * parts; };
 #pragma unroll
-      for (int i = 0; i < L::kSides; ++i) {
-        const float4 f = read_cluster4(base + ((t * L::kSides + i) * 128 + lane * 4) * 4, p);
-        v[i][0] += f.x; v[i][1] += f.y; v[i][2] += f.z; v[i][3] += f.w;
-      }
-    const int64_t m = t0 + t;
-    if constexpr (kGated) {
-      uint32_t top = 0;
+    for (int q = 0; q < L::kBatch; ++q) {
+      const int t = token(q);
+      if (t >= tokens) break;
+      if (!kGated && a.wide && a.residual != nullptr && n < a.N)
+        more[q] = *reinterpret_cast<const uint2*>(a.residual + (t0 + t) * a.residual_stride + n);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        v[0][i] = activation(v[0][i], a.gelu) * v[1][i];
-        top = max(top, abs_bits(v[0][i]));
-      }
+      for (int p = 0; p < L::kMaxParts; ++p)
+        if (p < parts)
 #pragma unroll
-      for (int o = 4; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-      const uint32_t b = mx_scale_byte(top);
-      const float by = mx_inverse(b);
-      *reinterpret_cast<uint32_t*>(a.codes + m * a.N + n0 + lane * 4) = mx_codes4(v[0][0] * by, v[0][1] * by, v[0][2] * by, v[0][3] * by);
-      uint32_t word = b << (lane / 8 * 8);
-      word |= __shfl_xor_sync(0xffffffffu, word, 8);
-      word |= __shfl_xor_sync(0xffffffffu, word, 16);
-      if (lane == 0) *reinterpret_cast<uint32_t*>(a.scales + mx_scale_at(m, n0 / 32, a.N)) = word;
-    } else {
-      const int n = n0 + lane * 4;
-      ple_bf16_t* const to = a.out + m * a.N + n;
-      const ple_bf16_t* const r = a.residual == nullptr ? nullptr : a.residual + m * a.residual_stride + n;
-      if (a.wide) {
-        if (n < a.N) {
-          if (r != nullptr) {
-            const uint2 w = *reinterpret_cast<const uint2*>(r);
-            v[0][0] += bf_lo(w.x); v[0][1] += bf_hi(w.x); v[0][2] += bf_lo(w.y); v[0][3] += bf_hi(w.y);
+          for (int i = 0; i < L::kSides; ++i) f[q][p][i] = read_cluster4(base + ((t * L::kSides + i) * 128 + lane * 4) * 4, p);
+    }
+#pragma unroll
+    for (int q = 0; q < L::kBatch; ++q) {
+      const int64_t m = t0 + token(q);
+      if (token(q) >= tokens) break;
+      float v[L::kSides][4] = {};
+#pragma unroll
+      for (int p = 0; p < L::kMaxParts; ++p)
+        if (p < parts)
+#pragma unroll
+          for (int i = 0; i < L::kSides; ++i) {
+            v[i][0] += f[q][p][i].x; v[i][1] += f[q][p][i].y; v[i][2] += f[q][p][i].z; v[i][3] += f[q][p][i].w;
           }
-          *reinterpret_cast<uint2*>(to) = make_uint2(pack2(v[0][0], v[0][1]), pack2(v[0][2], v[0][3]));
+      if constexpr (kGated) {
+        uint32_t top = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          v[0][i] = activation(v[0][i], a.gelu) * v[1][i];
+          top = max(top, abs_bits(v[0][i]));
+        }
+#pragma unroll
+        for (int o = 4; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+        const uint32_t b = mx_scale_byte(top);
+        const float by = mx_inverse(b);
+        *reinterpret_cast<uint32_t*>(a.codes + m * a.N + n) = mx_codes4(v[0][0] * by, v[0][1] * by, v[0][2] * by, v[0][3] * by);
+        uint32_t word = b << (lane / 8 * 8);
+        word |= __shfl_xor_sync(0xffffffffu, word, 8);
+        word |= __shfl_xor_sync(0xffffffffu, word, 16);
+        if (lane == 0) *reinterpret_cast<uint32_t*>(a.scales + mx_scale_at(m, n0 / 32, a.N)) = word;
+      } else if (a.wide) {
+        if (n < a.N) {
+          if (a.residual != nullptr) {
+            v[0][0] += bf_lo(more[q].x); v[0][1] += bf_hi(more[q].x); v[0][2] += bf_lo(more[q].y); v[0][3] += bf_hi(more[q].y);
+          }
+          *reinterpret_cast<uint2*>(a.out + m * a.N + n) = make_uint2(pack2(v[0][0], v[0][1]), pack2(v[0][2], v[0][3]));
         }
       } else {
 #pragma unroll
         for (int i = 0; i < 4; ++i)
           if (n + i < a.N) {
-            if (r != nullptr) v[0][i] += bf_lo(r[i]);
-            to[i] = static_cast<ple_bf16_t>(pack2(v[0][i], 0.0f) & 0xffffu);
+            if (a.residual != nullptr) v[0][i] += bf_lo(a.residual[m * a.residual_stride + n + i]);
+            a.out[m * a.N + n + i] = static_cast<ple_bf16_t>(pack2(v[0][i], 0.0f) & 0xffffu);
           }
       }
     }
@@ -566,8 +620,8 @@ template <bool kGated, int kTokens>
 ple_status launch_few(const ProductArgs& a, int32_t* dev_err, cudaStream_t stream, const char* name) {
   using L = Few<kGated, kTokens>;
   CUtensorMap x, w;
-  ple_status s = mx_codes_map(&x, a.x, a.T, a.E, kTokens, name);
-  if (s == PLE_OK) s = mx_codes_map(&w, a.w, kGated ? 2 * int64_t(a.N) : a.N, a.E, 128, name);
+  ple_status s = mx_codes_map(&x, a.x, a.T, a.E, kTokens, L::kStep, name);
+  if (s == PLE_OK) s = mx_codes_map(&w, a.w, kGated ? 2 * int64_t(a.N) : a.N, a.E, 128, L::kStep, name);
   if (s != PLE_OK) return s;
   const auto kernel = product_few_kernel<kGated, kTokens>;
   const cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kSmem);
@@ -575,7 +629,7 @@ ple_status launch_few(const ProductArgs& a, int32_t* dev_err, cudaStream_t strea
   const int tiles = (a.N + 127) / 128, blocks = static_cast<int>((a.T + kTokens - 1) / kTokens), atoms = a.E / 128;
   // parts of the columns, as long as all CTAs are on SMs at once and have some stages each
   int parts = 1;
-  while (parts < kMaxParts && int64_t(tiles) * blocks * parts * 2 <= int64_t(num_sms()) * L::kResident && atoms >= parts * 2 * 4)
+  while (parts < L::kMaxParts && int64_t(tiles) * blocks * parts * 2 <= int64_t(num_sms()) * L::kResident && atoms >= parts * 2 * 4)
     parts *= 2;
   const dim3 grid(static_cast<unsigned>(tiles * parts), static_cast<unsigned>(blocks));
   return check_cuda(launch_kernel(kernel, grid, dim3(kFewThreads), L::kSmem, stream, static_cast<unsigned>(parts), x, w, a,
@@ -617,27 +671,29 @@ bool meets_operands(const void* to, size_t n, const ProductArgs& a, int64_t w_ro
 
 }  // namespace
 
-ple_status encode_map(CUtensorMap* map, CUtensorMapDataType type, const void* at, int64_t columns, int64_t rows,
-                      int64_t row_bytes, int box_columns, int box_rows, CUtensorMapSwizzle swizzle, const char* name) {
+ple_status encode_map(CUtensorMap* map, CUtensorMapDataType type, const void* at, int dims, const cuuint64_t* size,
+                      const cuuint64_t* strides, const cuuint32_t* box, CUtensorMapSwizzle swizzle, const char* name) {
   const auto encode = tensor_map_encoder();
   if (encode == nullptr) return fail(PLE_ERR_CUDA, "%s: cuTensorMapEncodeTiled unavailable", name);
-  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(columns), static_cast<cuuint64_t>(rows)};
-  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(row_bytes)};
-  const cuuint32_t box[2] = {static_cast<cuuint32_t>(box_columns), static_cast<cuuint32_t>(box_rows)};
-  const cuuint32_t steps[2] = {1, 1};
-  const CUresult r = encode(map, type, 2, const_cast<void*>(at), dims, strides, box, steps, CU_TENSOR_MAP_INTERLEAVE_NONE,
+  const cuuint32_t steps[3] = {1, 1, 1};
+  const CUresult r = encode(map, type, dims, const_cast<void*>(at), size, strides, box, steps, CU_TENSOR_MAP_INTERLEAVE_NONE,
                             swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? PLE_OK : fail(PLE_ERR_CUDA, "%s: cuTensorMapEncodeTiled failed (%d)", name, static_cast<int>(r));
 }
 
-ple_status mx_codes_map(CUtensorMap* map, const void* codes, int64_t rows, int columns, int box_rows, const char* name) {
-  return encode_map(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, codes, columns, rows, columns, 128, box_rows,
-                    CU_TENSOR_MAP_SWIZZLE_128B, name);
+ple_status mx_codes_map(CUtensorMap* map, const void* codes, int64_t rows, int columns, int box_rows, int box_atoms,
+                        const char* name) {
+  const cuuint64_t size[3] = {128, static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(columns) / 128};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(columns), 128};
+  const cuuint32_t box[3] = {128, static_cast<cuuint32_t>(box_rows), static_cast<cuuint32_t>(box_atoms)};
+  return encode_map(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, codes, 3, size, strides, box, CU_TENSOR_MAP_SWIZZLE_128B, name);
 }
 
 ple_status mx_scales_map(CUtensorMap* map, const void* scales, int64_t rows, int columns, int box_pieces, const char* name) {
-  return encode_map(map, CU_TENSOR_MAP_DATA_TYPE_UINT32, scales, kMxPiece / 4, mx_scale_size(rows, columns) / kMxPiece,
-                    kMxPiece, kMxPiece / 4, box_pieces, CU_TENSOR_MAP_SWIZZLE_NONE, name);
+  const cuuint64_t size[2] = {kMxPiece / 4, static_cast<cuuint64_t>(mx_scale_size(rows, columns) / kMxPiece)};
+  const cuuint64_t strides[1] = {kMxPiece};
+  const cuuint32_t box[2] = {kMxPiece / 4, static_cast<cuuint32_t>(box_pieces)};
+  return encode_map(map, CU_TENSOR_MAP_DATA_TYPE_UINT32, scales, 2, size, strides, box, CU_TENSOR_MAP_SWIZZLE_NONE, name);
 }
 
 }  // namespace ple
@@ -674,7 +730,7 @@ PLE_EXPORT ple_status ple_proj_mx8(const uint8_t* x, const uint8_t* x_scales, in
   const ple_status s = check_product(name, x, x_scales, num_tokens, in_dim, w, w_scales, out_dim);
   if (s != PLE_OK || num_tokens == 0) return s;
   if (out == nullptr) return fail(PLE_ERR_INVALID_ARG, "%s: null out", name);
-  const bool wide = out_dim % 8 == 0 && aligned16(out) && (residual == nullptr || (aligned16(residual) && residual_stride % 8 == 0));
+  const bool wide = out_dim % 16 == 0 && aligned16(out) && (residual == nullptr || (aligned16(residual) && residual_stride % 8 == 0));
   const ProductArgs a{x, x_scales, w, w_scales, num_tokens, in_dim, out_dim, 0, wide, residual, residual_stride, out,
                       nullptr, nullptr};
   const size_t n = static_cast<size_t>(num_tokens) * out_dim * 2;

@@ -295,12 +295,20 @@ product_pair_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_cons
             for (int i = 0; i < 16; ++i) mine[lane * kRoomPitch + i] = v[c / 2][c % 2 * 16 + i];
             __syncwarp();
             const int n = n0 + c * 16 + lane % 16;
-            for (int r = lane / 16; r < 32; r += 2) {
-              const int64_t m = m0 + r;
-              if (m >= a.T || n >= a.N) break;
-              float y = mine[r * kRoomPitch + lane % 16];
-              if (a.residual != nullptr) y += bf_lo(a.residual[m * a.residual_stride + n]);
-              a.out[m * a.N + n] = static_cast<ple_bf16_t>(pack2(y, 0.0f) & 0xffffu);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {  // 8 rows of each half warp at once
+              float y[8];
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                const int r = h * 16 + 2 * i + lane / 16;
+                y[i] = mine[r * kRoomPitch + lane % 16];
+                if (a.residual != nullptr && m0 + r < a.T && n < a.N) y[i] += bf_lo(a.residual[(m0 + r) * a.residual_stride + n]);
+              }
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                const int r = h * 16 + 2 * i + lane / 16;
+                if (m0 + r < a.T && n < a.N) a.out[(m0 + r) * a.N + n] = static_cast<ple_bf16_t>(pack2(y[i], 0.0f) & 0xffffu);
+              }
             }
           }
         }
@@ -455,7 +463,7 @@ product_few_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_const
       // ---------------- copies ----------------
       Ring<L::kStages> ring;
       bool ok = true;
-      const uint8_t* const xs = a.x_scales + t0 / 128 * atoms * kMxPiece;
+      const uint8_t* const xs = a.x_scales + t0 / 128 * atoms * kMxPiece;  // (t0 is 0, or blocks are of 128 or 256)
       const uint8_t* ws[2];
       for (int i = 0; i < L::kSides; ++i) ws[i] = a.w_scales + (int64_t(i) * a.N + n0) / 128 * atoms * kMxPiece;
       // the second 128 tokens' scales, where there are such tokens
@@ -616,6 +624,15 @@ product_few_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_const
   if (parts > 1) cluster_barrier();  // no CTA leaves while its sums are read
 }
 
+// Parts that a cluster cuts the columns into: as many as keep all CTAs on SMs
+// at once and leave each some atoms.
+template <typename L>
+int parts_of(int64_t ctas, int atoms) {
+  int parts = 1;
+  while (parts < L::kMaxParts && ctas * parts * 2 <= int64_t(num_sms()) * L::kResident && atoms >= parts * 2 * 4) parts *= 2;
+  return parts;
+}
+
 template <bool kGated, int kTokens>
 ple_status launch_few(const ProductArgs& a, int32_t* dev_err, cudaStream_t stream, const char* name) {
   using L = Few<kGated, kTokens>;
@@ -626,24 +643,34 @@ ple_status launch_few(const ProductArgs& a, int32_t* dev_err, cudaStream_t strea
   const auto kernel = product_few_kernel<kGated, kTokens>;
   const cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kSmem);
   if (err != cudaSuccess) return check_cuda(err, name);
-  const int tiles = (a.N + 127) / 128, blocks = static_cast<int>((a.T + kTokens - 1) / kTokens), atoms = a.E / 128;
-  // parts of the columns, as long as all CTAs are on SMs at once and have some stages each
-  int parts = 1;
-  while (parts < L::kMaxParts && int64_t(tiles) * blocks * parts * 2 <= int64_t(num_sms()) * L::kResident && atoms >= parts * 2 * 4)
-    parts *= 2;
+  const int tiles = (a.N + 127) / 128, blocks = static_cast<int>((a.T + kTokens - 1) / kTokens);
+  const int parts = parts_of<L>(int64_t(tiles) * blocks, a.E / 128);
   const dim3 grid(static_cast<unsigned>(tiles * parts), static_cast<unsigned>(blocks));
   return check_cuda(launch_kernel(kernel, grid, dim3(kFewThreads), L::kSmem, stream, static_cast<unsigned>(parts), x, w, a,
                                   parts, dev_err), name);
 }
 
+// Up to 256 tokens (gated: 128) W is read by one CTA each: the second kernel.
+// More tokens, in blocks of 256, stay with it while pairs of CTAs would leave
+// most of the GPU idle. What a launch takes, in 10 ns, from measurements of
+// both: a pair's stage of 256 columns 73, a tile's change 160, all else 750; a
+// CTA's atom of 128 columns 48, taking out and joining 600, all else 350.
+// Measured, pairs / CTAs, us, tokens over columns x rows:
+//   300   8192 x 2048   32.1 / 17.8     512   4096 x 4096   21.3 / 18.4
+//  1023   2048 x 8192   21.9 / 31.7
 template <bool kGated>
 ple_status launch_product(const ProductArgs& a, int32_t* dev_err, cudaStream_t stream, const char* name) {
   if (a.T <= 16) return launch_few<kGated, 16>(a, dev_err, stream, name);
   if (a.T <= 32) return launch_few<kGated, 32>(a, dev_err, stream, name);
   if (a.T <= 64) return launch_few<kGated, 64>(a, dev_err, stream, name);
   if (a.T <= 128) return launch_few<kGated, 128>(a, dev_err, stream, name);
-  if constexpr (!kGated)
-    if (a.T <= 256) return launch_few<false, 256>(a, dev_err, stream, name);
+  if constexpr (!kGated) {
+    const int64_t ctas = (a.N + 127) / 128 * ((a.T + 255) / 256), units = (a.T + 255) / 256 * ((a.N + 255) / 256);
+    const int atoms = a.E / 128, parts = parts_of<Few<false, 256>>(ctas, atoms), pairs = resident_pairs<false>();
+    const int64_t by_pairs = (units + pairs - 1) / pairs * ((atoms + 1) / 2 * 73 + 160) + 750;
+    const int64_t by_ctas = (ctas * parts + num_sms() - 1) / num_sms() * ((atoms + parts - 1) / parts * 48 + 600) + 350;
+    if (a.T <= 256 || by_ctas < by_pairs) return launch_few<false, 256>(a, dev_err, stream, name);
+  }
   return launch_pair<kGated>(a, dev_err, stream, name);
 }
 

@@ -591,39 +591,48 @@ def ple_mx8_scale_bytes(rows, columns):
     return int(lib().ple_mx8_scale_bytes(int(rows), int(columns)))
 
 
+def _mx8_error(name, codes, scales):
+    """Why codes and scales are no 8-bit tensor."""
+    if (codes.dtype is not _U8 or scales.dtype is not _U8 or not (codes.is_contiguous() and scales.is_contiguous())
+            or not (codes.is_cuda and scales.is_cuda)):
+        return ValueError(f"{name}: contiguous CUDA uint8 tensors are needed, codes [R, C] and scales of one dimension")
+    return ValueError(f"{name}: codes {tuple(codes.shape)} (columns: a multiple of 128) and {scales.numel()} bytes of "
+                      "scales do not fit (ple_mx8_scale_bytes)")
+
+
 def _mx8(name, codes, scales):
     """Shape of an 8-bit tensor: codes uint8 [R, C], scales uint8, their bytes
     in one dimension, as many as ple_mx8_scale_bytes says or more."""
     if (codes.dtype is not _U8 or scales.dtype is not _U8 or not (codes.is_contiguous() and scales.is_contiguous())
             or not (codes.is_cuda and scales.is_cuda)):
-        raise ValueError(f"{name}: contiguous CUDA uint8 tensors are needed")
+        raise _mx8_error(name, codes, scales)
     (R, C), (n,) = codes.shape, scales.shape  # a ValueError, too, where there are more dimensions or fewer
     if C % 128 != 0 or n < (R + 127) // 128 * (C * 4):
-        raise ValueError(f"{name}: codes {R} x {C} (columns: a multiple of 128) need "
-                         f"{(R + 127) // 128 * (C * 4)} bytes of scales, not {n}")
+        raise _mx8_error(name, codes, scales)
     return R, C
 
 
-def _rows_of(name, t, rows, columns):
-    """Address and row stride of bf16 rows any distance apart."""
-    if t.dtype is not _BF16 or not t.is_cuda or t.shape != (rows, columns):
-        raise ValueError(f"{name}: a CUDA bf16 tensor [{rows}, {columns}] is needed")
+def _row_stride(name, t, shape):
+    """Distance of bf16 rows that need not lie together."""
+    if t.dtype is not _BF16 or not t.is_cuda or t.shape != shape:
+        raise ValueError(f"{name}: a CUDA bf16 tensor {tuple(shape)} is needed")
+    if t.is_contiguous():
+        return shape[1]
     stride, one = t.stride()
-    if one != 1 and columns > 1 and rows > 0:
+    if one != 1 and shape[1] > 1:
         raise ValueError(f"{name}: the columns of a row must lie together")
-    return t.data_ptr(), stride if rows > 1 else columns
+    return stride if shape[0] > 1 else shape[1]
 
 
 def ple_mx8_read(codes, scales, out, stream=None):
     """out [R, C] bf16: the values of an 8-bit tensor, codes uint8 [R, C] and
     scales uint8 [ple_mx8_scale_bytes(R, C)]."""
     R, C = _mx8("codes, scales", codes, scales)
-    at = _whole("out", out, _BF16, 2)
-    if out.shape != codes.shape:
-        raise ValueError("out must have the shape of codes")
+    if out.dtype is not _BF16 or not out.is_contiguous() or not out.is_cuda or out.shape != codes.shape:
+        raise ValueError("out: a contiguous CUDA bf16 tensor of the shape of codes is needed")
     if not _one_gpu:
         _same_gpu(codes, scales, out)
-    status = lib().ple_mx8_read(codes.data_ptr(), scales.data_ptr(), R, C, at, _raw_stream(stream, codes))
+    status = lib().ple_mx8_read(codes.data_ptr(), scales.data_ptr(), R, C, out.data_ptr(), _raw_stream(stream, codes))
     return status if status == PLE_OK else _check("ple_mx8_read", status)
 
 
@@ -633,19 +642,20 @@ def ple_norm_mx8(x, gamma, codes, scales, residual=None, sum_out=None, eps=1e-6,
     residual and sum_out bf16 [T, C], columns of a wider tensor will do;
     sum_out may be x or residual itself. gamma bf16 [C], or None for 1."""
     T, C = _mx8("codes, scales", codes, scales)
-    x_at, x_stride = _rows_of("x", x, T, C)
+    shape = codes.shape
+    x_stride = _row_stride("x", x, shape)
     r_at, r_stride, s_at, s_stride, g_at = None, C, None, C, None
     if residual is not None:
-        r_at, r_stride = _rows_of("residual", residual, T, C)
+        r_at, r_stride = residual.data_ptr(), _row_stride("residual", residual, shape)
     if sum_out is not None:
-        s_at, s_stride = _rows_of("sum_out", sum_out, T, C)
+        s_at, s_stride = sum_out.data_ptr(), _row_stride("sum_out", sum_out, shape)
     if gamma is not None:
-        g_at = _whole("gamma", gamma, _BF16, 1)
-        if gamma.shape[0] != C:
-            raise ValueError(f"gamma must have {C} entries")
+        if gamma.dtype is not _BF16 or not gamma.is_contiguous() or not gamma.is_cuda or gamma.shape != shape[1:]:
+            raise ValueError(f"gamma: a contiguous CUDA bf16 tensor of {C} entries is needed")
+        g_at = gamma.data_ptr()
     if not _one_gpu:
         _same_gpu(x, gamma, codes, scales, residual, sum_out)
-    status = lib().ple_norm_mx8(x_at, x_stride, r_at, r_stride, g_at, eps, T, C, s_at, s_stride, codes.data_ptr(),
+    status = lib().ple_norm_mx8(x.data_ptr(), x_stride, r_at, r_stride, g_at, eps, T, C, s_at, s_stride, codes.data_ptr(),
                                 scales.data_ptr(), _raw_stream(stream, x))
     return status if status == PLE_OK else _check("ple_norm_mx8", status)
 
@@ -676,16 +686,18 @@ def ple_proj_mx8(x, x_scales, w, w_scales, out, residual=None, dev_err=None, str
     may be out itself."""
     T, E = _mx8("x", x, x_scales)
     N, Ew = _mx8("w", w, w_scales)
-    at = _whole("out", out, _BF16, 2)
-    if Ew != E or out.shape != (T, N):
-        raise ValueError(f"x {tuple(x.shape)}, w {tuple(w.shape)} and out {tuple(out.shape)} do not fit")
+    if out.dtype is not _BF16 or not out.is_contiguous() or not out.is_cuda:
+        raise ValueError("out: a contiguous CUDA bf16 tensor is needed")
+    shape = out.shape
+    if Ew != E or shape != (T, N):
+        raise ValueError(f"x {tuple(x.shape)}, w {tuple(w.shape)} and out {tuple(shape)} do not fit")
     r_at, r_stride = None, N
     if residual is not None:
-        r_at, r_stride = _rows_of("residual", residual, T, N)
+        r_at, r_stride = residual.data_ptr(), _row_stride("residual", residual, shape)
     if not _one_gpu:
         _same_gpu(x, x_scales, w, w_scales, out, residual, dev_err)
     status = lib().ple_proj_mx8(
-        x.data_ptr(), x_scales.data_ptr(), T, E, w.data_ptr(), w_scales.data_ptr(), N, r_at, r_stride, at,
+        x.data_ptr(), x_scales.data_ptr(), T, E, w.data_ptr(), w_scales.data_ptr(), N, r_at, r_stride, out.data_ptr(),
         None if dev_err is None else _err_word(dev_err), _raw_stream(stream, x))
     return status if status == PLE_OK else _check("ple_proj_mx8", status)
 

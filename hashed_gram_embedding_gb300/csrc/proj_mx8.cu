@@ -362,7 +362,7 @@ ple_status launch_pair(const ProductArgs& a, int32_t* dev_err, cudaStream_t stre
   if (s == PLE_OK) s = mx_scales_map(&ws, a.w_scales, w_rows, a.E, kPairAtoms, name);
   if (s != PLE_OK) return s;
   const auto kernel = product_pair_kernel<kGated>;
-  cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kPairSmem);
+  const cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kPairSmem);
   if (err != cudaSuccess) return check_cuda(err, name);
   const int64_t units = (a.T + 255) / 256 * ((a.N + (kGated ? 127 : 255)) / (kGated ? 128 : 256));
   if (units > INT32_MAX / 2) return fail(PLE_ERR_UNSUPPORTED, "%s: %lld tokens", name, static_cast<long long>(a.T));

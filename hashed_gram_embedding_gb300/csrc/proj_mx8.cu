@@ -176,42 +176,50 @@ product_pair_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_cons
     for (int i = 0; i < kPairStages; ++i)
       if (armed & (1u << i)) mbar_wait(full(i), (armed_parity >> i) & 1u, nullptr);
   } else if (warp == 1) {
-    if (rank == 0 && lane == 0) {
+    if (rank == 0) {
       // ---------------- products (the even CTA, for both) ----------------
+      // The whole warp goes through the loop and one lane issues: operands
+      // are uniform registers then.
+      const uint32_t sums = __shfl_sync(0xffffffffu, tmem, 0);
       int s = 0;
       uint32_t phase = 0, tile_phase = 0;
       bool ok = true;
       for (int u = pair; ok && u < units; u += pairs, tile_phase ^= 1u) {
-        if (!mbar_wait(sums_free, tile_phase ^ 1u, abort_flag)) { ok = false; break; }
+        if (!(ok = __all_sync(0xffffffffu, wait_for(sums_free, tile_phase ^ 1u, abort_flag)))) break;
         fence_after();
         for (int k = 0; k < stages; ++k) {
-          if (!mbar_wait(full(s), phase, abort_flag)) { ok = false; break; }
+          if (!(ok = __all_sync(0xffffffffu, wait_for(full(s), phase, abort_flag)))) break;
           fence_after();
+          if (elected()) {
 #pragma unroll
-          for (int i = 0; i < kPairAtoms; ++i)
+            for (int i = 0; i < kPairAtoms; ++i)
 #pragma unroll
-            for (int j = 0; j < 3; ++j)
-              scales_to_tmem<2>(tmem + kScaleCols + (s * kPairAtoms + i) * kAtomCols + 4 * j,
-                                base + kAtScales + s * kPairScales + (j * kPairAtoms + i) * kMxPiece);
+              for (int j = 0; j < 3; ++j)
+                scales_to_tmem<2>(sums + kScaleCols + (s * kPairAtoms + i) * kAtomCols + 4 * j,
+                                  base + kAtScales + s * kPairScales + (j * kPairAtoms + i) * kMxPiece);
 #pragma unroll
-          for (int i = 0; i < kPairAtoms; ++i) {
-            if (k * kPairAtoms + i >= atoms) break;  // its scales are another row's
-            const uint32_t scales = tmem + kScaleCols + (s * kPairAtoms + i) * kAtomCols;
-            const uint64_t x = codes_operand(base + (s * 2 * kPairAtoms + i) * kAtom);
-            const uint64_t w = codes_operand(base + ((s * 2 + 1) * kPairAtoms + i) * kAtom);
+            for (int i = 0; i < kPairAtoms; ++i) {
+              if (k * kPairAtoms + i >= atoms) break;  // its scales are another row's
+              const uint32_t scales = sums + kScaleCols + (s * kPairAtoms + i) * kAtomCols;
+              const uint64_t x = codes_operand(base + (s * 2 * kPairAtoms + i) * kAtom);
+              const uint64_t w = codes_operand(base + ((s * 2 + 1) * kPairAtoms + i) * kAtom);
 #pragma unroll
-            for (int b = 0; b < 4; ++b)
-              mma_mx8<2>(tmem, x + 2 * b, w + 2 * b, mx_idesc(256, 256) | mx_block(b), scales, scales + 4, (k | i | b) != 0);
+              for (int b = 0; b < 4; ++b)
+                mma_mx8<2>(sums, x + 2 * b, w + 2 * b, mx_idesc(256, 256) | mx_block(b), scales, scales + 4, (k | i | b) != 0);
+            }
+            mma_commit_pair(free(s));
+            if (k == stages - 1) mma_commit_pair(sums_full);
           }
-          mma_commit_pair(free(s));
+          __syncwarp();
           if (++s == kPairStages) { s = 0; phase ^= 1u; }
         }
-        if (!ok) break;
-        mma_commit_pair(sums_full);
       }
-      if (!ok) { *abort_flag = 1; set_dev_err(dev_err, PLE_DEVERR_TIMEOUT); }
-      asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(done) : "memory");
-      mbar_wait(done, 0, nullptr);
+      if (!ok && lane == 0) { *abort_flag = 1; set_dev_err(dev_err, PLE_DEVERR_TIMEOUT); }
+      // however the loop ended, no product reads or writes after this
+      if (elected())
+        asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(done) : "memory");
+      __syncwarp();
+      wait_for(done, 0, nullptr);
     }
     __syncwarp();
   } else if (warp >= 2) {
@@ -490,44 +498,46 @@ product_few_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_const
     }
     __syncwarp();
   } else if (warp == 1) {
-    if (lane == 0) {
-      // ---------------- products ----------------
-      Ring<L::kStages> ring;
-      bool ok = true;
-      for (int k = first; k < last; k += L::kStep, ring.next()) {
-        const int s = ring.at;
-        if (!(ok = mbar_wait(full(s), ring.phase, abort_flag))) break;
-        fence_after();
+    // ---------------- products: one lane issues, in code that the whole warp runs ----------------
+    const uint32_t sums = __shfl_sync(0xffffffffu, tmem, 0);
+    Ring<L::kStages> ring;
+    bool ok = true;
+    for (int k = first; k < last; k += L::kStep, ring.next()) {
+      const int s = ring.at;
+      if (!(ok = __all_sync(0xffffffffu, wait_for(full(s), ring.phase, abort_flag)))) break;
+      fence_after();
+      if (elected()) {
         const uint32_t from = base + L::kAtScales + s * L::kScales;
 #pragma unroll
         for (int j = 0; j < L::kStep; ++j) {
           if (k + j >= last) break;
-          const uint32_t scales = tmem + L::kCols + s * L::kStageCols + j * L::kAtomCols;
+          const uint32_t scales = sums + L::kCols + s * L::kStageCols + j * L::kAtomCols;
 #pragma unroll
           for (int i = 0; i < L::kSides + L::kXPieces; ++i) scales_to_tmem<1>(scales + 4 * i, from + (i * L::kStep + j) * kMxPiece);
         }
 #pragma unroll
         for (int j = 0; j < L::kStep; ++j) {
           if (k + j >= last) break;
-          const uint32_t scales = tmem + L::kCols + s * L::kStageCols + j * L::kAtomCols;
+          const uint32_t scales = sums + L::kCols + s * L::kStageCols + j * L::kAtomCols;
           const uint64_t x = codes_operand(base + s * L::kCodes + L::kSides * L::kStep * kAtom + j * kTokens * 128);
 #pragma unroll
           for (int i = 0; i < L::kSides; ++i) {
             const uint64_t w = codes_operand(base + s * L::kCodes + (i * L::kStep + j) * kAtom);
 #pragma unroll
             for (int b = 0; b < 4; ++b)
-              mma_mx8<1>(tmem + i * kTokens, w + 2 * b, x + 2 * b, mx_idesc(128, kTokens) | mx_block(b), scales + 4 * i,
+              mma_mx8<1>(sums + i * kTokens, w + 2 * b, x + 2 * b, mx_idesc(128, kTokens) | mx_block(b), scales + 4 * i,
                          scales + 4 * L::kSides, k + j > first || b > 0);
           }
         }
         mma_commit(free(s));
       }
-      if (!ok) { *abort_flag = 1; set_dev_err(dev_err, PLE_DEVERR_TIMEOUT); }
-      // however the loop ended, no product reads or writes after this
-      mma_commit(sums_full);
-      mbar_wait(sums_full, 0, nullptr);
+      __syncwarp();
     }
+    if (!ok && lane == 0) { *abort_flag = 1; set_dev_err(dev_err, PLE_DEVERR_TIMEOUT); }
+    // however the loop ended, no product reads or writes after this
+    if (elected()) mma_commit(sums_full);
     __syncwarp();
+    wait_for(sums_full, 0, nullptr);
   } else if (warp < 6) {
     // ---------------- sums, where the codes were: [token][side][row] ----------------
     const bool ok = __all_sync(0xffffffffu, mbar_wait(sums_full, 0, nullptr)) && *abort_flag == 0;

@@ -57,7 +57,7 @@ constexpr int kPairScales = kPairAtoms * 3 * kMxPiece;     // bytes of a stage's
 constexpr int kPairStage = kPairAtoms * 2 * kAtom + kPairScales;
 constexpr int kAtScales = kPairStages * kPairAtoms * 2 * kAtom;
 constexpr int kAtRoom = kAtScales + kPairStages * kPairScales;
-constexpr int kRoomPitch = 17;                             // floats of a row of the epilogue's room
+constexpr int kRoomPitch = 17;                             // words of a row of the epilogue's room
 constexpr int kRoom = 32 * kRoomPitch * 4;                 // bytes of it for a warp
 constexpr int kPairEpilogue = 8;                           // warps
 constexpr int kAtBars = kAtRoom + kPairEpilogue * kRoom;
@@ -93,6 +93,105 @@ __device__ __forceinline__ PairTile pair_tile(int u, int m_tiles, int n_tiles, i
   const int group = u / (kGroupTiles * n_tiles), first = group * kGroupTiles;
   const int height = min(m_tiles - first, kGroupTiles), r = u - first * n_tiles;
   return {(first + r % height) * 256, r / height * rows};
+}
+
+// ---- 32 columns of bf16 rows at any address, between memory and threads ----
+// A thread has a row, memory is read and written by words of two elements,
+// 16 lanes a row. Word w of a row holds elements 2w and 2w + 1, or 2w - 1 and
+// 2w where the row begins at an odd place: every word lies on 4 bytes, and
+// only a row's ends are single elements. Rows an even number apart begin
+// alike, so a lane's place in its rows never changes.
+
+// 1 if row `row` begins at an odd place.
+__device__ __forceinline__ int odd_place(const ple_bf16_t* first, int64_t stride, int row) {
+  return static_cast<int>((reinterpret_cast<uintptr_t>(first) >> 1) + (row & stride)) & 1;
+}
+
+// What a lane takes of its rows' words: both elements, or one of them at a
+// row's ends. Decided once for all rows, so that nothing waits between them.
+struct RowPlace {
+  int64_t at;  // from the first row's first element
+  bool low, high;
+  __device__ __forceinline__ RowPlace(const ple_bf16_t* first, int64_t stride, int columns, int lane) {
+    const int e = 2 * (lane % 16) - odd_place(first, stride, lane / 16);
+    at = lane / 16 * stride + e;
+    low = e >= 0 && e < columns;
+    high = e + 1 < columns;
+  }
+};
+
+struct RowWords {
+  uint32_t words[16];  // of rows 2i and 2i + 1, a half warp each
+  uint32_t last;       // this lane's row's word 16, if it begins at an odd place
+  bool upper;          // words hold an upper element alone
+  __device__ __forceinline__ void ask(const ple_bf16_t* first, int64_t stride, int rows, int columns, int lane) {
+    const RowPlace p(first, stride, columns, lane);
+    const ple_bf16_t* at = first + p.at + (p.low ? 0 : 1);
+    const int mine = rows - lane / 16;
+    upper = !p.low;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) words[i] = 0;
+    last = 0;
+    if (p.low && p.high) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        if (2 * i < mine) words[i] = *reinterpret_cast<const uint32_t*>(at + 2 * i * stride);
+    } else if (p.low || p.high) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        if (2 * i < mine) words[i] = at[2 * i * stride];
+    }
+    if (lane < rows && columns == 32 && odd_place(first, stride, lane)) last = first[lane * stride + 31];
+  }
+  __device__ __forceinline__ void stage(uint32_t* room, int lane) const {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) room[(2 * i + lane / 16) * kRoomPitch + lane % 16] = upper ? words[i] << 16 : words[i];
+    room[lane * kRoomPitch + 16] = last;
+  }
+};
+
+// This thread's row out of the room, as pairs of elements, and into it.
+__device__ __forceinline__ void take_row(uint32_t (&pairs)[16], const uint32_t* row, int odd) {
+  uint32_t w = row[0];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const uint32_t next = row[i + 1];
+    pairs[i] = odd ? __byte_perm(w, next, 0x5432) : w;
+    w = next;
+  }
+}
+__device__ __forceinline__ void put_row(const uint32_t (&pairs)[16], uint32_t* row, int odd) {
+  uint32_t before = 0;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    row[i] = odd ? __byte_perm(before, pairs[i], 0x5432) : pairs[i];
+    before = pairs[i];
+  }
+  row[16] = before >> 16;
+}
+
+__device__ __forceinline__ void store_rows(const uint32_t* room, ple_bf16_t* first, int64_t stride, int rows, int columns, int lane) {
+  const RowPlace p(first, stride, columns, lane);
+  ple_bf16_t* const at = first + p.at;
+  const int mine = rows - lane / 16;
+  uint32_t words[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) words[i] = room[(2 * i + lane / 16) * kRoomPitch + lane % 16];
+  const uint32_t last = room[lane * kRoomPitch + 16];
+  if (p.low && p.high) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+      if (2 * i < mine) *reinterpret_cast<uint32_t*>(at + 2 * i * stride) = words[i];
+  } else if (p.low) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+      if (2 * i < mine) at[2 * i * stride] = static_cast<ple_bf16_t>(words[i]);
+  } else if (p.high) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+      if (2 * i < mine) at[2 * i * stride + 1] = static_cast<ple_bf16_t>(words[i] >> 16);
+  }
+  if (lane < rows && columns == 32 && odd_place(first, stride, lane)) first[lane * stride + 31] = static_cast<ple_bf16_t>(last);
 }
 
 template <bool kGated>
@@ -229,21 +328,44 @@ product_pair_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_cons
     uint32_t tile_phase = 0;
     for (int u = pair; u < units; u += pairs, tile_phase ^= 1u) {
       const PairTile t = pair_tile(u, m_tiles, n_tiles, kRows);
+      const int64_t m0 = t.m + static_cast<int64_t>(rank) * 128 + quad * 32;
+      const int rows = static_cast<int>(min(max(a.T - m0, int64_t(0)), int64_t(32)));  // of this warp's that exist
+      // The residual is brought while the products run, all of it: beside
+      // their operands a load takes some 3000 cycles.
+      uint32_t pairs[kGated ? 1 : 4][16];
+      uint32_t* const room = reinterpret_cast<uint32_t*>(smem + kAtRoom) + (warp - 2) * 32 * kRoomPitch;
+      if constexpr (!kGated) {
+        if (a.residual != nullptr) {
+          const ple_bf16_t* const first = a.residual + m0 * a.residual_stride + t.n + half * 128;
+          RowWords words[4];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) words[c].ask(first + 32 * c, a.residual_stride, rows, min(32, a.N - t.n - half * 128 - 32 * c), lane);
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            words[c].stage(room, lane);
+            __syncwarp();
+            take_row(pairs[c], room + lane * kRoomPitch, odd_place(first, a.residual_stride, lane));
+            __syncwarp();
+          }
+        }
+      }
       if (!__all_sync(0xffffffffu, mbar_wait(sums_full, tile_phase, abort_flag))) {
         if (lane == 0) { *abort_flag = 1; set_dev_err(dev_err, PLE_DEVERR_TIMEOUT); }
         break;
       }
       fence_after();
-      // gated: 64 columns of the gate and the 64 that meet them
-      float v[4][32];
-#pragma unroll
-      for (int c = 0; c < 4; ++c) tmem_ask(lanes + (kGated ? c / 2 * 128 + half * 64 + c % 2 * 32 : half * 128 + c * 32), v[c]);
-      tmem_wait(v);
-      fence_before();
-      __syncwarp();
-      if (lane == 0) arrive_cluster(at_rank(sums_free, 0));
-      const int64_t m0 = t.m + static_cast<int64_t>(rank) * 128 + quad * 32;
+      auto release = [&]() {
+        fence_before();
+        __syncwarp();
+        if (lane == 0) arrive_cluster(at_rank(sums_free, 0));
+      };
       if constexpr (kGated) {
+        // 64 columns of the gate and the 64 that meet them
+        float v[4][32];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_ask(lanes + c / 2 * 128 + half * 64 + c % 2 * 32, v[c]);
+        tmem_wait(v);
+        release();
         const int64_t m = m0 + lane;
         uint32_t word = 0;
 #pragma unroll
@@ -265,60 +387,29 @@ product_pair_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_cons
         }
         if (m < a.T) *reinterpret_cast<uint16_t*>(a.scales + mx_scale_at(m, (t.n + half * 64) / 32, a.N)) = static_cast<uint16_t>(word);
       } else {
-        const int n0 = t.n + half * 128;
-        if (a.wide) {
-          const int64_t m = m0 + lane;
-          if (m < a.T) {
 #pragma unroll
-            for (int c = 0; c < 4; ++c)
+        for (int c = 0; c < 4; ++c) {
+          float y[32];
+          tmem_load(lanes + half * 128 + c * 32, y);
 #pragma unroll
-              for (int q = 0; q < 2; ++q) {
-                const int n = n0 + c * 32 + q * 16;
-                if (n >= a.N) continue;
-                float* y = v[c] + 16 * q;
-                if (a.residual != nullptr) {
-                  const uint4* from = reinterpret_cast<const uint4*>(a.residual + m * a.residual_stride + n);
-                  const uint4 w[2] = {from[0], from[1]};
-                  float r[8];
-#pragma unroll
-                  for (int h = 0; h < 2; ++h) {
-                    unpack8(w[h], r);
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) y[8 * h + i] += r[i];
-                  }
-                }
-                uint32_t packed[8];
-#pragma unroll
-                for (int i = 0; i < 8; ++i) packed[i] = pack2(y[2 * i], y[2 * i + 1]);
-                store32(a.out + m * a.N + n, packed);
-              }
-          }
-        } else {
-          // rows at any address: 16 columns of two rows at a time
-          float* const mine = reinterpret_cast<float*>(smem + kAtRoom) + (warp - 2) * 32 * kRoomPitch;
-#pragma unroll
-          for (int c = 0; c < 8; ++c) {
-            __syncwarp();
-#pragma unroll
-            for (int i = 0; i < 16; ++i) mine[lane * kRoomPitch + i] = v[c / 2][c % 2 * 16 + i];
-            __syncwarp();
-            const int n = n0 + c * 16 + lane % 16;
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {  // 8 rows of each half warp at once
-              float y[8];
-#pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                const int r = h * 16 + 2 * i + lane / 16;
-                y[i] = mine[r * kRoomPitch + lane % 16];
-                if (a.residual != nullptr && m0 + r < a.T && n < a.N) y[i] += bf_lo(a.residual[(m0 + r) * a.residual_stride + n]);
-              }
-#pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                const int r = h * 16 + 2 * i + lane / 16;
-                if (m0 + r < a.T && n < a.N) a.out[(m0 + r) * a.N + n] = static_cast<ple_bf16_t>(pack2(y[i], 0.0f) & 0xffffu);
-              }
+          for (int i = 0; i < 16; ++i) {
+            if (a.residual != nullptr) {
+              y[2 * i] += bf_lo(pairs[c][i]);
+              y[2 * i + 1] += bf_hi(pairs[c][i]);
             }
+            pairs[c][i] = pack2(y[2 * i], y[2 * i + 1]);
           }
+        }
+        release();
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const int n = t.n + half * 128 + c * 32;
+          if (n >= a.N) break;
+          ple_bf16_t* const first = a.out + m0 * a.N + n;
+          put_row(pairs[c], room + lane * kRoomPitch, odd_place(first, a.N, lane));
+          __syncwarp();
+          store_rows(room, first, a.N, rows, min(32, a.N - n), lane);
+          __syncwarp();
         }
       }
     }
@@ -767,6 +858,8 @@ PLE_EXPORT ple_status ple_proj_mx8(const uint8_t* x, const uint8_t* x_scales, in
   const ple_status s = check_product(name, x, x_scales, num_tokens, in_dim, w, w_scales, out_dim);
   if (s != PLE_OK || num_tokens == 0) return s;
   if (out == nullptr) return fail(PLE_ERR_INVALID_ARG, "%s: null out", name);
+  if (((reinterpret_cast<uintptr_t>(out) | reinterpret_cast<uintptr_t>(residual)) & 1) != 0)
+    return fail(PLE_ERR_INVALID_ARG, "%s: out or the residual at an odd address", name);
   const bool wide = out_dim % 16 == 0 && aligned16(out) && (residual == nullptr || (aligned16(residual) && residual_stride % 8 == 0));
   const ProductArgs a{x, x_scales, w, w_scales, num_tokens, in_dim, out_dim, 0, wide, residual, residual_stride, out,
                       nullptr, nullptr};

@@ -105,7 +105,8 @@ def test_gated(lib):
 
 def test_proj(lib):
     for bad in (dict(T=-1), dict(T=1 << 31), dict(C=0), dict(N=0), dict(x=None), dict(xs=None), dict(w=None),
-                dict(ws=None), dict(out=None), dict(x=ODD), dict(xs=ODD), dict(w=ODD), dict(ws=ODD)):
+                dict(ws=None), dict(out=None), dict(x=ODD), dict(xs=ODD), dict(w=ODD), dict(ws=ODD),
+                dict(out=near(at(5), 1)), dict(r=near(at(4), 1))):
         assert proj(lib, **bad) == INVALID, bad
     assert proj(lib, C=64) == UNSUPPORTED
     assert proj(lib, T=0, x=None) == OK

@@ -1,5 +1,6 @@
-"""Serving with the 4-bit step: prompts through a PLE layer and an attention
-block, then single tokens, the step captured once in a CUDA graph.
+"""Serving with the 4-bit and 8-bit steps: prompts through a PLE layer, an
+attention block and a feed-forward block, then single tokens, the step
+captured once in a CUDA graph.
 
     python examples/decode.py [--requests 64] [--prompt 500] [--steps 100]
 
@@ -16,10 +17,10 @@ import torch
 
 sys.path.insert(0, os.path.join(os.path.dirname(os.path.abspath(__file__)), ".."))
 
-from hashed_gram_embedding_gb300 import PLEAttention, PLELayer, pack_w4  # noqa: E402
+from hashed_gram_embedding_gb300 import PLEAttention, PLEFeedForward, PLELayer, pack_mx8, pack_w4  # noqa: E402
 from hashed_gram_embedding_gb300 import workloads as wl  # noqa: E402
 
-HEADS, KV_HEADS, DIM, PAGE, GROUP = 16, 4, 128, 16, 128
+HEADS, KV_HEADS, DIM, PAGE, GROUP, WIDER = 16, 4, 128, 16, 128, 4
 
 
 def rotation(positions, dim):
@@ -29,6 +30,10 @@ def rotation(positions, dim):
 
 def random_w4(rows, columns):
     return pack_w4(torch.randn(rows, columns, device="cuda") * columns ** -0.5, GROUP)
+
+
+def random_mx8(rows, columns):
+    return pack_mx8(torch.randn(rows, columns, device="cuda") * columns ** -0.5)
 
 
 def main():
@@ -49,6 +54,9 @@ def main():
     pages = -(-total // PAGE)
     block = PLEAttention(random_w4((HEADS + 2 * KV_HEADS) * DIM, w.hidden), random_w4(w.hidden, HEADS * DIM),
                          HEADS, KV_HEADS, DIM, R * pages, PAGE, R * P, cos_sin=rotation(total, DIM))
+    inner = WIDER * w.hidden
+    feed_forward = PLEFeedForward(random_mx8(2 * inner, w.hidden), random_mx8(w.hidden, inner),
+                                  torch.ones(w.hidden, dtype=torch.bfloat16, device="cuda"), R * P)
     block_table = torch.randperm(R * pages, device="cuda").to(torch.int32).view(R, pages)
     kv_lens = torch.zeros(R, dtype=torch.int32, device="cuda")
     dev_err = torch.zeros(1, dtype=torch.int32, device="cuda")
@@ -58,10 +66,11 @@ def main():
     state = [torch.zeros((R, reach, w.hidden), dtype=torch.bfloat16, device="cuda") for _ in range(2)]
 
     def step(ids, qsl, hidden, longest, turn):
-        """hidden -> hidden, both parts added to it, in place."""
+        """hidden -> hidden, all three parts added to it, in place."""
         hidden.add_(layer.forward(ids, qsl, hidden, ngram_context=context[turn], ngram_context_out=context[1 - turn],
                                   conv_state=state[turn], conv_state_out=state[1 - turn], dev_err=dev_err))
-        hidden.add_(block.forward(hidden, block_table, qsl, kv_lens, max_query_len=longest, dev_err=dev_err))
+        delta = block.forward(hidden, block_table, qsl, kv_lens, max_query_len=longest, dev_err=dev_err)
+        feed_forward.forward(hidden, delta, dev_err=dev_err, out=hidden)
 
     def tokens(n):
         return torch.randint(3, w.token_vocab, (n,), device="cuda", dtype=torch.int32)
@@ -82,9 +91,12 @@ def main():
 
     ids, qsl = tokens(R), torch.arange(R + 1, dtype=torch.int32, device="cuda")
 
+    embedded = torch.randn(R, w.hidden, device="cuda").to(torch.bfloat16)  # what a step's tokens come in as
+
     def two_steps():
         for turn in (1, 0):
             kv_lens.add_(1)
+            hidden.copy_(embedded)
             step(ids, qsl, hidden, 1, turn)
 
     two_steps()

@@ -433,6 +433,7 @@ int resident_pairs() {
   if (cudaGetDevice(&dev) != cudaSuccess) return 1;
   if (dev >= 0 && dev < kDevices && known[dev].load() > 0) return known[dev].load();
   int pairs = num_sms() / 2, active = 0;
+  cudaFuncSetAttribute(product_pair_kernel<kGated>, cudaFuncAttributeMaxDynamicSharedMemorySize, kPairSmem);  // else none fits
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>(pairs) * 2);
   cfg.blockDim = dim3(kPairThreads);
@@ -783,6 +784,7 @@ ple_status check_product(const char* name, const uint8_t* x, const uint8_t* x_sc
   if (in_dim % kMxTile != 0)
     return fail(PLE_ERR_UNSUPPORTED, "%s: %d columns (a multiple of %d)", name, in_dim, kMxTile);
   if (num_tokens == 0) return PLE_OK;
+  if (rows > INT32_MAX - 255) return fail(PLE_ERR_UNSUPPORTED, "%s: %d rows", name, rows);  // tiles are counted in 32 bits
   if (num_tokens > 65535 * 64) return fail(PLE_ERR_UNSUPPORTED, "%s: %lld tokens", name, static_cast<long long>(num_tokens));
   if (x == nullptr || x_scales == nullptr || w == nullptr || w_scales == nullptr)
     return fail(PLE_ERR_INVALID_ARG, "%s: null codes or scales", name);

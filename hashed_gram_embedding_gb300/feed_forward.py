@@ -56,6 +56,8 @@ class PLEFeedForward:
         if rows != 2 * self.inner or out != self.hidden:
             raise ValueError(f"w_gate_up {tuple(w_gate_up[0].shape)} and w_down {tuple(w_down[0].shape)} "
                              "are not [2 I, C] and [C, I]")
+        if activation not in _lib._ACTIVATIONS:
+            raise ValueError(f"activation {activation!r}: one of {', '.join(_lib._ACTIVATIONS)} is needed")
         device = w_gate_up[0].device
 
         def room(columns):

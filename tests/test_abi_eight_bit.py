@@ -108,7 +108,7 @@ def test_proj(lib):
                 dict(ws=None), dict(out=None), dict(x=ODD), dict(xs=ODD), dict(w=ODD), dict(ws=ODD),
                 dict(out=near(at(5), 1)), dict(r=near(at(4), 1))):
         assert proj(lib, **bad) == INVALID, bad
-    assert proj(lib, C=64) == UNSUPPORTED
+    assert proj(lib, C=64) == UNSUPPORTED and proj(lib, N=2**31 - 1) == UNSUPPORTED and proj(lib, T=5 << 20) == UNSUPPORTED
     assert proj(lib, T=0, x=None) == OK
     for bad in (dict(out=at(0)), dict(out=at(1)), dict(out=near(at(2), 77 * 256 - 16)), dict(out=at(3)),
                 dict(out=at(4), rs=80), dict(out=near(at(4), 16), rs=77), dict(out=near(at(4), -16), rs=77)):

@@ -155,6 +155,8 @@ def test_refusals():
     pack = lambda w: tuple(a.cuda() for a in pack_mx8(w))  # noqa: E731
     with pytest.raises(ValueError):
         PLEFeedForward(pack(w1[:I]), pack(w2), g.cuda(), 4)
+    with pytest.raises(ValueError):
+        PLEFeedForward(pack(w1), pack(w2), g.cuda(), 4, activation="relu")
     ff = block(4)
     with pytest.raises(ValueError):
         ff.forward(hidden(5))
@@ -167,3 +169,14 @@ def test_refusals():
 
 def test_no_tokens():
     assert block(4).forward(hidden(0)).shape == (0, C)
+
+
+def test_the_serving_example_runs():
+    import os
+    import subprocess
+    import sys
+    root = os.path.join(os.path.dirname(os.path.abspath(__file__)), "..")
+    run = subprocess.run([sys.executable, os.path.join(root, "examples", "decode.py"), "--requests", "3", "--prompt", "21",
+                          "--steps", "4"], capture_output=True, text=True, timeout=300)
+    assert run.returncode == 0, run.stderr[-2000:]
+    assert "a step of 3 tokens" in run.stdout

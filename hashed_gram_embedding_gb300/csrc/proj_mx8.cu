@@ -4,10 +4,14 @@
 //   ple_proj_mx8    out = residual + x W^T, rounded once to bf16
 //   ple_gated_mx8   h = act(x Wg^T) * (x Wu^T), quantised as it is computed
 //
-// Two kernels: for many tokens a pair of CTAs takes 256 tokens against 256
-// rows of W (bound by the tensor cores); for few a CTA takes 128 rows of W
-// against all tokens, its columns shared out in a cluster (bound by reading
-// W).
+// Two kernels. For many tokens a pair of CTAs takes 256 tokens against 256
+// rows of W: bound by the tensor cores, their operands' way into the SMs and
+// the power limit. 8192 tokens, 16384 -> 4096: 318 us (3.46 PFLOP/s) in short
+// runs, 376 in long ones, where the clock falls to 1.7 GHz; gated, 4096 ->
+// 16384: 657 us (3.35). For few tokens a CTA takes 128 rows of W against all of
+// them, its columns shared out in a cluster: bound by reading W and some 4.5 us
+// of start and end. One token, gated 4096 -> 16384: 24.2 us (5.7 TB/s), 16384 ->
+// 4096: 14.8 (4.7); 203 tokens: 23.3.
 #include "mx8_tensor.cuh"
 
 #include <algorithm>
@@ -21,7 +25,7 @@ struct ProductArgs {
   int64_t T;
   int E, N;  // columns; rows of the result: of W, or half as many
   int gelu;
-  int wide;  // rows of out and the residual may be taken 16 bytes at a time
+  int wide;  // rows of out and the residual may be taken 8 bytes at a time
   const ple_bf16_t* residual;
   int64_t residual_stride;
   ple_bf16_t* out;
@@ -40,13 +44,21 @@ __device__ __forceinline__ float activation(float g, int gelu) {
 // one the gate's 128 rows, the other the 128 rows of the other half that meet
 // them, so that a thread of the epilogue finds both in its row), and the
 // scales of its tokens and of all W rows. A stage holds 256 columns; its
-// scales go to tensor memory in front of its products.
-// The sums take 256 of the 512 columns of tensor memory and the scales some
-// of the rest, so there is one set of sums: the epilogue's eight warps take
-// them into registers (128 a thread) and give the place back before they do
-// anything with them.
-// Tiles are walked in groups of 2048 tokens, tokens first: W is read once for
-// each group, and the group's tokens stay in L2.
+// scales go to tensor memory in front of its products, by copies of the
+// products' own queue. (Brought by other warps through registers they came
+// too late: 556 us against 375 for 8192 tokens, 16384 -> 4096, then.)
+// One lane of a warp that stays converged issues: the operands are uniform
+// registers then, and the copies cost nothing beside the products. (Issued
+// under a branch on the lane, each instruction took some 70 cycles, and a
+// stage 1418 instead of its products' 1024.)
+// The sums take 256 of the 512 columns of tensor memory and the scales 72, so
+// there is one set of sums: the epilogue's eight warps take them out, some
+// 2000 cycles a tile, and give the place back before they store anything. (A
+// second set that shares 72 columns with the first was no faster: what counts
+// between two tiles is when their operands arrive.)
+// Tiles are walked in groups of 4096 tokens, tokens first: W is read once for
+// each group, and the group's tokens stay in L2. (Groups of 2048, 1024: gated
+// 8192 tokens 680, 710 us against 657.)
 //
 // Warps: 0 copies, 1 issues, 2-9 the epilogue: two for each quarter of the
 // rows, half of the columns each.
@@ -64,7 +76,7 @@ constexpr int kAtBars = kAtRoom + kPairEpilogue * kRoom;
 constexpr int kPairBars = 2 * kPairStages + 3;
 constexpr int kPairSmem = kAtBars + kPairBars * 8 + 16 + 1024;  // and alignment
 constexpr int kPairThreads = 64 + 32 * kPairEpilogue;
-constexpr int kGroupTiles = 8;                             // of 256 tokens
+constexpr int kGroupTiles = 16;                            // of 256 tokens
 constexpr int kScaleCols = 256;                            // scales stand behind the sums
 constexpr int kAtomCols = 12;                              // 4 of x, 8 of W
 static_assert(kScaleCols + kPairStages * kPairAtoms * kAtomCols <= 512, "tensor memory");
@@ -480,6 +492,13 @@ ple_status launch_pair(const ProductArgs& a, int32_t* dev_err, cudaStream_t stre
 // leave SMs without work, a cluster of CTAs shares them: each takes a part of
 // the columns, and their sums meet through distributed shared memory, in the
 // order of the CTAs, each joining (and finishing) a share of the tokens.
+// Up to 64 tokens two CTAs share an SM: more of them are ready to ask for W
+// than SMs are there, and one starts while another ends (16384 -> 4096, 64
+// tokens: 18.4 us against 21.2 with one). A stage is one atom of columns: two
+// would leave too few of them (one token, 16384 -> 4096: 17.8 us against 15.7).
+// W's first stages are asked into L2 while the kernel before still runs, which
+// reads nothing of them and so may not wait for it (15.7 -> 14.8 with the
+// rest of the start).
 //
 // Warps: 0 copies, 1 issues, 2-5 take the sums out; all eight join.
 constexpr int kFewThreads = 256;
@@ -862,7 +881,8 @@ PLE_EXPORT ple_status ple_proj_mx8(const uint8_t* x, const uint8_t* x_scales, in
   if (out == nullptr) return fail(PLE_ERR_INVALID_ARG, "%s: null out", name);
   if (((reinterpret_cast<uintptr_t>(out) | reinterpret_cast<uintptr_t>(residual)) & 1) != 0)
     return fail(PLE_ERR_INVALID_ARG, "%s: out or the residual at an odd address", name);
-  const bool wide = out_dim % 16 == 0 && aligned16(out) && (residual == nullptr || (aligned16(residual) && residual_stride % 8 == 0));
+  const bool wide = out_dim % 4 == 0 && ((reinterpret_cast<uintptr_t>(out) | reinterpret_cast<uintptr_t>(residual)) & 7) == 0 &&
+                    (residual == nullptr || residual_stride % 4 == 0);
   const ProductArgs a{x, x_scales, w, w_scales, num_tokens, in_dim, out_dim, 0, wide, residual, residual_stride, out,
                       nullptr, nullptr};
   const size_t n = static_cast<size_t>(num_tokens) * out_dim * 2;

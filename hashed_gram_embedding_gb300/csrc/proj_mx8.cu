@@ -771,26 +771,53 @@ ple_status launch_few(const ProductArgs& a, int32_t* dev_err, cudaStream_t strea
                                   parts, dev_err), name);
 }
 
-// Up to 256 tokens (gated: 128) W is read by one CTA each: the second kernel.
-// More tokens, in blocks of 256, stay with it while pairs of CTAs would leave
-// most of the GPU idle. What a launch takes, in 10 ns, from measurements of
-// both: a pair's stage of 256 columns 73, a tile's change 160, all else 750; a
-// CTA's atom of 128 columns 48, taking out and joining 600, all else 350.
-// Measured, pairs / CTAs, us, tokens over columns x rows:
-//   300   8192 x 2048   32.1 / 17.8     512   4096 x 4096   21.3 / 18.4
-//  1023   2048 x 8192   21.9 / 31.7
+// What a launch takes, in 10 ns, from measurements: by pairs of CTAs a stage
+// of 256 columns 56, a tile's start and end 330, all else 480, and never less
+// than W's way from memory at 5.2 TB/s and 600; by single ones
+// an atom of 128 columns 41 (gated, 128 tokens: 70), a tile's start and end
+// 800 (300, and 6 for each token: its sums are taken out and joined), all else
+// 70.
+template <bool kGated>
+int64_t time_of_pairs(const ProductArgs& a) {
+  constexpr int kRows = kGated ? 128 : 256;
+  const int64_t units = (a.T + 255) / 256 * ((a.N + kRows - 1) / kRows), pairs = resident_pairs<kGated>();
+  const int64_t w = int64_t(kGated ? 2 : 1) * a.N * a.E;
+  return std::max((units + pairs - 1) / pairs * ((a.E / 128 + 1) / 2 * 56 + 330) + 480, w / 52000 + 600);
+}
+template <typename L>
+int64_t time_of_ctas(const ProductArgs& a, int tokens, int atom, int tile) {
+  const int64_t ctas = (a.N + 127) / 128 * ((a.T + tokens - 1) / tokens);
+  const int atoms = a.E / 128, parts = parts_of<L>(ctas, atoms);
+  return (ctas * parts + num_sms() - 1) / num_sms() * ((atoms + parts - 1) / parts * atom + tile) + 70;
+}
+
+// Few tokens go to single CTAs, with a tile that holds them; many, in blocks of
+// 256, stay there while pairs would leave too much of the GPU idle, and go to
+// pairs otherwise. Measured, pairs / single CTAs, us, tokens over columns x
+// rows:
+//   200  4096 x 4096  15.8 / 11.7   300  8192 x 2048  25.3 / 15.1   400  2048 x 1024  11.0 / 10.3
+//   512  4096 x 4096  16.7 / 15.6   512  2048 x 8192  12.9 / 15.3   768  4096 x 4096  17.2 / 20.6
+//  1023  2048 x 8192  20.0 / 30.1  1024 16384 x 4096  47.9 / 56.9
+// gated:
+//    33  4096 x 4096  16.0 / 11.6    48  2048 x 8192  12.7 / 12.7    64 4096 x 16384  32.2 / 29.3
+//    80  2048 x 8192  12.4 / 14.4   112  4096 x 4096  16.5 / 15.8   112 4096 x 16384  32.5 / 32.9
+//   150  4096 x 4096  16.5 / 19.3   256  2048 x 8192  13.1 / 20.8   512  4096 x  1024  14.4 / 15.4
+// The tiles: 16 tokens are worth one of their own only gated, whose stages are
+// twice as large (16 and 32 wide, one token 4096 x 16384 24.7 / 25.2; 16 tokens
+// 4096 x 4096, not gated, 7.4 / 6.9), 64 only otherwise (64 and 128 wide, 64 tokens
+// 16384 x 4096 17.3 / 17.8; gated 4096 x 4096 15.3 / 13.0).
 template <bool kGated>
 ple_status launch_product(const ProductArgs& a, int32_t* dev_err, cudaStream_t stream, const char* name) {
-  if (a.T <= 16) return launch_few<kGated, 16>(a, dev_err, stream, name);
-  if (a.T <= 32) return launch_few<kGated, 32>(a, dev_err, stream, name);
-  if (a.T <= 64) return launch_few<kGated, 64>(a, dev_err, stream, name);
-  if (a.T <= 128) return launch_few<kGated, 128>(a, dev_err, stream, name);
-  if constexpr (!kGated) {
-    const int64_t ctas = (a.N + 127) / 128 * ((a.T + 255) / 256), units = (a.T + 255) / 256 * ((a.N + 255) / 256);
-    const int atoms = a.E / 128, parts = parts_of<Few<false, 256>>(ctas, atoms), pairs = resident_pairs<false>();
-    const int64_t by_pairs = (units + pairs - 1) / pairs * ((atoms + 1) / 2 * 73 + 160) + 750;
-    const int64_t by_ctas = (ctas * parts + num_sms() - 1) / num_sms() * ((atoms + parts - 1) / parts * 48 + 600) + 350;
-    if (a.T <= 256 || by_ctas < by_pairs) return launch_few<false, 256>(a, dev_err, stream, name);
+  if constexpr (kGated) {
+    if (a.T <= 16) return launch_few<true, 16>(a, dev_err, stream, name);
+    if (a.T <= 32) return launch_few<true, 32>(a, dev_err, stream, name);
+    if (a.T <= 128 && time_of_ctas<Few<true, 128>>(a, 128, 70, 300 + 6 * static_cast<int>(a.T)) <= time_of_pairs<true>(a))
+      return launch_few<true, 128>(a, dev_err, stream, name);
+  } else {
+    if (a.T <= 32) return launch_few<false, 32>(a, dev_err, stream, name);
+    if (a.T <= 64) return launch_few<false, 64>(a, dev_err, stream, name);
+    if (a.T <= 128) return launch_few<false, 128>(a, dev_err, stream, name);
+    if (time_of_ctas<Few<false, 256>>(a, 256, 41, 800) < time_of_pairs<false>(a)) return launch_few<false, 256>(a, dev_err, stream, name);
   }
   return launch_pair<kGated>(a, dev_err, stream, name);
 }

@@ -862,7 +862,8 @@ typedef enum { PLE_SILU = 0, PLE_GELU = 1 } ple_activation;
 /*
  * ple_gated_mx8 -- the first half of a gated feed-forward block,
  *   h = act(x Wg^T) * (x Wu^T), (codes, scales) = mx8(h).
- * Float32 sums; h is not rounded before it is quantised.
+ * Float32 sums, in an order that the sizes decide (num_tokens among them);
+ * h is not rounded before it is quantised. Gates below about -87 give zeros.
  *   x, x_scales  mx8 [num_tokens][hidden].
  *   w, w_scales  mx8 [2 * inner][hidden]: Wg's rows, then Wu's.
  *   inner        a multiple of 128 (else PLE_ERR_UNSUPPORTED).
@@ -874,7 +875,8 @@ ple_status ple_gated_mx8(const uint8_t* x, const uint8_t* x_scales, int64_t num_
                          int32_t* dev_err, cudaStream_t stream);
 
 /*
- * ple_proj_mx8 -- out = residual + x W^T, float32 sums, rounded once.
+ * ple_proj_mx8 -- out = residual + x W^T, float32 sums in an order that the
+ * sizes decide, rounded once.
  *   x, x_scales  mx8 [num_tokens][in_dim].
  *   w, w_scales  mx8 [out_dim][in_dim].
  *   residual     bf16 rows of out_dim, residual_stride elements apart, or

@@ -126,6 +126,14 @@ def test_read(t, c):
     assert (out[t] == 7.0).all()
 
 
+def test_read_to_16_bytes():
+    (codes, scales), want = packed(np.random.default_rng(0).normal(0, 1, (33, 256)))
+    out = torch.zeros(33 * 256 + 8, dtype=torch.bfloat16, device="cuda")
+    moved = torch.zeros(33 * 256 + 16, dtype=torch.uint8, device="cuda")[16:].view(33, 256).copy_(codes)
+    ple.ple_mx8_read(moved, scales, out[8:].view(33, 256))
+    assert np.array_equal(f64(out[8:].view(33, 256)), want) and (out[:8] == 0).all()
+
+
 def test_read_every_code_and_scale():
     codes = torch.arange(256, dtype=torch.uint8).view(2, 128).repeat(128, 1)
     byte = np.arange(256, dtype=np.uint8)[:, None].repeat(4, 1)

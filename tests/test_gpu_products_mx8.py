@@ -46,7 +46,7 @@ def test_proj(t, e, n):
 
 
 @pytest.mark.parametrize("t,e,n", [(1, 512, 100), (40, 256, 129), (130, 384, 64), (600, 512, 777), (1024, 256, 512)])
-@pytest.mark.parametrize("kind", ["apart", "wide", "itself", "odd"])
+@pytest.mark.parametrize("kind", ["apart", "wide", "itself", "odd", "eighth", "one row"])
 def test_residual(t, e, n, kind):
     x8, x = packed(normal(t, e, 1))
     w8, w = packed(normal(n, e, 2, e ** -0.5))
@@ -61,6 +61,13 @@ def test_residual(t, e, n, kind):
     elif kind == "odd":  # rows at addresses of two bytes
         given = torch.zeros(t * n + 1, dtype=torch.bfloat16, device="cuda")[1:].view(t, n).copy_(r)
         out = torch.zeros(t * n + 3, dtype=torch.bfloat16, device="cuda")[3:].view(t, n)
+    elif kind == "eighth":  # of 8 bytes and no more
+        given = torch.zeros(t * n + 4, dtype=torch.bfloat16, device="cuda")[4:].view(t, n).copy_(r)
+        out = torch.zeros(t * n + 12, dtype=torch.bfloat16, device="cuda")[12:].view(t, n)
+    elif kind == "one row":  # for all tokens, as a bias
+        given = r[:1].expand(t, n)
+        want = oracle.proj(x, w, f64(r[:1]))
+        off = sum_off(x, w) + 2.0 ** -23 * (np.abs(want) + np.abs(f64(r[:1])))
     else:
         given = r
     ple.ple_proj_mx8(*x8, *w8, out, residual=given)
@@ -230,3 +237,44 @@ def test_many_tokens():
         pick = np.stack([oracle.scale_at(r, np.arange(i // 32), i) for r in (lo, lo + 1)])
         rows = oracle.values(out[0][lo:lo + 2].cpu().numpy(), out[1][torch.from_numpy(pick).cuda()].cpu().numpy())
         check_bf16(y[lo:lo + 2], rows @ w.T, sum_off(rows, w))
+
+
+def test_calls_at_once():
+    """Both kernels of both calls on two streams, captured and not: nothing is shared."""
+    cases = []
+    for t in (1, 50, 300, 900):
+        x8, _ = packed(normal(t, 640, t))
+        w8, _ = packed(normal(1024, 640, t + 1, 0.04))
+        codes, scales = room(t, 512)
+        out = torch.zeros((t, 1024), dtype=torch.bfloat16, device="cuda")
+
+        def run(x8=x8, w8=w8, codes=codes, scales=scales, out=out):
+            ple.ple_gated_mx8(*x8, *w8, codes, scales)
+            ple.ple_proj_mx8(*x8, *w8, out)
+
+        run()
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            run()
+        cases.append((run, graph, (codes, scales, out)))
+    want = []
+    for run, _, outs in cases:
+        run()
+        torch.cuda.synchronize()
+        want.append([o.clone() for o in outs])
+    streams = [torch.cuda.Stream() for _ in cases]
+    for _ in range(8):
+        for i, (run, graph, outs) in enumerate(cases):
+            with torch.cuda.stream(streams[i]):
+                for o in outs:
+                    o.zero_()
+                if i % 2 == 0:
+                    graph.replay()
+                else:
+                    run()
+        torch.cuda.synchronize()
+        for (_, _, outs), w in zip(cases, want):
+            assert torch.equal(outs[0], w[0]) and torch.equal(outs[2], w[2])
+            there = w[1] != 0xA5
+            assert torch.equal(outs[1][there], w[1][there])

@@ -75,6 +75,18 @@ __device__ __forceinline__ void store32(void* to, const uint32_t (&v)[8]) {
   }
 }
 
+__device__ __forceinline__ uint64_t f2_add(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+// Larger magnitude of three values, NaN if one is.
+__device__ __forceinline__ float abs_max(float a, float b, float c) {
+  float d;
+  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
 // Bytes of a tensor's scales, or -1 for sizes that have none.
 inline int64_t mx_scale_size(int64_t rows, int64_t columns) {
   if (rows < 0 || rows > INT32_MAX || columns < kMxTile || columns % kMxTile != 0 || columns > INT32_MAX) return -1;

@@ -5,15 +5,20 @@
 //   s = x + residual, n = s / sqrt(mean(s^2) + eps) * gamma, mx8(n)
 //
 // Bound by memory: 2 bytes each of x, the residual and the sum, and 33 / 32
-// of the result. A CTA takes a row and holds it in registers as float32, 8
-// neighbouring elements a thread and turn, so that loads and stores are wide;
-// four lanes hold a block of 32 and agree on its scale by two shuffles. The
-// norm is taken of the float32 sum, not of the bf16 that sum_out gets: the
-// rounding to 8 bits is the only one of the result. 16 elements a thread
-// (32 past 8192 columns): with 8 the joining of the warps' sums took more
-// instructions than the elements (8192 x 4096 with a residual 52.0 us, now
-// 44.5: 5.3 TB/s, 0.78 of the copy rate; 65 % of the issue slots). 1024 rows
-// 8.0 us, one 3.4: a launch, a trip to memory and two barriers.
+// of the result. A row stays in registers as float32, 8 neighbouring elements
+// a thread and turn, so that loads and stores are wide; four lanes hold a
+// block of 32 and agree on its scale by two shuffles; narrow rows share a CTA.
+// The norm is taken of the float32 sum, not of the bf16 that sum_out gets: the
+// rounding to 8 bits is the only one of the result. 16 elements a thread (32
+// past 8192 columns), in pairs, two an instruction: with 8 the joining of the
+// warps' sums took more instructions than the elements (8192 x 4096 with a
+// residual 52.0 us then).
+// Where each CTA would have more than four rows, CTAs stay and ask for their
+// next row while they have one: 8192 x 4096 40.0 us (5.9 TB/s, 0.87 of the copy
+// rate; 44.6 with a CTA a row), 2000 x 8192 23.4 (28.7). Fewer rows are dealt
+// out as CTAs end, by a kernel with room for half as many threads more an SM:
+// 3001 x 2176 8.2 (11.6 staying), 1024 x 4096 7.5, one row 3.4: a launch, a
+// trip to memory and a barrier.
 // ple_mx8_read takes two rows a thread in flight and stores whole sectors:
 // 8192 x 4096 17.2 us (5.9 TB/s; 22.0 with one and 16-byte stores).
 #include "mx8.cuh"
@@ -26,16 +31,19 @@ namespace {
 struct NormArgs {
   const ple_bf16_t *x, *residual, *gamma;
   int64_t x_stride, residual_stride, sum_stride;
+  int64_t rows;
   int C;
   float eps;
   ple_bf16_t* sum_out;
   uint8_t *codes, *scales;
 };
 
-// A value for the whole CTA, in an order that its size alone decides; `none`
-// changes nothing in a join.
+// A value for all threads of a row, in an order that the sizes alone decide;
+// `none` changes nothing in a join. All threads of a CTA come by. (Barriers of
+// their own for its rows, up to 16 of them, left an SM fewer CTAs: 3001 x 2176
+// 10.4 us against 8.2.)
 template <typename T, typename F>
-__device__ __forceinline__ T over_block(T v, T* room, T none, F join) {
+__device__ __forceinline__ T over_row(T v, T* room, T none, F join) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v = join(v, __shfl_xor_sync(0xffffffffu, v, o));
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, warps = blockDim.x / 32;
@@ -48,117 +56,146 @@ __device__ __forceinline__ T over_block(T v, T* room, T none, F join) {
   return __shfl_sync(0xffffffffu, v, 0);
 }
 
-__device__ __forceinline__ float square_sum(const float (&v)[8]) {
-  float a = 0.0f, b = 0.0f;
+// Values are held in pairs: two float32 operations an instruction.
+__device__ __forceinline__ void unpack_pairs(uint4 w, uint64_t (&v)[4]) {
+  v[0] = f2(bf_lo(w.x), bf_hi(w.x));
+  v[1] = f2(bf_lo(w.y), bf_hi(w.y));
+  v[2] = f2(bf_lo(w.z), bf_hi(w.z));
+  v[3] = f2(bf_lo(w.w), bf_hi(w.w));
+}
+__device__ __forceinline__ uint32_t pack_pair(uint64_t v) {
+  float a, b;
+  f2_split(v, a, b);
+  return pack2(a, b);
+}
+// Largest magnitude of eight values; NaN if one is.
+__device__ __forceinline__ float largest(const uint64_t (&v)[4]) {
+  float x[8];
 #pragma unroll
-  for (int i = 0; i < 8; i += 2) {
-    a = fmaf(v[i], v[i], a);
-    b = fmaf(v[i + 1], v[i + 1], b);
-  }
-  return a + b;
+  for (int i = 0; i < 4; ++i) f2_split(v[i], x[2 * i], x[2 * i + 1]);
+  return abs_max(abs_max(abs_max(x[0], x[1], x[2]), x[3], x[4]), abs_max(x[5], x[6], x[7]), 0.0f);
 }
 
-template <int kTurns>
-__global__ void __launch_bounds__(512)
+template <int kTurns, bool kMany>
+__global__ void __launch_bounds__(512, kTurns == 4 ? 1 : kMany ? 2 : 3)
 norm_mx8_kernel(const NormArgs a) {
-  __shared__ float sums[32];
-  __shared__ uint32_t tops[32];
-  __shared__ float again[32];
+  __shared__ float sums[2][16];
+  __shared__ uint32_t tops[16];
+  __shared__ float again[16];
   pdl_wait();
   pdl_trigger();
-  const int64_t row = blockIdx.x;
-  const ple_bf16_t* const x = a.x + row * a.x_stride;
-  const ple_bf16_t* const residual = a.residual == nullptr ? nullptr : a.residual + row * a.residual_stride;
-  float v[kTurns][8];
-  uint4 add[kTurns];
+  const int at = threadIdx.y * (blockDim.x / 32);  // this row's places in them
+  const bool adds = a.residual != nullptr;
+  const int64_t step = int64_t(gridDim.x) * blockDim.y;
+  uint4 next[kTurns], next_add[kTurns];
   // columns are a multiple of 128: whole groups of 16 lanes take part
+  auto ask = [&](int64_t row) {
 #pragma unroll
-  for (int t = 0; t < kTurns; ++t) {
-    const int c = (t * blockDim.x + threadIdx.x) * 8;
-    uint4 w = make_uint4(0, 0, 0, 0);
-    add[t] = w;
-    if (c < a.C) {
-      w = *reinterpret_cast<const uint4*>(x + c);
-      if (residual != nullptr) add[t] = *reinterpret_cast<const uint4*>(residual + c);
-    }
-    unpack8(w, v[t]);
-  }
-  float sum = 0.0f;
-#pragma unroll
-  for (int t = 0; t < kTurns; ++t) {
-    if (residual != nullptr) {
-      float r[8];
-      unpack8(add[t], r);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[t][i] += r[i];
-    }
-    const int c = (t * blockDim.x + threadIdx.x) * 8;
-    if (a.sum_out != nullptr && c < a.C)
-      *reinterpret_cast<uint4*>(a.sum_out + row * a.sum_stride + c) =
-          make_uint4(pack2(v[t][0], v[t][1]), pack2(v[t][2], v[t][3]), pack2(v[t][4], v[t][5]), pack2(v[t][6], v[t][7]));
-    sum += square_sum(v[t]);
-  }
-  const auto plus = [](float p, float q) { return p + q; };
-  sum = over_block(sum, sums, 0.0f, plus);
-  float by = 1.0f / sqrtf(sum / static_cast<float>(a.C) + a.eps);
-  if (!(sum < 1e38f) || (sum < 1e-28f && a.eps < 1e-18f)) {
-    // squares that leave float32: the row in units of a power of two near its
-    // largest value (infinities and NaN stay what they are)
-    uint32_t top = 0;
-#pragma unroll
-    for (int t = 0; t < kTurns; ++t)
-#pragma unroll
-      for (int i = 0; i < 8; ++i) top = max(top, abs_bits(v[t][i]));
-    top = over_block(top, tops, 0u, [](uint32_t p, uint32_t q) { return max(p, q); });
-    if (top < 0x7F800000u && top > 0) {
-      const float unit = __uint_as_float(min(max(254 - static_cast<int>(top >> 23), 1), 253) << 23);
-      sum = 0.0f;
-#pragma unroll
-      for (int t = 0; t < kTurns; ++t) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[t][i] *= unit;
-        sum += square_sum(v[t]);
+    for (int t = 0; t < kTurns; ++t) {
+      const int c = (t * blockDim.x + threadIdx.x) * 8;
+      next[t] = next_add[t] = make_uint4(0, 0, 0, 0);
+      if (c < a.C && row < a.rows) {
+        next[t] = *reinterpret_cast<const uint4*>(a.x + row * a.x_stride + c);
+        if (adds) next_add[t] = *reinterpret_cast<const uint4*>(a.residual + row * a.residual_stride + c);
       }
-      sum = over_block(sum, again, 0.0f, plus);
-      by = static_cast<float>(1.0 / sqrt(static_cast<double>(sum) / a.C + static_cast<double>(a.eps) * unit * unit));
     }
-  }
+  };
+  const int64_t begin = int64_t(blockIdx.x) * blockDim.y;
+  ask(begin + threadIdx.y);
+  for (int64_t first = begin, turn = 0; first < a.rows; first = kMany ? first + step : a.rows, turn ^= 1) {
+    const int64_t row = first + threadIdx.y;
+    const bool live = row < a.rows;  // a CTA's last rows may not exist: zeros
+    uint64_t v[kTurns][4];
+    uint64_t squares = 0;  // a pair of zeros
 #pragma unroll
-  for (int t = 0; t < kTurns; ++t) {
-    const int c = (t * blockDim.x + threadIdx.x) * 8;
-    if (a.gamma != nullptr) {
-      float g[8];
-      unpack8(c < a.C ? ldg16(a.gamma + c) : make_uint4(0, 0, 0, 0), g);
+    for (int t = 0; t < kTurns; ++t) {
+      unpack_pairs(next[t], v[t]);
+      if (adds) {
+        uint64_t r[4];
+        unpack_pairs(next_add[t], r);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[t][i] = v[t][i] * by * g[i];
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[t][i] *= by;
+        for (int i = 0; i < 4; ++i) v[t][i] = f2_add(v[t][i], r[i]);
+      }
     }
-    uint32_t top = 0;
+    if constexpr (kMany) ask(row + step);  // (what a row writes in place is its own)
 #pragma unroll
-    for (int i = 0; i < 8; ++i) top = max(top, abs_bits(v[t][i]));
-    top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-    top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-    const uint32_t b = mx_scale_byte(top);
-    const float m = mx_inverse(b);
-    // the bytes of the four blocks of a piece, in its first lane
-    uint32_t word = b << (threadIdx.x / 4 % 4 * 8);
-    word |= __shfl_xor_sync(0xffffffffu, word, 4);
-    word |= __shfl_xor_sync(0xffffffffu, word, 8);
-    if (c < a.C) {
-      *reinterpret_cast<uint2*>(a.codes + row * a.C + c) =
-          make_uint2(mx_codes4(v[t][0] * m, v[t][1] * m, v[t][2] * m, v[t][3] * m),
-                     mx_codes4(v[t][4] * m, v[t][5] * m, v[t][6] * m, v[t][7] * m));
-      if (threadIdx.x % 16 == 0) *reinterpret_cast<uint32_t*>(a.scales + mx_scale_at(row, c / kMxBlock, a.C)) = word;
+    for (int t = 0; t < kTurns; ++t) {
+      const int c = (t * blockDim.x + threadIdx.x) * 8;
+      if (a.sum_out != nullptr && c < a.C && live)
+        *reinterpret_cast<uint4*>(a.sum_out + row * a.sum_stride + c) =
+            make_uint4(pack_pair(v[t][0]), pack_pair(v[t][1]), pack_pair(v[t][2]), pack_pair(v[t][3]));
+#pragma unroll
+      for (int i = 0; i < 4; ++i) squares = f2_fma(v[t][i], v[t][i], squares);
+    }
+    const auto plus = [](float p, float q) { return p + q; };
+    const auto both = [](uint64_t p) {
+      float lo, hi;
+      f2_split(p, lo, hi);
+      return lo + hi;
+    };
+    float sum = over_row(both(squares), sums[turn] + at, 0.0f, plus);
+    float by = 1.0f / sqrtf(sum / static_cast<float>(a.C) + a.eps);
+    const bool far = live && (!(sum < 1e38f) || (sum < 1e-28f && a.eps < 1e-18f));
+    if (blockDim.y > 1 && blockDim.x > 32 ? __syncthreads_or(far) : far) {
+      // squares that leave float32: the row in units of a power of two near its
+      // largest value (infinities and NaN stay what they are, and so do other
+      // rows of the CTA)
+      uint32_t top = 0;
+#pragma unroll
+      for (int t = 0; t < kTurns; ++t) top = max(top, abs_bits(largest(v[t])));
+      top = over_row(top, tops + at, 0u, [](uint32_t p, uint32_t q) { return max(p, q); });
+      const bool mine = far && top < 0x7F800000u && top > 0;
+      const float unit = mine ? __uint_as_float(min(max(254 - static_cast<int>(top >> 23), 1), 253) << 23) : 1.0f;
+      squares = 0;
+#pragma unroll
+      for (int t = 0; t < kTurns; ++t)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          v[t][i] = f2_mul(v[t][i], f2(unit, unit));
+          squares = f2_fma(v[t][i], v[t][i], squares);
+        }
+      sum = over_row(both(squares), again + at, 0.0f, plus);
+      if (mine) by = static_cast<float>(1.0 / sqrt(static_cast<double>(sum) / a.C + static_cast<double>(a.eps) * unit * unit));
+    }
+#pragma unroll
+    for (int t = 0; t < kTurns; ++t) {
+      const int c = (t * blockDim.x + threadIdx.x) * 8;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[t][i] = f2_mul(v[t][i], f2(by, by));
+      if (a.gamma != nullptr) {
+        uint64_t g[4];
+        unpack_pairs(c < a.C ? ldg16(a.gamma + c) : make_uint4(0, 0, 0, 0), g);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[t][i] = f2_mul(v[t][i], g[i]);
+      }
+      uint32_t top = abs_bits(largest(v[t]));
+      top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      const uint32_t b = mx_scale_byte(top);
+      const float m = mx_inverse(b);
+      // the bytes of the four blocks of a piece, in its first lane
+      uint32_t word = b << (threadIdx.x / 4 % 4 * 8);
+      word |= __shfl_xor_sync(0xffffffffu, word, 4);
+      word |= __shfl_xor_sync(0xffffffffu, word, 8);
+      if (c < a.C && live) {
+        float y[8];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) f2_split(f2_mul(v[t][i], f2(m, m)), y[2 * i], y[2 * i + 1]);
+        *reinterpret_cast<uint2*>(a.codes + row * a.C + c) =
+            make_uint2(mx_codes4(y[0], y[1], y[2], y[3]), mx_codes4(y[4], y[5], y[6], y[7]));
+        if (threadIdx.x % 16 == 0) *reinterpret_cast<uint32_t*>(a.scales + mx_scale_at(row, c / kMxBlock, a.C)) = word;
+      }
     }
   }
 }
 
 template <int kTurns>
-cudaError_t launch_norm(const NormArgs& a, int64_t rows, cudaStream_t stream) {
-  const int threads = ((a.C / 8 + kTurns - 1) / kTurns + 31) / 32 * 32;
-  return launch_kernel(norm_mx8_kernel<kTurns>, dim3(static_cast<unsigned>(rows)), dim3(threads), 0, stream, 1, a);
+cudaError_t launch_norm(const NormArgs& a, cudaStream_t stream) {
+  const int threads = ((a.C / 8 + kTurns - 1) / kTurns + 31) / 32 * 32, at_once = threads <= 256 ? 256 / threads : 1;
+  const int64_t need = (a.rows + at_once - 1) / at_once, most = int64_t(num_sms()) * (kTurns == 2 ? 1024 : 512) / (threads * at_once);
+  const bool many = need > 4 * most;
+  return launch_kernel(many ? norm_mx8_kernel<kTurns, true> : norm_mx8_kernel<kTurns, false>,
+                       dim3(static_cast<unsigned>(many ? most : need)), dim3(threads, at_once), 0, stream, 1, a);
 }
 
 // 16 codes a thread and row, of two rows at a time: a CTA takes 4096 columns.
@@ -242,8 +279,8 @@ PLE_EXPORT ple_status ple_norm_mx8(const ple_bf16_t* x, int64_t x_stride, const 
   }
   if (sum_out != nullptr && num_tokens > 1 && (sum_stride < 0 ? -sum_stride : sum_stride) < hidden)
     return fail(PLE_ERR_INVALID_ARG, "%s: rows of sum_out overlap", name);
-  const NormArgs a{x, residual, gamma, x_stride, residual_stride, sum_stride, hidden, eps, sum_out, codes, scales};
-  return check_cuda(hidden <= 8192 ? launch_norm<2>(a, num_tokens, stream) : launch_norm<4>(a, num_tokens, stream), name);
+  const NormArgs a{x, residual, gamma, x_stride, residual_stride, sum_stride, num_tokens, hidden, eps, sum_out, codes, scales};
+  return check_cuda(hidden > 8192 ? launch_norm<4>(a, stream) : launch_norm<2>(a, stream), name);
 }
 
 PLE_EXPORT ple_status ple_mx8_read(const uint8_t* codes, const uint8_t* scales, int64_t rows, int32_t columns,

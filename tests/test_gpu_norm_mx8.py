@@ -88,6 +88,30 @@ def test_rows_of_any_size(exponent, eps):
     check(x, None, g, run(x, None, g, eps), float(np.float32(eps)))
 
 
+def test_rows_of_any_size_side_by_side():
+    # narrow rows share a CTA, and only some of them leave float32
+    for c in (128, 512, 640, 1408):
+        x = rows(23, c)
+        x[1::3] *= 2.0 ** 100
+        x[2::7] *= 2.0 ** -110
+        x[5] = 0
+        g = rows(1, c, 2)[0]
+        eps = float(np.float32(1e-30))
+        check(x, None, g, run(x, None, g, eps), eps)
+
+
+def test_many_narrow_rows():
+    # CTAs that stay: more than four rows each, in place, odd in number
+    t, c = 20_011, 384
+    x, r = rows(t, c), rows(t, c, 1)
+    want = run(x, r, None)
+    check(x, r, None, want)
+    d = x.cuda()
+    codes, scales = room(t, c)
+    ple.ple_norm_mx8(d, None, codes, scales, residual=r.cuda(), sum_out=d)
+    assert torch.equal(codes, want[0]) and torch.equal(scales, want[1]) and torch.equal(d, want[2])
+
+
 def test_rows_that_are_not_numbers():
     t, c = 6, 384
     x = rows(t, c)

@@ -12,8 +12,8 @@ namespace ple {
 // Instruction descriptor: both operands e4m3 and K-major, scales powers of
 // two (bit 23); the low bits of the two block numbers choose the scale's byte
 // in its column (operand B's at 4, A's at 29).
-constexpr uint32_t mx_idesc(int m, int n) { return (uint32_t(n >> 3) << 17) | (1u << 23) | (uint32_t(m >> 4) << 24); }
-constexpr uint32_t mx_block(int k) { return (uint32_t(k) << 4) | (uint32_t(k) << 29); }
+__host__ __device__ constexpr uint32_t mx_idesc(int m, int n) { return (uint32_t(n >> 3) << 17) | (1u << 23) | (uint32_t(m >> 4) << 24); }
+__host__ __device__ constexpr uint32_t mx_block(int k) { return (uint32_t(k) << 4) | (uint32_t(k) << 29); }
 
 // Descriptor of a piece of scales in shared memory: 32 rows of 16 bytes, no
 // swizzle, groups of 8 rows 128 bytes apart.

@@ -11,7 +11,7 @@
 // 16384: 657 us (3.35). For few tokens a CTA takes 128 rows of W against all of
 // them, its columns shared out in a cluster: bound by reading W and some 4.5 us
 // of start and end. One token, gated 4096 -> 16384: 24.2 us (5.7 TB/s), 16384 ->
-// 4096: 14.8 (4.7); 203 tokens: 23.3.
+// 4096: 14.8 (4.7); 203 tokens: 22.7.
 #include "mx8_tensor.cuh"
 
 #include <algorithm>
@@ -509,9 +509,8 @@ struct Few {
   static constexpr int kXPieces = kTokens > 128 ? 2 : 1;
   static constexpr int kResident = kTokens <= 64 ? 2 : 1;        // CTAs an SM
   static constexpr int kMaxParts = kResident == 2 ? 8 : 4;       // CTAs that share the columns
-  static constexpr int kStep = 1;                                // atoms of a stage
-  static constexpr int kCodes = kStep * (kSides * kAtom + kTokens * 128);  // bytes of a stage
-  static constexpr int kScales = kStep * (kSides + kXPieces) * kMxPiece;
+  static constexpr int kCodes = kSides * kAtom + kTokens * 128;  // bytes of a stage: an atom
+  static constexpr int kScales = (kSides + kXPieces) * kMxPiece;
   static constexpr int kBudget = kResident == 2 ? 110 << 10 : 220 << 10;
   static constexpr int kFit = kBudget / (kCodes + kScales);
   static constexpr int kStages = kFit > 8 ? 8 : kFit;
@@ -521,8 +520,7 @@ struct Few {
   static constexpr int kAsk = kTokens < 32 ? 16 : 32;            // tokens a thread takes out at once
   static constexpr int kBatch = 16 / (kMaxParts * kSides);       // tokens a warp joins at once
   static constexpr int kCols = kSides * kTokens;                 // of sums
-  static constexpr int kAtomCols = 4 * (kSides + kXPieces);      // of scales
-  static constexpr int kStageCols = kStep * kAtomCols;
+  static constexpr int kStageCols = 4 * (kSides + kXPieces);     // of scales
   static constexpr int kNeed = kCols + kStages * kStageCols;
   static constexpr int kTmem = kNeed <= 64 ? 64 : kNeed <= 128 ? 128 : kNeed <= 256 ? 256 : 512;
   static_assert(kNeed <= 512 / kResident && kTmem <= 512 / kResident, "tensor memory");
@@ -533,7 +531,7 @@ struct Few {
 template <bool kGated, int kTokens>
 __global__ void __launch_bounds__(kFewThreads, Few<kGated, kTokens>::kResident)
 product_few_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_w,
-                   const ProductArgs a, int parts, int32_t* dev_err) {
+                   const ProductArgs a, int parts, int wide, int32_t* dev_err) {
   using L = Few<kGated, kTokens>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* const smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -571,7 +569,7 @@ product_few_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_const
     // W into L2 while the kernel before this one ends: nothing is read of it
     prefetch_map(&map_w);
     prefetch_map(&map_x);
-    for (int k = first; k < last && k < first + L::kStages * L::kStep; k += L::kStep)
+    for (int k = first; k < last && k < first + L::kStages; ++k)
       for (int i = 0; i < L::kSides; ++i) prefetch_atoms(&map_w, k, i * a.N + n0);
   }
   pdl_wait();
@@ -587,21 +585,20 @@ product_few_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_const
       for (int i = 0; i < L::kSides; ++i) ws[i] = a.w_scales + (int64_t(i) * a.N + n0) / 128 * atoms * kMxPiece;
       // the second 128 tokens' scales, where there are such tokens
       const bool more = L::kXPieces == 2 && tokens > 128;
-      for (int k = first; k < last; k += L::kStep, ring.next()) {
+      for (int k = first; k < last; ++k, ring.next()) {
         const int s = ring.at;
         if (!(ok = mbar_wait(free(s), ring.phase ^ 1u, abort_flag))) break;
-        const uint32_t bytes = static_cast<uint32_t>(min(L::kStep, last - k)) * kMxPiece;  // of scales; codes come whole
-        mbar_arrive_expect_tx(full(s), L::kCodes + bytes * (L::kSides + (more ? 2 : 1)));
+        mbar_arrive_expect_tx(full(s), L::kSides * kAtom + wide * 128 + kMxPiece * (L::kSides + (more ? 2 : 1)));
         ring.arm();
         const uint32_t to = base + s * L::kCodes, scales = base + L::kAtScales + s * L::kScales;
         for (int i = 0; i < L::kSides; ++i) {
-          tma_load_atoms(to + i * L::kStep * kAtom, &map_w, full(s), k, i * a.N + n0);
-          bulk_copy_g2s(scales + i * L::kStep * kMxPiece, ws[i] + int64_t(k) * kMxPiece, bytes, full(s));
+          tma_load_atoms(to + i * kAtom, &map_w, full(s), k, i * a.N + n0);
+          bulk_copy_g2s(scales + i * kMxPiece, ws[i] + int64_t(k) * kMxPiece, kMxPiece, full(s));
         }
-        tma_load_atoms(to + L::kSides * L::kStep * kAtom, &map_x, full(s), k, static_cast<int>(t0));
-        bulk_copy_g2s(scales + L::kSides * L::kStep * kMxPiece, xs + int64_t(k) * kMxPiece, bytes, full(s));
+        tma_load_atoms(to + L::kSides * kAtom, &map_x, full(s), k, static_cast<int>(t0));
+        bulk_copy_g2s(scales + L::kSides * kMxPiece, xs + int64_t(k) * kMxPiece, kMxPiece, full(s));
         if (more)
-          bulk_copy_g2s(scales + (L::kSides + 1) * L::kStep * kMxPiece, xs + int64_t(atoms + k) * kMxPiece, bytes, full(s));
+          bulk_copy_g2s(scales + (L::kSides + 1) * kMxPiece, xs + int64_t(atoms + k) * kMxPiece, kMxPiece, full(s));
       }
       if (!ok) { *abort_flag = 1; set_dev_err(dev_err, PLE_DEVERR_TIMEOUT); }
       for (int i = 0; i < L::kStages; ++i)
@@ -613,32 +610,22 @@ product_few_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_const
     const uint32_t sums = __shfl_sync(0xffffffffu, tmem, 0);
     Ring<L::kStages> ring;
     bool ok = true;
-    for (int k = first; k < last; k += L::kStep, ring.next()) {
+    for (int k = first; k < last; ++k, ring.next()) {
       const int s = ring.at;
       if (!(ok = __all_sync(0xffffffffu, wait_for(full(s), ring.phase, abort_flag)))) break;
       fence_after();
       if (elected()) {
-        const uint32_t from = base + L::kAtScales + s * L::kScales;
+        const uint32_t from = base + L::kAtScales + s * L::kScales, scales = sums + L::kCols + s * L::kStageCols;
 #pragma unroll
-        for (int j = 0; j < L::kStep; ++j) {
-          if (k + j >= last) break;
-          const uint32_t scales = sums + L::kCols + s * L::kStageCols + j * L::kAtomCols;
+        for (int i = 0; i < L::kSides + L::kXPieces; ++i) scales_to_tmem<1>(scales + 4 * i, from + i * kMxPiece);
+        const uint64_t x = codes_operand(base + s * L::kCodes + L::kSides * kAtom);
 #pragma unroll
-          for (int i = 0; i < L::kSides + L::kXPieces; ++i) scales_to_tmem<1>(scales + 4 * i, from + (i * L::kStep + j) * kMxPiece);
-        }
+        for (int i = 0; i < L::kSides; ++i) {
+          const uint64_t w = codes_operand(base + s * L::kCodes + i * kAtom);
 #pragma unroll
-        for (int j = 0; j < L::kStep; ++j) {
-          if (k + j >= last) break;
-          const uint32_t scales = sums + L::kCols + s * L::kStageCols + j * L::kAtomCols;
-          const uint64_t x = codes_operand(base + s * L::kCodes + L::kSides * L::kStep * kAtom + j * kTokens * 128);
-#pragma unroll
-          for (int i = 0; i < L::kSides; ++i) {
-            const uint64_t w = codes_operand(base + s * L::kCodes + (i * L::kStep + j) * kAtom);
-#pragma unroll
-            for (int b = 0; b < 4; ++b)
-              mma_mx8<1>(sums + i * kTokens, w + 2 * b, x + 2 * b, mx_idesc(128, kTokens) | mx_block(b), scales + 4 * i,
-                         scales + 4 * L::kSides, k + j > first || b > 0);
-          }
+          for (int b = 0; b < 4; ++b)
+            mma_mx8<1>(sums + i * kTokens, w + 2 * b, x + 2 * b, mx_idesc(128, wide) | mx_block(b), scales + 4 * i,
+                       scales + 4 * L::kSides, k > first || b > 0);
         }
         mma_commit(free(s));
       }
@@ -758,8 +745,11 @@ template <bool kGated, int kTokens>
 ple_status launch_few(const ProductArgs& a, int32_t* dev_err, cudaStream_t stream, const char* name) {
   using L = Few<kGated, kTokens>;
   CUtensorMap x, w;
-  ple_status s = mx_codes_map(&x, a.x, a.T, a.E, kTokens, L::kStep, name);
-  if (s == PLE_OK) s = mx_codes_map(&w, a.w, kGated ? 2 * int64_t(a.N) : a.N, a.E, 128, L::kStep, name);
+  // a tile's tokens, in the products' steps of 16: a tile of 256 that holds 130
+  // is 144 wide (8192 x 4096, 14.4 us against 15.1)
+  const int wide = static_cast<int>(std::min<int64_t>((a.T + 15) / 16 * 16, kTokens));
+  ple_status s = mx_codes_map(&x, a.x, a.T, a.E, wide, 1, name);
+  if (s == PLE_OK) s = mx_codes_map(&w, a.w, kGated ? 2 * int64_t(a.N) : a.N, a.E, 128, 1, name);
   if (s != PLE_OK) return s;
   const auto kernel = product_few_kernel<kGated, kTokens>;
   const cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kSmem);
@@ -768,7 +758,7 @@ ple_status launch_few(const ProductArgs& a, int32_t* dev_err, cudaStream_t strea
   const int parts = parts_of<L>(int64_t(tiles) * blocks, a.E / 128);
   const dim3 grid(static_cast<unsigned>(tiles * parts), static_cast<unsigned>(blocks));
   return check_cuda(launch_kernel(kernel, grid, dim3(kFewThreads), L::kSmem, stream, static_cast<unsigned>(parts), x, w, a,
-                                  parts, dev_err), name);
+                                  parts, wide, dev_err), name);
 }
 
 // What a launch takes, in 10 ns, from measurements: by pairs of CTAs a stage

@@ -879,10 +879,12 @@ ple_status ple_gated_mx8(const uint8_t* x, const uint8_t* x_scales, int64_t num_
  * sizes decide, rounded once.
  *   x, x_scales  mx8 [num_tokens][in_dim].
  *   w, w_scales  mx8 [out_dim][in_dim].
- *   residual     bf16 rows of out_dim, residual_stride elements apart, or
- *                NULL; may be out itself (residual_stride = out_dim). Any
- *                other overlap with out is PLE_ERR_INVALID_ARG.
+ *   residual     bf16 rows of out_dim, residual_stride elements apart (0: one
+ *                row for all tokens), or NULL; may be out itself
+ *                (residual_stride = out_dim). Any other overlap with out is
+ *                PLE_ERR_INVALID_ARG.
  *   out          [num_tokens][out_dim] bf16, no part of it an operand's.
+ * out_dim is any; residual and out need no more than bf16's own alignment.
  */
 ple_status ple_proj_mx8(const uint8_t* x, const uint8_t* x_scales, int64_t num_tokens,
                         int32_t in_dim, const uint8_t* w, const uint8_t* w_scales,

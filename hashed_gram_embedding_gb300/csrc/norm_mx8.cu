@@ -76,7 +76,7 @@ __device__ __forceinline__ float largest(const uint64_t (&v)[4]) {
   return abs_max(abs_max(abs_max(x[0], x[1], x[2]), x[3], x[4]), abs_max(x[5], x[6], x[7]), 0.0f);
 }
 
-template <int kTurns, bool kMany>
+template <int kTurns, bool kMany, bool kAdds>
 __global__ void __launch_bounds__(512, kTurns == 4 ? 1 : kMany ? 2 : 3)
 norm_mx8_kernel(const NormArgs a) {
   __shared__ float sums[2][16];
@@ -85,24 +85,19 @@ norm_mx8_kernel(const NormArgs a) {
   pdl_wait();
   pdl_trigger();
   const int at = threadIdx.y * (blockDim.x / 32);  // this row's places in them
-  const bool adds = a.residual != nullptr;
   const int64_t step = int64_t(gridDim.x) * blockDim.y;
-  uint4 next[kTurns], next_add[kTurns];
   // columns are a multiple of 128: whole groups of 16 lanes take part
-  auto ask = [&](int64_t row) {
+  auto ask = [&](int64_t row, const ple_bf16_t* from, int64_t stride, uint4 (&to)[kTurns]) {
 #pragma unroll
     for (int t = 0; t < kTurns; ++t) {
       const int c = (t * blockDim.x + threadIdx.x) * 8;
-      next[t] = next_add[t] = make_uint4(0, 0, 0, 0);
-      if (c < a.C && row < a.rows) {
-        next[t] = *reinterpret_cast<const uint4*>(a.x + row * a.x_stride + c);
-        if (adds) next_add[t] = *reinterpret_cast<const uint4*>(a.residual + row * a.residual_stride + c);
-      }
+      to[t] = make_uint4(0, 0, 0, 0);
+      if (c < a.C && row < a.rows) to[t] = *reinterpret_cast<const uint4*>(from + row * stride + c);
     }
   };
-  const int64_t begin = int64_t(blockIdx.x) * blockDim.y;
-  ask(begin + threadIdx.y);
-  for (int64_t first = begin, turn = 0; first < a.rows; first = kMany ? first + step : a.rows, turn ^= 1) {
+  // One row for each threadIdx.y, from `first` on, out of x (and the residual);
+  // `ahead` rows on the next ones are asked for in their place.
+  auto norm = [&](int64_t first, int turn, uint4 (&next)[kTurns], uint4 (&next_add)[kTurns], int64_t ahead) {
     const int64_t row = first + threadIdx.y;
     const bool live = row < a.rows;  // a CTA's last rows may not exist: zeros
     uint64_t v[kTurns][4];
@@ -110,14 +105,17 @@ norm_mx8_kernel(const NormArgs a) {
 #pragma unroll
     for (int t = 0; t < kTurns; ++t) {
       unpack_pairs(next[t], v[t]);
-      if (adds) {
+      if constexpr (kAdds) {
         uint64_t r[4];
         unpack_pairs(next_add[t], r);
 #pragma unroll
         for (int i = 0; i < 4; ++i) v[t][i] = f2_add(v[t][i], r[i]);
       }
     }
-    if constexpr (kMany) ask(row + step);  // (what a row writes in place is its own)
+    if constexpr (kMany) {  // (what a row writes in place is its own)
+      ask(row + ahead, a.x, a.x_stride, next);
+      if constexpr (kAdds) ask(row + ahead, a.residual, a.residual_stride, next_add);
+    }
 #pragma unroll
     for (int t = 0; t < kTurns; ++t) {
       const int c = (t * blockDim.x + threadIdx.x) * 8;
@@ -186,6 +184,22 @@ norm_mx8_kernel(const NormArgs a) {
         if (threadIdx.x % 16 == 0) *reinterpret_cast<uint32_t*>(a.scales + mx_scale_at(row, c / kMxBlock, a.C)) = word;
       }
     }
+  };
+  const int64_t begin = int64_t(blockIdx.x) * blockDim.y;
+  uint4 one[kTurns], two[kTurns];
+  ask(begin + threadIdx.y, a.x, a.x_stride, one);
+  if constexpr (kAdds) {
+    ask(begin + threadIdx.y, a.residual, a.residual_stride, two);
+    int turn = 0;
+    for (int64_t first = begin; first < a.rows; first = kMany ? first + step : a.rows, turn ^= 1) norm(first, turn, one, two, step);
+  } else if constexpr (kMany) {  // half the bytes a row: two rows ahead
+    ask(begin + step + threadIdx.y, a.x, a.x_stride, two);
+    for (int64_t first = begin; first < a.rows; first += 2 * step) {
+      norm(first, 0, one, one, 2 * step);
+      if (first + step < a.rows) norm(first + step, 1, two, two, 2 * step);
+    }
+  } else {
+    norm(begin, 0, one, one, 0);
   }
 }
 
@@ -194,7 +208,9 @@ cudaError_t launch_norm(const NormArgs& a, cudaStream_t stream) {
   const int threads = ((a.C / 8 + kTurns - 1) / kTurns + 31) / 32 * 32, at_once = threads <= 256 ? 256 / threads : 1;
   const int64_t need = (a.rows + at_once - 1) / at_once, most = int64_t(num_sms()) * (kTurns == 2 ? 1024 : 512) / (threads * at_once);
   const bool many = need > 4 * most;
-  return launch_kernel(many ? norm_mx8_kernel<kTurns, true> : norm_mx8_kernel<kTurns, false>,
+  const bool adds = a.residual != nullptr;
+  return launch_kernel(many ? adds ? norm_mx8_kernel<kTurns, true, true> : norm_mx8_kernel<kTurns, true, false>
+                            : adds ? norm_mx8_kernel<kTurns, false, true> : norm_mx8_kernel<kTurns, false, false>,
                        dim3(static_cast<unsigned>(many ? most : need)), dim3(threads, at_once), 0, stream, 1, a);
 }
 

@@ -14,10 +14,10 @@
 // warps' sums took more instructions than the elements (8192 x 4096 with a
 // residual 52.0 us then).
 // Where each CTA would have more than four rows, CTAs stay and ask for their
-// next row while they have one: 8192 x 4096 40.0 us (5.9 TB/s, 0.87 of the copy
-// rate; 44.6 with a CTA a row), 2000 x 8192 23.4 (28.7). Fewer rows are dealt
+// next row while they have one: 8192 x 4096 38.9 us (6.1 TB/s, 0.89 of the copy
+// rate; 44.6 with a CTA a row), 2000 x 8192 22.6 (28.7). Fewer rows are dealt
 // out as CTAs end, by a kernel with room for half as many threads more an SM:
-// 3001 x 2176 8.2 (11.6 staying), 1024 x 4096 7.5, one row 3.4: a launch, a
+// 3001 x 2176 7.6 (11.6 staying), 1024 x 4096 7.4, one row 3.4: a launch, a
 // trip to memory and a barrier.
 // ple_mx8_read takes two rows a thread in flight and stores whole sectors:
 // 8192 x 4096 17.2 us (5.9 TB/s; 22.0 with one and 16-byte stores).
@@ -41,7 +41,7 @@ struct NormArgs {
 // A value for all threads of a row, in an order that the sizes alone decide;
 // `none` changes nothing in a join. All threads of a CTA come by. (Barriers of
 // their own for its rows, up to 16 of them, left an SM fewer CTAs: 3001 x 2176
-// 10.4 us against 8.2.)
+// 10.4 us against 7.6.)
 template <typename T, typename F>
 __device__ __forceinline__ T over_row(T v, T* room, T none, F join) {
 #pragma unroll
@@ -86,15 +86,21 @@ norm_mx8_kernel(const NormArgs a) {
   pdl_trigger();
   const int at = threadIdx.y * (blockDim.x / 32);  // this row's places in them
   const int64_t step = int64_t(gridDim.x) * blockDim.y;
-  // columns are a multiple of 128: whole groups of 16 lanes take part
+  // Columns are a multiple of 128: whole groups of 16 lanes take part. In
+  // every turn but the last they all do (the last may end inside a warp).
+  const int c0 = threadIdx.x * 8, turn_columns = blockDim.x * 8;
+  const bool all = c0 + (kTurns - 1) * turn_columns < a.C;
+  auto in = [&](int t) { return t < kTurns - 1 ? c0 + t * turn_columns < a.C : all; };
   auto ask = [&](int64_t row, const ple_bf16_t* from, int64_t stride, uint4 (&to)[kTurns]) {
+    const ple_bf16_t* const at_row = from + row * stride + c0;
+    const bool there = row < a.rows;
 #pragma unroll
     for (int t = 0; t < kTurns; ++t) {
-      const int c = (t * blockDim.x + threadIdx.x) * 8;
       to[t] = make_uint4(0, 0, 0, 0);
-      if (c < a.C && row < a.rows) to[t] = *reinterpret_cast<const uint4*>(from + row * stride + c);
+      if (there && in(t)) to[t] = *reinterpret_cast<const uint4*>(at_row + t * turn_columns);
     }
   };
+  const float inv_c = 1.0f / static_cast<float>(a.C);
   // One row for each threadIdx.y, from `first` on, out of x (and the residual);
   // `ahead` rows on the next ones are asked for in their place.
   auto norm = [&](int64_t first, int turn, uint4 (&next)[kTurns], uint4 (&next_add)[kTurns], int64_t ahead) {
@@ -116,11 +122,12 @@ norm_mx8_kernel(const NormArgs a) {
       ask(row + ahead, a.x, a.x_stride, next);
       if constexpr (kAdds) ask(row + ahead, a.residual, a.residual_stride, next_add);
     }
+    ple_bf16_t* const sum_row = a.sum_out + row * a.sum_stride + c0;
+    const bool stores = a.sum_out != nullptr && live;
 #pragma unroll
     for (int t = 0; t < kTurns; ++t) {
-      const int c = (t * blockDim.x + threadIdx.x) * 8;
-      if (a.sum_out != nullptr && c < a.C && live)
-        *reinterpret_cast<uint4*>(a.sum_out + row * a.sum_stride + c) =
+      if (stores && in(t))
+        *reinterpret_cast<uint4*>(sum_row + t * turn_columns) =
             make_uint4(pack_pair(v[t][0]), pack_pair(v[t][1]), pack_pair(v[t][2]), pack_pair(v[t][3]));
 #pragma unroll
       for (int i = 0; i < 4; ++i) squares = f2_fma(v[t][i], v[t][i], squares);
@@ -132,7 +139,10 @@ norm_mx8_kernel(const NormArgs a) {
       return lo + hi;
     };
     float sum = over_row(both(squares), sums[turn] + at, 0.0f, plus);
-    float by = 1.0f / sqrtf(sum / static_cast<float>(a.C) + a.eps);
+    const float mean = fmaf(sum, inv_c, a.eps);
+    float by = rsqrtf(mean);
+    // a step of Newton's: the quotient's own rounding is left (an infinite sum makes zeros, and keeps them)
+    if (by > 0.0f) by = by * fmaf(-0.5f * mean * by, by, 1.5f);
     const bool far = live && (!(sum < 1e38f) || (sum < 1e-28f && a.eps < 1e-18f));
     if (blockDim.y > 1 && blockDim.x > 32 ? __syncthreads_or(far) : far) {
       // squares that leave float32: the row in units of a power of two near its
@@ -155,14 +165,15 @@ norm_mx8_kernel(const NormArgs a) {
       sum = over_row(both(squares), again + at, 0.0f, plus);
       if (mine) by = static_cast<float>(1.0 / sqrt(static_cast<double>(sum) / a.C + static_cast<double>(a.eps) * unit * unit));
     }
+    uint8_t* const code_row = a.codes + row * a.C + c0;
+    uint8_t* const scale_row = a.scales + mx_scale_at(row, c0 / kMxBlock, a.C);  // a turn is so many pieces on
 #pragma unroll
     for (int t = 0; t < kTurns; ++t) {
-      const int c = (t * blockDim.x + threadIdx.x) * 8;
 #pragma unroll
       for (int i = 0; i < 4; ++i) v[t][i] = f2_mul(v[t][i], f2(by, by));
       if (a.gamma != nullptr) {
         uint64_t g[4];
-        unpack_pairs(c < a.C ? ldg16(a.gamma + c) : make_uint4(0, 0, 0, 0), g);
+        unpack_pairs(in(t) ? ldg16(a.gamma + c0 + t * turn_columns) : make_uint4(0, 0, 0, 0), g);
 #pragma unroll
         for (int i = 0; i < 4; ++i) v[t][i] = f2_mul(v[t][i], g[i]);
       }
@@ -175,13 +186,13 @@ norm_mx8_kernel(const NormArgs a) {
       uint32_t word = b << (threadIdx.x / 4 % 4 * 8);
       word |= __shfl_xor_sync(0xffffffffu, word, 4);
       word |= __shfl_xor_sync(0xffffffffu, word, 8);
-      if (c < a.C && live) {
+      if (live && in(t)) {
         float y[8];
 #pragma unroll
         for (int i = 0; i < 4; ++i) f2_split(f2_mul(v[t][i], f2(m, m)), y[2 * i], y[2 * i + 1]);
-        *reinterpret_cast<uint2*>(a.codes + row * a.C + c) =
+        *reinterpret_cast<uint2*>(code_row + t * turn_columns) =
             make_uint2(mx_codes4(y[0], y[1], y[2], y[3]), mx_codes4(y[4], y[5], y[6], y[7]));
-        if (threadIdx.x % 16 == 0) *reinterpret_cast<uint32_t*>(a.scales + mx_scale_at(row, c / kMxBlock, a.C)) = word;
+        if (threadIdx.x % 16 == 0) *reinterpret_cast<uint32_t*>(scale_row + t * turn_columns / kMxTile * kMxPiece) = word;
       }
     }
   };

@@ -124,6 +124,7 @@ def test_rows_that_are_not_numbers():
     v = f64(value)
     assert np.isnan(v[1]).all() and (v[2] == 0).all()
     assert np.isnan(v[3, 192:224]).all()  # inf / inf in its block
+    assert (v[3, :192] == 0).all() and (v[3, 224:] == 0).all()  # and x / inf beside it
     # rows beside them are as without them
     y = rows(t, c)
     again = run(y, None, None)

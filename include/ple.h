@@ -863,7 +863,9 @@ typedef enum { PLE_SILU = 0, PLE_GELU = 1 } ple_activation;
  * ple_gated_mx8 -- the first half of a gated feed-forward block,
  *   h = act(x Wg^T) * (x Wu^T), (codes, scales) = mx8(h).
  * Float32 sums, in an order that the sizes decide (num_tokens among them);
- * h is not rounded before it is quantised. Gates below about -87 give zeros.
+ * the activation by float32 functions (zeros where exp(-|x|) leaves float32:
+ * gates below about -104, of gelu below -10.7);
+ * h is not rounded before it is quantised.
  *   x, x_scales  mx8 [num_tokens][hidden].
  *   w, w_scales  mx8 [2 * inner][hidden]: Wg's rows, then Wu's.
  *   inner        a multiple of 128 (else PLE_ERR_UNSUPPORTED).

@@ -116,6 +116,21 @@ __device__ __forceinline__ float4 read_cluster4(uint32_t at, uint32_t rank) {
   return v;
 }
 
+// Limit of a wait for sums, a step of the products that they come from: the
+// waits of the warps that bring and issue these have it step by step.
+#ifndef PLE_SUMS_WAIT_NS
+#define PLE_SUMS_WAIT_NS kWaitLimitNs
+#endif
+// mbar_wait for the end of `steps` steps of products.
+__device__ __noinline__ inline bool sums_wait(uint32_t bar, uint32_t parity, const volatile int* abort_flag, int steps) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = global_ns(), limit = uint64_t(PLE_SUMS_WAIT_NS) * steps;
+  while (!*abort_flag && global_ns() - t0 < limit)
+    for (int i = 0; i < 32; ++i)
+      if (mbar_try_wait(bar, parity)) return true;
+  return false;
+}
+
 __device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
   asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
 }

@@ -340,11 +340,12 @@ product_pair_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_cons
         }
       }
       if (!ok && lane == 0) { *abort_flag = 1; set_dev_err(dev_err, PLE_DEVERR_TIMEOUT); }
+      __syncwarp();
       // however the loop ended, no product reads or writes after this
       if (elected())
         asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(done) : "memory");
       __syncwarp();
-      wait_for(done, 0, nullptr);
+      if (!wait_for(done, 0, nullptr) && lane == 0) { *abort_flag = 1; set_dev_err(dev_err, PLE_DEVERR_TIMEOUT); }
     }
     __syncwarp();
   } else if (warp >= 2) {
@@ -375,7 +376,7 @@ product_pair_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_cons
           }
         }
       }
-      if (!__all_sync(0xffffffffu, mbar_wait(sums_full, tile_phase, abort_flag))) {
+      if (!__all_sync(0xffffffffu, sums_wait(sums_full, tile_phase, abort_flag, stages))) {
         if (lane == 0) { *abort_flag = 1; set_dev_err(dev_err, PLE_DEVERR_TIMEOUT); }
         break;
       }
@@ -648,14 +649,17 @@ product_few_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_const
       }
       __syncwarp();
     }
+    // Before the commit: the sums' warps see that these are none.
     if (!ok && lane == 0) { *abort_flag = 1; set_dev_err(dev_err, PLE_DEVERR_TIMEOUT); }
+    __syncwarp();
     // however the loop ended, no product reads or writes after this
     if (elected()) mma_commit(sums_full);
     __syncwarp();
-    wait_for(sums_full, 0, nullptr);
+    if (!wait_for(sums_full, 0, nullptr) && lane == 0) { *abort_flag = 1; set_dev_err(dev_err, PLE_DEVERR_TIMEOUT); }
   } else if (warp < 6) {
     // ---------------- sums, where the codes were: [token][side][row] ----------------
-    const bool ok = __all_sync(0xffffffffu, mbar_wait(sums_full, 0, nullptr)) && *abort_flag == 0;
+    const bool ok = __all_sync(0xffffffffu, sums_wait(sums_full, 0, abort_flag, last - first) && *abort_flag == 0);
+    if (!ok && lane == 0) { *abort_flag = 1; set_dev_err(dev_err, PLE_DEVERR_TIMEOUT); }
     fence_after();
     if (ok) {
       const int row = (warp & 3) * 32 + lane;

@@ -67,6 +67,9 @@ class PLEFeedForward:
 
         self.normed, self.gated = room(self.hidden), room(self.inner)
         self.sum = torch.empty((self.max_tokens, self.hidden), dtype=torch.bfloat16, device=device)
+        # torch may give memory that this stream's earlier work still uses, and
+        # a first step may be on any stream
+        torch.cuda.current_stream(device).synchronize()
 
     def forward(self, hidden, delta=None, dev_err=None, stream=None, out=None):
         """hidden [T, C] bf16, delta [T, C] bf16 or None (the attention block's

@@ -21,7 +21,7 @@ def pack_mx8(weight):
     N, E = weight.shape
     if E % 128 != 0:
         raise ValueError(f"{E} columns are not a multiple of 128")
-    w = weight.to(torch.float32).view(N, E // 32, 32)
+    w = weight.to(torch.float32).contiguous().view(N, E // 32, 32)  # codes lie as w does
     top = w.abs().amax(2)
     part, power = torch.frexp(top)  # top = part * 2^power, part in [0.5, 1); 448 = 0.875 * 2^9
     byte = torch.where(top > 0, (power + (part > 0.875) + 118).clamp(min=0), 0)

@@ -20,7 +20,7 @@ def pack_w4(weight, group=128):
     N, E = weight.shape
     if E % group != 0:
         raise ValueError(f"{E} columns are not a multiple of the group {group}")
-    w = weight.to(torch.float32).view(N, E // group, group)
+    w = weight.detach().to(torch.float32).contiguous().view(N, E // group, group)  # codes lie as w does
     low, high = w.amin(2).clamp(max=0.0), w.amax(2).clamp(min=0.0)
     scales = ((high - low) / 15).clamp(min=2.0 ** -126).to(torch.bfloat16)  # as the kernel will use them
     step = scales.to(torch.float32)

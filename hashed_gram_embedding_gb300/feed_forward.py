@@ -52,7 +52,7 @@ class PLEFeedForward:
         self.w_gate_up, self.w_down, self.gamma = w_gate_up, w_down, gamma
         self.activation, self.eps = activation, float(eps)
         self.max_tokens = int(max_tokens)
-        (rows, self.hidden), (out, self.inner) = w_gate_up[0].shape, w_down[0].shape
+        (rows, self.hidden), (out, self.inner) = _lib._mx8("w_gate_up", *w_gate_up), _lib._mx8("w_down", *w_down)
         if rows != 2 * self.inner or out != self.hidden:
             raise ValueError(f"w_gate_up {tuple(w_gate_up[0].shape)} and w_down {tuple(w_down[0].shape)} "
                              "are not [2 I, C] and [C, I]")

@@ -583,12 +583,16 @@ def ple_proj_w4(x, codes, scales, out, zeros=None, dev_err=None, stream=None):
 # ---- the 8-bit step of the feed-forward block: norm, gated products, projection ----
 
 _ACTIVATIONS = {"silu": PLE_SILU, "gelu": PLE_GELU}
+_INT32_MAX = 2 ** 31 - 1
 
 
 def ple_mx8_scale_bytes(rows, columns):
     """Bytes of the scales of an 8-bit tensor [rows, columns] (0: sizes that
     have none)."""
-    return int(lib().ple_mx8_scale_bytes(int(rows), int(columns)))
+    rows, columns = int(rows), int(columns)
+    if max(abs(rows), abs(columns)) > _INT32_MAX:  # (they would reach the library as what is left in its integers)
+        return 0
+    return int(lib().ple_mx8_scale_bytes(rows, columns))
 
 
 def _mx8_error(name, codes, scales):
@@ -596,7 +600,7 @@ def _mx8_error(name, codes, scales):
     if (codes.dtype is not _U8 or scales.dtype is not _U8 or not (codes.is_contiguous() and scales.is_contiguous())
             or not (codes.is_cuda and scales.is_cuda)):
         return ValueError(f"{name}: contiguous CUDA uint8 tensors are needed, codes [R, C] and scales of one dimension")
-    return ValueError(f"{name}: codes {tuple(codes.shape)} (columns: a multiple of 128) and {scales.numel()} bytes of "
+    return ValueError(f"{name}: codes {tuple(codes.shape)} (columns: a multiple of 128 below 2^31) and {scales.numel()} bytes of "
                       "scales do not fit (ple_mx8_scale_bytes)")
 
 
@@ -607,7 +611,7 @@ def _mx8(name, codes, scales):
             or not (codes.is_cuda and scales.is_cuda)):
         raise _mx8_error(name, codes, scales)
     (R, C), (n,) = codes.shape, scales.shape  # a ValueError, too, where there are more dimensions or fewer
-    if C % 128 != 0 or n < (R + 127) // 128 * (C * 4):
+    if C % 128 != 0 or C > _INT32_MAX or n < (R + 127) // 128 * (C * 4):
         raise _mx8_error(name, codes, scales)
     return R, C
 

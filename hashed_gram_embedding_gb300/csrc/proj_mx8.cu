@@ -12,6 +12,7 @@
 // them, its columns shared out in a cluster: bound by reading W and some 4.5 us
 // of start and end. One token, gated 4096 -> 16384: 24.2 us (5.7 TB/s), 16384 ->
 // 4096: 14.8 (4.7); 203 tokens: 22.7.
+#include "mx8_rule.h"
 #include "mx8_tensor.cuh"
 
 #include <algorithm>
@@ -525,8 +526,8 @@ template <bool kGated, int kTokens>
 struct Few {
   static constexpr int kSides = kGated ? 2 : 1;  // of W
   static constexpr int kXPieces = kTokens > 128 ? 2 : 1;
-  static constexpr int kResident = kTokens <= 64 ? 2 : 1;        // CTAs an SM
-  static constexpr int kMaxParts = kResident == 2 ? 8 : 4;       // CTAs that share the columns
+  static constexpr int kResident = few_resident(kTokens);        // CTAs an SM
+  static constexpr int kMaxParts = few_max_parts(kTokens);       // CTAs that share the columns
   static constexpr int kCodes = kSides * kAtom + kTokens * 128;  // bytes of a stage: an atom
   static constexpr int kScales = (kSides + kXPieces) * kMxPiece;
   static constexpr int kBudget = kResident == 2 ? 110 << 10 : 220 << 10;
@@ -753,15 +754,6 @@ product_few_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_const
   if (parts > 1) cluster_barrier();  // no CTA leaves while its sums are read
 }
 
-// Parts that a cluster cuts the columns into: as many as keep all CTAs on SMs
-// at once and leave each some atoms.
-template <typename L>
-int parts_of(int64_t ctas, int atoms) {
-  int parts = 1;
-  while (parts < L::kMaxParts && ctas * parts * 2 <= int64_t(num_sms()) * L::kResident && atoms >= parts * 2 * 4) parts *= 2;
-  return parts;
-}
-
 template <bool kGated, int kTokens>
 ple_status launch_few(const ProductArgs& a, int32_t* dev_err, cudaStream_t stream, const char* name) {
   using L = Few<kGated, kTokens>;
@@ -776,59 +768,22 @@ ple_status launch_few(const ProductArgs& a, int32_t* dev_err, cudaStream_t strea
   const cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kSmem);
   if (err != cudaSuccess) return check_cuda(err, name);
   const int tiles = (a.N + 127) / 128, blocks = static_cast<int>((a.T + kTokens - 1) / kTokens);
-  const int parts = parts_of<L>(int64_t(tiles) * blocks, a.E / 128);
+  const int parts = few_parts(kTokens, int64_t(tiles) * blocks, a.E / 128, num_sms());
   const dim3 grid(static_cast<unsigned>(tiles * parts), static_cast<unsigned>(blocks));
   return check_cuda(launch_kernel(kernel, grid, dim3(kFewThreads), L::kSmem, stream, static_cast<unsigned>(parts), x, w, a,
                                   parts, wide, dev_err), name);
 }
 
-// What a launch takes, in 10 ns, from measurements: by pairs of CTAs a stage
-// of 256 columns 56, a tile's start and end 330, all else 480, and never less
-// than W's way from memory at 5.2 TB/s and 600; by single ones
-// an atom of 128 columns 41 (gated, 128 tokens: 70), a tile's start and end
-// 800 (300, and 6 for each token: its sums are taken out and joined), all else
-// 70.
-template <bool kGated>
-int64_t time_of_pairs(const ProductArgs& a) {
-  constexpr int kRows = kGated ? 128 : 256;
-  const int64_t units = (a.T + 255) / 256 * ((a.N + kRows - 1) / kRows), pairs = resident_pairs<kGated>();
-  const int64_t w = int64_t(kGated ? 2 : 1) * a.N * a.E;
-  return std::max((units + pairs - 1) / pairs * ((a.E / 128 + 1) / 2 * 56 + 330) + 480, w / 52000 + 600);
-}
-template <typename L>
-int64_t time_of_ctas(const ProductArgs& a, int tokens, int atom, int tile) {
-  const int64_t ctas = (a.N + 127) / 128 * ((a.T + tokens - 1) / tokens);
-  const int atoms = a.E / 128, parts = parts_of<L>(ctas, atoms);
-  return (ctas * parts + num_sms() - 1) / num_sms() * ((atoms + parts - 1) / parts * atom + tile) + 70;
-}
-
-// Few tokens go to single CTAs, with a tile that holds them; many, in blocks of
-// 256, stay there while pairs would leave too much of the GPU idle, and go to
-// pairs otherwise. Measured, pairs / single CTAs, us, tokens over columns x
-// rows:
-//   200  4096 x 4096  15.8 / 11.7   300  8192 x 2048  25.3 / 15.1   400  2048 x 1024  11.0 / 10.3
-//   512  4096 x 4096  16.7 / 15.6   512  2048 x 8192  12.9 / 15.3   768  4096 x 4096  17.2 / 20.6
-//  1023  2048 x 8192  20.0 / 30.1  1024 16384 x 4096  47.9 / 56.9
-// gated:
-//    33  4096 x 4096  16.0 / 11.6    48  2048 x 8192  12.7 / 12.7    64 4096 x 16384  32.2 / 29.3
-//    80  2048 x 8192  12.4 / 14.4   112  4096 x 4096  16.5 / 15.8   112 4096 x 16384  32.5 / 32.9
-//   150  4096 x 4096  16.5 / 19.3   256  2048 x 8192  13.1 / 20.8   512  4096 x  1024  14.4 / 15.4
-// The tiles: 16 tokens are worth one of their own only gated, whose stages are
-// twice as large (16 and 32 wide, one token 4096 x 16384 24.7 / 25.2; 16 tokens
-// 4096 x 4096, not gated, 7.4 / 6.9), 64 only otherwise (64 and 128 wide, 64 tokens
-// 16384 x 4096 17.3 / 17.8; gated 4096 x 4096 15.3 / 13.0).
 template <bool kGated>
 ple_status launch_product(const ProductArgs& a, int32_t* dev_err, cudaStream_t stream, const char* name) {
+  const int tile = product_tile({a.T, a.E, a.N, kGated}, num_sms(), [] { return resident_pairs<kGated>(); });
+  if (tile == 32) return launch_few<kGated, 32>(a, dev_err, stream, name);
+  if (tile == 128) return launch_few<kGated, 128>(a, dev_err, stream, name);
   if constexpr (kGated) {
-    if (a.T <= 16) return launch_few<true, 16>(a, dev_err, stream, name);
-    if (a.T <= 32) return launch_few<true, 32>(a, dev_err, stream, name);
-    if (a.T <= 128 && time_of_ctas<Few<true, 128>>(a, 128, 70, 300 + 6 * static_cast<int>(a.T)) <= time_of_pairs<true>(a))
-      return launch_few<true, 128>(a, dev_err, stream, name);
+    if (tile == 16) return launch_few<true, 16>(a, dev_err, stream, name);
   } else {
-    if (a.T <= 32) return launch_few<false, 32>(a, dev_err, stream, name);
-    if (a.T <= 64) return launch_few<false, 64>(a, dev_err, stream, name);
-    if (a.T <= 128) return launch_few<false, 128>(a, dev_err, stream, name);
-    if (time_of_ctas<Few<false, 256>>(a, 256, 41, 800) < time_of_pairs<false>(a)) return launch_few<false, 256>(a, dev_err, stream, name);
+    if (tile == 64) return launch_few<false, 64>(a, dev_err, stream, name);
+    if (tile == 256) return launch_few<false, 256>(a, dev_err, stream, name);
   }
   return launch_pair<kGated>(a, dev_err, stream, name);
 }

@@ -143,7 +143,8 @@ norm_mx8_kernel(const NormArgs a) {
     float by = rsqrtf(mean);
     // a step of Newton's: the quotient's own rounding is left (an infinite sum makes zeros, and keeps them)
     if (by > 0.0f) by = by * fmaf(-0.5f * mean * by, by, 1.5f);
-    const bool far = live && (!(sum < 1e38f) || (sum < 1e-28f && a.eps < 1e-18f));
+    // (3e38: an eps near float32's largest, with which the mean may leave it)
+    const bool far = live && (!(sum < 1e38f && mean < 3e38f) || (sum < 1e-28f && a.eps < 1e-18f));
     if (blockDim.y > 1 && blockDim.x > 32 ? __syncthreads_or(far) : far) {
       // squares that leave float32: the row in units of a power of two near its
       // largest value (infinities and NaN stay what they are, and so do other

@@ -600,8 +600,8 @@ def _mx8_error(name, codes, scales):
     if (codes.dtype is not _U8 or scales.dtype is not _U8 or not (codes.is_contiguous() and scales.is_contiguous())
             or not (codes.is_cuda and scales.is_cuda)):
         return ValueError(f"{name}: contiguous CUDA uint8 tensors are needed, codes [R, C] and scales of one dimension")
-    return ValueError(f"{name}: codes {tuple(codes.shape)} (columns: a multiple of 128 below 2^31) and {scales.numel()} bytes of "
-                      "scales do not fit (ple_mx8_scale_bytes)")
+    return ValueError(f"{name}: codes {tuple(codes.shape)} (columns: a multiple of 128, below 2^31) and "
+                      f"{scales.numel()} bytes of scales do not fit (ple_mx8_scale_bytes)")
 
 
 def _mx8(name, codes, scales):

@@ -52,6 +52,11 @@ inline int64_t time_of_ctas(const ProductSize& p, int tile, int sms) {
 //   200  4096 x 4096  15.8 / 11.7   300  8192 x 2048  25.3 / 15.1   400  2048 x 1024  11.0 / 10.3
 //   512  4096 x 4096  16.7 / 15.6   512  2048 x 8192  12.9 / 15.3   768  4096 x 4096  17.2 / 20.6
 //  1023  2048 x 8192  20.0 / 30.1  1024 16384 x 4096  47.9 / 56.9
+// up to 128 tokens, where single CTAs always take them; pairs are 6 to 11 %
+// faster past 152 tiles of rows, which is left at that:
+//    32 4096 x 16384  19.8 / 15.5    64 16384 x 4096  45.1 / 17.4    64  2048 x 8192  11.0 /  8.4
+//   128   512 x 8192   8.2 /  6.8   128  4096 x 4096  15.1 /  9.6   128 4096 x 16384  20.7 / 18.5
+//   128 16384 x 4096  45.8 / 19.3   128 4096 x 20000  32.1 / 34.0   128 1024 x 32768  15.9 / 17.8
 // gated:
 //    33  4096 x 4096  16.0 / 11.6    48  2048 x 8192  12.7 / 12.7    64 4096 x 16384  32.2 / 29.3
 //    80  2048 x 8192  12.4 / 14.4   112  4096 x 4096  16.5 / 15.8   112 4096 x 16384  32.5 / 32.9

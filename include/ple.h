@@ -825,6 +825,15 @@ ple_status ple_proj_w4(const ple_bf16_t* x, int64_t x_stride, int64_t num_tokens
  * is row r's of block j. ple_mx8_scale_bytes(rows, columns) is their size,
  * whole pieces; bytes of rows that do not exist are neither used nor written.
  * Codes and scales are 16-byte aligned device memory.
+ *
+ * Sums of the two products are float32 as the tensor cores keep them: where
+ * the products of 32 columns meet the sum, what lies below its last place is
+ * cut off, not rounded (2^-23 of the sum at most; whole numbers of one unit
+ * whose sums stay below 2^24 of it are exact), and products below 2^-126 may be
+ * lost. The order is decided by the sizes, num_tokens among them. The two calls
+ * take up to 4194240 tokens and 2^31 - 256 rows of w (else
+ * PLE_ERR_UNSUPPORTED). A wait inside them that runs out sets
+ * PLE_DEVERR_TIMEOUT in dev_err (or NULL); the result is not to be used then.
  */
 size_t ple_mx8_scale_bytes(int64_t rows, int32_t columns);
 
@@ -847,7 +856,8 @@ ple_status ple_mx8_read(const uint8_t* codes, const uint8_t* scales, int64_t row
  *                itself (same pointer and stride). Any other overlap of an
  *                output is PLE_ERR_INVALID_ARG.
  *   codes, scales  [num_tokens][hidden], as above.
- * Rows up to bf16's largest and down to its least are normalised as any other.
+ * Rows up to bf16's largest and down to its least are normalised as any other
+ * (a sum of two that leaves float32 is an infinity).
  */
 ple_status ple_norm_mx8(const ple_bf16_t* x, int64_t x_stride, const ple_bf16_t* residual,
                         int64_t residual_stride, const ple_bf16_t* gamma, float eps,
@@ -862,10 +872,10 @@ typedef enum { PLE_SILU = 0, PLE_GELU = 1 } ple_activation;
 /*
  * ple_gated_mx8 -- the first half of a gated feed-forward block,
  *   h = act(x Wg^T) * (x Wu^T), (codes, scales) = mx8(h).
- * Float32 sums, in an order that the sizes decide (num_tokens among them);
- * the activation by float32 functions (zeros where exp(-|x|) leaves float32:
- * gates below about -104, of gelu below -10.7);
- * h is not rounded before it is quantised.
+ * Float32 sums, as above; the activation by float32 functions, off by 2^-21 of
+ * itself and, of gelu, 2^-21 of it for each unit of the exponent (zeros where
+ * the exponential leaves float32: gates below about -104, of gelu below
+ * -10.7); h is not rounded before it is quantised.
  *   x, x_scales  mx8 [num_tokens][hidden].
  *   w, w_scales  mx8 [2 * inner][hidden]: Wg's rows, then Wu's.
  *   inner        a multiple of 128 (else PLE_ERR_UNSUPPORTED).
@@ -877,8 +887,7 @@ ple_status ple_gated_mx8(const uint8_t* x, const uint8_t* x_scales, int64_t num_
                          int32_t* dev_err, cudaStream_t stream);
 
 /*
- * ple_proj_mx8 -- out = residual + x W^T, float32 sums in an order that the
- * sizes decide, rounded once.
+ * ple_proj_mx8 -- out = residual + x W^T, float32 sums as above, rounded once.
  *   x, x_scales  mx8 [num_tokens][in_dim].
  *   w, w_scales  mx8 [out_dim][in_dim].
  *   residual     bf16 rows of out_dim, residual_stride elements apart (0: one

@@ -6,12 +6,12 @@
 //
 // Two kernels. For many tokens a pair of CTAs takes 256 tokens against 256
 // rows of W: bound by the tensor cores, their operands' way into the SMs and
-// the power limit. 8192 tokens, 16384 -> 4096: 318 us (3.46 PFLOP/s) in short
-// runs, 376 in long ones, where the clock falls to 1.7 GHz; gated, 4096 ->
-// 16384: 657 us (3.35). For few tokens a CTA takes 128 rows of W against all of
+// the power limit. 8192 tokens, 16384 -> 4096: 316 to 337 us (3.3 to 3.5 PFLOP/s)
+// in short runs, 380 in long ones, where the clock falls to 1.7 GHz; gated, 4096
+// -> 16384: 686 to 701 us (3.2). For few tokens a CTA takes 128 rows of W against all of
 // them, its columns shared out in a cluster: bound by reading W and some 4.5 us
-// of start and end. One token, gated 4096 -> 16384: 24.2 us (5.7 TB/s), 16384 ->
-// 4096: 14.8 (4.7); 203 tokens: 22.7.
+// of start and end. One token, gated 4096 -> 16384: 24.5 to 24.9 us (5.6 TB/s),
+// 16384 -> 4096: 14.5 to 15.1 (4.7); 203 tokens: 22.5 to 23.1.
 #include "mx8_rule.h"
 #include "mx8_tensor.cuh"
 
@@ -67,11 +67,12 @@ __device__ __forceinline__ float activation(float g, int gelu) {
 // The sums take 256 of the 512 columns of tensor memory and the scales 72, so
 // there is one set of sums: the epilogue's eight warps take them out, some
 // 2000 cycles a tile, and give the place back before they store anything. (A
-// second set that shares 72 columns with the first was no faster: what counts
-// between two tiles is when their operands arrive.)
+// second set that shares 72 columns with the first was no faster with tiles of
+// 32 and 64 atoms, where what counts between two tiles is when their operands
+// arrive; with 16 it was not tried.)
 // Tiles are walked in groups of 4096 tokens, tokens first: W is read once for
 // each group, and the group's tokens stay in L2. (Groups of 2048, 1024: gated
-// 8192 tokens 680, 710 us against 657.)
+// 8192 tokens 680, 710 us against 657, all three with a shorter activation.)
 //
 // Warps: 0 copies, 1 issues, 2-9 the epilogue: two for each quarter of the
 // rows, half of the columns each.

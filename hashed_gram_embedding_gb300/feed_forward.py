@@ -46,6 +46,9 @@ class PLEFeedForward:
       max_tokens: the most tokens of a step.
       activation: "silu" or "gelu" (its tanh form).
       eps: of the norm.
+
+    Building one waits for the current stream's work, and so is no part of a
+    graph's capture.
     """
 
     def __init__(self, w_gate_up, w_down, gamma, max_tokens, activation="silu", eps=1e-6):

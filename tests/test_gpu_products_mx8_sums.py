@@ -12,7 +12,7 @@ from oracle import eight_bit as oracle
 
 from _eight_bit import check_mx8, untouched_scales
 from _helpers import dev_err_word
-from _mx8_sums import GATED, PROJ, check_exact, check_sums, exact_operands, left_over, random_operands
+from _mx8_sums import GATED, PROJ, check_exact, check_sums, exact_operands, lay_out, left_over, random_operands
 
 pytestmark = pytest.mark.gpu
 
@@ -86,3 +86,23 @@ def test_gated_exact(t, c, i, name):
     off = np.abs(want) * (11 + (0 if name == "silu" else 5 * np.abs(turn))) * 2.0 ** -24 + np.abs(g * u) * 2.0 ** -148 + 2.0 ** -149
     check_mx8(codes, scales, want, off, name)
     assert untouched_scales(scales, t, i)
+
+
+@pytest.mark.parametrize("t,e,n", [(1, 4096, 300), (50, 4096, 300), (100, 4096, 300), (200, 4096, 300), (1500, 4096, 1000)])
+def test_proj_whole_numbers_to_24_bits(t, e, n):
+    """Sums of whole numbers, all of one sign, that grow past 2^23: float32 holds each on the way."""
+    g = torch.Generator(device="cuda").manual_seed(t)
+
+    def tensor(rows, low):
+        whole = torch.randint(low, 16, (rows, e), generator=g, device="cuda") * \
+            2 ** torch.randint(0, 5, (rows, e), generator=g, device="cuda")
+        codes = whole.float().to(torch.float8_e4m3fn).view(torch.uint8)
+        return (codes, lay_out(torch.full((rows, e // 32), 127, dtype=torch.uint8, device="cuda"))), whole.double()
+
+    (x8, x), (w8, w) = tensor(t, 1), tensor(n, 0)
+    want = x @ w.T
+    assert 2 ** 22.8 < float(want.max()) < 2 ** 24
+    out = torch.empty((t, n), dtype=torch.bfloat16, device="cuda")
+    r = left_over(want)
+    ple.ple_proj_mx8(*x8, *w8, out, residual=r)
+    check_exact(out, want, r)
